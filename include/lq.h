@@ -51,6 +51,7 @@
  *     the *_ragged calls take one per batch row from a device array.
  *   - Token vectors q, k, v and outputs o are fp32 or bf16 (lq_dims.io_dtype);
  *     everything else is fp32 (int8 / int32 where stated).
+ *   - `alpha` for LQ_ALPHA_HEADS ([H], lq_la_* only) needs 4-byte alignment.
  *   - Batch rows are independent: rows b0 .. b1-1 of a batch are a batch of
  *     their own (every pointer advanced by b0 rows, lq_dims.B = b1 - b0), and
  *     calls on disjoint row ranges may run at the same time on different
@@ -75,7 +76,8 @@ enum lq_status {
     LQ_ERR_WINDOW_FULL = 4,   /* decode_step with pos >= W: flush first */
     LQ_ERR_POS = 5,           /* pos < 0, n_buffered outside [0, W], T < 0 */
     LQ_ERR_ALIGN = 6,         /* a pointer is misaligned (see conventions) */
-    LQ_ERR_HIP = 7            /* kernel launch failed, see lq_last_hip_error() */
+    LQ_ERR_HIP = 7,           /* kernel launch failed, see lq_last_hip_error() */
+    LQ_ERR_WORKSPACE = 8      /* workspace smaller than lq_la_workspace_bytes() */
 };
 
 enum lq_decay_mode { LQ_DECAY_SCALAR = 0, LQ_DECAY_PER_KEY = 1 };
@@ -293,6 +295,131 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
                    const void *q, const void *k, const void *v,
                    const float *alpha, const float *beta, void *o, void *stream);
 
+/*
+ * Linear attention with a decay for each head (no delta rule):
+ *     H <- alpha H + k v^T,   o = H^T q  (after the update).
+ * The state has the shape of the delta rule's, so the codec, the window
+ * buffer and the flush are shared: a window slot holds (k_n, g_n, m_n) with
+ * m_n = v_n, and lq_gdn_window_flush(_ragged) rebuilds and requantizes it.
+ * The lq_la_* calls take decay_mode LQ_DECAY_SCALAR (LQ_ERR_UNSUPPORTED
+ * otherwise) and alpha in [0, 1] in one of two forms:
+ *   LQ_ALPHA_TOKENS  one decay per token and head (the token arrays' leading
+ *                    shape: [T,B,H], [B,H], [N,B,H]);
+ *   LQ_ALPHA_HEADS   one fixed decay per head, [H].
+ * alpha = 0 forgets everything before the token (the log decay kept for it,
+ * in buf_g and in sums, is -110: exp(-110) is 0 in fp32).  Values outside
+ * [0, 1] are not checked.
+ */
+enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
+
+/*
+ * Linear attention over a prompt, every head of a batch: outputs of T tokens
+ * and the state after them, computed in chunks (within a chunk o = the
+ * decayed causal products plus the chunk's starting state), accumulated in
+ * fp32.
+ *   h0     nullable fp32 [B,H,dk,dv]: the state before the prompt (NULL: zeros);
+ *   h      fp32 [B,H,dk,dv], out: the state after it; h == h0 is allowed,
+ *          any other overlap is not;
+ *   q, k   [T,B,H,dk];  v, o [T,B,H,dv]  (fp32 or bf16 per d->io_dtype);
+ *   o      nullable: no outputs are formed;
+ *   lens   nullable int32 [B] (device, 4-byte aligned): row b has
+ *          min(max(lens[b], 0), T) tokens.  Its later tokens are not used
+ *          (they may hold anything) and its later o rows are left as they were;
+ *   st     nullable: the codec of h is written (as lq_gdn_prefill);
+ *   workspace  device memory of at least lq_la_workspace_bytes(d, T) bytes,
+ *          16-byte aligned (NULL if that is 0), used until the call's work on
+ *          `stream` is done: calls that may run at the same time need their own.
+ * T = 0 (or a row with no tokens) copies h0 to h.  T = 1 is the recurrent
+ * form over an fp32 state.  With bf16 tokens, products that reach h keep
+ * fp32's 24 bits, those that reach only o at least 16.  A non-finite v reaches
+ * its own column from its own token on.
+ * Errors: LQ_ERR_POS if T < 0; LQ_ERR_DIMS for a bad alpha_kind;
+ * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ */
+int lq_la_prefill(const lq_dims *d, const lq_state *st, const float *h0, float *h, int32_t T,
+                  const void *q, const void *k, const void *v, const float *alpha,
+                  int32_t alpha_kind, const int32_t *lens, void *o, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/* Bytes of lq_la_prefill's workspace for prompts of up to T tokens of these
+ * dims (0: none; also 0 if d is invalid for the lq_la_* calls or T <= 0).
+ * Never less for a larger T. */
+size_t lq_la_workspace_bytes(const lq_dims *d, int32_t T);
+
+/*
+ * One token of linear attention for every (b, h), the recurrent form over the
+ * int8 state: appends slot n = pos = (k, g_n, v) to the window and writes
+ *     o = Hb^T (exp(g_n) q) + sum_{i<n} exp(g_n - g_i) <q, k_i> m_i + <q, k> v.
+ * Arguments as lq_gdn_decode_step without beta; the window is flushed by
+ * lq_gdn_window_flush.  Errors as lq_gdn_decode_step; LQ_ERR_DIMS for a bad
+ * alpha_kind; LQ_ERR_UNSUPPORTED for per-key decay.
+ */
+int lq_la_decode_step(const lq_dims *d, const lq_state *st, int32_t pos,
+                      const void *q, const void *k, const void *v,
+                      const float *alpha, int32_t alpha_kind, void *o, void *stream);
+
+/* Ragged windows: lq_la_decode_step with the position of batch row b read
+ * from the device array pos[b], as lq_gdn_decode_step_ragged (rows outside
+ * [0, W) are left untouched). */
+int lq_la_decode_step_ragged(const lq_dims *d, const lq_state *st, const int32_t *pos,
+                             const void *q, const void *k, const void *v,
+                             const float *alpha, int32_t alpha_kind, void *o, void *stream);
+
+/*
+ * Drafted tokens (speculative decoding): the outputs of a tree of N tokens
+ * per batch row, each as if the tokens on its path from the root had been
+ * decoded after the window's pos[b] slots, with the state, the window and pos
+ * left as they are.  For a node n with parent p (g_p: the parent's log decay;
+ * for p = -1 that of slot pos - 1, or 0) and the context c = window slots
+ * 0..pos-1 and n's ancestors,
+ *     g_n = g_p + log alpha_n,  E_c = exp(g_n - g_c),
+ *     m_n = beta_n (v_n - Hb^T (exp(g_n) o k_n) - sum_c <k_n, E_c o k_c> m_c),
+ *     o_n = Hb^T (exp(g_n) o q_n) + sum_c <q_n, E_c o k_c> m_c + <q_n, k_n> m_n,
+ * the decode step's own sums (lq_gdn_decode_step); m_n = v_n for
+ * lq_la_tree_step.
+ *   N       nodes per row, 1..64 (LQ_ERR_UNSUPPORTED above, LQ_ERR_DIMS below 1);
+ *   pos     int32 [B] (device, 4-byte aligned), buffered tokens of row b,
+ *           0..W; rows outside that range are left untouched;
+ *   parent  int32 [B,N] (device, 4-byte aligned): a node's parent is an
+ *           earlier node of the row or -1 (the last committed token).  Any
+ *           other value, or an absent parent, marks an absent node: its o,
+ *           tree_m and tree_g rows are left untouched and its tokens are not
+ *           used, so rows may draft fewer than N tokens;
+ *   q, k [N,B,H,dk];  v, o [N,B,H,dv];  beta fp32 [N,B,H];
+ *   alpha   as the decode step's with N leading (per-key: [N,B,H,dk]);
+ *   tree_m  fp32 [B,H,N,dv], tree_g fp32 [B,H,N,gd], out: the window slots
+ *           that the nodes would become (lq_tree_commit).
+ * Nodes' depth is not bounded by the window; committed paths are.  A
+ * non-finite node reaches itself and its descendants only.
+ */
+int lq_gdn_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
+                     const int32_t *parent, const void *q, const void *k, const void *v,
+                     const float *alpha, const float *beta, void *o, float *tree_m,
+                     float *tree_g, void *stream);
+int lq_la_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
+                    const int32_t *parent, const void *q, const void *k, const void *v,
+                    const float *alpha, int32_t alpha_kind, void *o, float *tree_m,
+                    float *tree_g, void *stream);
+
+/*
+ * Appends accepted nodes of a tree step to the windows: for row b, slots
+ * pos[b] .. pos[b] + n_path[b] - 1 become the nodes path[b][0..n_path[b]-1]
+ * (k of that node widened to fp32, its tree_m and tree_g rows), exactly the
+ * slots that decoding those tokens would have left.  The caller then advances
+ * pos[b] by n_path[b].
+ *   path    int32 [B,P] (device, 4-byte aligned), the path from its root node
+ *           on; n_path int32 [B] (device, 4-byte aligned);
+ *   N, k, tree_m, tree_g  those of the tree step;
+ *   P       1..N.
+ * A row is left untouched if n_path[b] is outside [1, min(P, W - pos[b])],
+ * pos[b] outside [0, W), or one of its path entries outside [0, N).
+ * Errors: LQ_ERR_DIMS if N < 1, P < 1 or P > N; LQ_ERR_UNSUPPORTED if N > 64;
+ * LQ_ERR_NULL, LQ_ERR_ALIGN.  Only the window buffer of st is used.
+ */
+int lq_tree_commit(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
+                   const int32_t *path, int32_t P, const int32_t *n_path, const void *k,
+                   const float *tree_m, const float *tree_g, void *stream);
+
 /* Bytes of one layer's codec arrays (sq, scales, compensators), i.e.
  * B*H*(dk*dv + 4dk + 4dv + C*(4dv + 4)); 0 if d is NULL or invalid. */
 size_t lq_state_bytes(const lq_dims *d);
@@ -325,7 +452,11 @@ enum {
     LQ_KERNEL_CHECKPOINT = 5,   /* lq_gdn_state_pack / lq_gdn_state_unpack */
     LQ_KERNEL_DECODE_FLUSH = 6, /* lq_gdn_decode_step_flush */
     LQ_KERNEL_PREFILL = 7,      /* lq_gdn_prefill (its quantization: LQ_KERNEL_QUANTIZE) */
-    LQ_KERNEL_MEASURE = 8       /* lq_measure_stream_read */
+    LQ_KERNEL_MEASURE = 8,      /* lq_measure_stream_read */
+    LQ_KERNEL_LA_PREFILL = 9,   /* lq_la_prefill (its quantization: LQ_KERNEL_QUANTIZE) */
+    LQ_KERNEL_LA_DECODE = 10,   /* lq_la_decode_step */
+    LQ_KERNEL_TREE = 11,        /* lq_gdn_tree_step / lq_la_tree_step */
+    LQ_KERNEL_COMMIT = 12       /* lq_tree_commit */
 };
 
 /* on = 1: drop earlier records and start recording (at most 65536 launches;

@@ -66,6 +66,35 @@ int check_ptrs(std::initializer_list<const void*> ps) {
     return LQ_OK;
 }
 
+// Shapes of the lq_la_* calls: one decay per head.
+int check_la(const lq_dims* d, int32_t alpha_kind) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if (alpha_kind != LQ_ALPHA_TOKENS && alpha_kind != LQ_ALPHA_HEADS) return LQ_ERR_DIMS;
+    return d->decay_mode == LQ_DECAY_SCALAR ? LQ_OK : LQ_ERR_UNSUPPORTED;
+}
+
+// Index arrays of a tree call: present and 4-byte aligned.
+int check_indices(std::initializer_list<const void*> ps) {
+    for (const void* p : ps)
+        if (!p) return LQ_ERR_NULL;
+    for (const void* p : ps)
+        if (!aligned4(p)) return LQ_ERR_ALIGN;
+    return LQ_OK;
+}
+
+// A tree's size and outputs.
+int check_tree(int32_t N, const int32_t* pos, const int32_t* parent, const float* tree_m, const float* tree_g,
+               bool per_key) {
+    if (N < 1) return LQ_ERR_DIMS;
+    if (N > lq::kTreeMax) return LQ_ERR_UNSUPPORTED;
+    int rc = check_indices({pos, parent});
+    if (rc) return rc;
+    if (!tree_m || !tree_g) return LQ_ERR_NULL;
+    if (!aligned16(tree_m) || (per_key ? !aligned16(tree_g) : !aligned4(tree_g))) return LQ_ERR_ALIGN;
+    return LQ_OK;
+}
+
 int finish(hipError_t e) {
     if (e != hipSuccess) {
         g_last_hip = (int)e;
@@ -258,6 +287,97 @@ int lq_gdn_prefill(const lq_dims* d, const lq_state* st, float* h, int32_t T, co
     return st ? finish(lq::launch_quantize(*d, h, *st, s)) : LQ_OK;
 }
 
+int lq_la_prefill(const lq_dims* d, const lq_state* st, const float* h0, float* h, int32_t T, const void* q,
+                  const void* k, const void* v, const float* alpha, int32_t alpha_kind, const int32_t* lens,
+                  void* o, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_la(d, alpha_kind);
+    if (rc) return rc;
+    if (st && (rc = check_state(d, st, false))) return rc;
+    if ((rc = check_ptrs({h}))) return rc;
+    if (h0 && !aligned16(h0)) return LQ_ERR_ALIGN;
+    if (lens && !aligned4(lens)) return LQ_ERR_ALIGN;
+    if (T < 0) return LQ_ERR_POS;
+    if (T > 0 && (rc = check_tokens(d, q, k, v, alpha, alpha, o, false))) return rc;
+    const size_t need = lq_la_workspace_bytes(d, T);
+    if (need > 0) {
+        if (!workspace) return LQ_ERR_NULL;
+        if (!aligned16(workspace)) return LQ_ERR_ALIGN;
+        if (workspace_bytes < need) return LQ_ERR_WORKSPACE;
+    }
+    const hipStream_t s = (hipStream_t)stream;
+    if ((rc = finish(lq::launch_la_prefill(*d, h0, h, T, q, k, v, alpha, alpha_kind == LQ_ALPHA_HEADS, lens, o,
+                                           workspace, s))))
+        return rc;
+    return st ? finish(lq::launch_quantize(*d, h, *st, s)) : LQ_OK;
+}
+
+size_t lq_la_workspace_bytes(const lq_dims* d, int32_t T) {
+    return check_la(d, LQ_ALPHA_TOKENS) == LQ_OK && T > 0 ? lq::la_workspace_bytes(*d, T) : 0;
+}
+
+int lq_la_decode_step(const lq_dims* d, const lq_state* st, int32_t pos, const void* q, const void* k,
+                      const void* v, const float* alpha, int32_t alpha_kind, void* o, void* stream) {
+    int rc = check_la(d, alpha_kind);
+    if (rc) return rc;
+    if ((rc = check_state(d, st, true))) return rc;
+    if ((rc = check_tokens(d, q, k, v, alpha, alpha, o, true))) return rc;
+    if (pos < 0) return LQ_ERR_POS;
+    if (pos >= d->W) return LQ_ERR_WINDOW_FULL;
+    return finish(lq::launch_la_decode(*d, *st, pos, nullptr, q, k, v, alpha, alpha_kind == LQ_ALPHA_HEADS, o,
+                                       (hipStream_t)stream));
+}
+
+int lq_la_decode_step_ragged(const lq_dims* d, const lq_state* st, const int32_t* pos, const void* q,
+                             const void* k, const void* v, const float* alpha, int32_t alpha_kind, void* o,
+                             void* stream) {
+    int rc = check_la(d, alpha_kind);
+    if (rc) return rc;
+    if ((rc = check_state(d, st, true))) return rc;
+    if ((rc = check_tokens(d, q, k, v, alpha, alpha, o, true))) return rc;
+    if ((rc = check_indices({pos}))) return rc;
+    return finish(lq::launch_la_decode(*d, *st, 0, pos, q, k, v, alpha, alpha_kind == LQ_ALPHA_HEADS, o,
+                                       (hipStream_t)stream));
+}
+
+int lq_gdn_tree_step(const lq_dims* d, const lq_state* st, const int32_t* pos, int32_t N, const int32_t* parent,
+                     const void* q, const void* k, const void* v, const float* alpha, const float* beta, void* o,
+                     float* tree_m, float* tree_g, void* stream) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if ((rc = check_state(d, st, true))) return rc;
+    if ((rc = check_tokens(d, q, k, v, alpha, beta, o, true))) return rc;
+    if ((rc = check_tree(N, pos, parent, tree_m, tree_g, d->decay_mode == LQ_DECAY_PER_KEY))) return rc;
+    return finish(lq::launch_tree(*d, *st, pos, N, parent, q, k, v, alpha, false, beta, o, tree_m, tree_g,
+                                  (hipStream_t)stream));
+}
+
+int lq_la_tree_step(const lq_dims* d, const lq_state* st, const int32_t* pos, int32_t N, const int32_t* parent,
+                    const void* q, const void* k, const void* v, const float* alpha, int32_t alpha_kind, void* o,
+                    float* tree_m, float* tree_g, void* stream) {
+    int rc = check_la(d, alpha_kind);
+    if (rc) return rc;
+    if ((rc = check_state(d, st, true))) return rc;
+    if ((rc = check_tokens(d, q, k, v, alpha, alpha, o, true))) return rc;
+    if ((rc = check_tree(N, pos, parent, tree_m, tree_g, false))) return rc;
+    return finish(lq::launch_tree(*d, *st, pos, N, parent, q, k, v, alpha, alpha_kind == LQ_ALPHA_HEADS, nullptr, o,
+                                  tree_m, tree_g, (hipStream_t)stream));
+}
+
+int lq_tree_commit(const lq_dims* d, const lq_state* st, const int32_t* pos, int32_t N, const int32_t* path,
+                   int32_t P, const int32_t* n_path, const void* k, const float* tree_m, const float* tree_g,
+                   void* stream) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if (!st) return LQ_ERR_NULL;
+    if (N < 1 || P < 1 || P > N) return LQ_ERR_DIMS;
+    if (N > lq::kTreeMax) return LQ_ERR_UNSUPPORTED;
+    if ((rc = check_indices({pos, path, n_path}))) return rc;
+    if ((rc = check_ptrs({st->buf_k, st->buf_m, st->buf_g, k, tree_m}))) return rc;
+    if (!tree_g) return LQ_ERR_NULL;
+    if (d->decay_mode == LQ_DECAY_PER_KEY ? !aligned16(tree_g) : !aligned4(tree_g)) return LQ_ERR_ALIGN;
+    return finish(lq::launch_tree_commit(*d, *st, pos, N, path, P, n_path, k, tree_m, tree_g, (hipStream_t)stream));
+}
+
 size_t lq_checkpoint_bytes(const lq_dims* d) {
     if (check_dims(d) != LQ_OK) return 0;
     return (size_t)d->B * d->H * lq::checkpoint_head_bytes(*d);
@@ -303,6 +423,7 @@ const char* lq_status_str(int status) {
         case LQ_ERR_POS: return "window position or token count out of range";
         case LQ_ERR_ALIGN: return "misaligned pointer (16 bytes; 4 for beta and scalar alpha)";
         case LQ_ERR_HIP: return "HIP launch failed";
+        case LQ_ERR_WORKSPACE: return "workspace smaller than lq_la_workspace_bytes()";
         default: return "unknown status";
     }
 }

@@ -21,9 +21,10 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("LQ_LIB") or os.path.join(_PKG, "liblq.so")
 
 LQ_OK, LQ_ERR_NULL, LQ_ERR_DIMS, LQ_ERR_UNSUPPORTED, LQ_ERR_WINDOW_FULL, LQ_ERR_POS, \
-    LQ_ERR_ALIGN, LQ_ERR_HIP = range(8)
+    LQ_ERR_ALIGN, LQ_ERR_HIP, LQ_ERR_WORKSPACE = range(9)
 LQ_DECAY_SCALAR, LQ_DECAY_PER_KEY = 0, 1
 LQ_IO_F32, LQ_IO_BF16 = 0, 1
+LQ_ALPHA_TOKENS, LQ_ALPHA_HEADS = 0, 1
 
 # every symbol include/lq.h declares
 EXPORTS = ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_ragged",
@@ -32,10 +33,13 @@ EXPORTS = ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_ragg
            "lq_buffer_bytes", "lq_status_str", "lq_last_hip_error", "lq_check_dims",
            "lq_timing_enable", "lq_timing_collect", "lq_checkpoint_bytes", "lq_gdn_state_pack",
            "lq_gdn_state_unpack", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
-           "lq_gdn_decode_step_flush_ragged", "lq_measure_stream_read")
+           "lq_gdn_decode_step_flush_ragged", "lq_measure_stream_read", "lq_la_prefill",
+           "lq_la_workspace_bytes", "lq_la_decode_step", "lq_la_decode_step_ragged",
+           "lq_gdn_tree_step", "lq_la_tree_step", "lq_tree_commit")
 LQ_KERNEL_DECODE, LQ_KERNEL_FLUSH, LQ_KERNEL_QUANTIZE, LQ_KERNEL_DEQUANTIZE, \
     LQ_KERNEL_FP32_RECURRENCE, LQ_KERNEL_CHECKPOINT, LQ_KERNEL_DECODE_FLUSH, \
-    LQ_KERNEL_PREFILL, LQ_KERNEL_MEASURE = range(9)
+    LQ_KERNEL_PREFILL, LQ_KERNEL_MEASURE, LQ_KERNEL_LA_PREFILL, LQ_KERNEL_LA_DECODE, \
+    LQ_KERNEL_TREE, LQ_KERNEL_COMMIT = range(13)
 
 
 class lq_dims(ct.Structure):
@@ -78,7 +82,17 @@ def load() -> ct.CDLL:
         L.lq_gdn_state_quantize.argtypes = [D, P, S, P]
         L.lq_gdn_state_dequantize.argtypes = [D, S, P, P]
         L.lq_gdn_fp32_recurrence.argtypes = [D, P, I, P, P, P, P, P, P, P]
+        L.lq_la_prefill.argtypes = [D, S, P, P, I, P, P, P, P, I, P, P, P, ct.c_size_t, P]
+        L.lq_la_workspace_bytes.argtypes = [D, I]
+        L.lq_la_workspace_bytes.restype = ct.c_size_t
+        L.lq_la_decode_step.argtypes = [D, S, I, P, P, P, P, I, P, P]
+        L.lq_la_decode_step_ragged.argtypes = [D, S, P, P, P, P, P, I, P, P]
+        L.lq_gdn_tree_step.argtypes = [D, S, P, I, P, P, P, P, P, P, P, P, P, P]
+        L.lq_la_tree_step.argtypes = [D, S, P, I, P, P, P, P, P, I, P, P, P, P]
+        L.lq_tree_commit.argtypes = [D, S, P, I, P, I, P, P, P, P, P]
         for f in ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
+                  "lq_la_prefill", "lq_la_decode_step", "lq_la_decode_step_ragged", "lq_gdn_tree_step",
+                  "lq_la_tree_step", "lq_tree_commit",
                   "lq_gdn_decode_step_flush_ragged", "lq_gdn_decode_step_ragged",
                   "lq_gdn_window_flush_ragged", "lq_gdn_state_quantize",
                   "lq_gdn_state_dequantize", "lq_gdn_fp32_recurrence", "lq_check_dims",
@@ -412,6 +426,171 @@ def lq_gdn_prefill(d: lq_dims, st, h, T: int, q, k, v, alpha, beta, o=None, stre
                                _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(o),
                                _stream(stream))
     _raise("lq_gdn_prefill", rc)
+
+
+def _launch(fn, device, stream, *args):
+    """Calls fn with the stream (None: device's current stream) on the device that
+    holds its tensors, whichever device is the current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    f = getattr(load(), fn)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream.cuda_stream)
+    _raise(fn, rc)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} on {t.device}, expected {device}")
+
+
+def _alpha_kind(d: lq_dims, alpha, shape):
+    """LQ_ALPHA_HEADS for one decay per head ([H]), LQ_ALPHA_TOKENS for one per token."""
+    if alpha is not None and alpha.dim() == 1:
+        _check(alpha, "alpha", (d.H,), torch.float32)
+        return LQ_ALPHA_HEADS
+    _check(alpha, "alpha", shape, torch.float32)
+    return LQ_ALPHA_TOKENS
+
+
+def lq_la_workspace_bytes(d: lq_dims, T: int) -> int:
+    """Bytes of lq_la_prefill's workspace for prompts of up to T tokens."""
+    return int(load().lq_la_workspace_bytes(ct.byref(d), int(T)))
+
+
+def lq_la_prefill(d: lq_dims, st, h0, h, T: int, q, k, v, alpha, o=None, lens=None, workspace=None,
+                  stream=None):
+    """Linear attention over a prompt: o (or None) and the state h after T tokens
+    from h0 (None: zeros; h0 may be h), then the codec of h into st (or None).
+    alpha: [T,B,H], or [H] for one fixed decay per head.  lens: device int32 [B]
+    tokens per row, or None.  workspace: device uint8 tensor of at least
+    lq_la_workspace_bytes(d, T) bytes (None: allocated for this call)."""
+    T = int(T)
+    _check(h, "h", (d.B, d.H, d.dk, d.dv), torch.float32)
+    dev = h.device
+    if h0 is not None:
+        _check(h0, "h0", (d.B, d.H, d.dk, d.dv), torch.float32)
+        if h0.data_ptr() != h.data_ptr():
+            n = h.numel() * 4
+            if abs(h0.data_ptr() - h.data_ptr()) < n:
+                raise ValueError("h0 and h overlap")
+    kind = LQ_ALPHA_TOKENS
+    if T > 0:
+        sh = _token_shapes(d, T)
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _check(t, name, sh[name], _dtype_of(d, name))
+        kind = _alpha_kind(d, alpha, sh["alpha"])
+        if o is not None:
+            _check(o, "o", sh["o"], _dtype_of(d, "o"))
+    if lens is not None:
+        _check(lens, "lens", (d.B,), torch.int32)
+    cs = None
+    if st is not None:
+        cs = st.ready(with_buffer=False)
+        _same_device(dev, st=st.sq)
+    need = lq_la_workspace_bytes(d, T)
+    if workspace is None and need:
+        with torch.cuda.stream(stream):              # memory of the stream that uses it
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    size = 0
+    if workspace is not None:
+        size = workspace.numel()
+        _check(workspace, "workspace", (size,), torch.uint8)
+    _same_device(dev, h0=h0, q=q, k=k, v=v, alpha=alpha, o=o, lens=lens, workspace=workspace)
+    _launch("lq_la_prefill", dev, stream, ct.byref(d), ct.byref(cs) if cs is not None else None, _ptr(h0), _ptr(h),
+            T, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), kind, _ptr(lens), _ptr(o),
+            _ptr(workspace) if size else None, size)
+
+
+def _la_decode(fn, st, pos, q, k, v, alpha, o, stream, pos_arg):
+    d = st.dims
+    sh = _token_shapes(d)
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+        _check(t, name, sh[name], _dtype_of(d, name))
+    kind = _alpha_kind(d, alpha, sh["alpha"])
+    cs = st.ready()
+    dev = st.sq.device
+    _same_device(dev, q=q, k=k, v=v, alpha=alpha, o=o)
+    _launch(fn, dev, stream, ct.byref(d), ct.byref(cs), pos_arg, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), kind,
+            _ptr(o))
+
+
+def lq_la_decode_step(st: LayerState, pos: int, q, k, v, alpha, o, stream=None):
+    """One token of linear attention into slot pos; alpha [B,H], or [H] (fixed per head)."""
+    _la_decode("lq_la_decode_step", st, pos, q, k, v, alpha, o, stream, int(pos))
+
+
+def lq_la_decode_step_ragged(st: LayerState, pos, q, k, v, alpha, o, stream=None):
+    """pos: device int32 [B], the window position of each batch row."""
+    _check(pos, "pos", (st.dims.B,), torch.int32)
+    _same_device(st.sq.device, pos=pos)
+    _la_decode("lq_la_decode_step_ragged", st, pos, q, k, v, alpha, o, stream, _ptr(pos))
+
+
+def _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, **more):
+    d = st.dims
+    if parent is None or parent.dim() != 2:
+        raise ValueError("parent: a [B,N] tensor is required")
+    N = parent.shape[1]
+    sh = _token_shapes(d, N)
+    _check(pos, "pos", (d.B,), torch.int32)
+    _check(parent, "parent", (d.B, N), torch.int32)
+    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
+        _check(t, name, sh[name], _dtype_of(d, name))
+    gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
+    _check(tree_m, "tree_m", (d.B, d.H, N, d.dv), torch.float32)
+    _check(tree_g, "tree_g", (d.B, d.H, N, gd), torch.float32)
+    _same_device(st.sq.device, pos=pos, parent=parent, q=q, k=k, v=v, o=o, tree_m=tree_m, tree_g=tree_g, **more)
+    return N, sh
+
+
+def lq_gdn_tree_step(st: LayerState, pos, parent, q, k, v, alpha, beta, o, tree_m, tree_g, stream=None):
+    """Outputs of the N drafted tokens of every row's tree (parent: device int32 [B,N])
+    after the window's pos (device int32 [B]) slots; state, window and pos are left as
+    they are.  tree_m [B,H,N,dv] and tree_g [B,H,N,gd] receive the nodes' slots."""
+    d = st.dims
+    N, sh = _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, alpha=alpha, beta=beta)
+    _check(alpha, "alpha", sh["alpha"], torch.float32)
+    _check(beta, "beta", sh["beta"], torch.float32)
+    cs = st.ready()
+    _launch("lq_gdn_tree_step", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(parent), _ptr(q),
+            _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(o), _ptr(tree_m), _ptr(tree_g))
+
+
+def lq_la_tree_step(st: LayerState, pos, parent, q, k, v, alpha, o, tree_m, tree_g, stream=None):
+    """lq_gdn_tree_step for plain linear attention; alpha [N,B,H], or [H] (fixed per head)."""
+    d = st.dims
+    N, sh = _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, alpha=alpha)
+    kind = _alpha_kind(d, alpha, sh["alpha"])
+    cs = st.ready()
+    _launch("lq_la_tree_step", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(parent), _ptr(q),
+            _ptr(k), _ptr(v), _ptr(alpha), kind, _ptr(o), _ptr(tree_m), _ptr(tree_g))
+
+
+def lq_tree_commit(st: LayerState, pos, path, n_path, k, tree_m, tree_g, stream=None):
+    """Appends the nodes path[b][:n_path[b]] (device int32 [B,P], [B]) of a tree step to
+    the windows, slots pos[b] on; the caller then advances pos by n_path."""
+    d = st.dims
+    if k is None or k.dim() != 4 or path is None or path.dim() != 2:
+        raise ValueError("k: the tree's [N,B,H,dk] tensor and path: a [B,P] tensor are required")
+    N, P = k.shape[0], path.shape[1]
+    gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
+    _check(pos, "pos", (d.B,), torch.int32)
+    _check(path, "path", (d.B, P), torch.int32)
+    _check(n_path, "n_path", (d.B,), torch.int32)
+    _check(k, "k", _token_shapes(d, N)["k"], _dtype_of(d, "k"))
+    _check(tree_m, "tree_m", (d.B, d.H, N, d.dv), torch.float32)
+    _check(tree_g, "tree_g", (d.B, d.H, N, gd), torch.float32)
+    cs = st.ready()
+    _same_device(st.sq.device, pos=pos, path=path, n_path=n_path, k=k, tree_m=tree_m, tree_g=tree_g)
+    _launch("lq_tree_commit", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(path), P,
+            _ptr(n_path), _ptr(k), _ptr(tree_m), _ptr(tree_g))
 
 
 def lq_checkpoint_bytes(d: lq_dims) -> int:
