@@ -164,9 +164,441 @@ __global__ __launch_bounds__(LP<D>::NT) void la_prefill_kernel(LaPrefillArgs a) 
                 a.h[hoff + (size_t)(rt * 16 + 4 * lg + v) * D + (w * CTW + ct) * 16 + li] = H[rt][ct][v];
 }
 
+// ---------------------------------------------------------------------------
+// bf16 tokens, d >= 64: chunks of 64 tokens on bf16 matrix products
+// ---------------------------------------------------------------------------
+// q, k and v enter the products as they are.  Every other operand is an fp32
+// value split into bf16 parts, whose products with a bf16 token are exact and
+// accumulate in fp32:
+//   state update   K^T (w o V), w_t = e^{g_L - g_t}: w v in 3 parts (24 bits);
+//   outputs        Q H with H in 2 parts and (E o Q K^T) V with the scores in 2
+//                  parts: at least 16 bits, 2^-16 of a sum of absolute values,
+//                  under the 2^-9 that the bf16 output keeps.
+// The wave's D/NW = 32 columns are 2 column tiles; tile ct holds the columns
+// 2 li + ct, so a lane's two columns are one dword of a token row: V is loaded
+// straight into operand order (lane group lg: tokens 8 lg .. 8 lg + 7 of 32),
+// and outputs and the state leave as whole dwords and 8-byte pairs.
+// H tiles are the B operand of Q H with the channels of each 32-block in the
+// order (4 lg + e, 16 + 4 lg + e); Q and K rows are stored in that order.
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int BL = 64;        // tokens per chunk
+
+struct LaSegArgs {
+    const float* start;       // states before each segment, or null: zeros
+    float* end;               // states after each segment, or null: not needed
+    float* decay;             // e^{g} over each segment, or null
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* alpha;
+    const int32_t* lens;
+    void* o;
+    size_t seg_stride;        // floats between the states of consecutive segments
+    int T, H, heads, alpha_tok;
+    int seg;                  // tokens per segment (a multiple of BL)
+};
+
 template <int D>
-hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, hipStream_t s) {
+struct LB {
+    static constexpr int NW = D / 32, NT = 64 * NW;
+    static constexpr int RT = D / 16;
+    static constexpr int QS = D + 8;           // shorts per Q / K row: 16-byte reads of 8 rows hit all banks
+    static constexpr int TS = BL + 8;          // shorts per K^T / score row
+};
+
+// Two fp32 values to packed bf16 (nearest even), low half first.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 r = {(__bf16)a, (__bf16)b};
+    return __builtin_bit_cast(uint32_t, r);
+}
+__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+// Upper halves of (a, b) as packed bf16: truncation to 8 bits.
+__device__ __forceinline__ uint32_t top_halves(float a, float b) {
+    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+__device__ __forceinline__ float top_f32(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// Whether either bf16 of x is infinite or NaN.
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+
+__device__ __forceinline__ v4f mfma_bf16(u32x4 a, u32x4 b, v4f c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(__attribute__((ext_vector_type(8))) __bf16, a),
+                                                   __builtin_bit_cast(__attribute__((ext_vector_type(8))) __bf16, b), c,
+                                                   0, 0, 0);
+}
+
+template <int D, bool OUT>
+__global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
+    using P = LB<D>;
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QS = P::QS, TS = P::TS;
+    __shared__ __align__(16) uint16_t sQ[OUT ? BL * QS : 8];
+    __shared__ __align__(16) uint16_t sK[OUT ? BL * QS : 8];
+    __shared__ __align__(16) uint16_t sT[D * TS];                  // K^T: [channel][token]
+    __shared__ __align__(16) uint16_t sP[OUT ? 2 * BL * TS : 8];   // scores, upper and lower parts
+    __shared__ double sG[BL];
+    __shared__ __align__(16) float sE[BL], sW[BL];                 // e^{g_n}, e^{g_L - g_n}
+
+    const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const size_t head = blockIdx.x, heads = (size_t)a.heads;
+    const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int t0 = (int)blockIdx.y * a.seg;                        // < T: one segment per started seg tokens
+    const int te = min(len, t0 + a.seg);
+    const uint32_t* gq = static_cast<const uint32_t*>(a.q);
+    const uint32_t* gk = static_cast<const uint32_t*>(a.k);
+    const uint32_t* gv = static_cast<const uint32_t*>(a.v);
+    constexpr int RD = D / 2;                                      // dwords per token row
+    const int band = 16 * w + li;                                  // the lane's dword of a V / O row
+    const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
+
+    // H[rt][ct][v] = H[16 rt + 4 lg + v][32 w + 2 li + ct]
+    v4f H[RT][2];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            f32x2 x = {0.f, 0.f};
+            if (a.start) x = *reinterpret_cast<const f32x2*>(a.start + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
+            H[rt][0][v] = x[0];
+            H[rt][1][v] = x[1];
+        }
+    if constexpr (OUT) {
+        // score tiles right of the diagonal inside a 32-token step: zeros, never written again
+        for (int e = t; e < 2 * 2 * 16 * 8; e += NT) {
+            const int part = e >> 8, blk = (e >> 7) & 1, row = (e >> 3) & 15, c = e & 7;
+            *reinterpret_cast<uint32_t*>(&sP[(part * BL + 32 * blk + row) * TS + 32 * blk + 16 + 2 * c]) = 0;
+        }
+    }
+
+    // chunk loads in registers, one chunk ahead; tokens past the end repeat the last one and are zeroed in LDS
+    const int kpair = lane % (D / 2), ksub = lane / (D / 2);       // channel pair; octet within a wave's pass
+    constexpr int OPW = 128 / D;                                   // octets per wave and pass (D = 64: 2)
+    uint32_t kd[2][8], vd[2][8];
+    u32x4 qd[4];
+    float al;
+    auto load = [&](int c0) {
+        const int last = te - 1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int tok = min(c0 + 8 * ((2 * w + j) * OPW + ksub) + e, last);
+                kd[j][e] = gk[((size_t)tok * heads + head) * RD + kpair];
+            }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int tok = min(c0 + 32 * j + 8 * lg + e, last);
+                vd[j][e] = gv[((size_t)tok * heads + head) * RD + band];
+            }
+        if constexpr (OUT)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = t + NT * j, tok = min(c0 + e / (D / 8), last);
+                qd[j] = *reinterpret_cast<const u32x4*>(gq + ((size_t)tok * heads + head) * RD + 4 * (e % (D / 8)));
+            }
+        if (w == 0) {
+            const int tok = min(c0 + lane, last);
+            al = a.alpha_tok ? a.alpha[(size_t)tok * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
+        }
+    };
+    if (t0 < te) load(t0);
+    double gtot = 0.0;                                             // (wave 0) log decay of the segment so far
+
+    for (int c0 = t0; c0 < te; c0 += BL) {
+        const int L = min(BL, te - c0);
+        // ---- registers -> LDS ----
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int oct = (2 * w + j) * OPW + ksub;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (8 * oct + e >= L) kd[j][e] = 0;
+            u32x4 x0, x1;                                          // 8 tokens of the pair's two channels
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x0[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x05040100u);
+                x1[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x07060302u);
+            }
+            *reinterpret_cast<u32x4*>(&sT[(2 * kpair) * TS + 8 * oct]) = x0;
+            *reinterpret_cast<u32x4*>(&sT[(2 * kpair + 1) * TS + 8 * oct]) = x1;
+            if constexpr (OUT) {
+                // channels (c, c + 1), c = 2 kpair, in the operand order of their 32-block
+                const int u = (2 * kpair & 31) >> 2;
+                const int at = (2 * kpair & ~31) + 8 * (u & 3) + 4 * (u >> 2) + (2 * kpair & 3);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(&sK[(8 * oct + e) * QS + at]) = kd[j][e];
+            }
+        }
+        if constexpr (OUT)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = t + NT * j, row = e / (D / 8), c = 8 * (e % (D / 8));
+                if (row >= L) qd[j] = u32x4{0, 0, 0, 0};
+                const int u = (c & 31) >> 2;                       // two groups of 4 channels: u, u + 1
+                uint16_t* at = &sQ[row * QS + (c & ~31) + 4 * (u >> 2)];
+                *reinterpret_cast<u32x2*>(at + 8 * (u & 3)) = u32x2{qd[j][0], qd[j][1]};
+                *reinterpret_cast<u32x2*>(at + 8 * ((u + 1) & 3)) = u32x2{qd[j][2], qd[j][3]};
+            }
+        u32x4 V[2][2];                                             // B operands: [32-token step][ct]
+        uint32_t odd = 0;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (32 * j + 8 * lg + e >= L) vd[j][e] = 0;
+                odd |= odd_bf16(vd[j][e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                V[j][0][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x05040100u);
+                V[j][1][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x07060302u);
+            }
+        }
+        if (w == 0) {
+            double g = lane < L ? (double)log_decay(al) : 0.0;
+#pragma unroll
+            for (int m = 1; m < 64; m <<= 1) {
+                const double x = __shfl_up(g, m, 64);
+                if (lane >= m) g += x;
+            }
+            const double gl = __shfl(g, 63, 64);
+            sG[lane] = g;
+            sE[lane] = expf((float)g);
+            sW[lane] = expf((float)(gl - g));
+            gtot += gl;
+        }
+        __syncthreads();
+        if (c0 + BL < te) load(c0 + BL);
+
+        const float egl = sE[BL - 1];
+        if constexpr (OUT) {
+            // ---- scores: the 10 tiles on and below the diagonal, over the waves ----
+#pragma unroll 1
+            for (int x = w; x < 10; x += NW) {
+                const int r = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, c = x - r * (r + 1) / 2;
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks)
+                    acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[(16 * r + li) * QS + 32 * ks + 8 * lg]),
+                                    *reinterpret_cast<const u32x4*>(&sK[(16 * c + li) * QS + 32 * ks + 8 * lg]), acc);
+                const int i = 16 * c + li;
+                const double gi = sG[i];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * r + 4 * lg + v;
+                    const float p = i <= n ? expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
+                    const float hi = top_f32(p);
+                    sP[n * TS + i] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sP[(BL + n) * TS + i] = (uint16_t)(pack_bf16(p - hi, 0.0f) & 0xffffu);
+                }
+            }
+            // ---- O = e^g o (Q H) ----
+            v4f O[4][2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) O[r][0] = O[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                u32x4 bh[2], bl[2];
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const v4f x = H[2 * ks + hf][ct];
+                        bh[ct][2 * hf] = top_halves(x[0], x[1]);
+                        bh[ct][2 * hf + 1] = top_halves(x[2], x[3]);
+                        bl[ct][2 * hf] = pack_bf16(x[0] - top_f32(x[0]), x[1] - top_f32(x[1]));
+                        bl[ct][2 * hf + 1] = pack_bf16(x[2] - top_f32(x[2]), x[3] - top_f32(x[3]));
+                    }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[(16 * r + li) * QS + 32 * ks + 8 * lg]);
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct) {
+                        O[r][ct] = mfma_bf16(aq, bh[ct], O[r][ct]);
+                        O[r][ct] = mfma_bf16(aq, bl[ct], O[r][ct]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const v4f e = *reinterpret_cast<const v4f*>(&sE[16 * r + 4 * lg]);
+                O[r][0] *= e;
+                O[r][1] *= e;
+            }
+            __syncthreads();                                       // the scores are written
+            // ---- O += (E o Q K^T) V ----
+            const bool any_odd = __any(odd != 0);
+            u32x4 VF[2][2];                                        // finite values only: 0 * v must stay 0
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) VF[j][ct] = V[j][ct];
+            if (any_odd)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t x = odd_bf16(V[j][ct][e]);
+                            VF[j][ct][e] &= ((x & 0x8000u) ? 0u : 0xffffu) | ((x & 0x80000000u) ? 0u : 0xffff0000u);
+                        }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j <= r / 2; ++j)
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        const u32x4 ap = *reinterpret_cast<const u32x4*>(&sP[(part * BL + 16 * r + li) * TS + 32 * j + 8 * lg]);
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(ap, VF[j][ct], O[r][ct]);
+                    }
+            if (any_odd)
+#pragma unroll 1
+                for (int i = 0; i < L; ++i) {
+                    const uint32_t x = gv[((size_t)(c0 + i) * heads + head) * RD + band];
+                    const uint32_t od = odd_bf16(x);
+                    if (od)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const int n = 16 * r + 4 * lg + v;
+                                const float p = n < i ? 0.0f
+                                                      : bf16_to_f32(sP[n * TS + i]) + bf16_to_f32(sP[(BL + n) * TS + i]);
+                                if (n >= i && (od & 0x8000u)) O[r][0][v] += p * lo_f32(x);
+                                if (n >= i && (od & 0x80000000u)) O[r][1][v] += p * hi_f32(x);
+                            }
+                }
+            uint32_t* go = static_cast<uint32_t*>(a.o);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * r + 4 * lg + v;
+                    if (n < L) st_nt(go + ((size_t)(c0 + n) * heads + head) * RD + band, pack_bf16(O[r][0][v], O[r][1][v]));
+                }
+        }
+        // ---- H = e^{g_L} H + K^T (w o V) ----
+        if (a.end || c0 + BL < te) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                H[rt][0] *= egl;
+                H[rt][1] *= egl;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const v4f w0 = *reinterpret_cast<const v4f*>(&sW[32 * j + 8 * lg]);
+                const v4f w1 = *reinterpret_cast<const v4f*>(&sW[32 * j + 8 * lg + 4]);
+                u32x4 b[3][2];
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x0 = (e < 2 ? w0[2 * e] : w1[2 * e - 4]) * lo_f32(V[j][ct][e]);
+                        const float x1 = (e < 2 ? w0[2 * e + 1] : w1[2 * e - 3]) * hi_f32(V[j][ct][e]);
+                        b[0][ct][e] = top_halves(x0, x1);
+                        const float y0 = x0 - top_f32(x0), y1 = x1 - top_f32(x1);
+                        b[1][ct][e] = top_halves(y0, y1);
+                        b[2][ct][e] = top_halves(y0 - top_f32(y0), y1 - top_f32(y1));
+                    }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const u32x4 ak = *reinterpret_cast<const u32x4*>(&sT[(16 * rt + li) * TS + 32 * j + 8 * lg]);
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                        for (int part = 0; part < 3; ++part) H[rt][ct] = mfma_bf16(ak, b[part][ct], H[rt][ct]);
+                }
+            }
+        }
+        __syncthreads();                                           // LDS is rewritten by the next chunk
+    }
+    if (a.end)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                *reinterpret_cast<f32x2*>(a.end + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band) =
+                    f32x2{H[rt][0][v], H[rt][1][v]};
+    if (a.decay && t == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
+}
+
+// States before each segment from the states of each segment alone, in place, and the
+// state after the last one: S_s = X, X <- decay_s X + S_s.  Four values per lane.
+struct LaScanArgs {
+    const float* h0;          // or null: zeros
+    float* h;
+    float* ws;                // [segments][heads][d*d]
+    const float* decay;       // [segments][heads]
+    size_t heads;
+    int dd4;                  // d*d / 4
+    int segs;
+};
+__global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
+    const size_t e = blockIdx.x * 256 + threadIdx.x, head = blockIdx.y;
+    if (e >= (size_t)a.dd4) return;
+    const size_t at = head * a.dd4 + e, stride = a.heads * a.dd4;
+    v4f x = {0.f, 0.f, 0.f, 0.f};
+    if (a.h0) x = reinterpret_cast<const v4f*>(a.h0)[at];
+    v4f* ws = reinterpret_cast<v4f*>(a.ws);
+#pragma unroll 4
+    for (int s = 0; s < a.segs; ++s) {
+        const v4f y = ws[s * stride + at];
+        const float d = a.decay[s * a.heads + head];
+        ws[s * stride + at] = x;
+        x = x * d + y;
+    }
+    reinterpret_cast<v4f*>(a.h)[at] = x;
+}
+
+// Tokens per segment: one segment per head where the heads alone fill the GPU.
+int segment_tokens(size_t heads, int T) {
+    const int chunks = (T + BL - 1) / BL;
+    const int want = (int)((512 + heads - 1) / heads);             // segments for 512 workgroups
+    const int per = want <= 1 ? chunks : (chunks + want - 1) / want;
+    return max(per, 1) * BL;
+}
+
+template <int D>
+hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
+    const size_t heads = (size_t)args.heads;
+    const int seg = segment_tokens(heads, args.T), segs = (args.T + seg - 1) / seg;
+    LaSegArgs sa{args.h0, args.h, nullptr, args.q, args.k, args.v, args.alpha, args.lens, args.o, 0,
+                 args.T, args.H, args.heads, args.alpha_tok, seg};
+    const dim3 grid((unsigned)heads, (unsigned)segs), block(LB<D>::NT);
+    if (segs == 1)
+        return args.o ? launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, true>, grid, block, s, sa)
+                      : launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, false>, grid, block, s, sa);
+    float* ws = static_cast<float*>(workspace);
+    float* decay = ws + (size_t)segs * heads * D * D;
+    sa.seg_stride = heads * D * D;
+    sa.start = nullptr;
+    sa.end = ws;
+    sa.decay = decay;
+    hipError_t e = launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, false>, grid, block, s, sa);
+    if (e != hipSuccess) return e;
+    LaScanArgs sc{args.h0, args.h, ws, decay, heads, D * D / 4, segs};
+    e = launch_kernel(LQ_KERNEL_LA_PREFILL, la_scan_kernel, dim3((D * D / 4 + 255) / 256, (unsigned)heads), dim3(256), s, sc);
+    if (e != hipSuccess || !args.o) return e;
+    sa.start = ws;
+    sa.end = nullptr;
+    sa.decay = nullptr;
+    return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, true>, grid, block, s, sa);
+}
+
+template <int D>
+hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
     const dim3 grid((unsigned)d.B * (unsigned)d.H);
+    if constexpr (D >= 64)
+        if (d.io_dtype == LQ_IO_BF16 && args.T > 0) return la_chunks<D>(d, args, workspace, s);
     if (d.io_dtype == LQ_IO_BF16)
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, uint16_t>, grid, dim3(LP<D>::NT), s, args);
     return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, float>, grid, dim3(LP<D>::NT), s, args);
@@ -175,20 +607,21 @@ hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, hipStream_t
 }  // namespace
 
 size_t la_workspace_bytes(const lq_dims& d, int T) {
-    (void)d;
-    (void)T;
-    return 0;
+    if (d.dk < 64 || d.io_dtype != LQ_IO_BF16) return 0;
+    // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
+    const size_t heads = (size_t)d.B * d.H;
+    const size_t segs = min((512 + heads - 1) / heads, ((size_t)T + BL - 1) / BL);
+    return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
 }
 
 hipError_t launch_la_prefill(const lq_dims& d, const float* h0, float* h, int T, const void* q, const void* k,
                              const void* v, const float* alpha, bool alpha_heads, const int32_t* lens, void* o,
                              void* workspace, hipStream_t s) {
-    (void)workspace;
     LaPrefillArgs args{h0, h, q, k, v, alpha, lens, o, T, d.H, d.B * d.H, alpha_heads ? 0 : d.B * d.H};
     switch (d.dk) {
-        case 16: return la_prefill_t<16>(d, args, s);
-        case 64: return la_prefill_t<64>(d, args, s);
-        default: return la_prefill_t<128>(d, args, s);
+        case 16: return la_prefill_t<16>(d, args, workspace, s);
+        case 64: return la_prefill_t<64>(d, args, workspace, s);
+        default: return la_prefill_t<128>(d, args, workspace, s);
     }
 }
 
