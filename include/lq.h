@@ -333,8 +333,8 @@ enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
  * form over an fp32 state.  With bf16 tokens, products that reach h keep
  * fp32's 24 bits, those that reach only o at least 16.  A non-finite v reaches
  * its own column from its own token on.
- * Errors: LQ_ERR_POS if T < 0; LQ_ERR_DIMS for a bad alpha_kind;
- * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30; LQ_ERR_DIMS
+ * for a bad alpha_kind; LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
 int lq_la_prefill(const lq_dims *d, const lq_state *st, const float *h0, float *h, int32_t T,
                   const void *q, const void *k, const void *v, const float *alpha,

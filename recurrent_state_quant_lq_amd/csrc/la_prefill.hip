@@ -531,6 +531,334 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     if (a.decay && t == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
 }
 
+// ---------------------------------------------------------------------------
+// fp32 tokens, d >= 64: chunks of 32 tokens, every operand in three bf16 parts
+// ---------------------------------------------------------------------------
+// An fp32 value is the exact sum of three bf16 parts (its 24 bits cut in three), so a
+// product is six bf16 products (the three below 2^-24 of it are left out) summed in
+// fp32: 6 x 16 cycles for 16x16x32 against 8 x 32 on the fp32 matrix instruction.
+// Wave w owns the 16 columns 16 w + li; otherwise as la_chunk_kernel.
+constexpr int FL = 32;        // tokens per chunk
+
+template <int D>
+struct LF {
+    static constexpr int NW = D / 16, NT = 64 * NW;
+    static constexpr int RT = D / 16;
+    static constexpr int QS = D + 8;           // shorts per Q / K row
+    static constexpr int TS = FL + 8;          // shorts per K^T / score row
+};
+
+// N values in three bf16 parts, packed.
+template <int N>
+__device__ __forceinline__ void split3(const float (&x)[N], uint32_t (&p)[3][N / 2]) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+        const float a = x[2 * e], b = x[2 * e + 1];
+        const float a1 = a - top_f32(a), b1 = b - top_f32(b);
+        p[0][e] = top_halves(a, b);
+        p[1][e] = top_halves(a1, b1);
+        p[2][e] = top_halves(a1 - top_f32(a1), b1 - top_f32(b1));
+    }
+}
+
+// c += a b, a and b in three parts each; small products first.
+__device__ __forceinline__ v4f mfma_split(const u32x4 (&a)[3], const u32x4 (&b)[3], v4f c) {
+    c = mfma_bf16(a[2], b[0], c);
+    c = mfma_bf16(a[0], b[2], c);
+    c = mfma_bf16(a[1], b[1], c);
+    c = mfma_bf16(a[1], b[0], c);
+    c = mfma_bf16(a[0], b[1], c);
+    return mfma_bf16(a[0], b[0], c);
+}
+
+template <int D, bool OUT>
+__global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
+    using P = LF<D>;
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QS = P::QS, TS = P::TS;
+    __shared__ __align__(16) uint16_t sQ[3][OUT ? FL * QS : 8];
+    __shared__ __align__(16) uint16_t sK[3][OUT ? FL * QS : 8];
+    __shared__ __align__(16) uint16_t sT[3][D * TS];               // K^T: [channel][token]
+    __shared__ __align__(16) uint16_t sP[3][OUT ? FL * TS : 8];    // scores
+    __shared__ double sG[FL];
+    __shared__ __align__(16) float sE[FL], sW[FL];                 // e^{g_n}, e^{g_L - g_n}
+
+    const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const size_t head = blockIdx.x, heads = (size_t)a.heads;
+    const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int t0 = (int)blockIdx.y * a.seg;
+    const int te = min(len, t0 + a.seg);
+    const float* gq = static_cast<const float*>(a.q);
+    const float* gk = static_cast<const float*>(a.k);
+    const float* gv = static_cast<const float*>(a.v);
+    const int col = 16 * w + li;
+    const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
+
+    v4f H[RT];                                                     // H[rt][v] = H[16 rt + 4 lg + v][col]
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) H[rt][v] = a.start ? a.start[soff + (size_t)(16 * rt + 4 * lg + v) * D + col] : 0.0f;
+    if constexpr (OUT)
+        for (int e = t; e < 3 * 16 * 16; e += NT) sP[e >> 8][((e >> 4) & 15) * TS + 16 + (e & 15)] = 0;   // right of the diagonal
+
+    // chunk loads, one chunk ahead; tokens past the end repeat the last one and are zeroed in LDS
+    const int kc = t % D, koct = t / D;                            // K^T: channel, 8 tokens (4 octets)
+    constexpr int CPR = D / 8;                                     // 8-channel pieces per row
+    const int row = t / CPR, c8 = 8 * (t % CPR);                   // Q, K rows: 32 rows of CPR pieces (D = 64, 128: one each)
+    static_assert(NT / CPR == FL && NT / D == FL / 8, "one piece and one octet per thread");
+    float kt[8], vr[8];
+    v4f qr[2], kr[2];
+    float al;
+    auto load = [&](int c0) {
+        const int last = te - 1;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            kt[e] = gk[((size_t)min(c0 + 8 * koct + e, last) * heads + head) * D + kc];
+            vr[e] = gv[((size_t)min(c0 + 8 * lg + e, last) * heads + head) * D + col];
+        }
+        if constexpr (OUT) {
+            const size_t at = ((size_t)min(c0 + row, last) * heads + head) * D + c8;
+            qr[0] = *reinterpret_cast<const v4f*>(gq + at);
+            qr[1] = *reinterpret_cast<const v4f*>(gq + at + 4);
+            kr[0] = *reinterpret_cast<const v4f*>(gk + at);
+            kr[1] = *reinterpret_cast<const v4f*>(gk + at + 4);
+        }
+        if (w == 0) {
+            const int tok = min(c0 + (lane & (FL - 1)), last);
+            al = a.alpha_tok ? a.alpha[(size_t)tok * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
+        }
+    };
+    if (t0 < te) load(t0);
+    double gtot = 0.0;
+
+    for (int c0 = t0; c0 < te; c0 += FL) {
+        const int L = min(FL, te - c0);
+        {
+            float x[8];
+            uint32_t p[3][4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 8 * koct + e < L ? kt[e] : 0.0f;
+            split3<8>(x, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m)
+                *reinterpret_cast<u32x4*>(&sT[m][kc * TS + 8 * koct]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            if constexpr (OUT) {
+                const int u = (c8 & 31) >> 2;                      // two groups of 4 channels, in operand order
+                const int at = row * QS + (c8 & ~31) + 4 * (u >> 2);
+#pragma unroll
+                for (int which = 0; which < 2; ++which) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = row < L ? (which ? kr[e / 4][e % 4] : qr[e / 4][e % 4]) : 0.0f;
+                    split3<8>(x, p);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) {
+                        uint16_t* dst = (which ? sK[m] : sQ[m]) + at;
+                        *reinterpret_cast<u32x2*>(dst + 8 * (u & 3)) = u32x2{p[m][0], p[m][1]};
+                        *reinterpret_cast<u32x2*>(dst + 8 * ((u + 1) & 3)) = u32x2{p[m][2], p[m][3]};
+                    }
+                }
+            }
+        }
+        float V[8];
+        bool odd = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            V[e] = 8 * lg + e < L ? vr[e] : 0.0f;
+            odd |= !finite_f32(V[e]);
+        }
+        if (w == 0) {
+            double g = lane < L ? (double)log_decay(al) : 0.0;     // lanes past FL: zeros
+#pragma unroll
+            for (int m = 1; m < FL; m <<= 1) {
+                const double x = __shfl_up(g, m, 64);
+                if (lane >= m) g += x;
+            }
+            const double gl = __shfl(g, FL - 1, 64);
+            if (lane < FL) {
+                sG[lane] = g;
+                sE[lane] = expf((float)g);
+                sW[lane] = expf((float)(gl - g));
+            }
+            gtot += gl;
+        }
+        __syncthreads();
+        if (c0 + FL < te) load(c0 + FL);
+
+        const float egl = sE[FL - 1];
+        if constexpr (OUT) {
+            // scores: tiles (0,0), (1,0), (1,1), one wave each
+            if (w < 3) {
+                const int r = (w + 1) >> 1, c = w >> 1;
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < D / 32; ++ks) {
+                    u32x4 x[3], y[3];
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) {
+                        x[m] = *reinterpret_cast<const u32x4*>(&sQ[m][(16 * r + li) * QS + 32 * ks + 8 * lg]);
+                        y[m] = *reinterpret_cast<const u32x4*>(&sK[m][(16 * c + li) * QS + 32 * ks + 8 * lg]);
+                    }
+                    acc = mfma_split(x, y, acc);
+                }
+                const int i = 16 * c + li;
+                const double gi = sG[i];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * r + 4 * lg + v;
+                    const float p = i <= n ? expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
+                    const float p1 = p - top_f32(p);
+                    sP[0][n * TS + i] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sP[1][n * TS + i] = (uint16_t)(__float_as_uint(p1) >> 16);
+                    sP[2][n * TS + i] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
+                }
+            }
+            v4f O[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                float x[8];
+                uint32_t p[3][4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = H[2 * ks + e / 4][e % 4];
+                split3<8>(x, p);
+                u32x4 b[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    u32x4 q[3];
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        q[m] = *reinterpret_cast<const u32x4*>(&sQ[m][(16 * r + li) * QS + 32 * ks + 8 * lg]);
+                    O[r] = mfma_split(q, b, O[r]);
+                }
+            }
+            O[0] *= *reinterpret_cast<const v4f*>(&sE[4 * lg]);
+            O[1] *= *reinterpret_cast<const v4f*>(&sE[16 + 4 * lg]);
+            __syncthreads();                                       // the scores are written
+            {
+                float x[8];
+                uint32_t p[3][4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = finite_f32(V[e]) ? V[e] : 0.0f;    // 0 * v must stay 0
+                split3<8>(x, p);
+                u32x4 b[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    u32x4 x3[3];
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        x3[m] = *reinterpret_cast<const u32x4*>(&sP[m][(16 * r + li) * TS + 8 * lg]);
+                    O[r] = mfma_split(x3, b, O[r]);
+                }
+            }
+            if (__any(odd))
+#pragma unroll 1
+                for (int i = 0; i < L; ++i) {
+                    const float x = gv[((size_t)(c0 + i) * heads + head) * D + col];
+                    if (!finite_f32(x))
+#pragma unroll
+                        for (int r = 0; r < 2; ++r)
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) {
+                                const int n = 16 * r + 4 * lg + v;
+                                if (n >= i)
+                                    O[r][v] += (bf16_to_f32(sP[0][n * TS + i]) + bf16_to_f32(sP[1][n * TS + i]) +
+                                                bf16_to_f32(sP[2][n * TS + i])) * x;
+                            }
+                }
+            float* go = static_cast<float*>(a.o);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * r + 4 * lg + v;
+                    if (n < L) st_nt(go + ((size_t)(c0 + n) * heads + head) * D + col, O[r][v]);
+                }
+        }
+        if (a.end || c0 + FL < te) {
+            float x[8];
+            uint32_t p[3][4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = sW[8 * lg + e] * V[e];
+            split3<8>(x, p);
+            u32x4 b[3];
+#pragma unroll
+            for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                H[rt] *= egl;
+                u32x4 k3[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) k3[m] = *reinterpret_cast<const u32x4*>(&sT[m][(16 * rt + li) * TS + 8 * lg]);
+                H[rt] = mfma_split(k3, b, H[rt]);
+            }
+        }
+        __syncthreads();                                           // LDS is rewritten by the next chunk
+    }
+    if (a.end)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) a.end[soff + (size_t)(16 * rt + 4 * lg + v) * D + col] = H[rt][v];
+    if (a.decay && t == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
+}
+
+// ---------------------------------------------------------------------------
+// a few tokens: the recurrence itself
+// ---------------------------------------------------------------------------
+// Reads the state once and writes it once; per token the decay, the rank-one update
+// and the column sums of H o q.  Lane t holds the columns 4 (t % (D/4)) .. +3 of the
+// rows t / (D/4) + RPP p.
+template <int D, typename TI>
+__global__ __launch_bounds__(256) void la_step_kernel(LaPrefillArgs a) {
+    constexpr int CP = D / 4, NT = D >= 64 ? 256 : 64, RPP = NT / CP, NP = D / RPP, NW = NT / 64;
+    __shared__ __align__(16) float so[2][NW][D];
+    const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+    const size_t head = blockIdx.x, heads = (size_t)a.heads;
+    const int T = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int rg = t / CP, c0 = 4 * (t % CP);
+    const float* h0 = a.h0 + head * (size_t)(D * D);
+    v4f H[NP];
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+        H[p] = v4f{0.f, 0.f, 0.f, 0.f};
+        if (a.h0) H[p] = ld_nt(reinterpret_cast<const v4f*>(h0 + (size_t)(p * RPP + rg) * D + c0));
+    }
+    for (int n = 0; n < T; ++n) {
+        const size_t th = (size_t)n * heads + head;
+        const float al = a.alpha_tok ? a.alpha[(size_t)n * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
+        v4f vv, o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vv[e] = tok_ld<TI>(a.v, th * D + c0 + e);
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const float kk = tok_ld<TI>(a.k, th * D + p * RPP + rg);
+            H[p] = H[p] * al + vv * kk;
+            if (a.o) o += H[p] * tok_ld<TI>(a.q, th * D + p * RPP + rg);
+        }
+        if (!a.o) continue;
+#pragma unroll
+        for (int m = CP; m < 64; m <<= 1)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], m, 64);
+        if (lane < CP) *reinterpret_cast<v4f*>(&so[n & 1][w][c0]) = o;
+        __syncthreads();                                           // (the other half is written meanwhile)
+        if (t < D) {
+            float x = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NW; ++i) x += so[n & 1][i][t];
+            tok_st<TI>(a.o, th * D + t, x);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+        __builtin_nontemporal_store(H[p], reinterpret_cast<v4f*>(a.h + head * (size_t)(D * D) + (size_t)(p * RPP + rg) * D + c0));
+}
+constexpr int kStepTokens = 4;
+
 // States before each segment from the states of each segment alone, in place, and the
 // state after the last one: S_s = X, X <- decay_s X + S_s.  Four values per lane.
 struct LaScanArgs {
@@ -559,31 +887,38 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
     reinterpret_cast<v4f*>(a.h)[at] = x;
 }
 
-// Tokens per segment: one segment per head where the heads alone fill the GPU.
-int segment_tokens(size_t heads, int T) {
-    const int chunks = (T + BL - 1) / BL;
-    const int want = (int)((512 + heads - 1) / heads);             // segments for 512 workgroups
-    const int per = want <= 1 ? chunks : (chunks + want - 1) / want;
-    return max(per, 1) * BL;
+// Tokens per segment (a multiple of the chunk): one segment per head where the heads
+// alone fill the GPU, else segments for kWant workgroups.
+constexpr size_t kWant = 512;
+int segment_tokens(size_t heads, int T, int chunk) {
+    const size_t chunks = ((size_t)T + chunk - 1) / chunk, want = (kWant + heads - 1) / heads;
+    return (int)(want <= 1 ? chunks : (chunks + want - 1) / want) * chunk;
+}
+int chunk_tokens(const lq_dims& d) { return d.io_dtype == LQ_IO_BF16 ? BL : FL; }
+
+template <int D, typename TI, bool OUT>
+hipError_t chunk_launch(dim3 grid, const LaSegArgs& sa, hipStream_t s) {
+    if constexpr (sizeof(TI) == 2)
+        return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, OUT>, grid, dim3(LB<D>::NT), s, sa);
+    else
+        return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk32_kernel<D, OUT>, grid, dim3(LF<D>::NT), s, sa);
 }
 
-template <int D>
+template <int D, typename TI>
 hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
     const size_t heads = (size_t)args.heads;
-    const int seg = segment_tokens(heads, args.T), segs = (args.T + seg - 1) / seg;
+    const int seg = segment_tokens(heads, args.T, chunk_tokens(d)), segs = (int)(((size_t)args.T + seg - 1) / seg);
     LaSegArgs sa{args.h0, args.h, nullptr, args.q, args.k, args.v, args.alpha, args.lens, args.o, 0,
                  args.T, args.H, args.heads, args.alpha_tok, seg};
-    const dim3 grid((unsigned)heads, (unsigned)segs), block(LB<D>::NT);
-    if (segs == 1)
-        return args.o ? launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, true>, grid, block, s, sa)
-                      : launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, false>, grid, block, s, sa);
+    const dim3 grid((unsigned)heads, (unsigned)segs);
+    if (segs == 1) return args.o ? chunk_launch<D, TI, true>(grid, sa, s) : chunk_launch<D, TI, false>(grid, sa, s);
     float* ws = static_cast<float*>(workspace);
     float* decay = ws + (size_t)segs * heads * D * D;
     sa.seg_stride = heads * D * D;
     sa.start = nullptr;
     sa.end = ws;
     sa.decay = decay;
-    hipError_t e = launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, false>, grid, block, s, sa);
+    hipError_t e = chunk_launch<D, TI, false>(grid, sa, s);
     if (e != hipSuccess) return e;
     LaScanArgs sc{args.h0, args.h, ws, decay, heads, D * D / 4, segs};
     e = launch_kernel(LQ_KERNEL_LA_PREFILL, la_scan_kernel, dim3((D * D / 4 + 255) / 256, (unsigned)heads), dim3(256), s, sc);
@@ -591,26 +926,31 @@ hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspac
     sa.start = ws;
     sa.end = nullptr;
     sa.decay = nullptr;
-    return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, true>, grid, block, s, sa);
+    return chunk_launch<D, TI, true>(grid, sa, s);
+}
+
+template <int D, typename TI>
+hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
+    const dim3 grid((unsigned)args.heads);
+    if (args.T <= kStepTokens)
+        return launch_kernel(LQ_KERNEL_LA_PREFILL, la_step_kernel<D, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
+    if constexpr (D >= 64) return la_chunks<D, TI>(d, args, workspace, s);
+    else return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, TI>, grid, dim3(LP<D>::NT), s, args);
 }
 
 template <int D>
-hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
-    const dim3 grid((unsigned)d.B * (unsigned)d.H);
-    if constexpr (D >= 64)
-        if (d.io_dtype == LQ_IO_BF16 && args.T > 0) return la_chunks<D>(d, args, workspace, s);
-    if (d.io_dtype == LQ_IO_BF16)
-        return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, uint16_t>, grid, dim3(LP<D>::NT), s, args);
-    return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, float>, grid, dim3(LP<D>::NT), s, args);
+hipError_t la_prefill_d(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
+    return d.io_dtype == LQ_IO_BF16 ? la_prefill_t<D, uint16_t>(d, args, workspace, s)
+                                    : la_prefill_t<D, float>(d, args, workspace, s);
 }
 
 }  // namespace
 
 size_t la_workspace_bytes(const lq_dims& d, int T) {
-    if (d.dk < 64 || d.io_dtype != LQ_IO_BF16) return 0;
+    if (d.dk < 64 || T <= kStepTokens) return 0;
     // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
-    const size_t heads = (size_t)d.B * d.H;
-    const size_t segs = min((512 + heads - 1) / heads, ((size_t)T + BL - 1) / BL);
+    const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d);
+    const size_t segs = min((kWant + heads - 1) / heads, ((size_t)T + chunk - 1) / chunk);
     return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
 }
 
@@ -619,9 +959,9 @@ hipError_t launch_la_prefill(const lq_dims& d, const float* h0, float* h, int T,
                              void* workspace, hipStream_t s) {
     LaPrefillArgs args{h0, h, q, k, v, alpha, lens, o, T, d.H, d.B * d.H, alpha_heads ? 0 : d.B * d.H};
     switch (d.dk) {
-        case 16: return la_prefill_t<16>(d, args, workspace, s);
-        case 64: return la_prefill_t<64>(d, args, workspace, s);
-        default: return la_prefill_t<128>(d, args, workspace, s);
+        case 16: return la_prefill_d<16>(d, args, workspace, s);
+        case 64: return la_prefill_d<64>(d, args, workspace, s);
+        default: return la_prefill_d<128>(d, args, workspace, s);
     }
 }
 

@@ -297,6 +297,7 @@ int lq_la_prefill(const lq_dims* d, const lq_state* st, const float* h0, float* 
     if (h0 && !aligned16(h0)) return LQ_ERR_ALIGN;
     if (lens && !aligned4(lens)) return LQ_ERR_ALIGN;
     if (T < 0) return LQ_ERR_POS;
+    if (T > lq::kLaMaxTokens) return LQ_ERR_UNSUPPORTED;
     if (T > 0 && (rc = check_tokens(d, q, k, v, alpha, alpha, o, false))) return rc;
     const size_t need = lq_la_workspace_bytes(d, T);
     if (need > 0) {
@@ -312,7 +313,7 @@ int lq_la_prefill(const lq_dims* d, const lq_state* st, const float* h0, float* 
 }
 
 size_t lq_la_workspace_bytes(const lq_dims* d, int32_t T) {
-    return check_la(d, LQ_ALPHA_TOKENS) == LQ_OK && T > 0 ? lq::la_workspace_bytes(*d, T) : 0;
+    return check_la(d, LQ_ALPHA_TOKENS) == LQ_OK && T > 0 && T <= lq::kLaMaxTokens ? lq::la_workspace_bytes(*d, T) : 0;
 }
 
 int lq_la_decode_step(const lq_dims* d, const lq_state* st, int32_t pos, const void* q, const void* k,

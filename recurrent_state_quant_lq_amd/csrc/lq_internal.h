@@ -39,6 +39,7 @@ hipError_t launch_la_prefill(const lq_dims& d, const float* h0, float* h, int T,
                              const void* v, const float* alpha, bool alpha_heads, const int32_t* lens, void* o,
                              void* workspace, hipStream_t s);
 size_t la_workspace_bytes(const lq_dims& d, int T);
+constexpr int kLaMaxTokens = 1 << 30;   // token counts and their rounding up to chunks stay in 32 bits
 hipError_t launch_la_decode(const lq_dims& d, const lq_state& st, int pos, const int32_t* pos_dev, const void* q,
                             const void* k, const void* v, const float* alpha, bool alpha_heads, void* o,
                             hipStream_t s);

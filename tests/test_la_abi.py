@@ -41,6 +41,8 @@ def test_prefill_argument_errors():
     assert call(_dims(dk=96, dv=96)) == lq.LQ_ERR_UNSUPPORTED
     assert call(kind=2) == lq.LQ_ERR_DIMS and call(kind=-1) == lq.LQ_ERR_DIMS
     assert call(T=-1) == lq.LQ_ERR_POS
+    assert call(T=(1 << 30) + 1) == lq.LQ_ERR_UNSUPPORTED
+    assert lq.lq_la_workspace_bytes(_dims(), (1 << 30) + 1) == 0
     assert call(h=None) == lq.LQ_ERR_NULL and call(h=B4) == lq.LQ_ERR_ALIGN
     assert call(h0=B4) == lq.LQ_ERR_ALIGN and call(lens=B2) == lq.LQ_ERR_ALIGN
     for name in ("q", "k", "v", "al"):
