@@ -16,6 +16,7 @@
 // layout is the B operand of the next products with the K index in register
 // order, so no value of H or V moves between lanes.
 #include "lq_internal.h"
+#include "lq_split.h"
 
 namespace lq {
 namespace {
@@ -34,8 +35,6 @@ struct LaPrefillArgs {
     int heads;                // B*H: stride between tokens, in heads
     int alpha_tok;            // token stride of alpha: heads, or 0 for one decay per head
 };
-
-__device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
 constexpr int CL = 16;        // tokens per chunk (the MFMA tile)
 
@@ -180,11 +179,6 @@ __global__ __launch_bounds__(LP<D>::NT) void la_prefill_kernel(LaPrefillArgs a) 
 // and outputs and the state leave as whole dwords and 8-byte pairs.
 // H tiles are the B operand of Q H with the channels of each 32-block in the
 // order (4 lg + e, 16 + 4 lg + e); Q and K rows are stored in that order.
-typedef short s16x8 __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
 constexpr int BL = 64;        // tokens per chunk
 
 struct LaSegArgs {
@@ -209,28 +203,6 @@ struct LB {
     static constexpr int QS = D + 8;           // shorts per Q / K row: 16-byte reads of 8 rows hit all banks
     static constexpr int TS = BL + 8;          // shorts per K^T / score row
 };
-
-// Two fp32 values to packed bf16 (nearest even), low half first.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 r = {(__bf16)a, (__bf16)b};
-    return __builtin_bit_cast(uint32_t, r);
-}
-__device__ __forceinline__ float lo_f32(uint32_t x) { return __uint_as_float(x << 16); }
-__device__ __forceinline__ float hi_f32(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
-// Upper halves of (a, b) as packed bf16: truncation to 8 bits.
-__device__ __forceinline__ uint32_t top_halves(float a, float b) {
-    return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-}
-__device__ __forceinline__ float top_f32(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
-// Whether either bf16 of x is infinite or NaN.
-__device__ __forceinline__ uint32_t odd_bf16(uint32_t x) { return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
-
-__device__ __forceinline__ v4f mfma_bf16(u32x4 a, u32x4 b, v4f c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(__attribute__((ext_vector_type(8))) __bf16, a),
-                                                   __builtin_bit_cast(__attribute__((ext_vector_type(8))) __bf16, b), c,
-                                                   0, 0, 0);
-}
 
 template <int D, bool OUT>
 __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
@@ -547,29 +519,6 @@ struct LF {
     static constexpr int QS = D + 8;           // shorts per Q / K row
     static constexpr int TS = FL + 8;          // shorts per K^T / score row
 };
-
-// N values in three bf16 parts, packed.
-template <int N>
-__device__ __forceinline__ void split3(const float (&x)[N], uint32_t (&p)[3][N / 2]) {
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-        const float a = x[2 * e], b = x[2 * e + 1];
-        const float a1 = a - top_f32(a), b1 = b - top_f32(b);
-        p[0][e] = top_halves(a, b);
-        p[1][e] = top_halves(a1, b1);
-        p[2][e] = top_halves(a1 - top_f32(a1), b1 - top_f32(b1));
-    }
-}
-
-// c += a b, a and b in three parts each; small products first.
-__device__ __forceinline__ v4f mfma_split(const u32x4 (&a)[3], const u32x4 (&b)[3], v4f c) {
-    c = mfma_bf16(a[2], b[0], c);
-    c = mfma_bf16(a[0], b[2], c);
-    c = mfma_bf16(a[1], b[1], c);
-    c = mfma_bf16(a[1], b[0], c);
-    c = mfma_bf16(a[0], b[1], c);
-    return mfma_bf16(a[0], b[0], c);
-}
 
 template <int D, bool OUT>
 __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
