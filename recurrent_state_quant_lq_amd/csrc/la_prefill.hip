@@ -196,6 +196,24 @@ struct LaSegArgs {
     int seg;                  // tokens per segment (a multiple of BL)
 };
 
+// Inclusive prefix sum over the 64 lanes: lane shifts within 16 lanes, then the last lane
+// of a row to the rows above it (data-parallel moves, no LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x) {
+    const uint64_t u = __double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return x + __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_scan(double x) {
+    x = scan_step<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
+    x = scan_step<0x112, 0xf>(x);
+    x = scan_step<0x114, 0xf>(x);
+    x = scan_step<0x118, 0xf>(x);
+    x = scan_step<0x142, 0xa>(x);      // row_bcast 15 into rows 1, 3
+    return scan_step<0x143, 0xc>(x);   // row_bcast 31 into rows 2, 3
+}
+
 template <int D>
 struct LB {
     static constexpr int NW = D / 32, NT = 64 * NW;
@@ -215,30 +233,30 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     __shared__ double sG[BL];
     __shared__ __align__(16) float sE[BL], sW[BL];                 // e^{g_n}, e^{g_L - g_n}
 
-    const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+    const int t = threadIdx.x, lane = t & 63;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
     const size_t head = blockIdx.x, heads = (size_t)a.heads;
     const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
     const int t0 = (int)blockIdx.y * a.seg;                        // < T: one segment per started seg tokens
     const int te = min(len, t0 + a.seg);
-    const uint32_t* gq = static_cast<const uint32_t*>(a.q);
-    const uint32_t* gk = static_cast<const uint32_t*>(a.k);
-    const uint32_t* gv = static_cast<const uint32_t*>(a.v);
-    constexpr int RD = D / 2;                                      // dwords per token row
-    const int band = 16 * w + li;                                  // the lane's dword of a V / O row
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
 
     // H[rt][ct][v] = H[16 rt + 4 lg + v][32 w + 2 li + ct]
     v4f H[RT][2];
+    if (a.start) {
+        const int lg = lane >> 4, band = 16 * w + (lane & 15);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            f32x2 x = {0.f, 0.f};
-            if (a.start) x = *reinterpret_cast<const f32x2*>(a.start + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
-            H[rt][0][v] = x[0];
-            H[rt][1][v] = x[1];
-        }
+            for (int v = 0; v < 4; ++v) {
+                const f32x2 x = *reinterpret_cast<const f32x2*>(a.start + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
+                H[rt][0][v] = x[0];
+                H[rt][1][v] = x[1];
+            }
+    } else {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) H[rt][0] = H[rt][1] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
     if constexpr (OUT) {
         // score tiles right of the diagonal inside a 32-token step: zeros, never written again
         for (int e = t; e < 2 * 2 * 16 * 8; e += NT) {
@@ -247,51 +265,54 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
         }
     }
 
-    // chunk loads in registers, one chunk ahead; tokens past the end repeat the last one and are zeroed in LDS
-    const int kpair = lane % (D / 2), ksub = lane / (D / 2);       // channel pair; octet within a wave's pass
+    // chunk loads in registers, one chunk ahead; tokens past the end read as zeros
+    // (each phase of the chunk loop forms its lane indices anew: addresses kept across the
+    // phases would spill, and a reload waits for the loads in flight)
     constexpr int OPW = 128 / D;                                   // octets per wave and pass (D = 64: 2)
+    const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= kChunkHeads)
     uint32_t kd[2][8], vd[2][8];
     u32x4 qd[4];
-    float al;
-    auto load = [&](int c0) {
-        const int last = te - 1;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int tok = min(c0 + 8 * ((2 * w + j) * OPW + ksub) + e, last);
-                kd[j][e] = gk[((size_t)tok * heads + head) * RD + kpair];
-            }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int tok = min(c0 + 32 * j + 8 * lg + e, last);
-                vd[j][e] = gv[((size_t)tok * heads + head) * RD + band];
-            }
-        if constexpr (OUT)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int e = t + NT * j, tok = min(c0 + e / (D / 8), last);
-                qd[j] = *reinterpret_cast<const u32x4*>(gq + ((size_t)tok * heads + head) * RD + 4 * (e % (D / 8)));
-            }
-        if (w == 0) {
-            const int tok = min(c0 + lane, last);
-            al = a.alpha_tok ? a.alpha[(size_t)tok * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
-        }
+    float al = 0.0f;
+    auto rows = [&](const void* x, int c0) {                       // tokens c0 .. min(c0 + BL, te) - 1 of this head
+        return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (2 * D),
+                         (uint32_t)(min(te - c0, BL) - 1) * rb + 2 * D);
     };
-    if (t0 < te) load(t0);
+    auto load_v = [&](int c0) {
+        const rsrc_t rv = rows(a.v, c0);
+        const uint32_t ln = fresh(lane), voff = 8 * (ln >> 4) * rb + 4 * (16 * w + (ln & 15));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) vd[j][e] = row_ld(rv, voff + (32 * j + e) * rb);
+    };
+    auto load_kq = [&](int c0) {
+        const rsrc_t rk = rows(a.k, c0);
+        const uint32_t ln = fresh(lane), koff = 8 * (2 * w * OPW + ln / (D / 2)) * rb + 4 * (ln % (D / 2));
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) kd[j][e] = row_ld(rk, koff + (8 * j * OPW + e) * rb);
+        if constexpr (OUT) {
+            const rsrc_t rq = rows(a.q, c0);
+            const uint32_t tt = 64 * w + ln, qoff = (tt / (D / 8)) * rb + 16 * (tt % (D / 8));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) qd[j] = row_ld4(rq, qoff + (j * (NT / (D / 8))) * rb);
+        }
+        if (w == 0) al = a.alpha[a.alpha_tok ? (size_t)min(c0 + (int)ln, te - 1) * a.alpha_tok + head : head % (unsigned)a.H];
+    };
+    if (t0 < te) {
+        load_kq(t0);
+        load_v(t0);
+    }
     double gtot = 0.0;                                             // (wave 0) log decay of the segment so far
 
     for (int c0 = t0; c0 < te; c0 += BL) {
         const int L = min(BL, te - c0);
         // ---- registers -> LDS ----
+        const int ln = fresh(lane), kpair = ln % (D / 2), ksub = ln / (D / 2);   // channel pair; octet within a wave's pass
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int oct = (2 * w + j) * OPW + ksub;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * oct + e >= L) kd[j][e] = 0;
             u32x4 x0, x1;                                          // 8 tokens of the pair's two channels
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -311,35 +332,22 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
         if constexpr (OUT)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int e = t + NT * j, row = e / (D / 8), c = 8 * (e % (D / 8));
-                if (row >= L) qd[j] = u32x4{0, 0, 0, 0};
+                const int e = 64 * w + ln + NT * j, row = e / (D / 8), c = 8 * (e % (D / 8));
                 const int u = (c & 31) >> 2;                       // two groups of 4 channels: u, u + 1
                 uint16_t* at = &sQ[row * QS + (c & ~31) + 4 * (u >> 2)];
                 *reinterpret_cast<u32x2*>(at + 8 * (u & 3)) = u32x2{qd[j][0], qd[j][1]};
                 *reinterpret_cast<u32x2*>(at + 8 * ((u + 1) & 3)) = u32x2{qd[j][2], qd[j][3]};
             }
         u32x4 V[2][2];                                             // B operands: [32-token step][ct]
-        uint32_t odd = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (32 * j + 8 * lg + e >= L) vd[j][e] = 0;
-                odd |= odd_bf16(vd[j][e]);
-            }
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 V[j][0][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x05040100u);
                 V[j][1][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x07060302u);
             }
-        }
         if (w == 0) {
-            double g = lane < L ? (double)log_decay(al) : 0.0;
-#pragma unroll
-            for (int m = 1; m < 64; m <<= 1) {
-                const double x = __shfl_up(g, m, 64);
-                if (lane >= m) g += x;
-            }
+            const double g = wave_scan(lane < L ? (double)log_decay(al) : 0.0);
             const double gl = __shfl(g, 63, 64);
             sG[lane] = g;
             sE[lane] = expf((float)g);
@@ -347,30 +355,33 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
             gtot += gl;
         }
         __syncthreads();
-        if (c0 + BL < te) load(c0 + BL);
 
         const float egl = sE[BL - 1];
         if constexpr (OUT) {
+            const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
             // ---- scores: the 10 tiles on and below the diagonal, over the waves ----
-#pragma unroll 1
-            for (int x = w; x < 10; x += NW) {
+            // (one branch per tile on the wave's index, so that every LDS address is a constant
+            // away from the lane's)
+#pragma unroll
+            for (int x = 0; x < 10; ++x) {
+                if (x % NW != w) continue;
                 const int r = x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3, c = x - r * (r + 1) / 2;
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < D / 32; ++ks)
                     acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[(16 * r + li) * QS + 32 * ks + 8 * lg]),
                                     *reinterpret_cast<const u32x4*>(&sK[(16 * c + li) * QS + 32 * ks + 8 * lg]), acc);
-                const int i = 16 * c + li;
-                const double gi = sG[i];
+                const double gi = sG[16 * c + li];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int n = 16 * r + 4 * lg + v;
-                    const float p = i <= n ? expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
-                    const float hi = top_f32(p);
-                    sP[n * TS + i] = (uint16_t)(__float_as_uint(p) >> 16);
-                    sP[(BL + n) * TS + i] = (uint16_t)(pack_bf16(p - hi, 0.0f) & 0xffffu);
+                    float p = __expf((float)(sG[n] - gi)) * acc[v];
+                    if (r == c) p = li <= 4 * lg + v ? p : 0.0f;
+                    sP[n * TS + 16 * c + li] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sP[(BL + n) * TS + 16 * c + li] = (uint16_t)(__float_as_uint(p - top_f32(p)) >> 16);
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
             // ---- O = e^g o (Q H) ----
             v4f O[4][2];
 #pragma unroll
@@ -397,6 +408,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                         O[r][ct] = mfma_bf16(aq, bl[ct], O[r][ct]);
                     }
                 }
+                __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -406,13 +418,16 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
             }
             __syncthreads();                                       // the scores are written
             // ---- O += (E o Q K^T) V ----
-            const bool any_odd = __any(odd != 0);
-            u32x4 VF[2][2];                                        // finite values only: 0 * v must stay 0
+            // a column's plain sum over the chunk is finite unless one of its values is not
+            // (or they overflow: then the careful path is taken for nothing)
+            v4f sum[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) VF[j][ct] = V[j][ct];
-            if (any_odd)
+                for (int ct = 0; ct < 2; ++ct)
+                    sum[ct] = mfma_bf16(u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}, V[j][ct], sum[ct]);
+            const bool any_odd = __any(!finite_f32(sum[0][0]) | !finite_f32(sum[1][0]));
+            if (any_odd)                                           // finite values first: 0 * v must stay 0
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -420,7 +435,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const uint32_t x = odd_bf16(V[j][ct][e]);
-                            VF[j][ct][e] &= ((x & 0x8000u) ? 0u : 0xffffu) | ((x & 0x80000000u) ? 0u : 0xffff0000u);
+                            V[j][ct][e] &= ((x & 0x8000u) ? 0u : 0xffffu) | ((x & 0x80000000u) ? 0u : 0xffff0000u);
                         }
 #pragma unroll
             for (int r = 0; r < 4; ++r)
@@ -430,35 +445,51 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                     for (int part = 0; part < 2; ++part) {
                         const u32x4 ap = *reinterpret_cast<const u32x4*>(&sP[(part * BL + 16 * r + li) * TS + 32 * j + 8 * lg]);
 #pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(ap, VF[j][ct], O[r][ct]);
+                        for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(ap, V[j][ct], O[r][ct]);
                     }
-            if (any_odd)
+            if (any_odd) {
+                const rsrc_t rv = rows(a.v, c0);
+                const int lq = fresh(4 * lg), vband = fresh(4 * (16 * w + li));
 #pragma unroll 1
-                for (int i = 0; i < L; ++i) {
-                    const uint32_t x = gv[((size_t)(c0 + i) * heads + head) * RD + band];
+                for (int i = 0; i < L; ++i) {                      // then the others, from their own token on
+                    const uint32_t x = row_ld(rv, i * rb + vband);
                     const uint32_t od = odd_bf16(x);
                     if (od)
 #pragma unroll
                         for (int r = 0; r < 4; ++r)
 #pragma unroll
                             for (int v = 0; v < 4; ++v) {
-                                const int n = 16 * r + 4 * lg + v;
+                                const int n = 16 * r + lq + v;
                                 const float p = n < i ? 0.0f
                                                       : bf16_to_f32(sP[n * TS + i]) + bf16_to_f32(sP[(BL + n) * TS + i]);
                                 if (n >= i && (od & 0x8000u)) O[r][0][v] += p * lo_f32(x);
                                 if (n >= i && (od & 0x80000000u)) O[r][1][v] += p * hi_f32(x);
                             }
                 }
-            uint32_t* go = static_cast<uint32_t*>(a.o);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)                        // the state takes them all
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t x0 = row_ld(rv, (32 * j + 2 * lq + 2 * e) * rb + vband);
+                        const uint32_t x1 = row_ld(rv, (32 * j + 2 * lq + 2 * e + 1) * rb + vband);
+                        V[j][0][e] = __builtin_amdgcn_perm(x1, x0, 0x05040100u);
+                        V[j][1][e] = __builtin_amdgcn_perm(x1, x0, 0x07060302u);
+                    }
+            }
+            const rsrc_t ro = rows(a.o, c0);                       // rows past the end are left as they were
+            const uint32_t ooff = 4 * lg * rb + 4 * (16 * w + li);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = 16 * r + 4 * lg + v;
-                    if (n < L) st_nt(go + ((size_t)(c0 + n) * heads + head) * RD + band, pack_bf16(O[r][0][v], O[r][1][v]));
-                }
+                for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, pack_bf16(O[r][0][v], O[r][1][v]));
         }
+        if (c0 + BL < te) {                                        // (here and not earlier: the registers of O are free)
+            load_kq(c0 + BL);
+            load_v(c0 + BL);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         // ---- H = e^{g_L} H + K^T (w o V) ----
+        const int lk = fresh(lane), li = lk & 15, lg = lk >> 4;
         if (a.end || c0 + BL < te) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
@@ -488,11 +519,14 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                     for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
                         for (int part = 0; part < 3; ++part) H[rt][ct] = mfma_bf16(ak, b[part][ct], H[rt][ct]);
+                    if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk
     }
+    if (!a.end && !a.decay) return;
+    const int lf = fresh(lane), lg = lf >> 4, band = 16 * w + (lf & 15);
     if (a.end)
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
@@ -617,13 +651,8 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
             odd |= !finite_f32(V[e]);
         }
         if (w == 0) {
-            double g = lane < L ? (double)log_decay(al) : 0.0;     // lanes past FL: zeros
-#pragma unroll
-            for (int m = 1; m < FL; m <<= 1) {
-                const double x = __shfl_up(g, m, 64);
-                if (lane >= m) g += x;
-            }
-            const double gl = __shfl(g, FL - 1, 64);
+            const double g = wave_scan(lane < L ? (double)log_decay(al) : 0.0);   // lanes past FL: zeros
+            const double gl = __shfl(g, 63, 64);
             if (lane < FL) {
                 sG[lane] = g;
                 sE[lane] = expf((float)g);
@@ -655,7 +684,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int n = 16 * r + 4 * lg + v;
-                    const float p = i <= n ? expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
+                    const float p = i <= n ? __expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
                     const float p1 = p - top_f32(p);
                     sP[0][n * TS + i] = (uint16_t)(__float_as_uint(p) >> 16);
                     sP[1][n * TS + i] = (uint16_t)(__float_as_uint(p1) >> 16);
@@ -807,6 +836,7 @@ __global__ __launch_bounds__(256) void la_step_kernel(LaPrefillArgs a) {
         __builtin_nontemporal_store(H[p], reinterpret_cast<v4f*>(a.h + head * (size_t)(D * D) + (size_t)(p * RPP + rg) * D + c0));
 }
 constexpr int kStepTokens = 4;
+constexpr int kChunkHeads = 1 << 17;   // a chunk's rows lie within 32-bit byte offsets (64 rows of 256 B, 32 of 512 B)
 
 // States before each segment from the states of each segment alone, in place, and the
 // state after the last one: S_s = X, X <- decay_s X + S_s.  Four values per lane.
@@ -881,7 +911,7 @@ hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspac
 template <int D, typename TI>
 hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
     const dim3 grid((unsigned)args.heads);
-    if (args.T <= kStepTokens)
+    if (args.T <= kStepTokens || args.heads > kChunkHeads)
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_step_kernel<D, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
     if constexpr (D >= 64) return la_chunks<D, TI>(d, args, workspace, s);
     else return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, TI>, grid, dim3(LP<D>::NT), s, args);

@@ -16,6 +16,29 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ bool finite_f32(float x) { return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u; }
 
+// x, as a value the compiler must form here: offsets derived from it are computed where
+// they are used instead of held in registers across a loop.
+__device__ __forceinline__ uint32_t fresh(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// Token rows of a chunk as a buffer of `bytes` bytes from base (both wave-uniform): loads
+// past its end give zeros and stores past it are dropped, by the hardware's range check,
+// so the rows of a partial chunk need no masks, and an address is one 32-bit register.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rows(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+}
+__device__ __forceinline__ uint32_t row_ld(rsrc_t r, uint32_t off) { return __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0); }
+__device__ __forceinline__ u32x4 row_ld4(rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+// Streaming store (non-temporal).
+__device__ __forceinline__ void row_st(rsrc_t r, uint32_t off, uint32_t x) {
+    __builtin_amdgcn_raw_buffer_store_b32(x, r, off, 0, 2);
+}
+
 // Two fp32 values to packed bf16 (nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
