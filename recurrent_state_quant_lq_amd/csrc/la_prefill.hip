@@ -426,7 +426,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct)
                     sum[ct] = mfma_bf16(u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u}, V[j][ct], sum[ct]);
-            const bool any_odd = __any(!finite_f32(sum[0][0]) | !finite_f32(sum[1][0]));
+            const bool any_odd = __any(!finite_f32(sum[0][0]) || !finite_f32(sum[1][0]));
             if (any_odd)                                           // finite values first: 0 * v must stay 0
 #pragma unroll
                 for (int j = 0; j < 2; ++j)

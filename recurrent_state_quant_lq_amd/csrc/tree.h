@@ -48,8 +48,8 @@ hipError_t launch_tree_rule(const lq_dims& d, const TreeArgs& args, hipStream_t 
 #ifdef LQ_TREE_KERNELS
 namespace {
 
-// Presence and ancestors of a row's nodes, lane n = node n: own = whether the node's
-// parent entry is valid (-1 or an earlier node), mask = its ancestors while every
+// Presence and ancestors of a row's nodes, lane n = node n with parent entry p (-2: no such node): own = whether the
+// entry is valid (-1 or an earlier node), mask = its ancestors while every
 // entry on the way up is valid.  A node is present if its own entry and all its
 // ancestors' are; no index depends on an unchecked value.  sum: of x over the path
 // (the node included), by pointer doubling.
@@ -59,16 +59,14 @@ struct TreeNode {
     int parent;               // -1: the last committed token
     bool here;
 };
-__device__ __forceinline__ TreeNode tree_node(const int32_t* parent, int N, int lane, float x) {
-    const int p = lane < N ? parent[lane] : -2;
+__device__ __forceinline__ TreeNode tree_node(int p, int lane, float x) {
     const bool own = p == -1 || (p >= 0 && p < lane);
     int jump = own ? p : -1;
     TreeNode t;
     t.parent = jump;
     t.mask = jump >= 0 ? 1ull << jump : 0;
     t.sum = x;
-#pragma unroll
-    for (int i = 0; i < 6; ++i) {                          // paths of doubling length; at most 64 nodes
+    while (__any(jump >= 0)) {                             // paths of doubling length: at most 6 rounds for 64 nodes
         const int from = jump >= 0 ? jump : lane;
         const uint64_t m = __shfl(t.mask, from, 64);
         const float y = __shfl(t.sum, from, 64);
@@ -197,15 +195,16 @@ struct TreeTables {
 };
 
 template <int D, int RULE, typename TI>
-__global__ __launch_bounds__((D < 64 ? 64 : D)) void tree_kernel(TreeArgs a) {
-    constexpr int NT = D < 64 ? 64 : D;
+__global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
+    constexpr int NT = 64;
+    static_assert(D <= NT, "a lane per channel");
     __shared__ TreeTables s_t;
     __shared__ TreeSimple<D> s_s;
     const unsigned b = blockIdx.x / (unsigned)a.H;
     const int pos = a.pos[b];
     if (pos < 0 || pos > a.W) return;                      // a row outside its window: untouched
     if (threadIdx.x < 64) {
-        const TreeNode nd = tree_node(a.parent + (size_t)b * a.N, a.N, threadIdx.x, 0.0f);
+        const TreeNode nd = tree_node((int)threadIdx.x < a.N ? a.parent[(size_t)b * a.N + threadIdx.x] : -2, threadIdx.x, 0.0f);
         s_t.mask[threadIdx.x] = nd.mask;
         s_t.par[threadIdx.x] = (int8_t)nd.parent;
         const uint64_t here = __ballot(nd.here);
@@ -218,29 +217,33 @@ __global__ __launch_bounds__((D < 64 ? 64 : D)) void tree_kernel(TreeArgs a) {
 // ---------------------------------------------------------------------------
 // d >= 64: blocks of 16 nodes on matrix products
 // ---------------------------------------------------------------------------
-// Wave w owns the 32 value columns 32 w + 2 li + ct.  Per block of 16 nodes:
-//   1. the block's q and k rows to LDS as bf16 parts (one for bf16 tokens with a
-//      decay per head; else three; per-key decay: rows scaled by e^{g_n - g_pos},
-//      at most 1);
+// Wave w owns the 16 value columns 16 w + li.  Per group of 32 nodes (two blocks of 16):
+//   1. the q and k rows to LDS as bf16 parts (one for bf16 tokens with a decay per
+//      head; else three; per-key decay: rows scaled by e^{g_n - g_pos}, at most 1);
 //   2. scores against the window's keys (three parts in LDS; per-key decay: scaled by
 //      e^{g_pos - g_c}) and the nodes' keys, times E and the ancestor mask; those of
 //      k times -beta.  Per-key decay takes the nodes' scores pair by pair, with the
 //      exponential of each channel's difference: a product of two factors could
 //      overflow;
-//   3. one wave inverts the block's I + A, A_{n,i} = beta_n <k_n, E k_i> (strictly
+//   3. one wave per block inverts its I + A, A_{n,i} = beta_n <k_n, E k_i> (strictly
 //      lower triangular in node order); the others begin
-//   4. the products with the state, r o sq in three bf16 parts in registers;
-//   5. R = beta (v - Hb^T k) - A_ctx M_ctx, M = (I + A)^{-1} R, O = Hb^T q + S M on the
-//      fp32 matrix instruction: accumulators are its B operand as they are, so M
-//      never leaves the registers.
+//   4. the products with the state, r o sq in three bf16 parts;
+//   5. block after block, without barriers: R = beta (v - Hb^T k) - A_ctx M_ctx,
+//      M = (I + A)^{-1} R, O = Hb^T q + S M on the fp32 matrix instruction:
+//      accumulators are its B operand as they are, so M never leaves the registers.
+// A head's work is a chain of short phases, so what counts is that few of them wait
+// for memory: everything that needs no table is requested at once (state, scales,
+// rows and values of the first group), the window as soon as pos is known, the next
+// group's rows while a group is computed; rows past the end are read from a row that
+// exists, so that no load sits behind a branch.
 // A product of a masked zero with a value that is not finite would spread it: if any
 // m is not finite, the row is computed again node after node.
 template <int D, int NB, int WT, int RULE, typename TI>
 struct TM {
-    static constexpr int NW = D / 32, NT = 64 * NW;
+    static constexpr int NW = D / 16, NT = 64 * NW;
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
-    static constexpr int KB = KDA ? 1 : NB;                        // blocks whose keys stay in LDS
+    static constexpr int KB = KDA ? 2 : NB;                        // blocks whose keys stay in LDS
     static constexpr int QS = D + 8;                               // shorts per row
     static constexpr int WC = 16 * WT;                             // window columns of the scores
     static constexpr int SS = WC + 16 * NB + 4;                    // floats per score row
@@ -248,11 +251,12 @@ struct TM {
         TreeTables t;
         float g[kTreeMax], e[kTreeMax], beta[kTreeMax];            // scalar decay: g_n, e^{g_n}
         float wg[32];                                              // scalar decay: the window's g
-        __align__(16) uint16_t q[NP][16 * QS];
+        __align__(16) float r[D];                                  // row scales (per-key decay: e^{g_pos} r)
+        __align__(16) uint16_t q[NP][32 * QS];
         __align__(16) uint16_t k[NP][16 * KB * QS];
         __align__(16) uint16_t wk[3][WC * QS];
-        __align__(16) float s[2][16 * SS];                         // scores of q; -beta times those of k
-        __align__(16) float inv[16 * 20];                          // (I + A)^{-1}
+        __align__(16) float s[2][32 * SS];                         // scores of q; -beta times those of k
+        __align__(16) float inv[2][16 * 20];                       // (I + A)^{-1} of the group's blocks
         __align__(16) float gk[KDA ? 16 * NB * D : 4];             // per-key decay: g_n
         __align__(16) float gp[KDA ? D : 4];                       // per-key decay: g of slot pos - 1
     };
@@ -263,6 +267,9 @@ struct TM {
             TreeSimple<D> s;
         } f;
     };
+    // waves per SIMD: as many workgroups as the LDS of a CU holds, at most 16 waves per CU
+    static constexpr int FIT = 160 * 1024 / (int)sizeof(Space);
+    static constexpr int WPE = FIT * NW >= 16 ? 4 : FIT * NW >= 12 ? 3 : 2;
 };
 
 // c += a b with a in NP parts, b in three; small products first.
@@ -274,8 +281,29 @@ __device__ __forceinline__ v4f mfma_parts(const u32x4 (&a)[NP], const u32x4 (&b)
     return mfma_bf16(a[0], b[0], c);
 }
 
+// Eight consecutive token values as loaded.
+template <typename TI> struct Raw8 { u32x4 x[sizeof(TI) / 2]; };
+template <typename TI>
+__device__ __forceinline__ Raw8<TI> raw8(const void* base, size_t at) {
+    Raw8<TI> r;
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const TI*>(base) + at);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(TI) / 2); ++i) r.x[i] = p[i];
+    return r;
+}
+template <typename TI>
+__device__ __forceinline__ void widen8(const Raw8<TI>& r, float (&y)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+        if constexpr (sizeof(TI) == 4) y[u] = __uint_as_float(r.x[u / 4][u % 4]);
+        else y[u] = u & 1 ? hi_f32(r.x[0][u / 2]) : lo_f32(r.x[0][u / 2]);
+    }
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
+
 template <int D, int NB, int WT, int RULE, typename TI>
-__global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_kernel(TreeArgs a) {
+__global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE, TI>::WPE)) void tree_mfma_kernel(TreeArgs a) {
     using X = TM<D, NB, WT, RULE, TI>;
     constexpr int NW = X::NW, NT = X::NT, NP = X::NP, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
     constexpr bool KDA = X::KDA, DELTA = X::DELTA;
@@ -288,254 +316,243 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_ke
     const size_t head = blockIdx.x, heads = (size_t)a.heads;
     const unsigned b = blockIdx.x / (unsigned)a.H;
     const int W = a.W, C = a.C, N = a.N;
-    const int pos = a.pos[b];
-    if (pos < 0 || pos > W) return;                        // a row outside its window: untouched
     const float* bk = a.bk + head * (size_t)W * D;
     const float* bm = a.bm + head * (size_t)W * D;
     const float* bg = a.bg + head * (size_t)W * GD;
-    const int col = 32 * w + 2 * li;                       // and col + 1
+    const int col = 16 * w + li;
 
-    // ---- the state's bytes: columns col + ct, channels 64 ks + 16 lg .. + 15 ----
-    v4i raw[KS][2];
+    // ---- requests that depend on nothing ----
+    const int pos = a.pos[b];
+    float nal = 0.0f, nbeta = 0.0f;                        // wave 0: node `lane`
+    int npar = -2;
+    if (w == 0) {
+        const int n = min(lane, N - 1);
+        npar = a.parent[(size_t)b * N + n];
+        if constexpr (!KDA) nal = a.alpha[a.alpha_tok ? (size_t)n * a.alpha_tok + head : head % (unsigned)a.H];
+        if constexpr (DELTA) nbeta = a.beta[(size_t)n * heads + head];
+    }
+    // of each of the group's two blocks: one 8-channel piece of one of its 16 q rows (the lower
+    // half of the lanes) or k rows, and the lane's values
+    constexpr int CPR = D / 8;
+    static_assert(NT == 2 * 16 * CPR, "one piece per lane");
+    const int xk = w >= NW / 2, row = (t - xk * (NT / 2)) / CPR, c8 = 8 * (t % CPR);
+    Raw8<TI> rr[2];
+    TI vr[2][4];
+    auto request = [&](int g) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int n = min(32 * g + 16 * e + row, N - 1);
+            rr[e] = raw8<TI>(xk ? a.k : a.q, ((size_t)n * heads + head) * D + c8);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int m = min(32 * g + 16 * e + 4 * lg + v, N - 1);
+                vr[e][v] = static_cast<const TI*>(a.v)[((size_t)m * heads + head) * D + col];
+            }
+            if (32 * g + 16 < N) continue;                 // (one block: its pieces only)
+            rr[1] = rr[0];
+            break;
+        }
+    };
+    request(0);
+    v4i raw[KS];                                           // column col, channels 64 ks + 16 lg .. + 15
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
+        raw[ks] = ld_nt(reinterpret_cast<const v4i*>(a.sq + head * (size_t)(D * D) + sq_off<D>(64 * ks + 16 * lg, col)));
+    float rs = a.r[head * D + (t & (D - 1))];
+    const float sj = a.s[head * D + col];
+    // compensator rows: B operand of two k = 4 steps, row 4 u + lg
+    float cb[2] = {0.0f, 0.0f};
+    int ci[2] = {0, 0};
+    if (C > 0)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct)
-            raw[ks][ct] = *reinterpret_cast<const v4i*>(a.sq + head * (size_t)(D * D) + sq_off<D>(64 * ks + 16 * lg, col + ct));
-
-    // ---- node tables ----
-    if (w == 0) {
-        float al = 0.0f;
-        const size_t th = (size_t)min(lane, N - 1) * heads + head;
-        if constexpr (!KDA) {
-            al = a.alpha_tok ? a.alpha[(size_t)min(lane, N - 1) * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
-            al = DELTA ? logf(al) : log_decay(al);
+        for (int u = 0; u < 2; ++u) {
+            const size_t c = head * C + min(4 * u + lg, C - 1);
+            ci[u] = a.idx[c];
+            cb[u] = a.cv[c * D + col];
         }
-        const TreeNode nd = tree_node(a.parent + (size_t)b * N, N, lane, al);
+    if (pos < 0 || pos > W) return;                        // a row outside its window: untouched
+
+    // ---- the window's requests: one 8-channel piece of a key row per lane, the column's m rows ----
+    const int wt = (pos + 15) >> 4;                        // window tiles in use
+    const int wrow = t / CPR, last = max(pos - 1, 0);
+    float wx[8], wgc[KDA ? 8 : 1];
+    float gpos = 0.0f, gw = 0.0f;                          // g of slot pos - 1 (per-key decay: channel t); of slot `lane`
+    v4f WM[WT];
+    if (pos > 0) {
+        const size_t at = (size_t)min(wrow, last) * D + c8;
+        load_floats<8>(bk + at, wx);
+        if constexpr (KDA) load_floats<8>(bg + at, wgc);
+#pragma unroll
+        for (int c = 0; c < WT; ++c)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) WM[c][v] = bm[(size_t)min(16 * c + 4 * lg + v, last) * D + col];
+        if constexpr (KDA) gpos = bg[(size_t)last * D + (t & (D - 1))];
+        else if (w == 0) {
+            gpos = bg[last];
+            gw = bg[min(lane, last)];
+        }
+    }
+    // ---- tables ----
+    if (w == 0) {
+        const TreeNode nd = tree_node(lane < N ? npar : -2, lane, KDA ? 0.0f : DELTA ? logf(nal) : log_decay(nal));
         s.t.mask[lane] = nd.here ? nd.mask : 0;
         s.t.par[lane] = (int8_t)nd.parent;
         const uint64_t here = __ballot(nd.here);
         if (lane == 0) s.t.here = here;
-        if constexpr (DELTA) s.beta[lane] = nd.here ? a.beta[th] : 0.0f;
+        if constexpr (DELTA) s.beta[lane] = nd.here ? nbeta : 0.0f;
         if constexpr (!KDA) {
-            const float g = nd.sum + (pos > 0 ? bg[pos - 1] : 0.0f);
+            const float g = nd.sum + gpos;
             s.g[lane] = g;
             s.e[lane] = expf(g);
             if (nd.here) a.tg[head * N + lane] = g;
-            if (lane < 32) s.wg[lane] = lane < pos ? bg[lane] : 0.0f;
+            if (lane < 32) s.wg[lane] = gw;
         }
     }
     if constexpr (KDA)
-        if (t < D) s.gp[t] = pos > 0 ? bg[(size_t)(pos - 1) * D + t] : 0.0f;
+        if (t < D) {
+            s.gp[t] = gpos;
+            rs *= expf(gpos);
+        }
+    if (t < D) s.r[t] = rs;
+    // ---- window keys in three parts ----
+    if constexpr (KDA) __syncthreads();                    // gp
+    if (wrow < 16 * wt) {
+        uint32_t p[3][4];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if constexpr (KDA) wx[u] *= expf(s.gp[c8 + u] - wgc[u]);
+            wx[u] = wrow < pos ? wx[u] : 0.0f;
+        }
+        split3<8>(wx, p);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+            *reinterpret_cast<u32x4*>(&s.wk[m][wrow * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+    }
+#pragma unroll
+    for (int c = 0; c < WT; ++c)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) WM[c][v] = 16 * c + 4 * lg + v < pos ? WM[c][v] : 0.0f;
     __syncthreads();
     const uint64_t here = s.t.here;
     if constexpr (KDA) {
         // g of every node, channel t
         if (t < D)
-            for (int n = 0; n < 16 * NB; ++n) {
-                float g = 0.0f;
-                if ((here >> n) & 1u) {
-                    const int par = s.t.par[n];
-                    g = (par >= 0 ? s.gk[par * D + t] : s.gp[t]) + logf(a.alpha[((size_t)n * heads + head) * D + t]);
-                    a.tg[(head * N + n) * D + t] = g;
+            for (int n0 = 0; n0 < N; n0 += 8) {
+                float al[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) al[u] = a.alpha[((size_t)min(n0 + u, N - 1) * heads + head) * D + t];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int n = n0 + u;
+                    float g = 0.0f;
+                    if ((here >> n) & 1u) {
+                        const int par = s.t.par[n];
+                        g = (par >= 0 ? s.gk[par * D + t] : gpos) + logf(al[u]);
+                        a.tg[(head * N + n) * D + t] = g;
+                    }
+                    s.gk[n * D + t] = g;
                 }
-                s.gk[n * D + t] = g;
             }
         __syncthreads();
     }
-    // ---- the window: keys in three parts to LDS, m rows to registers ----
-    const int wt = (pos + 15) >> 4;                        // window tiles in use
-    for (int e = t; e < 16 * wt * (D / 8); e += NT) {
-        const int c = e / (D / 8), c8 = 8 * (e % (D / 8));
-        float x[8];
-        uint32_t p[3][4];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = 0.0f;
-        if (c < pos) {
-            load_floats<8>(bk + (size_t)c * D + c8, x);
-            if constexpr (KDA) {
-                float gc[8];
-                load_floats<8>(bg + (size_t)c * D + c8, gc);
-#pragma unroll
-                for (int u = 0; u < 8; ++u) x[u] *= expf(s.gp[c8 + u] - gc[u]);
-            }
-        }
-        split3<8>(x, p);
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-            *reinterpret_cast<u32x4*>(&s.wk[m][c * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
-    }
-    v4f WM[WT][2];
-#pragma unroll
-    for (int c = 0; c < WT; ++c)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int n = 16 * c + 4 * lg + v;
-            f32x2 x = {0.f, 0.f};
-            if (n < pos) x = *reinterpret_cast<const f32x2*>(bm + (size_t)n * D + col);
-            WM[c][0][v] = x[0];
-            WM[c][1][v] = x[1];
-        }
-    // ---- r o sq (per-key decay: o e^{g_pos}) in three parts: B operands, half hf of 64 channels ks
-    //      holds channels 64 ks + 16 lg + 8 hf .. + 7 ----
-    u32x4 st[KS][2][2][3];                                 // [ks][hf][ct][part]
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            float r[8];
-            load_floats<8>(a.r + head * D + 64 * ks + 16 * lg + 8 * hf, r);
-            if constexpr (KDA)
-#pragma unroll
-                for (int u = 0; u < 8; ++u) r[u] *= expf(s.gp[64 * ks + 16 * lg + 8 * hf + u]);
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                float x[8];
-                uint32_t p[3][4];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) x[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
-                split3<8>(x, p);
-#pragma unroll
-                for (int m = 0; m < 3; ++m) st[ks][hf][ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
-            }
-        }
-    const f32x2 sj = *reinterpret_cast<const f32x2*>(a.s + head * D + col);
-    // compensator rows: B operand of two k = 4 steps, row 4 u + lg
-    float cb[2][2];
-    int ci[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        const int c = 4 * u + lg;
-        f32x2 x = {0.f, 0.f};
-        ci[u] = 0;
-        if (c < C) {
-            ci[u] = a.idx[head * C + c] & (D - 1);
-            x = *reinterpret_cast<const f32x2*>(a.cv + (head * C + c) * (size_t)D + col);
-            if constexpr (KDA) x *= expf(s.gp[ci[u]]);
-        }
-        cb[u][0] = x[0];
-        cb[u][1] = x[1];
+        ci[u] &= D - 1;
+        if constexpr (KDA) cb[u] *= expf(s.gp[ci[u]]);
+        cb[u] = 4 * u + lg < C ? cb[u] : 0.0f;
     }
 
-    v4f M[NB][2];
+    v4f M[NB];
     bool odd = false;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        if (16 * j >= N) break;
-        // values, ahead of the rows' work
-        f32x2 vr[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int n = 16 * j + 4 * lg + v;
-            vr[v] = f32x2{0.f, 0.f};
-            if ((here >> n) & 1u) {
-                const size_t at = ((size_t)n * heads + head) * D + col;
-                if constexpr (sizeof(TI) == 4) vr[v] = *reinterpret_cast<const f32x2*>(static_cast<const float*>(a.v) + at);
-                else {
-                    const uint32_t x = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.v) + at);
-                    vr[v] = f32x2{lo_f32(x), hi_f32(x)};
-                }
-            }
-        }
+    for (int g = 0; g < NB / 2; ++g) {
+        if (32 * g >= N) break;
+        const int nb = 32 * g + 16 < N ? 2 : 1;            // blocks of this group
         // ---- 1. rows ----
-        {
-            constexpr int CPR = D / 8;
-            static_assert(NT == 16 * CPR, "one 8-channel piece of one row per lane");
-            const int row = t / CPR, c8 = 8 * (t % CPR), n = 16 * j + row;
-            const size_t at = ((size_t)n * heads + head) * D + c8;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 16 * e + row, n = 32 * g + r;
             const bool on = (here >> n) & 1u;              // absent nodes: zeros
-            float sc[8];
-            if constexpr (KDA)
+            uint16_t* dst = xk ? &s.k[0][((KB > 2 ? 32 * g : 0) + r) * QS + c8] : &s.q[0][r * QS + c8];
+            if constexpr (NP == 1) {
+                *reinterpret_cast<u32x4*>(dst) = on ? rr[e].x[0] : u32x4{0, 0, 0, 0};
+            } else {
+                const size_t plane = xk ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
+                float y[8];
+                uint32_t p[3][4];
+                widen8<TI>(rr[e], y);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) sc[u] = on ? expf(s.gk[n * D + c8 + u] - s.gp[c8 + u]) : 0.0f;
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (KDA && !DELTA && x) break;
-                uint16_t* dst = x ? &s.k[0][((KB > 1 ? 16 * j : 0) + row) * QS + c8] : &s.q[0][row * QS + c8];
-                const size_t plane = x ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
-                if constexpr (NP == 1) {
-                    u32x4 y = {0, 0, 0, 0};
-                    if (on) y = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x ? a.k : a.q) + at);
-                    *reinterpret_cast<u32x4*>(dst) = y;
-                } else {
-                    float y[8];
-                    uint32_t p[3][4];
-#pragma unroll
-                    for (int u = 0; u < 8; ++u) y[u] = 0.0f;
-                    if (on) {
-                        if constexpr (sizeof(TI) == 4) load_floats<8>(static_cast<const float*>(x ? a.k : a.q) + at, y);
-                        else {
-                            const u32x4 z = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x ? a.k : a.q) + at);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                y[2 * u] = lo_f32(z[u]);
-                                y[2 * u + 1] = hi_f32(z[u]);
-                            }
-                        }
-                        if constexpr (KDA)
-#pragma unroll
-                            for (int u = 0; u < 8; ++u) y[u] *= sc[u];
-                    }
-                    split3<8>(y, p);
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) *reinterpret_cast<u32x4*>(dst + m * plane) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                for (int u = 0; u < 8; ++u) {
+                    if constexpr (KDA) y[u] *= on ? expf(s.gk[n * D + c8 + u] - s.gp[c8 + u]) : 0.0f;
+                    y[u] = on ? y[u] : 0.0f;
                 }
+                split3<8>(y, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) *reinterpret_cast<u32x4*>(dst + m * plane) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
         }
+        float vv[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) vv[e][v] = (here >> (32 * g + 16 * e + 4 * lg + v)) & 1u ? widen(vr[e][v]) : 0.0f;
+        if (g + 1 < NB / 2 && 32 * (g + 1) < N) request(g + 1);
         __syncthreads();
         // ---- 2. scores ----
         {
-            const int nt = wt + (KDA ? 0 : j + 1);         // context tiles of matrix products
-            for (int it = w; it < NX * nt; it += NW) {
-                const int x = it >= nt, c = x ? it - nt : it;
-                const uint16_t* arow = x ? &s.k[0][((KB > 1 ? 16 * j : 0) + li) * QS] : &s.q[0][li * QS];
+            const int nt0 = wt + (KDA ? 0 : 2 * g + 1), per = nb == 1 ? nt0 : 2 * nt0 + (KDA ? 0 : 1);   // tiles of block 0, of the group
+            for (int it = w; it < NX * per; it += NW) {
+                const int x = it >= per, y0 = x ? it - per : it, e = y0 >= nt0, c = e ? y0 - nt0 : y0;
                 const size_t plane = x ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
-                v4f acc = {0.f, 0.f, 0.f, 0.f};
+                const uint16_t* arow = (x ? &s.k[0][((KB > 2 ? 32 * g : 0) + 16 * e + li) * QS] : &s.q[0][(16 * e + li) * QS]) + 8 * lg;
                 const bool win = c < wt;
+                const int i = 16 * (c - wt) + li;          // node of this lane's column (node tiles)
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+                if (win) {
+                    const uint16_t* brow = &s.wk[0][(16 * c + li) * QS + 8 * lg];
 #pragma unroll
-                for (int ks = 0; ks < D / 32; ++ks) {
-                    const int ch = 32 * ks + 8 * lg;
-                    u32x4 ar[NP];
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        u32x4 ar[NP], br[3];
 #pragma unroll
-                    for (int m = 0; m < NP; ++m) ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + ch);
-                    if (win) {
-                        u32x4 br[3];
+                        for (int m = 0; m < NP; ++m) ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 32 * ks);
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(&s.wk[m][(16 * c + li) * QS + ch]);
+                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(brow + m * (sizeof(s.wk[0]) / 2) + 32 * ks);
                         acc = mfma_parts<NP>(ar, br, acc);
-                    } else if constexpr (NP == 1) {
-                        acc = mfma_bf16(ar[0], *reinterpret_cast<const u32x4*>(&s.k[0][(16 * (c - wt) + li) * QS + ch]), acc);
-                    } else if constexpr (!KDA) {
-                        u32x4 br[3];
+                    }
+                } else if constexpr (!KDA) {
+                    const uint16_t* brow = &s.k[0][i * QS + 8 * lg];
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(&s.k[m][(16 * (c - wt) + li) * QS + ch]);
-                        acc = mfma_split(ar, br, acc);
+                    for (int ks = 0; ks < D / 32; ++ks) {
+                        u32x4 ar[NP], br[NP];
+#pragma unroll
+                        for (int m = 0; m < NP; ++m) {
+                            ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 32 * ks);
+                            br[m] = *reinterpret_cast<const u32x4*>(brow + m * (sizeof(s.k[0]) / 2) + 32 * ks);
+                        }
+                        if constexpr (NP == 1) acc = mfma_bf16(ar[0], br[0], acc);
+                        else acc = mfma_split(ar, br, acc);
                     }
                 }
-                const int i = 16 * (c - wt) + li;          // node of this lane's column (node tiles)
+                const float gc = KDA ? 0.0f : win ? s.wg[(16 * c + li) & 31] : s.g[i & 63];
+                const int n0 = 32 * g + 16 * e + 4 * lg;
+                float* dst = &s.s[x][(16 * e + 4 * lg) * SS + (win ? 16 * c : WC + 16 * (c - wt)) + li];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    const int r = 4 * lg + v, n = 16 * j + r;
+                    const int n = n0 + v;
+                    const bool on = win ? 16 * c + li < pos && ((here >> n) & 1u) : (s.t.mask[n] >> (i & 63)) & 1u;
                     float y = acc[v];
-                    bool on;
-                    if (win) {
-                        on = 16 * c + li < pos && ((here >> n) & 1u);
-                        if constexpr (!KDA) y *= on ? expf(s.g[n] - s.wg[(16 * c + li) & 31]) : 0.0f;
-                    } else {
-                        on = (s.t.mask[n] >> i) & 1u;
-                        if constexpr (!KDA) y *= on ? expf(s.g[n] - s.g[i]) : 1.0f;
-                        if (!x && i == n) on = true;       // <q_n, k_n>
-                    }
+                    if constexpr (!KDA) y *= on ? expf(s.g[n] - gc) : 1.0f;
                     if (DELTA && x) y *= -s.beta[n];
-                    s.s[x][r * SS + (win ? 16 * c : WC + 16 * (c - wt)) + li] = on ? y : 0.0f;
+                    // (the diagonal of the q scores: <q_n, k_n>)
+                    dst[v * SS] = on || (!win && !x && i == n) ? y : 0.0f;
                 }
             }
             if constexpr (KDA) {
                 // node pairs, a row per wave at a time, four ancestors at once (16 lanes each)
                 constexpr int CH = D / 16;
-                for (int r = w; r < 16; r += NW) {
-                    const int n = 16 * j + r;
-                    for (int c = lane; c < 16 * (j + 1); c += 64) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
+                for (int r = w; r < 16 * nb; r += NW) {
+                    const int n = 32 * g + r;
+                    for (int c = lane; c < 32 * g + 16 * nb; c += 64) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
                     if (!((here >> n) & 1u)) continue;
                     const size_t at = ((size_t)n * heads + head) * D + CH * li;
                     float qn[CH], kn[CH], gn[CH];
@@ -545,7 +562,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_ke
                         kn[u] = tok_ld<TI>(a.k, at + u);
                     }
                     load_floats<CH>(&s.gk[n * D + CH * li], gn);
-                    const float nb = -s.beta[n];
+                    const float nbt = -s.beta[n];
                     uint64_t left = s.t.mask[n] | (1ull << n);
                     left = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(left >> 32)) << 32) |
                            (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)left);
@@ -559,7 +576,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_ke
                                 if (lg == u) i = f;
                             }
                         }
-                        float xq = 0.0f, xk = 0.0f;
+                        float xq = 0.0f, xk2 = 0.0f;
                         if (i >= 0) {
                             float gi[CH];
                             load_floats<CH>(&s.gk[i * D + CH * li], gi);
@@ -568,27 +585,29 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_ke
                                 float ki = tok_ld<TI>(a.k, ((size_t)i * heads + head) * D + CH * li + u);
                                 if (i != n) ki *= __expf(gn[u] - gi[u]);
                                 xq += qn[u] * ki;
-                                xk += kn[u] * ki;
+                                xk2 += kn[u] * ki;
                             }
                         }
                         xq = group_sum<16>(xq);
-                        xk = group_sum<16>(xk);
+                        xk2 = group_sum<16>(xk2);
                         if (li == 0 && i >= 0) {
                             s.s[0][r * SS + WC + i] = xq;
-                            if (i != n) s.s[1][r * SS + WC + i] = nb * xk;
+                            if (i != n) s.s[1][r * SS + WC + i] = nbt * xk2;
                         }
                     }
                 }
             }
         }
         __syncthreads();
-        // ---- 3. (I + A)^{-1}, lane c < 16 its column c ----
-        if (DELTA && w == NW - 1 && lane < 16) {
+        // ---- 3. (I + A)^{-1} of block NW - 1 - w, lane c < 16 its column c ----
+        if (DELTA && w >= NW - nb && lane < 16) {
+            const int e = NW - 1 - w;
+            const float* arow = &s.s[1][16 * e * SS + WC + 32 * g + 16 * e];
             float tc[16];
 #pragma unroll
             for (int n = 0; n < 16; ++n) {
                 float ar[16];
-                load_floats<16>(&s.s[1][n * SS + WC + 16 * j], ar);
+                load_floats<16>(arow + n * SS, ar);
                 float x0 = n == lane ? 1.0f : 0.0f, x1 = 0.0f;
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
@@ -596,97 +615,108 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), 2) void tree_mfma_ke
                     else x0 = __builtin_fmaf(ar[i], tc[i], x0);
                 }
                 tc[n] = x0 + x1;
-                s.inv[n * 20 + lane] = tc[n];
+                s.inv[e][n * 20 + lane] = tc[n];
             }
         }
         // ---- 4. products with the state ----
-        v4f acc[NX][2], cmp[NX][2];
+        v4f acc[2][NX];
 #pragma unroll
-        for (int x = 0; x < NX; ++x) {
-            const uint16_t* arow = x ? &s.k[0][((KB > 1 ? 16 * j : 0) + li) * QS] : &s.q[0][li * QS];
-            const size_t plane = x ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
-            acc[x][0] = acc[x][1] = cmp[x][0] = cmp[x][1] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+            for (int x = 0; x < NX; ++x) acc[e][x] = v4f{0.f, 0.f, 0.f, 0.f};
+        const uint16_t* qrow = &s.q[0][li * QS];
+        const uint16_t* krow = &s.k[0][((KB > 2 ? 32 * g : 0) + li) * QS];
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                    u32x4 ar[NP];
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int m = 0; m < NP; ++m)
-                        ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 64 * ks + 16 * lg + 8 * hf);
+            for (int hf = 0; hf < 2; ++hf) {
+                // B operand: channels 64 ks + 16 lg + 8 hf .. + 7 of column col
+                const int ch = 64 * ks + 16 * lg + 8 * hf;
+                float r[8], x8[8];
+                uint32_t p[3][4];
+                u32x4 st[3];
+                load_floats<8>(&s.r[ch], r);
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) acc[x][ct] = mfma_parts<NP>(ar, st[ks][hf][ct], acc[x][ct]);
+                for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][2 * hf + u / 4], u % 4) * r[u];
+                split3<8>(x8, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) st[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (e >= nb) break;
+#pragma unroll
+                    for (int x = 0; x < NX; ++x) {
+                        u32x4 ar[NP];
+#pragma unroll
+                        for (int m = 0; m < NP; ++m)
+                            ar[m] = *reinterpret_cast<const u32x4*>((x ? krow + m * (sizeof(s.k[0]) / 2) : qrow + m * (sizeof(s.q[0]) / 2)) +
+                                                                    16 * e * QS + ch);
+                        acc[e][x] = mfma_parts<NP>(ar, st, acc[e][x]);
+                    }
                 }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float y = 0.0f;
-#pragma unroll
-                for (int m = NP - 1; m >= 0; --m) y += bf16_to_f32(arow[m * plane + ci[u]]);
-                if (C > 4 * u)
-#pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) cmp[x][ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(y, cb[u][ct], cmp[x][ct], 0, 0, 0);
             }
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                acc[x][ct] = acc[x][ct] * sj[ct] + cmp[x][ct];
-                if constexpr (!KDA) acc[x][ct] *= *reinterpret_cast<const v4f*>(&s.e[16 * j + 4 * lg]);
+        for (int e = 0; e < 2; ++e) {
+            if (e >= nb) break;
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                v4f cmp = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int m = NP - 1; m >= 0; --m)
+                        z += bf16_to_f32((x ? krow + m * (sizeof(s.k[0]) / 2) : qrow + m * (sizeof(s.q[0]) / 2))[16 * e * QS + ci[u]]);
+                    if (C > 4 * u) cmp = __builtin_amdgcn_mfma_f32_16x16x4f32(z, cb[u], cmp, 0, 0, 0);
+                }
+                acc[e][x] = acc[e][x] * sj + cmp;
+                if constexpr (!KDA) acc[e][x] *= *reinterpret_cast<const v4f*>(&s.e[32 * g + 16 * e + 4 * lg]);
             }
         }
-        __syncthreads();                                   // the inverse; the rows may be overwritten
+        __syncthreads();                                   // the inverses; the rows may be overwritten
         // ---- 5. m and o ----
-        auto context = [&](int x, v4f (&y)[2]) {           // y += scores x context
 #pragma unroll
-            for (int c = 0; c < WT + NB; ++c) {
-                if (c < WT ? c >= wt : c - WT >= j) continue;
-                const int cc = c < WT ? 16 * c : WC + 16 * (c - WT);
-                const v4f sr = *reinterpret_cast<const v4f*>(&s.s[x][li * SS + cc + 4 * lg]);
+        for (int e = 0; e < 2; ++e) {
+            if (e >= nb) break;
+            const int j = 2 * g + e;
+            auto context = [&](int x, v4f y) {             // y + scores x context
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
+                for (int c = 0; c < WT + NB; ++c) {
+                    if (c < WT ? c >= wt : c - WT >= j) continue;
+                    const int cc = c < WT ? 16 * c : WC + 16 * (c - WT);
+                    const v4f sr = *reinterpret_cast<const v4f*>(&s.s[x][(16 * e + li) * SS + cc + 4 * lg]);
+                    const v4f m = c < WT ? WM[c < WT ? c : 0] : M[c < WT ? 0 : c - WT];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v)
-                        y[ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], c < WT ? WM[c < WT ? c : 0][ct][v] : M[c < WT ? 0 : c - WT][ct][v],
-                                                                     y[ct], 0, 0, 0);
+                    for (int v = 0; v < 4; ++v) y = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], m[v], y, 0, 0, 0);
+                }
+                return y;
+            };
+            v4f o = context(0, acc[e][0]);
+            if constexpr (DELTA) {
+                const v4f be = *reinterpret_cast<const v4f*>(&s.beta[16 * j + 4 * lg]);
+                v4f R;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) R[v] = be[v] * (vv[e][v] - acc[e][NX - 1][v]);
+                R = context(1, R);
+                const v4f ti = *reinterpret_cast<const v4f*>(&s.inv[e][li * 20 + 4 * lg]);
+                M[j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int v = 0; v < 4; ++v) M[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[v], R[v], M[j], 0, 0, 0);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) M[j][v] = vv[e][v];
             }
-        };
-        if constexpr (DELTA) {
-            const v4f be = *reinterpret_cast<const v4f*>(&s.beta[16 * j + 4 * lg]);
-            v4f R[2];
+            const v4f sr = *reinterpret_cast<const v4f*>(&s.s[0][(16 * e + li) * SS + WC + 16 * j + 4 * lg]);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) R[ct][v] = be[v] * (vr[v][ct] - acc[1][ct][v]);
-            context(1, R);
-            const v4f ti = *reinterpret_cast<const v4f*>(&s.inv[li * 20 + 4 * lg]);
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
-                M[j][ct] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int v = 0; v < 4; ++v) M[j][ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[v], R[ct][v], M[j][ct], 0, 0, 0);
-            }
-        } else {
+            for (int v = 0; v < 4; ++v) o = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], M[j][v], o, 0, 0, 0);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                M[j][0][v] = vr[v][0];
-                M[j][1][v] = vr[v][1];
+                const int n = 16 * j + 4 * lg + v;
+                odd |= !finite_f32(M[j][v]);
+                if (!((here >> n) & 1u)) continue;
+                tok_st<TI>(a.o, ((size_t)n * heads + head) * D + col, o[v]);
+                st_nt(a.tm + (head * N + n) * (size_t)D + col, M[j][v]);
             }
-        }
-        context(0, acc[0]);
-        {
-            const v4f sr = *reinterpret_cast<const v4f*>(&s.s[0][li * SS + WC + 16 * j + 4 * lg]);
-#pragma unroll
-            for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[0][ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], M[j][ct][v], acc[0][ct], 0, 0, 0);
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int n = 16 * j + 4 * lg + v;
-            odd |= !finite_f32(M[j][0][v]) | !finite_f32(M[j][1][v]);
-            if (!((here >> n) & 1u)) continue;
-            const size_t at = ((size_t)n * heads + head) * D + col;
-            if constexpr (sizeof(TI) == 4) *reinterpret_cast<f32x2*>(static_cast<float*>(a.o) + at) = f32x2{acc[0][0][v], acc[0][1][v]};
-            else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at) = pack_bf16(acc[0][0][v], acc[0][1][v]);
-            *reinterpret_cast<f32x2*>(a.tm + (head * N + n) * (size_t)D + col) = f32x2{M[j][0][v], M[j][1][v]};
         }
     }
     if (__syncthreads_or(odd)) tree_simple<D, RULE, TI, NT>(a, pos, sp.f.t.mask, sp.f.t.par, here, sp.f.s);
@@ -696,10 +726,10 @@ template <int D, int RULE, typename TI>
 hipError_t tree_mfma(const lq_dims& d, const TreeArgs& args, hipStream_t s) {
     const dim3 grid((unsigned)args.heads);
     if (args.N <= 32)
-        return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 1, RULE, TI>, grid, dim3(2 * D), s, args)
-                         : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 2, RULE, TI>, grid, dim3(2 * D), s, args);
-    return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 1, RULE, TI>, grid, dim3(2 * D), s, args)
-                     : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 2, RULE, TI>, grid, dim3(2 * D), s, args);
+        return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 1, RULE, TI>, grid, dim3(4 * D), s, args)
+                         : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 2, RULE, TI>, grid, dim3(4 * D), s, args);
+    return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 1, RULE, TI>, grid, dim3(4 * D), s, args)
+                     : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 2, RULE, TI>, grid, dim3(4 * D), s, args);
 }
 
 template <int RULE, typename TI>

@@ -18,32 +18,39 @@ struct CommitArgs {
     int N, P, W, H, heads, gd;
 };
 
-// One workgroup per (b, h): the path's slots, copied.
+// One workgroup per (b, h): the path's slots, copied; D/4 lanes per slot (four values
+// of each row a lane), all slots of up to 1024/D nodes at once.
 template <int D, typename TI>
-__global__ __launch_bounds__((D < 64 ? 64 : D)) void commit_kernel(CommitArgs a) {
-    const int t = threadIdx.x;
+__global__ __launch_bounds__(256) void commit_kernel(CommitArgs a) {
+    constexpr int LPS = D / 4, SPP = 256 / LPS;            // lanes per slot, slots per pass
+    const int t = threadIdx.x, lane = t & 63;
     const size_t head = blockIdx.x;
     const unsigned b = blockIdx.x / (unsigned)a.H;
     const int pos = a.pos[b], n = a.n_path[b];
+    const int node_l = lane < a.P ? a.path[(size_t)b * a.P + lane] : 0;    // P <= 64
     if (pos < 0 || pos >= a.W || n < 1 || n > a.P || n > a.W - pos) return;
-    const int32_t* path = a.path + (size_t)b * a.P;
-    bool ok = true;
-    for (int i = 0; i < n; ++i) ok &= path[i] >= 0 && path[i] < a.N;
-    if (!ok) return;
-    for (int i = 0; i < n; ++i) {
-        const int node = path[i];
+    if (__any(lane < n && (node_l < 0 || node_l >= a.N))) return;          // (every wave sees the whole path)
+    const int c = 4 * (t % LPS);
+    for (int i = t / LPS; i < n; i += SPP) {
+        const int node = a.path[(size_t)b * a.P + i];
         const size_t slot = head * a.W + pos + i, from = head * a.N + node;
-        if (t < D) {
-            a.bk[slot * D + t] = tok_ld<TI>(a.k, ((size_t)node * a.heads + head) * D + t);
-            a.bm[slot * D + t] = a.tm[from * D + t];
-        }
-        if (t < a.gd) a.bg[slot * a.gd + t] = a.tg[from * a.gd + t];
+        const size_t kf = ((size_t)node * a.heads + head) * D + c;
+        float k[4], m[4], g[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) k[u] = tok_ld<TI>(a.k, kf + u);
+        load_floats<4>(a.tm + from * D + c, m);
+        if (a.gd > 1) load_floats<4>(a.tg + from * D + c, g);
+        else if (c == 0) g[0] = a.tg[from];
+        store_floats<4>(a.bk + slot * D + c, k);
+        store_floats<4>(a.bm + slot * D + c, m);
+        if (a.gd > 1) store_floats<4>(a.bg + slot * D + c, g);
+        else if (c == 0) a.bg[slot] = g[0];
     }
 }
 
 template <int D>
 hipError_t commit_t(const lq_dims& d, const CommitArgs& args, hipStream_t s) {
-    const dim3 grid((unsigned)d.B * (unsigned)d.H), block(D < 64 ? 64 : D);
+    const dim3 grid((unsigned)d.B * (unsigned)d.H), block(256);
     if (d.io_dtype == LQ_IO_BF16) return launch_kernel(LQ_KERNEL_COMMIT, commit_kernel<D, uint16_t>, grid, block, s, args);
     return launch_kernel(LQ_KERNEL_COMMIT, commit_kernel<D, float>, grid, block, s, args);
 }
