@@ -217,7 +217,8 @@ __global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
 // ---------------------------------------------------------------------------
 // d >= 64: blocks of 16 nodes on matrix products
 // ---------------------------------------------------------------------------
-// Wave w owns the 16 value columns 16 w + li.  Per group of 32 nodes (two blocks of 16):
+// Wave w owns the 32 value columns 32 w + 2 li + ct (a lane's two columns are neighbours:
+// one dword of bf16 values, one 8-byte pair of fp32 ones).  Per group of GB blocks:
 //   1. the q and k rows to LDS as bf16 parts (one for bf16 tokens with a decay per
 //      head; else three; per-key decay: rows scaled by e^{g_n - g_pos}, at most 1);
 //   2. scores against the window's keys (three parts in LDS; per-key decay: scaled by
@@ -225,12 +226,12 @@ __global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
 //      k times -beta.  Per-key decay takes the nodes' scores pair by pair, with the
 //      exponential of each channel's difference: a product of two factors could
 //      overflow;
-//   3. one wave per block inverts its I + A, A_{n,i} = beta_n <k_n, E k_i> (strictly
-//      lower triangular in node order); the others begin
-//   4. the products with the state, r o sq in three bf16 parts;
-//   5. block after block, without barriers: R = beta (v - Hb^T k) - A_ctx M_ctx,
-//      M = (I + A)^{-1} R, O = Hb^T q + S M on the fp32 matrix instruction:
-//      accumulators are its B operand as they are, so M never leaves the registers.
+//   3. the products with the state, r o sq in three bf16 parts formed on the way;
+//   4. block after block, without barriers: R = beta (v - Hb^T k) - A_ctx M_ctx,
+//      M = (I + A)^{-1} R with A_{n,i} = beta_n <k_n, E k_i> (strictly lower triangular in
+//      node order, solved four rows at a time), O = Hb^T q + S M, on the fp32 matrix
+//      instruction: accumulators are its B operand as they are, so M never leaves the
+//      registers.
 // A head's work is a chain of short phases, so what counts is that few of them wait
 // for memory: everything that needs no table is requested at once (state, scales,
 // rows and values of the first group), the window as soon as pos is known, the next
@@ -240,25 +241,29 @@ __global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
 // m is not finite, the row is computed again node after node.
 template <int D, int NB, int WT, int RULE, typename TI>
 struct TM {
-    static constexpr int NW = D / 16, NT = 64 * NW;
+    static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
-    static constexpr int KB = KDA ? 2 : NB;                        // blocks whose keys stay in LDS
+    static constexpr int GB = NP == 1 ? 2 : 1;                     // blocks per group
+    static constexpr int KB = KDA ? GB : NB;                       // blocks whose keys stay in LDS
+    static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
     static constexpr int QS = D + 8;                               // shorts per row
     static constexpr int WC = 16 * WT;                             // window columns of the scores
     static constexpr int SS = WC + 16 * NB + 4;                    // floats per score row
     struct Shared {
         TreeTables t;
-        float g[kTreeMax], e[kTreeMax], beta[kTreeMax];            // scalar decay: g_n, e^{g_n}
+        __align__(16) float g[kTreeMax];                           // scalar decay: g_n (absent nodes: that of slot pos - 1)
+        __align__(16) float e[kTreeMax];                           // scalar decay: e^{g_n}
+        __align__(16) float beta[kTreeMax];
         float wg[32];                                              // scalar decay: the window's g
         __align__(16) float r[D];                                  // row scales (per-key decay: e^{g_pos} r)
-        __align__(16) uint16_t q[NP][32 * QS];
+        __align__(16) uint16_t q[NP][16 * GB * QS];
         __align__(16) uint16_t k[NP][16 * KB * QS];
         __align__(16) uint16_t wk[3][WC * QS];
-        __align__(16) float s[2][32 * SS];                         // scores of q; -beta times those of k
-        __align__(16) float inv[2][16 * 20];                       // (I + A)^{-1} of the group's blocks
+        __align__(16) float s[2][16 * GB * SS];                    // scores of q; -beta times those of k
         __align__(16) float gk[KDA ? 16 * NB * D : 4];             // per-key decay: g_n
         __align__(16) float gp[KDA ? D : 4];                       // per-key decay: g of slot pos - 1
+        __align__(16) TI kr[RK ? 16 * NB * D : 8];                 // per-key decay: the nodes' keys as they are
     };
     union Space {
         Shared m;
@@ -267,21 +272,23 @@ struct TM {
             TreeSimple<D> s;
         } f;
     };
-    // waves per SIMD: as many workgroups as the LDS of a CU holds, at most 16 waves per CU
-    static constexpr int FIT = 160 * 1024 / (int)sizeof(Space);
-    static constexpr int WPE = FIT * NW >= 16 ? 4 : FIT * NW >= 12 ? 3 : 2;
+    // waves per SIMD the registers are sized for: the workgroups that fit the LDS of a CU, 3 at most
+    static constexpr int FIT = 160 * 1024 / (int)sizeof(Space) * NW / 4;
+    static constexpr int WPE = FIT >= 3 ? 3 : FIT >= 2 ? 2 : 1;
 };
 
-// c += a b with a in NP parts, b in three; small products first.
-template <int NP>
-__device__ __forceinline__ v4f mfma_parts(const u32x4 (&a)[NP], const u32x4 (&b)[3], v4f c) {
-    if constexpr (NP == 3) return mfma_split(a, b, c);
-    c = mfma_bf16(a[0], b[2], c);
-    c = mfma_bf16(a[0], b[1], c);
+// c += a b with a in NP parts, b in NQ parts; small products first.
+template <int NP, int NQ>
+__device__ __forceinline__ v4f mfma_parts(const u32x4 (&a)[NP], const u32x4 (&b)[NQ], v4f c) {
+    if constexpr (NP == 3 && NQ == 3) return mfma_split(a, b, c);
+    if constexpr (NQ == 3) {
+        c = mfma_bf16(a[0], b[2], c);
+        c = mfma_bf16(a[0], b[1], c);
+    }
     return mfma_bf16(a[0], b[0], c);
 }
 
-// Eight consecutive token values as loaded.
+// Eight consecutive token values, and two, as loaded.
 template <typename TI> struct Raw8 { u32x4 x[sizeof(TI) / 2]; };
 template <typename TI>
 __device__ __forceinline__ Raw8<TI> raw8(const void* base, size_t at) {
@@ -299,15 +306,22 @@ __device__ __forceinline__ void widen8(const Raw8<TI>& r, float (&y)[8]) {
         else y[u] = u & 1 ? hi_f32(r.x[0][u / 2]) : lo_f32(r.x[0][u / 2]);
     }
 }
+template <typename TI> struct Pair;
+template <> struct Pair<float> { typedef f32x2 T; };
+template <> struct Pair<uint16_t> { typedef uint32_t T; };
+__device__ __forceinline__ f32x2 widen2(f32x2 x) { return x; }
+__device__ __forceinline__ f32x2 widen2(uint32_t x) { return f32x2{lo_f32(x), hi_f32(x)}; }
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
+
+__device__ __forceinline__ v4f mfma4(float a, float b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 template <int D, int NB, int WT, int RULE, typename TI>
 __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE, TI>::WPE)) void tree_mfma_kernel(TreeArgs a) {
     using X = TM<D, NB, WT, RULE, TI>;
-    constexpr int NW = X::NW, NT = X::NT, NP = X::NP, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
+    constexpr int NW = X::NW, NT = X::NT, NP = X::NP, GB = X::GB, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
     constexpr bool KDA = X::KDA, DELTA = X::DELTA;
-    constexpr int NX = DELTA ? 2 : 1, GD = KDA ? D : 1, KS = D / 64;
+    constexpr int NX = DELTA ? 2 : 1, GD = KDA ? D : 1, KS = D / 64, NG = NB / GB;
     __shared__ typename X::Space sp;
     auto& s = sp.m;
 
@@ -319,7 +333,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     const float* bk = a.bk + head * (size_t)W * D;
     const float* bm = a.bm + head * (size_t)W * D;
     const float* bg = a.bg + head * (size_t)W * GD;
-    const int col = 16 * w + li;
+    const int col = 32 * w + 2 * li;                       // and col + 1
 
     // ---- requests that depend on nothing ----
     const int pos = a.pos[b];
@@ -331,61 +345,72 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         if constexpr (!KDA) nal = a.alpha[a.alpha_tok ? (size_t)n * a.alpha_tok + head : head % (unsigned)a.H];
         if constexpr (DELTA) nbeta = a.beta[(size_t)n * heads + head];
     }
-    // of each of the group's two blocks: one 8-channel piece of one of its 16 q rows (the lower
-    // half of the lanes) or k rows, and the lane's values
+    // of each block of a group: one 8-channel piece of one of its 16 q rows and k rows, and the lane's values
     constexpr int CPR = D / 8;
-    static_assert(NT == 2 * 16 * CPR, "one piece per lane");
-    const int xk = w >= NW / 2, row = (t - xk * (NT / 2)) / CPR, c8 = 8 * (t % CPR);
-    Raw8<TI> rr[2];
-    TI vr[2][4];
+    static_assert(NT == 16 * CPR, "one piece of one row per lane");
+    const int row = t / CPR, c8 = 8 * (t % CPR);
+    Raw8<TI> rq[GB], rk[GB];
+    typename Pair<TI>::T vr[GB][4];
     auto request = [&](int g) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int n = min(32 * g + 16 * e + row, N - 1);
-            rr[e] = raw8<TI>(xk ? a.k : a.q, ((size_t)n * heads + head) * D + c8);
+        for (int e = 0; e < GB; ++e) {
+            const size_t at = ((size_t)min(16 * (GB * g + e) + row, N - 1) * heads + head) * D + c8;
+            rq[e] = raw8<TI>(a.q, at);
+            rk[e] = raw8<TI>(a.k, at);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const int m = min(32 * g + 16 * e + 4 * lg + v, N - 1);
-                vr[e][v] = static_cast<const TI*>(a.v)[((size_t)m * heads + head) * D + col];
+                const int m = min(16 * (GB * g + e) + 4 * lg + v, N - 1);
+                vr[e][v] = *reinterpret_cast<const typename Pair<TI>::T*>(static_cast<const TI*>(a.v) + ((size_t)m * heads + head) * D + col);
             }
-            if (32 * g + 16 < N) continue;                 // (one block: its pieces only)
-            rr[1] = rr[0];
-            break;
         }
     };
     request(0);
-    v4i raw[KS];                                           // column col, channels 64 ks + 16 lg .. + 15
+    f32x2 na[KDA ? NB / 2 : 1][8];                         // per-key decay: alpha of nodes 32 g + 8 lg .. + 7, columns col, col + 1
+    if constexpr (KDA)
+#pragma unroll
+        for (int g = 0; g < NB / 2; ++g)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                na[g][u] = *reinterpret_cast<const f32x2*>(a.alpha + ((size_t)min(32 * g + 8 * lg + u, N - 1) * heads + head) * D + col);
+    v4i raw[KS][2];                                        // columns col + ct, channels 64 ks + 16 lg .. + 15
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
-        raw[ks] = ld_nt(reinterpret_cast<const v4i*>(a.sq + head * (size_t)(D * D) + sq_off<D>(64 * ks + 16 * lg, col)));
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct)
+            raw[ks][ct] = *reinterpret_cast<const v4i*>(a.sq + head * (size_t)(D * D) + sq_off<D>(64 * ks + 16 * lg, col + ct));
     float rs = a.r[head * D + (t & (D - 1))];
-    const float sj = a.s[head * D + col];
+    const f32x2 sj = *reinterpret_cast<const f32x2*>(a.s + head * D + col);
     // compensator rows: B operand of two k = 4 steps, row 4 u + lg
-    float cb[2] = {0.0f, 0.0f};
+    f32x2 cb[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
     int ci[2] = {0, 0};
     if (C > 0)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const size_t c = head * C + min(4 * u + lg, C - 1);
             ci[u] = a.idx[c];
-            cb[u] = a.cv[c * D + col];
+            cb[u] = *reinterpret_cast<const f32x2*>(a.cv + c * D + col);
         }
     if (pos < 0 || pos > W) return;                        // a row outside its window: untouched
 
-    // ---- the window's requests: one 8-channel piece of a key row per lane, the column's m rows ----
-    const int wt = (pos + 15) >> 4;                        // window tiles in use
-    const int wrow = t / CPR, last = max(pos - 1, 0);
-    float wx[8], wgc[KDA ? 8 : 1];
+    // ---- the window's requests: one 8-channel piece of a key row per lane and tile, the columns' m rows ----
+    const int wt = max(1, (pos + 15) >> 4);                // window tiles in use (the first always: zeros if empty)
+    const int last = max(pos - 1, 0);
+    float wx[WT][8], wgc[KDA ? WT : 1][8];
     float gpos = 0.0f, gw = 0.0f;                          // g of slot pos - 1 (per-key decay: channel t); of slot `lane`
-    v4f WM[WT];
+    v4f WM[WT][2];
     if (pos > 0) {
-        const size_t at = (size_t)min(wrow, last) * D + c8;
-        load_floats<8>(bk + at, wx);
-        if constexpr (KDA) load_floats<8>(bg + at, wgc);
 #pragma unroll
-        for (int c = 0; c < WT; ++c)
+        for (int c = 0; c < WT; ++c) {
+            const size_t at = (size_t)min(16 * c + row, last) * D + c8;
+            load_floats<8>(bk + at, wx[c]);
+            if constexpr (KDA) load_floats<8>(bg + at, wgc[c]);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) WM[c][v] = bm[(size_t)min(16 * c + 4 * lg + v, last) * D + col];
+            for (int v = 0; v < 4; ++v) {
+                const f32x2 x = *reinterpret_cast<const f32x2*>(bm + (size_t)min(16 * c + 4 * lg + v, last) * D + col);
+                WM[c][0][v] = x[0];
+                WM[c][1][v] = x[1];
+            }
+        }
         if constexpr (KDA) gpos = bg[(size_t)last * D + (t & (D - 1))];
         else if (w == 0) {
             gpos = bg[last];
@@ -401,7 +426,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         if (lane == 0) s.t.here = here;
         if constexpr (DELTA) s.beta[lane] = nd.here ? nbeta : 0.0f;
         if constexpr (!KDA) {
-            const float g = nd.sum + gpos;
+            const float g = nd.here ? nd.sum + gpos : gpos;
             s.g[lane] = g;
             s.e[lane] = expf(g);
             if (nd.here) a.tg[head * N + lane] = g;
@@ -416,99 +441,142 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     if (t < D) s.r[t] = rs;
     // ---- window keys in three parts ----
     if constexpr (KDA) __syncthreads();                    // gp
-    if (wrow < 16 * wt) {
+#pragma unroll
+    for (int c = 0; c < WT; ++c) {
+        if (c > 0 && c >= wt) break;
+        const bool on = 16 * c + row < pos;
         uint32_t p[3][4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            if constexpr (KDA) wx[u] *= expf(s.gp[c8 + u] - wgc[u]);
-            wx[u] = wrow < pos ? wx[u] : 0.0f;
+            if constexpr (KDA) wx[c][u] *= expf(s.gp[c8 + u] - wgc[c][u]);
+            wx[c][u] = on ? wx[c][u] : 0.0f;
         }
-        split3<8>(wx, p);
+        split3<8>(wx[c], p);
 #pragma unroll
         for (int m = 0; m < 3; ++m)
-            *reinterpret_cast<u32x4*>(&s.wk[m][wrow * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            *reinterpret_cast<u32x4*>(&s.wk[m][(16 * c + row) * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
     }
 #pragma unroll
     for (int c = 0; c < WT; ++c)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) WM[c][v] = 16 * c + 4 * lg + v < pos ? WM[c][v] : 0.0f;
+        for (int v = 0; v < 4; ++v) {
+            const bool on = 16 * c + 4 * lg + v < pos;
+            WM[c][0][v] = on ? WM[c][0][v] : 0.0f;
+            WM[c][1][v] = on ? WM[c][1][v] : 0.0f;
+        }
     __syncthreads();
     const uint64_t here = s.t.here;
     if constexpr (KDA) {
-        // g of every node, channel t
-        if (t < D)
-            for (int n0 = 0; n0 < N; n0 += 8) {
-                float al[8];
+        // g of every node, channels col and col + 1: the path sums of log alpha as the product of the
+        // 0/1 matrix of paths (exact in bf16) and the logarithms in three parts, plus g of slot pos - 1
+        const f32x2 g0 = *reinterpret_cast<const f32x2*>(&s.gp[col]);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) al[u] = a.alpha[((size_t)min(n0 + u, N - 1) * heads + head) * D + t];
+        for (int ct = 0; ct < 2; ++ct) {
+            u32x4 lp[NB / 2][3];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int n = n0 + u;
-                    float g = 0.0f;
-                    if ((here >> n) & 1u) {
-                        const int par = s.t.par[n];
-                        g = (par >= 0 ? s.gk[par * D + t] : gpos) + logf(al[u]);
-                        a.tg[(head * N + n) * D + t] = g;
-                    }
-                    s.gk[n * D + t] = g;
+            for (int g = 0; g < NB / 2; ++g) {
+                float x[8];
+                uint32_t p[3][4];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) x[u] = (here >> (32 * g + 8 * lg + u)) & 1u ? logf(na[g][u][ct]) : 0.0f;
+                split3<8>(x, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) lp[g][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                if (16 * j >= N) break;
+                const int n = 16 * j + li;
+                const uint64_t path = s.t.mask[n] | (1ull << n);
+                v4f y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int g = 0; g <= j / 2; ++g) {
+                    u32x4 ar[1];
+                    const uint32_t bits = (uint32_t)(path >> (32 * g)) >> (8 * lg);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        ar[0][u] = ((bits >> (2 * u)) & 1u ? 0x3f80u : 0u) | ((bits >> (2 * u + 1)) & 1u ? 0x3f800000u : 0u);
+                    y = mfma_parts<1, 3>(ar, lp[g], y);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int m = 16 * j + 4 * lg + v;
+                    s.gk[m * D + col + ct] = y[v] + g0[ct];
+                    if ((here >> m) & 1u) a.tg[(head * N + m) * D + col + ct] = y[v] + g0[ct];
                 }
             }
+        }
         __syncthreads();
     }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         ci[u] &= D - 1;
         if constexpr (KDA) cb[u] *= expf(s.gp[ci[u]]);
-        cb[u] = 4 * u + lg < C ? cb[u] : 0.0f;
+        cb[u] = 4 * u + lg < C ? cb[u] : f32x2{0.0f, 0.0f};
     }
 
-    v4f M[NB];
+    v4f M[NB][2];
     bool odd = false;
 #pragma unroll
-    for (int g = 0; g < NB / 2; ++g) {
-        if (32 * g >= N) break;
-        const int nb = 32 * g + 16 < N ? 2 : 1;            // blocks of this group
+    for (int g = 0; g < NG; ++g) {
+        if (16 * GB * g >= N) break;
+        const int nb = 16 * GB * g + 16 < N ? GB : 1;      // blocks of this group
+        uint16_t* kbase = &s.k[0][KB > GB ? 16 * GB * g * QS : 0];
+        constexpr size_t QP = sizeof(s.q[0]) / 2, KP = sizeof(s.k[0]) / 2, WP = sizeof(s.wk[0]) / 2;   // shorts per part
         // ---- 1. rows ----
+        f32x2 vv[GB][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 16 * e + row, n = 32 * g + r;
+        for (int e = 0; e < GB; ++e) {
+            const int r = 16 * e + row, n = 16 * GB * g + r;
             const bool on = (here >> n) & 1u;              // absent nodes: zeros
-            uint16_t* dst = xk ? &s.k[0][((KB > 2 ? 32 * g : 0) + r) * QS + c8] : &s.q[0][r * QS + c8];
+            if constexpr (X::RK)
+#pragma unroll
+                for (int i = 0; i < (int)(sizeof(TI) / 2); ++i)
+                    *reinterpret_cast<u32x4*>(&s.kr[n * D + c8 + i * (16 / (int)sizeof(TI))]) = rk[e].x[i];
             if constexpr (NP == 1) {
-                *reinterpret_cast<u32x4*>(dst) = on ? rr[e].x[0] : u32x4{0, 0, 0, 0};
+                *reinterpret_cast<u32x4*>(&s.q[0][r * QS + c8]) = on ? rq[e].x[0] : u32x4{0, 0, 0, 0};
+                *reinterpret_cast<u32x4*>(kbase + r * QS + c8) = on ? rk[e].x[0] : u32x4{0, 0, 0, 0};
             } else {
-                const size_t plane = xk ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
-                float y[8];
-                uint32_t p[3][4];
-                widen8<TI>(rr[e], y);
+                float sc[8];
+                if constexpr (KDA)
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    if constexpr (KDA) y[u] *= on ? expf(s.gk[n * D + c8 + u] - s.gp[c8 + u]) : 0.0f;
-                    y[u] = on ? y[u] : 0.0f;
+                    for (int u = 0; u < 8; ++u) sc[u] = __expf(s.gk[n * D + c8 + u] - s.gp[c8 + u]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float y[8];
+                    uint32_t p[3][4];
+                    widen8<TI>(x ? rk[e] : rq[e], y);
+#pragma unroll
+                    for (int u = 0; u < 8; ++u) {
+                        if constexpr (KDA) y[u] *= sc[u];
+                        y[u] = on ? y[u] : 0.0f;
+                    }
+                    split3<8>(y, p);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        *reinterpret_cast<u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + r * QS + c8) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
                 }
-                split3<8>(y, p);
-#pragma unroll
-                for (int m = 0; m < 3; ++m) *reinterpret_cast<u32x4*>(dst + m * plane) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                vv[e][v] = (here >> (16 * (GB * g + e) + 4 * lg + v)) & 1u ? widen2(vr[e][v]) : f32x2{0.f, 0.f};
         }
-        float vv[2][4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) vv[e][v] = (here >> (32 * g + 16 * e + 4 * lg + v)) & 1u ? widen(vr[e][v]) : 0.0f;
-        if (g + 1 < NB / 2 && 32 * (g + 1) < N) request(g + 1);
         __syncthreads();
-        // ---- 2. scores ----
+        // ---- 2. scores: tile (x, e, c) = rows of block e, context tile c (window tiles, then node blocks) ----
         {
-            const int nt0 = wt + (KDA ? 0 : 2 * g + 1), per = nb == 1 ? nt0 : 2 * nt0 + (KDA ? 0 : 1);   // tiles of block 0, of the group
+            const int nt0 = wt + (KDA ? 0 : GB * g + 1), per = nb == 1 ? nt0 : 2 * nt0 + (KDA ? 0 : 1);   // tiles of block 0, of the group
+#pragma unroll 1
             for (int it = w; it < NX * per; it += NW) {
                 const int x = it >= per, y0 = x ? it - per : it, e = y0 >= nt0, c = e ? y0 - nt0 : y0;
-                const size_t plane = x ? sizeof(s.k[0]) / 2 : sizeof(s.q[0]) / 2;
-                const uint16_t* arow = (x ? &s.k[0][((KB > 2 ? 32 * g : 0) + 16 * e + li) * QS] : &s.q[0][(16 * e + li) * QS]) + 8 * lg;
-                const bool win = c < wt;
-                const int i = 16 * (c - wt) + li;          // node of this lane's column (node tiles)
-                v4f acc = {0.f, 0.f, 0.f, 0.f};
-                if (win) {
+                const size_t plane = x ? KP : QP;
+                const uint16_t* arow = (x ? kbase : &s.q[0][0]) + (16 * e + li) * QS + 8 * lg;
+                const int n0 = 16 * (GB * g + e) + 4 * lg;
+                const v4f gn = KDA ? v4f{0.f, 0.f, 0.f, 0.f} : *reinterpret_cast<const v4f*>(&s.g[n0]);
+                const v4f bn = DELTA && x ? -*reinterpret_cast<const v4f*>(&s.beta[n0]) : v4f{1.f, 1.f, 1.f, 1.f};
+                float* dst = &s.s[x][(16 * e + 4 * lg) * SS + li];
+                v4f acc = {0.f, 0.f, 0.f, 0.f}, acc2 = acc;
+                // (an exponent is at most 0: off by 2^-24 of it, weighted by its exponential)
+                if (c < wt) {
                     const uint16_t* brow = &s.wk[0][(16 * c + li) * QS + 8 * lg];
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks) {
@@ -516,10 +584,16 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
                         for (int m = 0; m < NP; ++m) ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 32 * ks);
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(brow + m * (sizeof(s.wk[0]) / 2) + 32 * ks);
-                        acc = mfma_parts<NP>(ar, br, acc);
+                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(brow + m * WP + 32 * ks);
+                        if (ks & 1) acc2 = mfma_parts<NP, 3>(ar, br, acc2);
+                        else acc = mfma_parts<NP, 3>(ar, br, acc);
                     }
+                    acc += acc2;
+                    const float gc = KDA ? 0.0f : s.wg[(16 * c + li) & 31];
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) dst[v * SS + 16 * c] = acc[v] * (KDA ? 1.0f : __expf(gn[v] - gc)) * bn[v];
                 } else if constexpr (!KDA) {
+                    const int i = 16 * (c - wt) + li;      // node of this lane's column
                     const uint16_t* brow = &s.k[0][i * QS + 8 * lg];
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks) {
@@ -527,39 +601,35 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
                         for (int m = 0; m < NP; ++m) {
                             ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 32 * ks);
-                            br[m] = *reinterpret_cast<const u32x4*>(brow + m * (sizeof(s.k[0]) / 2) + 32 * ks);
+                            br[m] = *reinterpret_cast<const u32x4*>(brow + m * KP + 32 * ks);
                         }
-                        if constexpr (NP == 1) acc = mfma_bf16(ar[0], br[0], acc);
-                        else acc = mfma_split(ar, br, acc);
+                        if (ks & 1) acc2 = mfma_parts<NP, NP>(ar, br, acc2);
+                        else acc = mfma_parts<NP, NP>(ar, br, acc);
                     }
-                }
-                const float gc = KDA ? 0.0f : win ? s.wg[(16 * c + li) & 31] : s.g[i & 63];
-                const int n0 = 32 * g + 16 * e + 4 * lg;
-                float* dst = &s.s[x][(16 * e + 4 * lg) * SS + (win ? 16 * c : WC + 16 * (c - wt)) + li];
+                    acc += acc2;
+                    const float gc = s.g[i];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = n0 + v;
-                    const bool on = win ? 16 * c + li < pos && ((here >> n) & 1u) : (s.t.mask[n] >> (i & 63)) & 1u;
-                    float y = acc[v];
-                    if constexpr (!KDA) y *= on ? expf(s.g[n] - gc) : 1.0f;
-                    if (DELTA && x) y *= -s.beta[n];
-                    // (the diagonal of the q scores: <q_n, k_n>)
-                    dst[v * SS] = on || (!win && !x && i == n) ? y : 0.0f;
+                    for (int v = 0; v < 4; ++v) {
+                        const uint64_t anc = s.t.mask[n0 + v];
+                        const float y = acc[v] * __expf(gn[v] - gc) * bn[v];
+                        // (the diagonal of the q scores: <q_n, k_n>; its exponential is 1)
+                        dst[v * SS + WC + 16 * (c - wt)] = ((anc >> i) & 1u) || (!x && i == n0 + v) ? y : 0.0f;
+                    }
                 }
             }
             if constexpr (KDA) {
                 // node pairs, a row per wave at a time, four ancestors at once (16 lanes each)
                 constexpr int CH = D / 16;
                 for (int r = w; r < 16 * nb; r += NW) {
-                    const int n = 32 * g + r;
-                    for (int c = lane; c < 32 * g + 16 * nb; c += 64) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
+                    const int n = 16 * GB * g + r;
+                    for (int c = lane; c < 16 * (GB * g + nb); c += 64) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
                     if (!((here >> n) & 1u)) continue;
                     const size_t at = ((size_t)n * heads + head) * D + CH * li;
                     float qn[CH], kn[CH], gn[CH];
 #pragma unroll
                     for (int u = 0; u < CH; ++u) {
                         qn[u] = tok_ld<TI>(a.q, at + u);
-                        kn[u] = tok_ld<TI>(a.k, at + u);
+                        kn[u] = X::RK ? widen(s.kr[X::RK ? n * D + CH * li + u : 0]) : tok_ld<TI>(a.k, at + u);
                     }
                     load_floats<CH>(&s.gk[n * D + CH * li], gn);
                     const float nbt = -s.beta[n];
@@ -582,7 +652,8 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                             load_floats<CH>(&s.gk[i * D + CH * li], gi);
 #pragma unroll
                             for (int u = 0; u < CH; ++u) {
-                                float ki = tok_ld<TI>(a.k, ((size_t)i * heads + head) * D + CH * li + u);
+                                float ki = X::RK ? widen(s.kr[X::RK ? i * D + CH * li + u : 0])
+                                                 : tok_ld<TI>(a.k, ((size_t)i * heads + head) * D + CH * li + u);
                                 if (i != n) ki *= __expf(gn[u] - gi[u]);
                                 xq += qn[u] * ki;
                                 xk2 += kn[u] * ki;
@@ -599,123 +670,153 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             }
         }
         __syncthreads();
-        // ---- 3. (I + A)^{-1} of block NW - 1 - w, lane c < 16 its column c ----
-        if (DELTA && w >= NW - nb && lane < 16) {
-            const int e = NW - 1 - w;
-            const float* arow = &s.s[1][16 * e * SS + WC + 32 * g + 16 * e];
-            float tc[16];
+        // ---- 3. products with the state ----
+        v4f acc[GB][NX][2];
 #pragma unroll
-            for (int n = 0; n < 16; ++n) {
-                float ar[16];
-                load_floats<16>(arow + n * SS, ar);
-                float x0 = n == lane ? 1.0f : 0.0f, x1 = 0.0f;
+        for (int e = 0; e < GB; ++e)
 #pragma unroll
-                for (int i = 0; i < n; ++i) {
-                    if (i & 1) x1 = __builtin_fmaf(ar[i], tc[i], x1);
-                    else x0 = __builtin_fmaf(ar[i], tc[i], x0);
-                }
-                tc[n] = x0 + x1;
-                s.inv[e][n * 20 + lane] = tc[n];
-            }
-        }
-        // ---- 4. products with the state ----
-        v4f acc[2][NX];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int x = 0; x < NX; ++x) acc[e][x] = v4f{0.f, 0.f, 0.f, 0.f};
-        const uint16_t* qrow = &s.q[0][li * QS];
-        const uint16_t* krow = &s.k[0][((KB > 2 ? 32 * g : 0) + li) * QS];
+            for (int x = 0; x < NX; ++x) acc[e][x][0] = acc[e][x][1] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
-                // B operand: channels 64 ks + 16 lg + 8 hf .. + 7 of column col
+                // B operands: channels 64 ks + 16 lg + 8 hf .. + 7 of columns col + ct
                 const int ch = 64 * ks + 16 * lg + 8 * hf;
-                float r[8], x8[8];
-                uint32_t p[3][4];
-                u32x4 st[3];
+                float r[8];
+                u32x4 st[2][3];
                 load_floats<8>(&s.r[ch], r);
 #pragma unroll
-                for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][2 * hf + u / 4], u % 4) * r[u];
-                split3<8>(x8, p);
+                for (int ct = 0; ct < 2; ++ct) {
+                    float x8[8];
+                    uint32_t p[3][4];
 #pragma unroll
-                for (int m = 0; m < 3; ++m) st[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                    for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
+                    split3<8>(x8, p);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                    for (int m = 0; m < 3; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                }
+#pragma unroll
+                for (int e = 0; e < GB; ++e) {
                     if (e >= nb) break;
 #pragma unroll
                     for (int x = 0; x < NX; ++x) {
                         u32x4 ar[NP];
 #pragma unroll
                         for (int m = 0; m < NP; ++m)
-                            ar[m] = *reinterpret_cast<const u32x4*>((x ? krow + m * (sizeof(s.k[0]) / 2) : qrow + m * (sizeof(s.q[0]) / 2)) +
-                                                                    16 * e * QS + ch);
-                        acc[e][x] = mfma_parts<NP>(ar, st, acc[e][x]);
+                            ar[m] = *reinterpret_cast<const u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + (16 * e + li) * QS + ch);
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, 3>(ar, st[ct], acc[e][x][ct]);
                     }
                 }
             }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < GB; ++e) {
             if (e >= nb) break;
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
-                v4f cmp = {0.f, 0.f, 0.f, 0.f};
+                v4f cmp[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float z = 0.0f;
 #pragma unroll
-                    for (int m = NP - 1; m >= 0; --m)
-                        z += bf16_to_f32((x ? krow + m * (sizeof(s.k[0]) / 2) : qrow + m * (sizeof(s.q[0]) / 2))[16 * e * QS + ci[u]]);
-                    if (C > 4 * u) cmp = __builtin_amdgcn_mfma_f32_16x16x4f32(z, cb[u], cmp, 0, 0, 0);
+                    for (int m = NP - 1; m >= 0; --m) z += bf16_to_f32((x ? kbase + m * KP : &s.q[m][0])[(16 * e + li) * QS + ci[u]]);
+                    if (C > 4 * u) {
+                        cmp[0] = mfma4(z, cb[u][0], cmp[0]);
+                        cmp[1] = mfma4(z, cb[u][1], cmp[1]);
+                    }
                 }
-                acc[e][x] = acc[e][x] * sj + cmp;
-                if constexpr (!KDA) acc[e][x] *= *reinterpret_cast<const v4f*>(&s.e[32 * g + 16 * e + 4 * lg]);
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) {
+                    acc[e][x][ct] = acc[e][x][ct] * sj[ct] + cmp[ct];
+                    if constexpr (!KDA) acc[e][x][ct] *= *reinterpret_cast<const v4f*>(&s.e[16 * (GB * g + e) + 4 * lg]);
+                }
             }
         }
-        __syncthreads();                                   // the inverses; the rows may be overwritten
-        // ---- 5. m and o ----
+        if (g + 1 < NG && 16 * GB * (g + 1) < N) {
+            request(g + 1);
+            __syncthreads();                               // the rows are overwritten by the next group
+        }
+        // ---- 4. m and o ----
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < GB; ++e) {
             if (e >= nb) break;
-            const int j = 2 * g + e;
-            auto context = [&](int x, v4f y) {             // y + scores x context
+            const int j = GB * g + e;
+            auto context = [&](int x, v4f (&y)[2]) {       // y += scores x context
 #pragma unroll
                 for (int c = 0; c < WT + NB; ++c) {
-                    if (c < WT ? c >= wt : c - WT >= j) continue;
+                    if (c < WT ? c > 0 && c >= wt : c - WT >= j) continue;
                     const int cc = c < WT ? 16 * c : WC + 16 * (c - WT);
                     const v4f sr = *reinterpret_cast<const v4f*>(&s.s[x][(16 * e + li) * SS + cc + 4 * lg]);
-                    const v4f m = c < WT ? WM[c < WT ? c : 0] : M[c < WT ? 0 : c - WT];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) y = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], m[v], y, 0, 0, 0);
+                    for (int v = 0; v < 4; ++v)
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct)
+                            y[ct] = mfma4(sr[v], c < WT ? WM[c < WT ? c : 0][ct][v] : M[c < WT ? 0 : c - WT][ct][v], y[ct]);
                 }
-                return y;
             };
-            v4f o = context(0, acc[e][0]);
             if constexpr (DELTA) {
                 const v4f be = *reinterpret_cast<const v4f*>(&s.beta[16 * j + 4 * lg]);
-                v4f R;
+                v4f R[2];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) R[v] = be[v] * (vv[e][v] - acc[e][NX - 1][v]);
-                R = context(1, R);
-                const v4f ti = *reinterpret_cast<const v4f*>(&s.inv[e][li * 20 + 4 * lg]);
-                M[j] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) M[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[v], R[v], M[j], 0, 0, 0);
+                    for (int v = 0; v < 4; ++v) R[ct][v] = be[v] * (vv[e][v][ct] - acc[e][NX - 1][ct][v]);
+                context(1, R);
+                // M = (I + A)^{-1} R, four rows at a time: lane group p solves its rows, then the
+                // matrix instruction takes them (column 4 p + v of -A, rows below) to the others
+                const float* ab = &s.s[1][16 * e * SS + WC + 16 * j];
+                const v4f below = *reinterpret_cast<const v4f*>(ab + li * SS + 4 * lg);   // -A[li][4 lg + v]
+                v4f own[3];                                                               // -A[4 lg + 1 + i][4 lg + v]
+#pragma unroll
+                for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(ab + (4 * lg + 1 + i) * SS + 4 * lg);
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    if (lg == p)
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct) {
+                            R[ct][1] += own[0][0] * R[ct][0];
+                            R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
+                            R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
+                        }
+                    if (p < 3) {
+                        const bool on = lg == p && (li >> 2) > p;
+                        v4f y[2] = {R[0], R[1]};
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const float x = on ? below[v] : 0.0f;
+                            y[0] = mfma4(x, R[0][v], y[0]);
+                            y[1] = mfma4(x, R[1][v], y[1]);
+                        }
+                        R[0] = y[0];
+                        R[1] = y[1];
+                    }
+                }
+                M[j][0] = R[0];
+                M[j][1] = R[1];
             } else {
 #pragma unroll
-                for (int v = 0; v < 4; ++v) M[j][v] = vv[e][v];
+                for (int v = 0; v < 4; ++v) {
+                    M[j][0][v] = vv[e][v][0];
+                    M[j][1][v] = vv[e][v][1];
+                }
             }
+            context(0, acc[e][0]);
             const v4f sr = *reinterpret_cast<const v4f*>(&s.s[0][(16 * e + li) * SS + WC + 16 * j + 4 * lg]);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o = __builtin_amdgcn_mfma_f32_16x16x4f32(sr[v], M[j][v], o, 0, 0, 0);
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int ct = 0; ct < 2; ++ct) acc[e][0][ct] = mfma4(sr[v], M[j][ct][v], acc[e][0][ct]);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const int n = 16 * j + 4 * lg + v;
-                odd |= !finite_f32(M[j][v]);
+                odd |= !finite_f32(M[j][0][v]) || !finite_f32(M[j][1][v]);
                 if (!((here >> n) & 1u)) continue;
-                tok_st<TI>(a.o, ((size_t)n * heads + head) * D + col, o[v]);
-                st_nt(a.tm + (head * N + n) * (size_t)D + col, M[j][v]);
+                const size_t at = ((size_t)n * heads + head) * D + col;
+                if constexpr (sizeof(TI) == 4)
+                    __builtin_nontemporal_store(f32x2{acc[e][0][0][v], acc[e][0][1][v]}, reinterpret_cast<f32x2*>(static_cast<float*>(a.o) + at));
+                else
+                    st_nt(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at), pack_bf16(acc[e][0][0][v], acc[e][0][1][v]));
+                __builtin_nontemporal_store(f32x2{M[j][0][v], M[j][1][v]}, reinterpret_cast<f32x2*>(a.tm + (head * N + n) * (size_t)D + col));
             }
         }
     }
@@ -726,10 +827,10 @@ template <int D, int RULE, typename TI>
 hipError_t tree_mfma(const lq_dims& d, const TreeArgs& args, hipStream_t s) {
     const dim3 grid((unsigned)args.heads);
     if (args.N <= 32)
-        return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 1, RULE, TI>, grid, dim3(4 * D), s, args)
-                         : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 2, RULE, TI>, grid, dim3(4 * D), s, args);
-    return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 1, RULE, TI>, grid, dim3(4 * D), s, args)
-                     : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 2, RULE, TI>, grid, dim3(4 * D), s, args);
+        return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 1, RULE, TI>, grid, dim3(2 * D), s, args)
+                         : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 2, 2, RULE, TI>, grid, dim3(2 * D), s, args);
+    return d.W <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 1, RULE, TI>, grid, dim3(2 * D), s, args)
+                     : launch_kernel(LQ_KERNEL_TREE, tree_mfma_kernel<D, 4, 2, RULE, TI>, grid, dim3(2 * D), s, args);
 }
 
 template <int RULE, typename TI>
