@@ -319,8 +319,11 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 x0[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x05040100u);
                 x1[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x07060302u);
             }
-            *reinterpret_cast<u32x4*>(&sT[(2 * kpair) * TS + 8 * oct]) = x0;
-            *reinterpret_cast<u32x4*>(&sT[(2 * kpair + 1) * TS + 8 * oct]) = x1;
+            // (octets swapped in pairs in every other 16 rows: the writes of 16 lanes, two rows
+            // apart each, then hit all banks)
+            const int so = 8 * oct;
+            *reinterpret_cast<u32x4*>(&sT[(2 * kpair) * TS + so]) = x0;
+            *reinterpret_cast<u32x4*>(&sT[(2 * kpair + 1) * TS + so]) = x1;
             if constexpr (OUT) {
                 // channels (c, c + 1), c = 2 kpair, in the operand order of their 32-block
                 const int u = (2 * kpair & 31) >> 2;
@@ -866,11 +869,16 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
     reinterpret_cast<v4f*>(a.h)[at] = x;
 }
 
-// Tokens per segment (a multiple of the chunk): one segment per head where the heads
-// alone fill the GPU, else segments for kWant workgroups.
-constexpr size_t kWant = 512;
+// Tokens per segment (a multiple of the chunk).  Segments cost a second read of k and v and
+// the states between them, so they pay where the heads alone leave most CUs idle: up to
+// kSplitHeads heads, enough segments for kWant workgroups (two a CU).  Measured at d = 128,
+// bf16 (fp32), 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192
+// heads 109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
+// (291, 282, 290) for 256, 512 and 768 workgroups.
+constexpr size_t kWant = 512, kSplitHeads = 128;
+size_t segments_wanted(size_t heads) { return heads > kSplitHeads ? 1 : (kWant + heads - 1) / heads; }
 int segment_tokens(size_t heads, int T, int chunk) {
-    const size_t chunks = ((size_t)T + chunk - 1) / chunk, want = (kWant + heads - 1) / heads;
+    const size_t chunks = ((size_t)T + chunk - 1) / chunk, want = segments_wanted(heads);
     return (int)(want <= 1 ? chunks : (chunks + want - 1) / want) * chunk;
 }
 int chunk_tokens(const lq_dims& d) { return d.io_dtype == LQ_IO_BF16 ? BL : FL; }
@@ -929,7 +937,7 @@ size_t la_workspace_bytes(const lq_dims& d, int T) {
     if (d.dk < 64 || T <= kStepTokens) return 0;
     // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
     const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d);
-    const size_t segs = min((kWant + heads - 1) / heads, ((size_t)T + chunk - 1) / chunk);
+    const size_t segs = min(segments_wanted(heads), ((size_t)T + chunk - 1) / chunk);
     return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
 }
 
