@@ -222,6 +222,25 @@ struct LB {
     static constexpr int TS = BL + 8;          // shorts per K^T / score row
 };
 
+// Gates of a chunk: prefix sums of log alpha, e^{g_n}, e^{g_L - g_n}.
+template <int L>
+struct Gates {
+    double g[L];
+    __align__(16) float e[L], w[L];
+};
+// Formed by one wave, lane n = token n; tokens from `left` on decay nothing.  Returns g_L.
+template <int L>
+__device__ __forceinline__ double make_gates(float alpha, int left, int lane, Gates<L>& s) {
+    const double g = wave_scan(lane < min(left, L) ? (double)log_decay(alpha) : 0.0);
+    const double gl = __shfl(g, 63, 64);
+    if (lane < L) {
+        s.g[lane] = g;
+        s.e[lane] = expf((float)g);
+        s.w[lane] = expf((float)(gl - g));
+    }
+    return gl;
+}
+
 template <int D, bool OUT>
 __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     using P = LB<D>;
@@ -230,8 +249,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     __shared__ __align__(16) uint16_t sK[OUT ? BL * QS : 8];
     __shared__ __align__(16) uint16_t sT[D * TS];                  // K^T: [channel][token]
     __shared__ __align__(16) uint16_t sP[OUT ? 2 * BL * TS : 8];   // scores, upper and lower parts
-    __shared__ double sG[BL];
-    __shared__ __align__(16) float sE[BL], sW[BL];                 // e^{g_n}, e^{g_L - g_n}
+    __shared__ Gates<BL> s_gate[2];                                // of this chunk and the next
 
     const int t = threadIdx.x, lane = t & 63;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -272,7 +290,6 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= kChunkHeads)
     uint32_t kd[2][8], vd[2][8];
     u32x4 qd[4];
-    float al = 0.0f;
     auto rows = [&](const void* x, int c0) {                       // tokens c0 .. min(c0 + BL, te) - 1 of this head
         return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (2 * D),
                          (uint32_t)(min(te - c0, BL) - 1) * rb + 2 * D);
@@ -298,16 +315,26 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) qd[j] = row_ld4(rq, qoff + (j * (NT / (D / 8))) * rb);
         }
-        if (w == 0) al = a.alpha[a.alpha_tok ? (size_t)min(c0 + (int)ln, te - 1) * a.alpha_tok + head : head % (unsigned)a.H];
+    };
+    // the chunk's gates: formed by the last wave, one chunk ahead, off the other waves' path
+    auto load_gates = [&](int c0) {
+        return a.alpha[a.alpha_tok ? (size_t)min(c0 + lane, te - 1) * a.alpha_tok + head : head % (unsigned)a.H];
     };
     if (t0 < te) {
         load_kq(t0);
         load_v(t0);
     }
-    double gtot = 0.0;                                             // (wave 0) log decay of the segment so far
+    double gtot = 0.0;                                             // (last wave) log decay of the segment so far
+    if (w == NW - 1 && t0 < te) gtot = make_gates<BL>(load_gates(t0), te - t0, lane, s_gate[0]);
 
-    for (int c0 = t0; c0 < te; c0 += BL) {
+    int cur = 0;
+    for (int c0 = t0; c0 < te; c0 += BL, cur ^= 1) {
         const int L = min(BL, te - c0);
+        const double* sG = s_gate[cur].g;
+        const float *sE = s_gate[cur].e, *sW = s_gate[cur].w;
+        const bool ahead = w == NW - 1 && c0 + BL < te;
+        float al = 0.0f;
+        if (ahead) al = load_gates(c0 + BL);
         // ---- registers -> LDS ----
         const int ln = fresh(lane), kpair = ln % (D / 2), ksub = ln / (D / 2);   // channel pair; octet within a wave's pass
 #pragma unroll
@@ -349,17 +376,10 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 V[j][0][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x05040100u);
                 V[j][1][e] = __builtin_amdgcn_perm(vd[j][2 * e + 1], vd[j][2 * e], 0x07060302u);
             }
-        if (w == 0) {
-            const double g = wave_scan(lane < L ? (double)log_decay(al) : 0.0);
-            const double gl = __shfl(g, 63, 64);
-            sG[lane] = g;
-            sE[lane] = expf((float)g);
-            sW[lane] = expf((float)(gl - g));
-            gtot += gl;
-        }
         __syncthreads();
 
         const float egl = sE[BL - 1];
+        if (!OUT && ahead) gtot += make_gates<BL>(al, te - c0 - BL, lane, s_gate[cur ^ 1]);
         if constexpr (OUT) {
             const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
             // ---- scores: the 10 tiles on and below the diagonal, over the waves ----
@@ -419,6 +439,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 O[r][0] *= e;
                 O[r][1] *= e;
             }
+            if (ahead) gtot += make_gates<BL>(al, te - c0 - BL, lane, s_gate[cur ^ 1]);
             __syncthreads();                                       // the scores are written
             // ---- O += (E o Q K^T) V ----
             // a column's plain sum over the chunk is finite unless one of its values is not
@@ -537,7 +558,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
             for (int v = 0; v < 4; ++v)
                 *reinterpret_cast<f32x2*>(a.end + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band) =
                     f32x2{H[rt][0][v], H[rt][1][v]};
-    if (a.decay && t == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
+    if (a.decay && t == NT - 64) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
 }
 
 // ---------------------------------------------------------------------------
@@ -563,10 +584,9 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
     constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QS = P::QS, TS = P::TS;
     __shared__ __align__(16) uint16_t sQ[3][OUT ? FL * QS : 8];
     __shared__ __align__(16) uint16_t sK[3][OUT ? FL * QS : 8];
-    __shared__ __align__(16) uint16_t sT[3][D * TS];               // K^T: [channel][token]
+    __shared__ __align__(16) uint16_t sT[3][D * TS];               // (w o K)^T: [channel][token]
     __shared__ __align__(16) uint16_t sP[3][OUT ? FL * TS : 8];    // scores
-    __shared__ double sG[FL];
-    __shared__ __align__(16) float sE[FL], sW[FL];                 // e^{g_n}, e^{g_L - g_n}
+    __shared__ Gates<FL> s_gate[2];                                // of this chunk and the next
 
     const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -574,68 +594,85 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
     const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
     const int t0 = (int)blockIdx.y * a.seg;
     const int te = min(len, t0 + a.seg);
-    const float* gq = static_cast<const float*>(a.q);
-    const float* gk = static_cast<const float*>(a.k);
-    const float* gv = static_cast<const float*>(a.v);
     const int col = 16 * w + li;
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
 
     v4f H[RT];                                                     // H[rt][v] = H[16 rt + 4 lg + v][col]
+    if (a.start) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) H[rt][v] = a.start ? a.start[soff + (size_t)(16 * rt + 4 * lg + v) * D + col] : 0.0f;
+            for (int v = 0; v < 4; ++v) H[rt][v] = a.start[soff + (size_t)(16 * rt + 4 * lg + v) * D + col];
+    } else {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) H[rt] = v4f{0.f, 0.f, 0.f, 0.f};
+    }
     if constexpr (OUT)
         for (int e = t; e < 3 * 16 * 16; e += NT) sP[e >> 8][((e >> 4) & 15) * TS + 16 + (e & 15)] = 0;   // right of the diagonal
 
-    // chunk loads, one chunk ahead; tokens past the end repeat the last one and are zeroed in LDS
-    const int kc = t % D, koct = t / D;                            // K^T: channel, 8 tokens (4 octets)
+    // chunk loads, one chunk ahead; tokens past the end read as zeros
     constexpr int CPR = D / 8;                                     // 8-channel pieces per row
-    const int row = t / CPR, c8 = 8 * (t % CPR);                   // Q, K rows: 32 rows of CPR pieces (D = 64, 128: one each)
     static_assert(NT / CPR == FL && NT / D == FL / 8, "one piece and one octet per thread");
-    float kt[8], vr[8];
-    v4f qr[2], kr[2];
-    float al;
+    const uint32_t rb = (uint32_t)heads * (4 * D);                 // bytes between tokens (heads <= kChunkHeads)
+    uint32_t kt[8], vr[8];
+    u32x4 qr[2], kr[2];
+    auto rows = [&](const void* x, int c0) {                       // tokens c0 .. min(c0 + FL, te) - 1 of this head
+        return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (4 * D),
+                         (uint32_t)(min(te - c0, FL) - 1) * rb + 4 * D);
+    };
     auto load = [&](int c0) {
-        const int last = te - 1;
+        const uint32_t tt = fresh(t), ln = tt & 63;
+        const rsrc_t rk = rows(a.k, c0), rv = rows(a.v, c0);
+        const uint32_t koff = 8 * (tt / D) * rb + 4 * (tt % D), voff = 8 * (ln >> 4) * rb + 4 * (16 * w + (ln & 15));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            kt[e] = gk[((size_t)min(c0 + 8 * koct + e, last) * heads + head) * D + kc];
-            vr[e] = gv[((size_t)min(c0 + 8 * lg + e, last) * heads + head) * D + col];
+            kt[e] = row_ld(rk, koff + e * rb);
+            vr[e] = row_ld(rv, voff + e * rb);
         }
         if constexpr (OUT) {
-            const size_t at = ((size_t)min(c0 + row, last) * heads + head) * D + c8;
-            qr[0] = *reinterpret_cast<const v4f*>(gq + at);
-            qr[1] = *reinterpret_cast<const v4f*>(gq + at + 4);
-            kr[0] = *reinterpret_cast<const v4f*>(gk + at);
-            kr[1] = *reinterpret_cast<const v4f*>(gk + at + 4);
-        }
-        if (w == 0) {
-            const int tok = min(c0 + (lane & (FL - 1)), last);
-            al = a.alpha_tok ? a.alpha[(size_t)tok * a.alpha_tok + head] : a.alpha[head % (unsigned)a.H];
+            const rsrc_t rq = rows(a.q, c0);
+            const uint32_t off = (tt / CPR) * rb + 32 * (tt % CPR);
+            qr[0] = row_ld4(rq, off);
+            qr[1] = row_ld4(rq, off + 16);
+            kr[0] = row_ld4(rk, off);
+            kr[1] = row_ld4(rk, off + 16);
         }
     };
+    auto load_gates = [&](int c0) {
+        return a.alpha[a.alpha_tok ? (size_t)min(c0 + (lane & (FL - 1)), te - 1) * a.alpha_tok + head : head % (unsigned)a.H];
+    };
     if (t0 < te) load(t0);
-    double gtot = 0.0;
+    double gtot = 0.0;                                             // (last wave) log decay of the segment so far
+    if (w == NW - 1 && t0 < te) gtot = make_gates<FL>(load_gates(t0), te - t0, lane, s_gate[0]);
+    __syncthreads();
 
-    for (int c0 = t0; c0 < te; c0 += FL) {
+    int cur = 0;
+    for (int c0 = t0; c0 < te; c0 += FL, cur ^= 1) {
         const int L = min(FL, te - c0);
+        const double* sG = s_gate[cur].g;
+        const float *sE = s_gate[cur].e, *sW = s_gate[cur].w;
+        const bool ahead = w == NW - 1 && c0 + FL < te;
+        float al = 0.0f;
+        if (ahead) al = load_gates(c0 + FL);
         {
-            float x[8];
+            const int tt = fresh(t), kc = tt % D, koct = tt / D;   // K^T: channel, 8 tokens
+            float x[8], wt[8];
             uint32_t p[3][4];
+            load_floats<8>(sW + 8 * koct, wt);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = 8 * koct + e < L ? kt[e] : 0.0f;
+            for (int e = 0; e < 8; ++e) x[e] = wt[e] * __uint_as_float(kt[e]);
             split3<8>(x, p);
 #pragma unroll
             for (int m = 0; m < 3; ++m)
                 *reinterpret_cast<u32x4*>(&sT[m][kc * TS + 8 * koct]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             if constexpr (OUT) {
+                const int row = tt / CPR, c8 = 8 * (tt % CPR);
                 const int u = (c8 & 31) >> 2;                      // two groups of 4 channels, in operand order
                 const int at = row * QS + (c8 & ~31) + 4 * (u >> 2);
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = row < L ? (which ? kr[e / 4][e % 4] : qr[e / 4][e % 4]) : 0.0f;
+                    for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(which ? kr[e / 4][e % 4] : qr[e / 4][e % 4]);
                     split3<8>(x, p);
 #pragma unroll
                     for (int m = 0; m < 3; ++m) {
@@ -650,23 +687,21 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
         bool odd = false;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            V[e] = 8 * lg + e < L ? vr[e] : 0.0f;
+            V[e] = __uint_as_float(vr[e]);
             odd |= !finite_f32(V[e]);
-        }
-        if (w == 0) {
-            const double g = wave_scan(lane < L ? (double)log_decay(al) : 0.0);   // lanes past FL: zeros
-            const double gl = __shfl(g, 63, 64);
-            if (lane < FL) {
-                sG[lane] = g;
-                sE[lane] = expf((float)g);
-                sW[lane] = expf((float)(gl - g));
-            }
-            gtot += gl;
         }
         __syncthreads();
         if (c0 + FL < te) load(c0 + FL);
 
         const float egl = sE[FL - 1];
+        if (!OUT && ahead) gtot += make_gates<FL>(al, te - c0 - FL, lane, s_gate[cur ^ 1]);
+        u32x4 vp[3];                                               // B operand: the values in parts
+        {
+            uint32_t p[3][4];
+            split3<8>(V, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) vp[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+        }
         if constexpr (OUT) {
             // scores: tiles (0,0), (1,0), (1,1), one wave each
             if (w < 3) {
@@ -716,29 +751,30 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
             }
             O[0] *= *reinterpret_cast<const v4f*>(&sE[4 * lg]);
             O[1] *= *reinterpret_cast<const v4f*>(&sE[16 + 4 * lg]);
+            if (ahead) gtot += make_gates<FL>(al, te - c0 - FL, lane, s_gate[cur ^ 1]);
             __syncthreads();                                       // the scores are written
-            {
+            u32x4 fp[3] = {vp[0], vp[1], vp[2]};                   // finite values: 0 * v must stay 0
+            if (__any(odd)) {
                 float x[8];
                 uint32_t p[3][4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = finite_f32(V[e]) ? V[e] : 0.0f;    // 0 * v must stay 0
+                for (int e = 0; e < 8; ++e) x[e] = finite_f32(V[e]) ? V[e] : 0.0f;
                 split3<8>(x, p);
-                u32x4 b[3];
 #pragma unroll
-                for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                for (int m = 0; m < 3; ++m) fp[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    u32x4 x3[3];
+            for (int r = 0; r < 2; ++r) {
+                u32x4 x3[3];
 #pragma unroll
-                    for (int m = 0; m < 3; ++m)
-                        x3[m] = *reinterpret_cast<const u32x4*>(&sP[m][(16 * r + li) * TS + 8 * lg]);
-                    O[r] = mfma_split(x3, b, O[r]);
-                }
+                for (int m = 0; m < 3; ++m)
+                    x3[m] = *reinterpret_cast<const u32x4*>(&sP[m][(16 * r + li) * TS + 8 * lg]);
+                O[r] = mfma_split(x3, fp, O[r]);
             }
             if (__any(odd))
 #pragma unroll 1
                 for (int i = 0; i < L; ++i) {
-                    const float x = gv[((size_t)(c0 + i) * heads + head) * D + col];
+                    const float x = __uint_as_float(row_ld(rows(a.v, c0), i * rb + 4 * col));
                     if (!finite_f32(x))
 #pragma unroll
                         for (int r = 0; r < 2; ++r)
@@ -750,31 +786,21 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                                                 bf16_to_f32(sP[2][n * TS + i])) * x;
                             }
                 }
-            float* go = static_cast<float*>(a.o);
+            const rsrc_t ro = rows(a.o, c0);                       // rows past the end are left as they were
+            const uint32_t ln = fresh(lane), ooff = 4 * (ln >> 4) * rb + 4 * (16 * w + (ln & 15));
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = 16 * r + 4 * lg + v;
-                    if (n < L) st_nt(go + ((size_t)(c0 + n) * heads + head) * D + col, O[r][v]);
-                }
+                for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, __float_as_uint(O[r][v]));
         }
         if (a.end || c0 + FL < te) {
-            float x[8];
-            uint32_t p[3][4];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = sW[8 * lg + e] * V[e];
-            split3<8>(x, p);
-            u32x4 b[3];
-#pragma unroll
-            for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 H[rt] *= egl;
                 u32x4 k3[3];
 #pragma unroll
                 for (int m = 0; m < 3; ++m) k3[m] = *reinterpret_cast<const u32x4*>(&sT[m][(16 * rt + li) * TS + 8 * lg]);
-                H[rt] = mfma_split(k3, b, H[rt]);
+                H[rt] = mfma_split(k3, vp, H[rt]);
             }
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk
@@ -784,7 +810,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int v = 0; v < 4; ++v) a.end[soff + (size_t)(16 * rt + 4 * lg + v) * D + col] = H[rt][v];
-    if (a.decay && t == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
+    if (a.decay && t == NT - 64) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
 }
 
 // ---------------------------------------------------------------------------
