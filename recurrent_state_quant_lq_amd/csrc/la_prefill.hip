@@ -218,8 +218,7 @@ template <int D>
 struct LB {
     static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr int RT = D / 16;
-    static constexpr int QS = D + 8;           // shorts per Q / K row: 16-byte reads of 8 rows hit all banks
-    static constexpr int TS = BL + 8;          // shorts per K^T / score row
+    static constexpr int QP = D / 8, TP = BL / 8;   // pieces per Q / K row, per K^T / score row
 };
 
 // Gates of a chunk: prefix sums of log alpha, e^{g_n}, e^{g_L - g_n}.
@@ -244,11 +243,11 @@ __device__ __forceinline__ double make_gates(float alpha, int left, int lane, Ga
 template <int D, bool OUT>
 __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     using P = LB<D>;
-    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QS = P::QS, TS = P::TS;
-    __shared__ __align__(16) uint16_t sQ[OUT ? BL * QS : 8];
-    __shared__ __align__(16) uint16_t sK[OUT ? BL * QS : 8];
-    __shared__ __align__(16) uint16_t sT[D * TS];                  // K^T: [channel][token]
-    __shared__ __align__(16) uint16_t sP[OUT ? 2 * BL * TS : 8];   // scores, upper and lower parts
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, TP = P::TP;
+    __shared__ __align__(16) uint16_t sQ[OUT ? pm_shorts<BL>(QP) : 8];
+    __shared__ __align__(16) uint16_t sK[OUT ? pm_shorts<BL>(QP) : 8];
+    __shared__ __align__(16) uint16_t sT[pm_shorts<D>(TP)];        // K^T: [channel][token]
+    __shared__ __align__(16) uint16_t sP[2][OUT ? pm_shorts<BL>(TP) : 8];   // scores, upper and lower parts
     __shared__ Gates<BL> s_gate[2];                                // of this chunk and the next
 
     const int t = threadIdx.x, lane = t & 63;
@@ -279,7 +278,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
         // score tiles right of the diagonal inside a 32-token step: zeros, never written again
         for (int e = t; e < 2 * 2 * 16 * 8; e += NT) {
             const int part = e >> 8, blk = (e >> 7) & 1, row = (e >> 3) & 15, c = e & 7;
-            *reinterpret_cast<uint32_t*>(&sP[(part * BL + 32 * blk + row) * TS + 32 * blk + 16 + 2 * c]) = 0;
+            *reinterpret_cast<uint32_t*>(&sP[part][pm<BL>(32 * blk + row, 4 * blk + 2 + (c >> 2)) + 2 * (c & 3)]) = 0;
         }
     }
 
@@ -346,17 +345,14 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 x0[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x05040100u);
                 x1[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x07060302u);
             }
-            // (octets swapped in pairs in every other 16 rows: the writes of 16 lanes, two rows
-            // apart each, then hit all banks)
-            const int so = 8 * oct;
-            *reinterpret_cast<u32x4*>(&sT[(2 * kpair) * TS + so]) = x0;
-            *reinterpret_cast<u32x4*>(&sT[(2 * kpair + 1) * TS + so]) = x1;
+            *reinterpret_cast<u32x4*>(&sT[pm<D>(2 * kpair, oct)]) = x0;
+            *reinterpret_cast<u32x4*>(&sT[pm<D>(2 * kpair + 1, oct)]) = x1;
             if constexpr (OUT) {
                 // channels (c, c + 1), c = 2 kpair, in the operand order of their 32-block
                 const int u = (2 * kpair & 31) >> 2;
-                const int at = (2 * kpair & ~31) + 8 * (u & 3) + 4 * (u >> 2) + (2 * kpair & 3);
+                const int piece = (kpair >> 4) * 4 + (u & 3), in = 4 * (u >> 2) + (2 * kpair & 3);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(&sK[(8 * oct + e) * QS + at]) = kd[j][e];
+                for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(&sK[pm<BL>(8 * oct + e, piece) + in]) = kd[j][e];
             }
         }
         if constexpr (OUT)
@@ -364,9 +360,9 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
             for (int j = 0; j < 4; ++j) {
                 const int e = 64 * w + ln + NT * j, row = e / (D / 8), c = 8 * (e % (D / 8));
                 const int u = (c & 31) >> 2;                       // two groups of 4 channels: u, u + 1
-                uint16_t* at = &sQ[row * QS + (c & ~31) + 4 * (u >> 2)];
-                *reinterpret_cast<u32x2*>(at + 8 * (u & 3)) = u32x2{qd[j][0], qd[j][1]};
-                *reinterpret_cast<u32x2*>(at + 8 * ((u + 1) & 3)) = u32x2{qd[j][2], qd[j][3]};
+                const int p0 = (c >> 5) * 4, in = 4 * (u >> 2);
+                *reinterpret_cast<u32x2*>(&sQ[pm<BL>(row, p0 + (u & 3)) + in]) = u32x2{qd[j][0], qd[j][1]};
+                *reinterpret_cast<u32x2*>(&sQ[pm<BL>(row, p0 + ((u + 1) & 3)) + in]) = u32x2{qd[j][2], qd[j][3]};
             }
         u32x4 V[2][2];                                             // B operands: [32-token step][ct]
 #pragma unroll
@@ -382,6 +378,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
         if (!OUT && ahead) gtot += make_gates<BL>(al, te - c0 - BL, lane, s_gate[cur ^ 1]);
         if constexpr (OUT) {
             const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
+            const int at = pm<BL>(li, lg);                         // operand reads: row li, piece lg
             // ---- scores: the 10 tiles on and below the diagonal, over the waves ----
             // (one branch per tile on the wave's index, so that every LDS address is a constant
             // away from the lane's)
@@ -392,16 +389,17 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int ks = 0; ks < D / 32; ++ks)
-                    acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[(16 * r + li) * QS + 32 * ks + 8 * lg]),
-                                    *reinterpret_cast<const u32x4*>(&sK[(16 * c + li) * QS + 32 * ks + 8 * lg]), acc);
+                    acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[at + pm<BL>(16 * r, 4 * ks)]),
+                                    *reinterpret_cast<const u32x4*>(&sK[at + pm<BL>(16 * c, 4 * ks)]), acc);
                 const double gi = sG[16 * c + li];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const int n = 16 * r + 4 * lg + v;
                     float p = __expf((float)(sG[n] - gi)) * acc[v];
                     if (r == c) p = li <= 4 * lg + v ? p : 0.0f;
-                    sP[n * TS + 16 * c + li] = (uint16_t)(__float_as_uint(p) >> 16);
-                    sP[(BL + n) * TS + 16 * c + li] = (uint16_t)(__float_as_uint(p - top_f32(p)) >> 16);
+                    const int to = pm<BL>(n, 2 * c) + pm<BL>(0, li >> 3) + (li & 7);
+                    sP[0][to] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sP[1][to] = (uint16_t)(__float_as_uint(p - top_f32(p)) >> 16);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -424,7 +422,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                     }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[(16 * r + li) * QS + 32 * ks + 8 * lg]);
+                    const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[at + pm<BL>(16 * r, 4 * ks)]);
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct) {
                         O[r][ct] = mfma_bf16(aq, bh[ct], O[r][ct]);
@@ -467,7 +465,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                 for (int j = 0; j <= r / 2; ++j)
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
-                        const u32x4 ap = *reinterpret_cast<const u32x4*>(&sP[(part * BL + 16 * r + li) * TS + 32 * j + 8 * lg]);
+                        const u32x4 ap = *reinterpret_cast<const u32x4*>(&sP[part][at + pm<BL>(16 * r, 4 * j)]);
 #pragma unroll
                         for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(ap, V[j][ct], O[r][ct]);
                     }
@@ -484,8 +482,8 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 #pragma unroll
                             for (int v = 0; v < 4; ++v) {
                                 const int n = 16 * r + lq + v;
-                                const float p = n < i ? 0.0f
-                                                      : bf16_to_f32(sP[n * TS + i]) + bf16_to_f32(sP[(BL + n) * TS + i]);
+                                const int from = pm<BL>(n, i >> 3) + (i & 7);
+                                const float p = n < i ? 0.0f : bf16_to_f32(sP[0][from]) + bf16_to_f32(sP[1][from]);
                                 if (n >= i && (od & 0x8000u)) O[r][0][v] += p * lo_f32(x);
                                 if (n >= i && (od & 0x80000000u)) O[r][1][v] += p * hi_f32(x);
                             }
@@ -538,7 +536,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                     }
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    const u32x4 ak = *reinterpret_cast<const u32x4*>(&sT[(16 * rt + li) * TS + 32 * j + 8 * lg]);
+                    const u32x4 ak = *reinterpret_cast<const u32x4*>(&sT[pm<D>(li, lg) + pm<D>(16 * rt, 4 * j)]);
 #pragma unroll
                     for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
@@ -574,18 +572,17 @@ template <int D>
 struct LF {
     static constexpr int NW = D / 16, NT = 64 * NW;
     static constexpr int RT = D / 16;
-    static constexpr int QS = D + 8;           // shorts per Q / K row
-    static constexpr int TS = FL + 8;          // shorts per K^T / score row
+    static constexpr int QP = D / 8, TP = FL / 8;   // pieces per Q / K row, per K^T / score row
 };
 
 template <int D, bool OUT>
 __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
     using P = LF<D>;
-    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QS = P::QS, TS = P::TS;
-    __shared__ __align__(16) uint16_t sQ[3][OUT ? FL * QS : 8];
-    __shared__ __align__(16) uint16_t sK[3][OUT ? FL * QS : 8];
-    __shared__ __align__(16) uint16_t sT[3][D * TS];               // (w o K)^T: [channel][token]
-    __shared__ __align__(16) uint16_t sP[3][OUT ? FL * TS : 8];    // scores
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, TP = P::TP;
+    __shared__ __align__(16) uint16_t sQ[3][OUT ? pm_shorts<FL>(QP) : 8];
+    __shared__ __align__(16) uint16_t sK[3][OUT ? pm_shorts<FL>(QP) : 8];
+    __shared__ __align__(16) uint16_t sT[3][pm_shorts<D>(TP)];               // (w o K)^T: [channel][token]
+    __shared__ __align__(16) uint16_t sP[3][OUT ? pm_shorts<FL>(TP) : 8];    // scores
     __shared__ Gates<FL> s_gate[2];                                // of this chunk and the next
 
     const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
@@ -608,7 +605,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
         for (int rt = 0; rt < RT; ++rt) H[rt] = v4f{0.f, 0.f, 0.f, 0.f};
     }
     if constexpr (OUT)
-        for (int e = t; e < 3 * 16 * 16; e += NT) sP[e >> 8][((e >> 4) & 15) * TS + 16 + (e & 15)] = 0;   // right of the diagonal
+        for (int e = t; e < 3 * 16 * 16; e += NT) sP[e >> 8][pm<FL>((e >> 4) & 15, 2 + ((e >> 3) & 1)) + (e & 7)] = 0;   // right of the diagonal
 
     // chunk loads, one chunk ahead; tokens past the end read as zeros
     constexpr int CPR = D / 8;                                     // 8-channel pieces per row
@@ -664,11 +661,12 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
             split3<8>(x, p);
 #pragma unroll
             for (int m = 0; m < 3; ++m)
-                *reinterpret_cast<u32x4*>(&sT[m][kc * TS + 8 * koct]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                *reinterpret_cast<u32x4*>(&sT[m][pm<D>(kc, koct)]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             if constexpr (OUT) {
                 const int row = tt / CPR, c8 = 8 * (tt % CPR);
                 const int u = (c8 & 31) >> 2;                      // two groups of 4 channels, in operand order
-                const int at = row * QS + (c8 & ~31) + 4 * (u >> 2);
+                const int at0 = pm<FL>(row, (c8 >> 5) * 4 + (u & 3)) + 4 * (u >> 2);
+                const int at1 = pm<FL>(row, (c8 >> 5) * 4 + ((u + 1) & 3)) + 4 * (u >> 2);
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
 #pragma unroll
@@ -676,9 +674,9 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                     split3<8>(x, p);
 #pragma unroll
                     for (int m = 0; m < 3; ++m) {
-                        uint16_t* dst = (which ? sK[m] : sQ[m]) + at;
-                        *reinterpret_cast<u32x2*>(dst + 8 * (u & 3)) = u32x2{p[m][0], p[m][1]};
-                        *reinterpret_cast<u32x2*>(dst + 8 * ((u + 1) & 3)) = u32x2{p[m][2], p[m][3]};
+                        uint16_t* dst = which ? sK[m] : sQ[m];
+                        *reinterpret_cast<u32x2*>(dst + at0) = u32x2{p[m][0], p[m][1]};
+                        *reinterpret_cast<u32x2*>(dst + at1) = u32x2{p[m][2], p[m][3]};
                     }
                 }
             }
@@ -712,8 +710,8 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                     u32x4 x[3], y[3];
 #pragma unroll
                     for (int m = 0; m < 3; ++m) {
-                        x[m] = *reinterpret_cast<const u32x4*>(&sQ[m][(16 * r + li) * QS + 32 * ks + 8 * lg]);
-                        y[m] = *reinterpret_cast<const u32x4*>(&sK[m][(16 * c + li) * QS + 32 * ks + 8 * lg]);
+                        x[m] = *reinterpret_cast<const u32x4*>(&sQ[m][pm<FL>(li, lg) + pm<FL>(16 * r, 4 * ks)]);
+                        y[m] = *reinterpret_cast<const u32x4*>(&sK[m][pm<FL>(li, lg) + pm<FL>(16 * c, 4 * ks)]);
                     }
                     acc = mfma_split(x, y, acc);
                 }
@@ -724,9 +722,10 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                     const int n = 16 * r + 4 * lg + v;
                     const float p = i <= n ? __expf((float)(sG[n] - gi)) * acc[v] : 0.0f;
                     const float p1 = p - top_f32(p);
-                    sP[0][n * TS + i] = (uint16_t)(__float_as_uint(p) >> 16);
-                    sP[1][n * TS + i] = (uint16_t)(__float_as_uint(p1) >> 16);
-                    sP[2][n * TS + i] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
+                    const int at = pm<FL>(n, i >> 3) + (i & 7);
+                    sP[0][at] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sP[1][at] = (uint16_t)(__float_as_uint(p1) >> 16);
+                    sP[2][at] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
                 }
             }
             v4f O[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -745,7 +744,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                     u32x4 q[3];
 #pragma unroll
                     for (int m = 0; m < 3; ++m)
-                        q[m] = *reinterpret_cast<const u32x4*>(&sQ[m][(16 * r + li) * QS + 32 * ks + 8 * lg]);
+                        q[m] = *reinterpret_cast<const u32x4*>(&sQ[m][pm<FL>(li, lg) + pm<FL>(16 * r, 4 * ks)]);
                     O[r] = mfma_split(q, b, O[r]);
                 }
             }
@@ -768,7 +767,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                 u32x4 x3[3];
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
-                    x3[m] = *reinterpret_cast<const u32x4*>(&sP[m][(16 * r + li) * TS + 8 * lg]);
+                    x3[m] = *reinterpret_cast<const u32x4*>(&sP[m][pm<FL>(li, lg) + pm<FL>(16 * r, 0)]);
                 O[r] = mfma_split(x3, fp, O[r]);
             }
             if (__any(odd))
@@ -781,9 +780,9 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
 #pragma unroll
                             for (int v = 0; v < 4; ++v) {
                                 const int n = 16 * r + 4 * lg + v;
+                                const int at = pm<FL>(n, i >> 3) + (i & 7);
                                 if (n >= i)
-                                    O[r][v] += (bf16_to_f32(sP[0][n * TS + i]) + bf16_to_f32(sP[1][n * TS + i]) +
-                                                bf16_to_f32(sP[2][n * TS + i])) * x;
+                                    O[r][v] += (bf16_to_f32(sP[0][at]) + bf16_to_f32(sP[1][at]) + bf16_to_f32(sP[2][at])) * x;
                             }
                 }
             const rsrc_t ro = rows(a.o, c0);                       // rows past the end are left as they were
@@ -799,7 +798,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
                 H[rt] *= egl;
                 u32x4 k3[3];
 #pragma unroll
-                for (int m = 0; m < 3; ++m) k3[m] = *reinterpret_cast<const u32x4*>(&sT[m][(16 * rt + li) * TS + 8 * lg]);
+                for (int m = 0; m < 3; ++m) k3[m] = *reinterpret_cast<const u32x4*>(&sT[m][pm<D>(li, lg) + pm<D>(16 * rt, 0)]);
                 H[rt] = mfma_split(k3, vp, H[rt]);
             }
         }

@@ -39,6 +39,18 @@ __device__ __forceinline__ void row_st(rsrc_t r, uint32_t off, uint32_t x) {
     __builtin_amdgcn_raw_buffer_store_b32(x, r, off, 0, 2);
 }
 
+// Operand rows in LDS, R rows of pieces of 16 bytes (8 bf16), piece after piece: the rows'
+// pieces p are contiguous, so a matrix operand's 16-byte reads (16 rows, four pieces over
+// the lane groups) are free of bank conflicts: one serves lanes of the pieces 2 i and 2 i + 1
+// together, rows 0-3 and 12-15 of one, 4-11 of the other.  16 bytes of padding after every
+// second piece spread the writes of a row.  (Row after row with 16 bytes of padding, the
+// chunk kernels spent 40% of their LDS time in conflicts.)  Every address is a constant
+// away from the lane's.
+template <int R>
+__device__ __forceinline__ constexpr int pm(int row, int piece) { return 8 * (piece * R + (piece >> 1) + row); }
+template <int R>
+constexpr int pm_shorts(int pieces) { return 8 * (pieces * R + (pieces + 1) / 2); }
+
 // Two fp32 values to packed bf16 (nearest even), low half first.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
