@@ -9,12 +9,14 @@
 // The prefix sums are kept in 64 bits: tokens after a strong decay (or a
 // forget) still see differences g_n - g_i exact to fp32.
 //
-// One workgroup per (b, h); NW waves, wave w owns the columns
-// [w*DV/NW, (w+1)*DV/NW) of H in v_mfma_f32_16x16x4_f32 accumulator tiles
-// (tile (rt, ct): rows rt*16 + 4*(lane/16) + v, column lane%16), so the state
-// stays in registers from the first load to the final store.  Its accumulator
-// layout is the B operand of the next products with the K index in register
-// order, so no value of H or V moves between lanes.
+// Four kernels: chunks of 64 bf16 tokens, chunks of 32 fp32 tokens (d = 64, 128), chunks of
+// 16 tokens (d = 16), and the recurrence itself for a few tokens.  In the first two a
+// workgroup owns a head's state in matrix-instruction accumulators (tile (rt, ct): rows
+// 16 rt + 4 (lane / 16) + v, column lane % 16) from the first load to the final store; the
+// accumulator layout is the B operand of the next products with the K index in register
+// order, so no value of H or V moves between lanes.  Where the heads alone leave most of
+// the GPU idle, a prompt is cut into segments: their states alone, a scan over the
+// segments, then their outputs from the states before them.
 #include "lq_internal.h"
 #include "lq_split.h"
 
@@ -35,133 +37,6 @@ struct LaPrefillArgs {
     int heads;                // B*H: stride between tokens, in heads
     int alpha_tok;            // token stride of alpha: heads, or 0 for one decay per head
 };
-
-constexpr int CL = 16;        // tokens per chunk (the MFMA tile)
-
-template <int D>
-struct LP {
-    static constexpr int NW = D / 16 < 4 ? D / 16 : 4;     // waves
-    static constexpr int NT = 64 * NW;
-    static constexpr int RT = D / 16;                      // row tiles
-    static constexpr int CTW = D / 16 / NW;                // column tiles per wave
-    static constexpr int DP = D + 4;                       // padded LDS row (banks 4n + c)
-};
-
-template <int D, typename TI>
-__global__ __launch_bounds__(LP<D>::NT) void la_prefill_kernel(LaPrefillArgs a) {
-    using P = LP<D>;
-    constexpr int NT = P::NT, RT = P::RT, CTW = P::CTW, DP = P::DP;
-    __shared__ __align__(16) float sQ[CL * DP];
-    __shared__ __align__(16) float sK[CL * DP];
-    __shared__ __align__(16) float sV[CL * DP];
-    __shared__ __align__(16) float sP[CL * CL];            // E o (Q K^T), lower triangle
-    __shared__ double sG[CL];                              // chunk-local log-decay prefix
-
-    const int t = threadIdx.x;
-    const int lane = t & 63, li = lane & 15, lg = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-    const size_t head = blockIdx.x, heads = (size_t)a.heads;
-    const int hh = (int)(head % (unsigned)a.H);
-    const int T = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
-
-    const size_t hoff = head * (size_t)D * D;
-    v4f H[RT][CTW];
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                H[rt][ct][v] = a.h0 ? a.h0[hoff + (size_t)(rt * 16 + 4 * lg + v) * D + (w * CTW + ct) * 16 + li] : 0.0f;
-
-    for (int c0 = 0; c0 < T; c0 += CL) {
-        const int L = min(CL, T - c0);                     // tokens of this chunk; the rows past it are zeros
-        for (int e = t; e < CL * D; e += NT) {
-            const int n = e / D, c = e % D;
-            const size_t at = ((size_t)(c0 + n) * heads + head) * D + c;
-            sQ[n * DP + c] = n < L ? tok_ld<TI>(a.q, at) : 0.0f;
-            sK[n * DP + c] = n < L ? tok_ld<TI>(a.k, at) : 0.0f;
-            sV[n * DP + c] = n < L ? tok_ld<TI>(a.v, at) : 0.0f;
-        }
-        if (t == 0) {
-            double g = 0.0;
-            for (int n = 0; n < CL; ++n) {
-                if (n < L) g += (double)log_decay(a.alpha_tok ? a.alpha[(size_t)(c0 + n) * a.alpha_tok + head] : a.alpha[hh]);
-                sG[n] = g;
-            }
-        }
-        __syncthreads();
-        if (w == 0 && a.o) {
-            // P[n][i] = E_{n,i} <q_n, k_i>
-            v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-            for (int ks = 0; ks < D / 4; ++ks)
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(sQ[li * DP + 4 * ks + lg], sK[li * DP + 4 * ks + lg], acc, 0, 0, 0);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int n = 4 * lg + v, i = li;
-                sP[n * CL + i] = i <= n ? expf((float)(sG[n] - sG[i])) * acc[v] : 0.0f;
-            }
-        }
-        __syncthreads();
-        const float eg = expf((float)sG[li]);              // rows of HQ: token li
-        const float egl = expf((float)sG[CL - 1]);
-        float ekt[4];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) ekt[v] = expf((float)(sG[CL - 1] - sG[4 * lg + v]));
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct) {
-            const int col = (w * CTW + ct) * 16 + li;
-            float vv[4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v) vv[v] = sV[(4 * lg + v) * DP + col];
-            if (a.o) {
-                v4f o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    float aq[4];
-                    load_floats<4>(sQ + li * DP + rt * 16 + 4 * lg, aq);
-#pragma unroll
-                    for (int v = 0; v < 4; ++v) o = __builtin_amdgcn_mfma_f32_16x16x4f32(aq[v] * eg, H[rt][ct][v], o, 0, 0, 0);
-                }
-                // a non-finite v would reach earlier tokens as 0 * v: left out here, added below
-                bool odd = false;
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    odd |= !finite_f32(vv[v]);
-                    o = __builtin_amdgcn_mfma_f32_16x16x4f32(sP[li * CL + 4 * lg + v], finite_f32(vv[v]) ? vv[v] : 0.0f, o, 0, 0, 0);
-                }
-                if (__any(odd))
-                    for (int i = 0; i < L; ++i) {
-                        const float x = sV[i * DP + col];
-                        if (!finite_f32(x))
-#pragma unroll
-                            for (int v = 0; v < 4; ++v)
-                                if (4 * lg + v >= i) o[v] += sP[(4 * lg + v) * CL + i] * x;
-                    }
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    if (4 * lg + v < L) tok_st<TI>(a.o, ((size_t)(c0 + 4 * lg + v) * heads + head) * D + col, o[v]);
-            }
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                H[rt][ct] *= egl;
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    H[rt][ct] = __builtin_amdgcn_mfma_f32_16x16x4f32(sK[(4 * lg + v) * DP + rt * 16 + li] * ekt[v], vv[v],
-                                                                     H[rt][ct], 0, 0, 0);
-            }
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int ct = 0; ct < CTW; ++ct)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                a.h[hoff + (size_t)(rt * 16 + 4 * lg + v) * D + (w * CTW + ct) * 16 + li] = H[rt][ct][v];
-}
 
 // ---------------------------------------------------------------------------
 // bf16 tokens, d >= 64: chunks of 64 tokens on bf16 matrix products
@@ -866,6 +741,116 @@ __global__ __launch_bounds__(256) void la_step_kernel(LaPrefillArgs a) {
 constexpr int kStepTokens = 4;
 constexpr int kChunkHeads = 1 << 17;   // a chunk's rows lie within 32-bit byte offsets (64 rows of 256 B, 32 of 512 B)
 
+// ---------------------------------------------------------------------------
+// d = 16: chunks of 16 tokens, one wave a segment, no LDS
+// ---------------------------------------------------------------------------
+// With d = 16 every product is one 16 x 16 x 16 of the fp32 matrix instruction, and each
+// operand is loaded in the layout that the instruction takes (lane (lg, li), step v: row or
+// column li, index 4 lg + v).  The scores are formed transposed (K Q^T): their accumulators
+// are then the A operand of P V as they are.  Everything stays in registers, so waves need
+// no barrier and many fit; the next chunk's loads are in flight during a chunk.
+template <typename TI, bool OUT>
+__global__ __launch_bounds__(256) void la_small_kernel(LaSegArgs a) {
+    constexpr int D = 16, CS = 16;
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    const size_t heads = (size_t)a.heads;
+    const size_t head = (size_t)blockIdx.x * 4 + (threadIdx.x >> 6);      // one head a wave
+    if (head >= heads) return;
+    const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int t0 = (int)blockIdx.y * a.seg, te = min(len, t0 + a.seg);
+    const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
+    v4f H = {0.f, 0.f, 0.f, 0.f};                                         // H[4 lg + v][li]
+    if (a.start)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) H[v] = a.start[soff + (4 * lg + v) * D + li];
+    // token li: q, k channels 4 lg + v; tokens 4 lg + v: k, v channel li
+    struct Chunk {
+        float q[4], k[4], kt[4], vt[4], al;
+    };
+    auto load = [&](int c0, Chunk& x) {                                   // (past the end: the last token, zeroed on use)
+        const int n = min(c0 + li, te - 1);
+        const size_t at = ((size_t)n * heads + head) * D + 4 * lg;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const size_t to = ((size_t)min(c0 + 4 * lg + v, te - 1) * heads + head) * D + li;
+            if (OUT) {
+                x.q[v] = tok_ld<TI>(a.q, at + v);
+                x.k[v] = tok_ld<TI>(a.k, at + v);
+            }
+            x.kt[v] = tok_ld<TI>(a.k, to);
+            x.vt[v] = tok_ld<TI>(a.v, to);
+        }
+        x.al = a.alpha[a.alpha_tok ? (size_t)n * a.alpha_tok + head : head % (unsigned)a.H];
+    };
+    Chunk cur, nxt;
+    if (t0 < te) load(t0, cur);
+    double gtot = 0.0;
+    for (int c0 = t0; c0 < te; c0 += CS) {
+        const int L = min(CS, te - c0);
+        if (c0 + CS < te) load(c0 + CS, nxt);
+        // every 16 lanes hold the chunk's prefix sums
+        double g = li < L ? (double)log_decay(cur.al) : 0.0;
+        g = scan_step<0x111, 0xf>(g);
+        g = scan_step<0x112, 0xf>(g);
+        g = scan_step<0x114, 0xf>(g);
+        g = scan_step<0x118, 0xf>(g);
+        const double gl = __shfl(g, 15, 16);
+        double gi[4];                                                     // of tokens 4 lg + v
+#pragma unroll
+        for (int v = 0; v < 4; ++v) gi[v] = __shfl(g, 4 * lg + v, 16);
+        float vt[4], kw[4];
+        bool odd = false;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const bool on = 4 * lg + v < L;
+            vt[v] = on ? cur.vt[v] : 0.0f;
+            kw[v] = on ? expf((float)(gl - gi[v])) * cur.kt[v] : 0.0f;
+            odd |= !finite_f32(vt[v]);
+        }
+        if constexpr (OUT) {
+            // P^T[i = 4 lg + v][n = li]
+            v4f p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float x = li < L ? cur.k[v] : 0.0f, y = li < L ? cur.q[v] : 0.0f;
+                p = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, p, 0, 0, 0);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) p[v] = 4 * lg + v <= li ? expf((float)(g - gi[v])) * p[v] : 0.0f;
+            const float en = expf((float)g);
+            v4f o = {0.f, 0.f, 0.f, 0.f};                                 // o[n = 4 lg + v][li]
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                o = __builtin_amdgcn_mfma_f32_16x16x4f32(li < L ? en * cur.q[v] : 0.0f, H[v], o, 0, 0, 0);
+                o = __builtin_amdgcn_mfma_f32_16x16x4f32(p[v], finite_f32(vt[v]) ? vt[v] : 0.0f, o, 0, 0, 0);
+            }
+            if (__any(odd))                                               // the others, from their own token on
+#pragma unroll 1
+                for (int i = 0; i < L; ++i) {
+                    const float x = tok_ld<TI>(a.v, ((size_t)(c0 + i) * heads + head) * D + li);
+                    const float p0 = i & 2 ? (i & 1 ? p[3] : p[2]) : (i & 1 ? p[1] : p[0]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const float pn = __shfl(p0, 16 * (i >> 2) + 4 * lg + v, 64);   // P[4 lg + v][i]
+                        if (!finite_f32(x) && 4 * lg + v >= i) o[v] += pn * x;
+                    }
+                }
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (4 * lg + v < L) tok_st<TI>(a.o, ((size_t)(c0 + 4 * lg + v) * heads + head) * D + li, o[v]);
+        }
+        H *= expf((float)gl);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) H = __builtin_amdgcn_mfma_f32_16x16x4f32(kw[v], vt[v], H, 0, 0, 0);
+        gtot += gl;
+        cur = nxt;
+    }
+    if (a.end)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.end[soff + (4 * lg + v) * D + li] = H[v];
+    if (a.decay && lane == 0) a.decay[blockIdx.y * heads + head] = expf((float)gtot);
+}
+
 // States before each segment from the states of each segment alone, in place, and the
 // state after the last one: S_s = X, X <- decay_s X + S_s.  Four values per lane.
 struct LaScanArgs {
@@ -900,17 +885,23 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
 // bf16 (fp32), 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192
 // heads 109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
 // (291, 282, 290) for 256, 512 and 768 workgroups.
-constexpr size_t kWant = 512, kSplitHeads = 128;
-size_t segments_wanted(size_t heads) { return heads > kSplitHeads ? 1 : (kWant + heads - 1) / heads; }
-int segment_tokens(size_t heads, int T, int chunk) {
-    const size_t chunks = ((size_t)T + chunk - 1) / chunk, want = segments_wanted(heads);
-    return (int)(want <= 1 ? chunks : (chunks + want - 1) / want) * chunk;
+// d = 16 (one wave a segment): enough segments for kWantSmall waves, of 8 chunks at least.
+constexpr size_t kWant = 512, kSplitHeads = 128, kWantSmall = 4096, kMinSmall = 128;
+size_t segments_wanted(size_t heads, int d) {
+    return d == 16 ? (kWantSmall + heads - 1) / heads : heads > kSplitHeads ? 1 : (kWant + heads - 1) / heads;
 }
-int chunk_tokens(const lq_dims& d) { return d.io_dtype == LQ_IO_BF16 ? BL : FL; }
+int chunk_tokens(const lq_dims& d) { return d.dk == 16 ? (int)kMinSmall : d.io_dtype == LQ_IO_BF16 ? BL : FL; }
+int segment_tokens(const lq_dims& d, int T) {
+    const size_t chunk = chunk_tokens(d), chunks = ((size_t)T + chunk - 1) / chunk;
+    const size_t want = segments_wanted((size_t)d.B * d.H, d.dk);
+    return (int)((chunks + want - 1) / want * chunk);
+}
 
 template <int D, typename TI, bool OUT>
 hipError_t chunk_launch(dim3 grid, const LaSegArgs& sa, hipStream_t s) {
-    if constexpr (sizeof(TI) == 2)
+    if constexpr (D == 16)
+        return launch_kernel(LQ_KERNEL_LA_PREFILL, la_small_kernel<TI, OUT>, dim3((grid.x + 3) / 4, grid.y), dim3(256), s, sa);
+    else if constexpr (sizeof(TI) == 2)
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk_kernel<D, OUT>, grid, dim3(LB<D>::NT), s, sa);
     else
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_chunk32_kernel<D, OUT>, grid, dim3(LF<D>::NT), s, sa);
@@ -919,7 +910,7 @@ hipError_t chunk_launch(dim3 grid, const LaSegArgs& sa, hipStream_t s) {
 template <int D, typename TI>
 hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
     const size_t heads = (size_t)args.heads;
-    const int seg = segment_tokens(heads, args.T, chunk_tokens(d)), segs = (int)(((size_t)args.T + seg - 1) / seg);
+    const int seg = segment_tokens(d, args.T), segs = (int)(((size_t)args.T + seg - 1) / seg);
     LaSegArgs sa{args.h0, args.h, nullptr, args.q, args.k, args.v, args.alpha, args.lens, args.o, 0,
                  args.T, args.H, args.heads, args.alpha_tok, seg};
     const dim3 grid((unsigned)heads, (unsigned)segs);
@@ -946,8 +937,7 @@ hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* works
     const dim3 grid((unsigned)args.heads);
     if (args.T <= kStepTokens || args.heads > kChunkHeads)
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_step_kernel<D, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
-    if constexpr (D >= 64) return la_chunks<D, TI>(d, args, workspace, s);
-    else return launch_kernel(LQ_KERNEL_LA_PREFILL, la_prefill_kernel<D, TI>, grid, dim3(LP<D>::NT), s, args);
+    return la_chunks<D, TI>(d, args, workspace, s);
 }
 
 template <int D>
@@ -959,10 +949,10 @@ hipError_t la_prefill_d(const lq_dims& d, const LaPrefillArgs& args, void* works
 }  // namespace
 
 size_t la_workspace_bytes(const lq_dims& d, int T) {
-    if (d.dk < 64 || T <= kStepTokens) return 0;
-    // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
     const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d);
-    const size_t segs = min(segments_wanted(heads), ((size_t)T + chunk - 1) / chunk);
+    if (T <= kStepTokens || heads > (size_t)kChunkHeads) return 0;
+    // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
+    const size_t segs = min(segments_wanted(heads, d.dk), ((size_t)T + chunk - 1) / chunk);
     return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
 }
 
