@@ -221,12 +221,12 @@ __global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
 // one dword of bf16 values, one 8-byte pair of fp32 ones).  Per group of GB blocks:
 //   1. the q and k rows to LDS as bf16 parts (one for bf16 tokens with a decay per
 //      head; else three; per-key decay: rows scaled by e^{g_n - g_pos}, at most 1);
-//   2. scores against the window's keys (three parts in LDS; per-key decay: scaled by
+//   2. scores against the window's keys (in parts in LDS; per-key decay: scaled by
 //      e^{g_pos - g_c}) and the nodes' keys, times E and the ancestor mask; those of
 //      k times -beta.  Per-key decay takes the nodes' scores pair by pair, with the
 //      exponential of each channel's difference: a product of two factors could
 //      overflow;
-//   3. the products with the state, r o sq in three bf16 parts formed on the way;
+//   3. the products with the state, r o sq in bf16 parts formed on the way;
 //   4. block after block, without barriers: R = beta (v - Hb^T k) - A_ctx M_ctx,
 //      M = (I + A)^{-1} R with A_{n,i} = beta_n <k_n, E k_i> (strictly lower triangular in
 //      node order, solved four rows at a time), O = Hb^T q + S M, on the fp32 matrix
@@ -244,6 +244,9 @@ struct TM {
     static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
+    // parts of the window's keys and of the state: three (24 bits); two (16 bits and a rounding,
+    // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-9
+    static constexpr int NS = !DELTA && sizeof(TI) == 2 ? 2 : 3;
     static constexpr int GB = NP == 1 ? 2 : 1;                     // blocks per group
     static constexpr int KB = KDA ? GB : NB;                       // blocks whose keys stay in LDS
     static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
@@ -259,7 +262,7 @@ struct TM {
         __align__(16) float r[D];                                  // row scales (per-key decay: e^{g_pos} r)
         __align__(16) uint16_t q[NP][16 * GB * QS];
         __align__(16) uint16_t k[NP][16 * KB * QS];
-        __align__(16) uint16_t wk[3][WC * QS];
+        __align__(16) uint16_t wk[NS][WC * QS];
         __align__(16) float s[2][16 * GB * SS];                    // scores of q; -beta times those of k
         __align__(16) float gk[KDA ? 16 * NB * D : 4];             // per-key decay: g_n
         __align__(16) float gp[KDA ? D : 4];                       // per-key decay: g of slot pos - 1
@@ -281,10 +284,8 @@ struct TM {
 template <int NP, int NQ>
 __device__ __forceinline__ v4f mfma_parts(const u32x4 (&a)[NP], const u32x4 (&b)[NQ], v4f c) {
     if constexpr (NP == 3 && NQ == 3) return mfma_split(a, b, c);
-    if constexpr (NQ == 3) {
-        c = mfma_bf16(a[0], b[2], c);
-        c = mfma_bf16(a[0], b[1], c);
-    }
+    if constexpr (NQ >= 3) c = mfma_bf16(a[0], b[2], c);
+    if constexpr (NQ >= 2) c = mfma_bf16(a[0], b[1], c);
     return mfma_bf16(a[0], b[0], c);
 }
 
@@ -321,6 +322,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     using X = TM<D, NB, WT, RULE, TI>;
     constexpr int NW = X::NW, NT = X::NT, NP = X::NP, GB = X::GB, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
     constexpr bool KDA = X::KDA, DELTA = X::DELTA;
+    constexpr int NS = X::NS;
     constexpr int NX = DELTA ? 2 : 1, GD = KDA ? D : 1, KS = D / 64, NG = NB / GB;
     __shared__ typename X::Space sp;
     auto& s = sp.m;
@@ -445,15 +447,15 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     for (int c = 0; c < WT; ++c) {
         if (c > 0 && c >= wt) break;
         const bool on = 16 * c + row < pos;
-        uint32_t p[3][4];
+        uint32_t p[NS][4];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if constexpr (KDA) wx[c][u] *= expf(s.gp[c8 + u] - wgc[c][u]);
             wx[c][u] = on ? wx[c][u] : 0.0f;
         }
-        split3<8>(wx[c], p);
+        split<NS, 8>(wx[c], p);
 #pragma unroll
-        for (int m = 0; m < 3; ++m)
+        for (int m = 0; m < NS; ++m)
             *reinterpret_cast<u32x4*>(&s.wk[m][(16 * c + row) * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
     }
 #pragma unroll
@@ -580,13 +582,13 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                     const uint16_t* brow = &s.wk[0][(16 * c + li) * QS + 8 * lg];
 #pragma unroll
                     for (int ks = 0; ks < D / 32; ++ks) {
-                        u32x4 ar[NP], br[3];
+                        u32x4 ar[NP], br[NS];
 #pragma unroll
                         for (int m = 0; m < NP; ++m) ar[m] = *reinterpret_cast<const u32x4*>(arow + m * plane + 32 * ks);
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) br[m] = *reinterpret_cast<const u32x4*>(brow + m * WP + 32 * ks);
-                        if (ks & 1) acc2 = mfma_parts<NP, 3>(ar, br, acc2);
-                        else acc = mfma_parts<NP, 3>(ar, br, acc);
+                        for (int m = 0; m < NS; ++m) br[m] = *reinterpret_cast<const u32x4*>(brow + m * WP + 32 * ks);
+                        if (ks & 1) acc2 = mfma_parts<NP, NS>(ar, br, acc2);
+                        else acc = mfma_parts<NP, NS>(ar, br, acc);
                     }
                     acc += acc2;
                     const float gc = KDA ? 0.0f : s.wg[(16 * c + li) & 31];
@@ -683,17 +685,17 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 // B operands: channels 64 ks + 16 lg + 8 hf .. + 7 of columns col + ct
                 const int ch = 64 * ks + 16 * lg + 8 * hf;
                 float r[8];
-                u32x4 st[2][3];
+                u32x4 st[2][NS];
                 load_floats<8>(&s.r[ch], r);
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) {
                     float x8[8];
-                    uint32_t p[3][4];
+                    uint32_t p[NS][4];
 #pragma unroll
                     for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
-                    split3<8>(x8, p);
+                    split<NS, 8>(x8, p);
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                    for (int m = 0; m < NS; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
                 }
 #pragma unroll
                 for (int e = 0; e < GB; ++e) {
@@ -705,7 +707,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                         for (int m = 0; m < NP; ++m)
                             ar[m] = *reinterpret_cast<const u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + (16 * e + li) * QS + ch);
 #pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, 3>(ar, st[ct], acc[e][x][ct]);
+                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, NS>(ar, st[ct], acc[e][x][ct]);
                     }
                 }
             }

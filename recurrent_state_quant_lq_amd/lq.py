@@ -432,31 +432,38 @@ def _launch(fn, device, stream, *args):
     """Calls fn with the stream (None: device's current stream) on the device that
     holds its tensors, whichever device is the current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
     elif stream.device != device:
         raise ValueError(f"stream on {stream.device}, tensors on {device}")
-    f = getattr(load(), fn)
+    else:
+        raw = stream.cuda_stream
+    f = getattr(_lib or load(), fn)
     if device.index == torch.cuda.current_device():
-        rc = f(*args, stream.cuda_stream)
+        rc = f(*args, raw)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, stream.cuda_stream)
-    _raise(fn, rc)
+            rc = f(*args, raw)
+    if rc:
+        raise LQError(fn, rc)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
+def _check_all(device, dtype_io, *items):
+    """Items (name, tensor, shape, dtype): dtype None is the token dtype.  Every tensor
+    of the shape and dtype, contiguous, on device."""
+    for name, t, shape, dtype in items:
+        if dtype is None:
+            dtype = dtype_io
+        if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+            _check(t, name, shape, dtype)
             raise ValueError(f"{name} on {t.device}, expected {device}")
 
 
-def _alpha_kind(d: lq_dims, alpha, shape):
-    """LQ_ALPHA_HEADS for one decay per head ([H]), LQ_ALPHA_TOKENS for one per token."""
+def _alpha(d: lq_dims, alpha, shape):
+    """LQ_ALPHA_HEADS and the shape [H] for one decay per head, LQ_ALPHA_TOKENS and the
+    token shape for one per token."""
     if alpha is not None and alpha.dim() == 1:
-        _check(alpha, "alpha", (d.H,), torch.float32)
-        return LQ_ALPHA_HEADS
-    _check(alpha, "alpha", shape, torch.float32)
-    return LQ_ALPHA_TOKENS
+        return LQ_ALPHA_HEADS, (d.H,)
+    return LQ_ALPHA_TOKENS, shape
 
 
 def lq_la_workspace_bytes(d: lq_dims, T: int) -> int:
@@ -472,28 +479,31 @@ def lq_la_prefill(d: lq_dims, st, h0, h, T: int, q, k, v, alpha, o=None, lens=No
     tokens per row, or None.  workspace: device uint8 tensor of at least
     lq_la_workspace_bytes(d, T) bytes (None: allocated for this call)."""
     T = int(T)
-    _check(h, "h", (d.B, d.H, d.dk, d.dv), torch.float32)
+    f32 = torch.float32
+    hs = (d.B, d.H, d.dk, d.dv)
+    _check(h, "h", hs, f32)
     dev = h.device
+    items = []
     if h0 is not None:
-        _check(h0, "h0", (d.B, d.H, d.dk, d.dv), torch.float32)
-        if h0.data_ptr() != h.data_ptr():
-            n = h.numel() * 4
-            if abs(h0.data_ptr() - h.data_ptr()) < n:
-                raise ValueError("h0 and h overlap")
+        items.append(("h0", h0, hs, f32))
+        off = abs(h0.data_ptr() - h.data_ptr())
+        if 0 < off < h.numel() * 4:
+            raise ValueError("h0 and h overlap")
     kind = LQ_ALPHA_TOKENS
     if T > 0:
         sh = _token_shapes(d, T)
-        for name, t in (("q", q), ("k", k), ("v", v)):
-            _check(t, name, sh[name], _dtype_of(d, name))
-        kind = _alpha_kind(d, alpha, sh["alpha"])
+        kind, ash = _alpha(d, alpha, sh["alpha"])
+        items += [("q", q, sh["q"], None), ("k", k, sh["k"], None), ("v", v, sh["v"], None), ("alpha", alpha, ash, f32)]
         if o is not None:
-            _check(o, "o", sh["o"], _dtype_of(d, "o"))
+            items.append(("o", o, sh["o"], None))
     if lens is not None:
-        _check(lens, "lens", (d.B,), torch.int32)
+        items.append(("lens", lens, (d.B,), torch.int32))
     cs = None
     if st is not None:
-        cs = st.ready(with_buffer=False)
-        _same_device(dev, st=st.sq)
+        cs = ct.byref(st.ready(with_buffer=False))
+        items.append(("the state", st.sq, st.sq.shape, torch.int8))
+        if any(getattr(st.dims, n) != getattr(d, n) for n in ("B", "H", "dk", "dv", "C")):
+            raise ValueError("the state's dims are not d")
     need = lq_la_workspace_bytes(d, T)
     if workspace is None and need:
         with torch.cuda.stream(stream):              # memory of the stream that uses it
@@ -501,53 +511,45 @@ def lq_la_prefill(d: lq_dims, st, h0, h, T: int, q, k, v, alpha, o=None, lens=No
     size = 0
     if workspace is not None:
         size = workspace.numel()
-        _check(workspace, "workspace", (size,), torch.uint8)
-    _same_device(dev, h0=h0, q=q, k=k, v=v, alpha=alpha, o=o, lens=lens, workspace=workspace)
-    _launch("lq_la_prefill", dev, stream, ct.byref(d), ct.byref(cs) if cs is not None else None, _ptr(h0), _ptr(h),
-            T, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), kind, _ptr(lens), _ptr(o),
-            _ptr(workspace) if size else None, size)
+        items.append(("workspace", workspace, (size,), torch.uint8))
+    _check_all(dev, io_torch_dtype(d), *items)
+    _launch("lq_la_prefill", dev, stream, ct.byref(d), cs, _ptr(h0), h.data_ptr(), T, _ptr(q), _ptr(k), _ptr(v),
+            _ptr(alpha), kind, _ptr(lens), _ptr(o), _ptr(workspace) if size else None, size)
 
 
-def _la_decode(fn, st, pos, q, k, v, alpha, o, stream, pos_arg):
+def _la_decode(fn, st, pos_arg, q, k, v, alpha, o, stream, *more):
     d = st.dims
     sh = _token_shapes(d)
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-        _check(t, name, sh[name], _dtype_of(d, name))
-    kind = _alpha_kind(d, alpha, sh["alpha"])
     cs = st.ready()
     dev = st.sq.device
-    _same_device(dev, q=q, k=k, v=v, alpha=alpha, o=o)
-    _launch(fn, dev, stream, ct.byref(d), ct.byref(cs), pos_arg, _ptr(q), _ptr(k), _ptr(v), _ptr(alpha), kind,
-            _ptr(o))
+    kind, ash = _alpha(d, alpha, sh["alpha"])
+    _check_all(dev, io_torch_dtype(d), ("q", q, sh["q"], None), ("k", k, sh["k"], None), ("v", v, sh["v"], None),
+               ("alpha", alpha, ash, torch.float32), ("o", o, sh["o"], None), *more)
+    _launch(fn, dev, stream, ct.byref(d), ct.byref(cs), pos_arg, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            alpha.data_ptr(), kind, o.data_ptr())
 
 
 def lq_la_decode_step(st: LayerState, pos: int, q, k, v, alpha, o, stream=None):
     """One token of linear attention into slot pos; alpha [B,H], or [H] (fixed per head)."""
-    _la_decode("lq_la_decode_step", st, pos, q, k, v, alpha, o, stream, int(pos))
+    _la_decode("lq_la_decode_step", st, int(pos), q, k, v, alpha, o, stream)
 
 
 def lq_la_decode_step_ragged(st: LayerState, pos, q, k, v, alpha, o, stream=None):
     """pos: device int32 [B], the window position of each batch row."""
-    _check(pos, "pos", (st.dims.B,), torch.int32)
-    _same_device(st.sq.device, pos=pos)
-    _la_decode("lq_la_decode_step_ragged", st, pos, q, k, v, alpha, o, stream, _ptr(pos))
+    _la_decode("lq_la_decode_step_ragged", st, _ptr(pos), q, k, v, alpha, o, stream,
+               ("pos", pos, (st.dims.B,), torch.int32))
 
 
-def _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, **more):
-    d = st.dims
+def _tree_items(d, pos, parent, q, k, v, o, tree_m, tree_g):
     if parent is None or parent.dim() != 2:
         raise ValueError("parent: a [B,N] tensor is required")
     N = parent.shape[1]
     sh = _token_shapes(d, N)
-    _check(pos, "pos", (d.B,), torch.int32)
-    _check(parent, "parent", (d.B, N), torch.int32)
-    for name, t in (("q", q), ("k", k), ("v", v), ("o", o)):
-        _check(t, name, sh[name], _dtype_of(d, name))
     gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
-    _check(tree_m, "tree_m", (d.B, d.H, N, d.dv), torch.float32)
-    _check(tree_g, "tree_g", (d.B, d.H, N, gd), torch.float32)
-    _same_device(st.sq.device, pos=pos, parent=parent, q=q, k=k, v=v, o=o, tree_m=tree_m, tree_g=tree_g, **more)
-    return N, sh
+    f32, i32 = torch.float32, torch.int32
+    return N, sh, (("pos", pos, (d.B,), i32), ("parent", parent, (d.B, N), i32), ("q", q, sh["q"], None),
+                   ("k", k, sh["k"], None), ("v", v, sh["v"], None), ("o", o, sh["o"], None),
+                   ("tree_m", tree_m, (d.B, d.H, N, d.dv), f32), ("tree_g", tree_g, (d.B, d.H, N, gd), f32))
 
 
 def lq_gdn_tree_step(st: LayerState, pos, parent, q, k, v, alpha, beta, o, tree_m, tree_g, stream=None):
@@ -555,22 +557,27 @@ def lq_gdn_tree_step(st: LayerState, pos, parent, q, k, v, alpha, beta, o, tree_
     after the window's pos (device int32 [B]) slots; state, window and pos are left as
     they are.  tree_m [B,H,N,dv] and tree_g [B,H,N,gd] receive the nodes' slots."""
     d = st.dims
-    N, sh = _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, alpha=alpha, beta=beta)
-    _check(alpha, "alpha", sh["alpha"], torch.float32)
-    _check(beta, "beta", sh["beta"], torch.float32)
+    N, sh, items = _tree_items(d, pos, parent, q, k, v, o, tree_m, tree_g)
     cs = st.ready()
-    _launch("lq_gdn_tree_step", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(parent), _ptr(q),
-            _ptr(k), _ptr(v), _ptr(alpha), _ptr(beta), _ptr(o), _ptr(tree_m), _ptr(tree_g))
+    dev = st.sq.device
+    _check_all(dev, io_torch_dtype(d), *items, ("alpha", alpha, sh["alpha"], torch.float32),
+               ("beta", beta, sh["beta"], torch.float32))
+    _launch("lq_gdn_tree_step", dev, stream, ct.byref(d), ct.byref(cs), pos.data_ptr(), N, parent.data_ptr(),
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), beta.data_ptr(), o.data_ptr(),
+            tree_m.data_ptr(), tree_g.data_ptr())
 
 
 def lq_la_tree_step(st: LayerState, pos, parent, q, k, v, alpha, o, tree_m, tree_g, stream=None):
     """lq_gdn_tree_step for plain linear attention; alpha [N,B,H], or [H] (fixed per head)."""
     d = st.dims
-    N, sh = _tree_checks(st, pos, parent, q, k, v, o, tree_m, tree_g, alpha=alpha)
-    kind = _alpha_kind(d, alpha, sh["alpha"])
+    N, sh, items = _tree_items(d, pos, parent, q, k, v, o, tree_m, tree_g)
+    kind, ash = _alpha(d, alpha, sh["alpha"])
     cs = st.ready()
-    _launch("lq_la_tree_step", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(parent), _ptr(q),
-            _ptr(k), _ptr(v), _ptr(alpha), kind, _ptr(o), _ptr(tree_m), _ptr(tree_g))
+    dev = st.sq.device
+    _check_all(dev, io_torch_dtype(d), *items, ("alpha", alpha, ash, torch.float32))
+    _launch("lq_la_tree_step", dev, stream, ct.byref(d), ct.byref(cs), pos.data_ptr(), N, parent.data_ptr(),
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), kind, o.data_ptr(), tree_m.data_ptr(),
+            tree_g.data_ptr())
 
 
 def lq_tree_commit(st: LayerState, pos, path, n_path, k, tree_m, tree_g, stream=None):
@@ -581,16 +588,14 @@ def lq_tree_commit(st: LayerState, pos, path, n_path, k, tree_m, tree_g, stream=
         raise ValueError("k: the tree's [N,B,H,dk] tensor and path: a [B,P] tensor are required")
     N, P = k.shape[0], path.shape[1]
     gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
-    _check(pos, "pos", (d.B,), torch.int32)
-    _check(path, "path", (d.B, P), torch.int32)
-    _check(n_path, "n_path", (d.B,), torch.int32)
-    _check(k, "k", _token_shapes(d, N)["k"], _dtype_of(d, "k"))
-    _check(tree_m, "tree_m", (d.B, d.H, N, d.dv), torch.float32)
-    _check(tree_g, "tree_g", (d.B, d.H, N, gd), torch.float32)
     cs = st.ready()
-    _same_device(st.sq.device, pos=pos, path=path, n_path=n_path, k=k, tree_m=tree_m, tree_g=tree_g)
-    _launch("lq_tree_commit", st.sq.device, stream, ct.byref(d), ct.byref(cs), _ptr(pos), N, _ptr(path), P,
-            _ptr(n_path), _ptr(k), _ptr(tree_m), _ptr(tree_g))
+    dev = st.sq.device
+    f32, i32 = torch.float32, torch.int32
+    _check_all(dev, io_torch_dtype(d), ("pos", pos, (d.B,), i32), ("path", path, (d.B, P), i32),
+               ("n_path", n_path, (d.B,), i32), ("k", k, (N, d.B, d.H, d.dk), None),
+               ("tree_m", tree_m, (d.B, d.H, N, d.dv), f32), ("tree_g", tree_g, (d.B, d.H, N, gd), f32))
+    _launch("lq_tree_commit", dev, stream, ct.byref(d), ct.byref(cs), pos.data_ptr(), N, path.data_ptr(), P,
+            n_path.data_ptr(), k.data_ptr(), tree_m.data_ptr(), tree_g.data_ptr())
 
 
 def lq_checkpoint_bytes(d: lq_dims) -> int:
