@@ -331,8 +331,10 @@ enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
  *          `stream` is done: calls that may run at the same time need their own.
  * T = 0 (or a row with no tokens) copies h0 to h.  T = 1 is the recurrent
  * form over an fp32 state.  With bf16 tokens, products that reach h keep
- * fp32's 24 bits, those that reach only o at least 16.  A non-finite v reaches
- * its own column from its own token on.
+ * fp32's 24 bits, those that reach only o at least 16 (2^-16 of a sum of
+ * absolute values, under the output's own rounding).  A non-finite v reaches
+ * its own column from its own token on.  The result does not depend on
+ * earlier calls, on the workspace's content or on other rows.
  * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30; LQ_ERR_DIMS
  * for a bad alpha_kind; LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
@@ -390,7 +392,9 @@ int lq_la_decode_step_ragged(const lq_dims *d, const lq_state *st, const int32_t
  *   tree_m  fp32 [B,H,N,dv], tree_g fp32 [B,H,N,gd], out: the window slots
  *           that the nodes would become (lq_tree_commit).
  * Nodes' depth is not bounded by the window; committed paths are.  A
- * non-finite node reaches itself and its descendants only.
+ * non-finite node reaches itself and its descendants only.  For
+ * lq_la_tree_step with bf16 tokens the products with the state and the
+ * window, which reach only o, keep 16 bits.
  */
 int lq_gdn_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
                      const int32_t *parent, const void *q, const void *k, const void *v,
@@ -434,7 +438,8 @@ const char *lq_status_str(int status);
 /* hipError_t of the last LQ_ERR_HIP returned on the calling thread (0 if none). */
 int lq_last_hip_error(void);
 
-/* LQ_OK if every entry point accepts the shape d (same checks they run). */
+/* LQ_OK if every entry point accepts the shape d (same checks they run; the
+ * lq_la_* calls besides need decay_mode LQ_DECAY_SCALAR). */
 int lq_check_dims(const lq_dims *d);
 
 /*

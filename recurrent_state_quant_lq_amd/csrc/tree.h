@@ -822,7 +822,10 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             }
         }
     }
-    if (__syncthreads_or(odd)) tree_simple<D, RULE, TI, NT>(a, pos, sp.f.t.mask, sp.f.t.par, here, sp.f.s);
+    if (__syncthreads_or(odd)) {
+        all_loads_barrier();                               // (this pass's stores are done: the rows are written again)
+        tree_simple<D, RULE, TI, NT>(a, pos, sp.f.t.mask, sp.f.t.par, here, sp.f.s);
+    }
 }
 
 template <int D, int RULE, typename TI>

@@ -84,7 +84,7 @@ def check_prefill(o, h, q, k, v, alpha, h0, io, lens=None, what=""):
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [16, 64, 128])
-@pytest.mark.parametrize("T", [1, 2, 7, 15, 16, 17, 33, 63, 64, 65, 130])
+@pytest.mark.parametrize("T", [1, 2, 4, 5, 7, 15, 16, 17, 31, 32, 33, 63, 64, 65, 130])
 def test_prefill_lengths(T, d, io):
     c = prefill_case(T * 100 + d, 2, 3, d, T, io, heads=T % 2 == 0, start=T % 3 != 0)
     o, h = run_prefill(*c, io)
@@ -100,14 +100,25 @@ def test_prefill_long_prompts_of_few_heads(B, H, d, T, io):
     check_prefill(o, h, *c, io)
 
 
-def test_prefill_many_heads():
-    c = prefill_case(5, 40, 33, 128, 40, "bf16", heads=True, start=False)
-    o, h = run_prefill(*c, "bf16")
-    check_prefill(o, h, *c, "bf16")
+@pytest.mark.parametrize("B,H,d,T,io", [(40, 33, 128, 40, "bf16"), (10, 13, 128, 200, "f32"), (13, 10, 128, 300, "bf16"),
+                                        (129, 1, 64, 150, "f32"), (64, 2, 64, 150, "bf16"), (150, 30, 16, 40, "bf16")])
+def test_prefill_many_heads(B, H, d, T, io):
+    c = prefill_case(5, B, H, d, T, io, heads=True, start=False)
+    o, h = run_prefill(*c, io)
+    check_prefill(o, h, *c, io)
+
+
+@pytest.mark.parametrize("T", [3, 40, 1300])
+def test_prefill_rows_without_tokens_and_without_a_start(T):
+    """A row of length 0 from zeros ends with zeros; its o rows stay."""
+    c = prefill_case(T, 2, 2, 128, T, "bf16", start=False)
+    o, h = run_prefill(*c, "bf16", lens=[0, T])
+    check_prefill(o, h, *c, "bf16", lens=[0, T])
+    assert float(h[0].abs().max()) == 0.0
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
-@pytest.mark.parametrize("d,T", [(128, 70), (64, 70), (16, 70), (128, 1400), (128, 3)])
+@pytest.mark.parametrize("d,T", [(128, 70), (64, 70), (16, 70), (128, 1400), (64, 1400), (16, 1400), (128, 3)])
 def test_prefill_padded_rows(d, T, io):
     """Tokens past a row's length may hold NaN; their o rows stay; rows without tokens keep h0."""
     q, k, v, alpha, h0 = prefill_case(7 * d + T, 7, 2, d, T, io)
@@ -418,6 +429,52 @@ def test_tree_nonfinite_nodes_reach_their_descendants_only(rule, d):
             near(tm[0, 1, n], rm[0, 1, n], em[0, 1, n], f"m {n}")
         elif rule != "la":
             assert torch.isnan(o[n, 0, 1]).all()
+
+
+@pytest.mark.parametrize("d", [128, 64, 16])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_tree_linear_forget(d, io):
+    """alpha = 0 at a node: it and its descendants see nothing before it; strong decays do not overflow."""
+    N, W, pos = 36, 16, [5, 16]
+    dims, st, hb, bk, bm, bg = make_state(d + 1, 2, 2, d, W, 4, io, slots=pos)
+    q, k, v, alpha, _ = tokens(d + 2, (N, 2, 2), d, io)
+    parent = [[SHAPES["two chains"](n) for n in range(N)], [SHAPES["mixed"](n) for n in range(N)]]
+    alpha[6, 0], alpha[13, 0], alpha[20:24, 1] = 0.0, 0.0, 0.0
+    alpha[9, 0, 0], alpha[3, 1] = 1e-38, 1e-30
+    got = run_tree(st, pos, parent, q, k, v, alpha, None)
+    o, tm, tg = (x.cpu() for x in got)
+    ro, rm, rg, eo, em, here = R.tree(hb, bk, bm, bg, pos, parent, q, k, v, alpha)
+    near(o, ro, eo, "o", q.dtype)
+    assert torch.equal(tm, v.float().permute(1, 2, 0, 3))
+    near(tg, rg, 100 * 2.0 ** -23 * (rg.abs() + 0.05), "tree_g")
+
+
+def test_tree_in_a_graph_with_other_trees():
+    """A captured tree step replayed with other positions, parents and path lengths (all on the device)."""
+    d, W, B, H, N = 128, 16, 3, 2, 33
+    dims, st, hb, bk, bm, bg = make_state(40, B, H, d, W, 4, "bf16")
+    q, k, v, alpha, beta = tokens(41, (N, B, H), d, "bf16")
+    dev = [x.cuda() for x in (q, k, v, alpha, beta)]
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    full = lambda *s, dt=torch.float32: torch.full(s, MARK, dtype=dt, device="cuda")
+    o, tm, tg = full(N, B, H, d, dt=torch.bfloat16), full(B, H, N, d), full(B, H, N, 1)
+    pos, parent = i32([0] * B), i32([[-1] * N] * B)
+    call = lambda: lq.lq_gdn_tree_step(st, pos, parent, *dev, o, tm, tg)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for new_pos, shape in (([16, 0, 7], "chain"), ([1, 17, 15], "mixed"), ([-1, 3, 16], "binary")):
+        par = [[SHAPES[shape](n) for n in range(N)] for _ in range(B)]
+        par[1][4] = -3
+        pos.copy_(i32(new_pos)), parent.copy_(i32(par))
+        for x in (o, tm, tg):
+            x.fill_(MARK)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        check_tree((o, tm, tg), hb, bk, bm, bg, new_pos, par, q, k, v, alpha, beta)
 
 
 @pytest.mark.parametrize("rule,io", [("gdn", "f32"), ("gdn", "bf16"), ("kda", "f32"), ("la", "bf16")])
