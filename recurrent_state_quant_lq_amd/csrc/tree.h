@@ -764,13 +764,16 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
                     for (int v = 0; v < 4; ++v) R[ct][v] = be[v] * (vv[e][v][ct] - acc[e][NX - 1][ct][v]);
                 context(1, R);
-                // M = (I + A)^{-1} R, four rows at a time: lane group p solves its rows, then the
-                // matrix instruction takes them (column 4 p + v of -A, rows below) to the others
+                // M = (I + A)^{-1} R, four rows at a time: lane group p solves its rows; row swaps bring
+                // its row 4 p + i to lane group i, the B operand of one k = 4 step with -A's columns
+                // 4 p .. 4 p + 3 (rows below them)
                 const float* ab = &s.s[1][16 * e * SS + WC + 16 * j];
-                const v4f below = *reinterpret_cast<const v4f*>(ab + li * SS + 4 * lg);   // -A[li][4 lg + v]
                 v4f own[3];                                                               // -A[4 lg + 1 + i][4 lg + v]
 #pragma unroll
                 for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(ab + (4 * lg + 1 + i) * SS + 4 * lg);
+                float below[3];                                                           // -A[li][4 p + lg]
+#pragma unroll
+                for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? ab[li * SS + 4 * p + lg] : 0.0f;
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
                     if (lg == p)
@@ -780,18 +783,13 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                             R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
                             R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
                         }
-                    if (p < 3) {
-                        const bool on = lg == p && (li >> 2) > p;
-                        v4f y[2] = {R[0], R[1]};
+                    if (p < 3)
 #pragma unroll
-                        for (int v = 0; v < 4; ++v) {
-                            const float x = on ? below[v] : 0.0f;
-                            y[0] = mfma4(x, R[0][v], y[0]);
-                            y[1] = mfma4(x, R[1][v], y[1]);
+                        for (int ct = 0; ct < 2; ++ct) {
+                            const bool on = lg == p;
+                            const float x = rows_sum4(on ? R[ct][0] : 0.0f, on ? R[ct][1] : 0.0f, on ? R[ct][2] : 0.0f, on ? R[ct][3] : 0.0f);
+                            R[ct] = mfma4(below[p], x, R[ct]);
                         }
-                        R[0] = y[0];
-                        R[1] = y[1];
-                    }
                 }
                 M[j][0] = R[0];
                 M[j][1] = R[1];
