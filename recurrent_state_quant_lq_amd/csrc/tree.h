@@ -252,7 +252,12 @@ struct TM {
     static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
     static constexpr int QS = D + 8;                               // shorts per row
     static constexpr int WC = 16 * WT;                             // window columns of the scores
-    static constexpr int SS = WC + 16 * NB + 4;                    // floats per score row
+    // plain linear attention, bf16: m = v is exact in bf16, so the nodes' scores are kept in two
+    // bf16 parts (off by 2^-16 of themselves, against the 2^-8 of the output) and meet the values
+    // of two blocks in one bf16 matrix instruction a part
+    static constexpr bool VB = !DELTA && sizeof(TI) == 2;
+    static constexpr int SS = WC + (VB ? 0 : 16 * NB) + 4;         // floats per score row
+    static constexpr int SB = VB ? 16 * NB + 8 : 8;                // shorts per row of the nodes' scores in parts
     struct Shared {
         TreeTables t;
         __align__(16) float g[kTreeMax];                           // scalar decay: g_n (absent nodes: that of slot pos - 1)
@@ -263,7 +268,8 @@ struct TM {
         __align__(16) uint16_t q[NP][16 * GB * QS];
         __align__(16) uint16_t k[NP][16 * KB * QS];
         __align__(16) uint16_t wk[NS][WC * QS];
-        __align__(16) float s[2][16 * GB * SS];                    // scores of q; -beta times those of k
+        __align__(16) float s[DELTA ? 2 : 1][16 * GB * SS];        // scores of q; -beta times those of k
+        __align__(16) uint16_t sb[2][VB ? 16 * GB * SB : 8];
         __align__(16) float gk[KDA ? 16 * NB * D : 4];             // per-key decay: g_n
         __align__(16) float gp[KDA ? D : 4];                       // per-key decay: g of slot pos - 1
         __align__(16) TI kr[RK ? 16 * NB * D : 8];                 // per-key decay: the nodes' keys as they are
@@ -275,9 +281,10 @@ struct TM {
             TreeSimple<D> s;
         } f;
     };
-    // waves per SIMD the registers are sized for: the workgroups that fit the LDS of a CU, 3 at most
+    // waves per SIMD the registers are sized for: the workgroups that fit the LDS of a CU, 3 at
+    // most (2 with 64 nodes, whose registers would spill: 92 us instead of 68, plain rule)
     static constexpr int FIT = 160 * 1024 / (int)sizeof(Space) * NW / 4;
-    static constexpr int WPE = FIT >= 3 ? 3 : FIT >= 2 ? 2 : 1;
+    static constexpr int WPE = FIT >= 3 && NB == 2 ? 3 : FIT >= 2 ? 2 : 1;
 };
 
 // c += a b with a in NP parts, b in NQ parts; small products first.
@@ -322,7 +329,8 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     using X = TM<D, NB, WT, RULE, TI>;
     constexpr int NW = X::NW, NT = X::NT, NP = X::NP, GB = X::GB, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
     constexpr bool KDA = X::KDA, DELTA = X::DELTA;
-    constexpr int NS = X::NS;
+    constexpr int NS = X::NS, SB = X::SB;
+    constexpr bool VB = X::VB;
     constexpr int NX = DELTA ? 2 : 1, GD = KDA ? D : 1, KS = D / 64, NG = NB / GB;
     __shared__ typename X::Space sp;
     auto& s = sp.m;
@@ -517,7 +525,8 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         cb[u] = 4 * u + lg < C ? cb[u] : f32x2{0.0f, 0.0f};
     }
 
-    v4f M[NB][2];
+    v4f M[VB ? 1 : NB][2];
+    u32x2 V[VB ? NB : 1][2];                               // VB: values of the blocks, nodes 4 lg .. + 3, as bf16
     bool odd = false;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -615,7 +624,14 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                         const uint64_t anc = s.t.mask[n0 + v];
                         const float y = acc[v] * __expf(gn[v] - gc) * bn[v];
                         // (the diagonal of the q scores: <q_n, k_n>; its exponential is 1)
-                        dst[v * SS + WC + 16 * (c - wt)] = ((anc >> i) & 1u) || (!x && i == n0 + v) ? y : 0.0f;
+                        const float z = ((anc >> i) & 1u) || (!x && i == n0 + v) ? y : 0.0f;
+                        if constexpr (VB) {
+                            const int to = (16 * e + 4 * lg + v) * SB + i;
+                            s.sb[0][to] = (uint16_t)(__float_as_uint(z) >> 16);
+                            s.sb[1][to] = (uint16_t)(pack_bf16(z - top_f32(z), 0.0f) & 0xffffu);
+                        } else {
+                            dst[v * SS + WC + 16 * (c - wt)] = z;
+                        }
                     }
                 }
             }
@@ -745,7 +761,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             const int j = GB * g + e;
             auto context = [&](int x, v4f (&y)[2]) {       // y += scores x context
 #pragma unroll
-                for (int c = 0; c < WT + NB; ++c) {
+                for (int c = 0; c < WT + (VB ? 0 : NB); ++c) {
                     if (c < WT ? c > 0 && c >= wt : c - WT >= j) continue;
                     const int cc = c < WT ? 16 * c : WC + 16 * (c - WT);
                     const v4f sr = *reinterpret_cast<const v4f*>(&s.s[x][(16 * e + li) * SS + cc + 4 * lg]);
@@ -753,7 +769,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                     for (int v = 0; v < 4; ++v)
 #pragma unroll
                         for (int ct = 0; ct < 2; ++ct)
-                            y[ct] = mfma4(sr[v], c < WT ? WM[c < WT ? c : 0][ct][v] : M[c < WT ? 0 : c - WT][ct][v], y[ct]);
+                            y[ct] = mfma4(sr[v], c < WT ? WM[c < WT ? c : 0][ct][v] : M[c < WT || VB ? 0 : c - WT][ct][v], y[ct]);
                 }
             };
             if constexpr (DELTA) {
@@ -796,27 +812,51 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             } else {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    M[j][0][v] = vv[e][v][0];
-                    M[j][1][v] = vv[e][v][1];
+                    M[VB ? 0 : j][0][v] = vv[e][v][0];
+                    M[VB ? 0 : j][1][v] = vv[e][v][1];
                 }
             }
             context(0, acc[e][0]);
-            const v4f sr = *reinterpret_cast<const v4f*>(&s.s[0][(16 * e + li) * SS + WC + 16 * j + 4 * lg]);
+            if constexpr (VB) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+                for (int ct = 0; ct < 2; ++ct)
+                    V[VB ? j : 0][ct] = u32x2{top_halves(vv[e][0][ct], vv[e][1][ct]), top_halves(vv[e][2][ct], vv[e][3][ct])};
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) acc[e][0][ct] = mfma4(sr[v], M[j][ct][v], acc[e][0][ct]);
+                for (int c = 0; c <= j / 2; ++c) {         // blocks 2 c and 2 c + 1 (none past j: zeros)
+                    const bool two = 2 * c + 1 <= j;
+                    u32x4 vb[2];
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct) {
+                        const u32x2 lo = V[VB ? 2 * c : 0][ct], hi = two ? V[VB && two ? 2 * c + 1 : 0][ct] : u32x2{0, 0};
+                        vb[ct] = u32x4{lo[0], lo[1], hi[0], hi[1]};
+                    }
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        const uint16_t* sr = &s.sb[part][(16 * e + li) * SB + 32 * c + 4 * lg];
+                        const u32x2 lo = *reinterpret_cast<const u32x2*>(sr), hi = two ? *reinterpret_cast<const u32x2*>(sr + 16) : u32x2{0, 0};
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct) acc[e][0][ct] = mfma_bf16(u32x4{lo[0], lo[1], hi[0], hi[1]}, vb[ct], acc[e][0][ct]);
+                    }
+                }
+            } else {
+                const v4f sr = *reinterpret_cast<const v4f*>(&s.s[0][(16 * e + li) * SS + WC + 16 * j + 4 * lg]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v)
+#pragma unroll
+                    for (int ct = 0; ct < 2; ++ct) acc[e][0][ct] = mfma4(sr[v], M[VB ? 0 : j][ct][v], acc[e][0][ct]);
+            }
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const int n = 16 * j + 4 * lg + v;
-                odd |= !finite_f32(M[j][0][v]) || !finite_f32(M[j][1][v]);
+                const f32x2 m = {M[VB ? 0 : j][0][v], M[VB ? 0 : j][1][v]};
+                odd |= !finite_f32(m[0]) || !finite_f32(m[1]);
                 if (!((here >> n) & 1u)) continue;
                 const size_t at = ((size_t)n * heads + head) * D + col;
                 if constexpr (sizeof(TI) == 4)
                     __builtin_nontemporal_store(f32x2{acc[e][0][0][v], acc[e][0][1][v]}, reinterpret_cast<f32x2*>(static_cast<float*>(a.o) + at));
                 else
                     st_nt(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + at), pack_bf16(acc[e][0][0][v], acc[e][0][1][v]));
-                __builtin_nontemporal_store(f32x2{M[j][0][v], M[j][1][v]}, reinterpret_cast<f32x2*>(a.tm + (head * N + n) * (size_t)D + col));
+                __builtin_nontemporal_store(m, reinterpret_cast<f32x2*>(a.tm + (head * N + n) * (size_t)D + col));
             }
         }
     }
