@@ -245,7 +245,7 @@ struct TM {
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
     // parts of the window's keys and of the state: three (24 bits); two (16 bits and a rounding,
-    // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-9
+    // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-8
     static constexpr int NS = !DELTA && sizeof(TI) == 2 ? 2 : 3;
     static constexpr int GB = NP == 1 ? 2 : 1;                     // blocks per group
     static constexpr int KB = KDA ? GB : NB;                       // blocks whose keys stay in LDS
