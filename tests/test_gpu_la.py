@@ -169,6 +169,24 @@ def test_prefill_nonfinite_values_reach_their_column_from_their_token(d, T, io):
     near(h[ok_h], rh[ok_h], (c * ha)[ok_h], "h")
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,T", [(128, 50), (64, 50), (16, 50), (128, 1200), (16, 1200), (128, 4)])
+def test_prefill_nonfinite_queries_and_keys_reach_nothing_before_them(d, T, io):
+    """A query's reaches its own output only; a key's reaches the outputs from its token on."""
+    q, k, v, alpha, h0 = prefill_case(3 * T + d, 1, 3, d, T, io)
+    at = min(T - 2, 37 if T < 100 else 1001)
+    bad_q, bad_k = q.clone(), k.clone()
+    bad_q[at, 0, 0, 3], bad_q[at, 0, 1, 2] = float("inf"), float("nan")
+    bad_k[at, 0, 2, 5] = float("nan")
+    o, h = run_prefill(bad_q, bad_k, v, alpha, h0, io)
+    assert not torch.isfinite(o[at, 0, :2]).any() and torch.isnan(o[at:, 0, 2]).all() and torch.isnan(h[0, 2, 5]).all()
+    o2, h2 = run_prefill(q, k, v, alpha, h0, io)
+    check_prefill(o2, h2, q, k, v, alpha, h0, io)
+    fine = torch.ones(T, 1, 3, dtype=torch.bool, device="cuda")
+    fine[at, 0, :2], fine[at:, 0, 2] = False, False
+    assert torch.equal(o[fine], o2[fine]) and torch.equal(h[0, :2], h2[0, :2])
+
+
 @pytest.mark.parametrize("T", [0, 1, 70, 1100])
 def test_prefill_in_place_without_outputs_and_codec(T):
     """h may be h0; o may be left out; the codec written is that of the h written; T = 0 copies h0."""
@@ -446,6 +464,26 @@ def test_tree_linear_forget(d, io):
     ro, rm, rg, eo, em, here = R.tree(hb, bk, bm, bg, pos, parent, q, k, v, alpha)
     near(o, ro, eo, "o", q.dtype)
     assert torch.equal(tm, v.float().permute(1, 2, 0, 3))
+    near(tg, rg, 100 * 2.0 ** -23 * (rg.abs() + 0.05), "tree_g")
+
+
+@pytest.mark.parametrize("rule", ["gdn", "kda"])
+@pytest.mark.parametrize("d,io", [(128, "f32"), (128, "bf16"), (64, "f32"), (16, "f32")])
+def test_tree_strong_decays(rule, d, io):
+    """Decays down to e^-12 a token: exponentials between nodes that are not on one path do not reach a result."""
+    N, W, pos = 64, 16, [0, 7, 16]
+    per_key = rule == "kda"
+    dims, st, hb, bk, bm, bg = make_state(d + 3, 3, 2, d, W, 4, io, per_key, slots=pos)
+    q, k, v, alpha, beta = tokens(d + 4, (N, 3, 2), d, io, per_key)
+    alpha = torch.exp(-12 * ((alpha - 0.3) / 0.7) ** 4)
+    parent = [[SHAPES[x](n) for n in range(N)] for x in ("chain", "mixed", "star")]
+    o, tm, tg = (x.cpu() for x in run_tree(st, pos, parent, q, k, v, alpha, beta))
+    ro, rm, rg, eo, em, here = R.tree(hb, bk, bm, bg, pos, parent, q, k, v, alpha, beta)
+    # log decays are sums in fp32: at most 8 roundings of |g| on either side of a difference, each a
+    # relative error of its exponential, on top of the bounds' c per term
+    more = 1 + 16 * float(rg.abs().max()) * R.U / R.c_of(d)
+    near(o, ro, more * eo, "o", q.dtype)
+    near(tm, rm, more * em, "tree_m")
     near(tg, rg, 100 * 2.0 ** -23 * (rg.abs() + 0.05), "tree_g")
 
 
