@@ -480,9 +480,9 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         // g of every node, channels col and col + 1: the path sums of log alpha as the product of the
         // 0/1 matrix of paths (exact in bf16) and the logarithms in three parts, plus g of slot pos - 1
         const f32x2 g0 = *reinterpret_cast<const f32x2*>(&s.gp[col]);
+        u32x4 lp[2][NB / 2][3];
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            u32x4 lp[NB / 2][3];
+        for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
             for (int g = 0; g < NB / 2; ++g) {
                 float x[8];
@@ -491,29 +491,30 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 for (int u = 0; u < 8; ++u) x[u] = (here >> (32 * g + 8 * lg + u)) & 1u ? logf(na[g][u][ct]) : 0.0f;
                 split3<8>(x, p);
 #pragma unroll
-                for (int m = 0; m < 3; ++m) lp[g][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                for (int m = 0; m < 3; ++m) lp[ct][g][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                if (16 * j >= N) break;
-                const int n = 16 * j + li;
-                const uint64_t path = s.t.mask[n] | (1ull << n);
-                v4f y = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NB; ++j) {
+            if (16 * j >= N) break;
+            const int n = 16 * j + li;
+            const uint64_t path = s.t.mask[n] | (1ull << n);
+            v4f y[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-                for (int g = 0; g <= j / 2; ++g) {
-                    u32x4 ar[1];
-                    const uint32_t bits = (uint32_t)(path >> (32 * g)) >> (8 * lg);
+            for (int g = 0; g <= j / 2; ++g) {
+                u32x4 ar[1];
+                const uint32_t bits = (uint32_t)(path >> (32 * g)) >> (8 * lg);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        ar[0][u] = ((bits >> (2 * u)) & 1u ? 0x3f80u : 0u) | ((bits >> (2 * u + 1)) & 1u ? 0x3f800000u : 0u);
-                    y = mfma_parts<1, 3>(ar, lp[g], y);
-                }
+                for (int u = 0; u < 4; ++u)
+                    ar[0][u] = ((bits >> (2 * u)) & 1u ? 0x3f80u : 0u) | ((bits >> (2 * u + 1)) & 1u ? 0x3f800000u : 0u);
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int m = 16 * j + 4 * lg + v;
-                    s.gk[m * D + col + ct] = y[v] + g0[ct];
-                    if ((here >> m) & 1u) a.tg[(head * N + m) * D + col + ct] = y[v] + g0[ct];
-                }
+                for (int ct = 0; ct < 2; ++ct) y[ct] = mfma_parts<1, 3>(ar, lp[ct][g], y[ct]);
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int m = 16 * j + 4 * lg + v;
+                const f32x2 x = f32x2{y[0][v], y[1][v]} + g0;
+                *reinterpret_cast<f32x2*>(&s.gk[m * D + col]) = x;
+                if ((here >> m) & 1u) *reinterpret_cast<f32x2*>(a.tg + (head * N + m) * (size_t)D + col) = x;
             }
         }
         __syncthreads();
@@ -574,6 +575,18 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         }
         __syncthreads();
         // ---- 2. scores: tile (x, e, c) = rows of block e, context tile c (window tiles, then node blocks) ----
+        // per-key decay, node pairs: 16 lanes a row (lane li: channels 4 li .. + 3 and 64 + 4 li .. + 3), the
+        // row's q on its way meanwhile
+        constexpr int CH = D / 16, PP = 16 / (4 * NW);       // passes over the group's rows
+        static_assert(!KDA || GB == 1, "one block of rows");
+        TI qraw[PP][KDA ? CH : 1];
+        if constexpr (KDA)
+#pragma unroll
+            for (int p = 0; p < PP; ++p) {
+                const size_t at = ((size_t)min(16 * g + w + NW * (lg + 4 * p), N - 1) * heads + head) * D + 4 * li;
+#pragma unroll
+                for (int u = 0; u < CH; ++u) qraw[p][u] = static_cast<const TI*>(a.q)[at + 64 * (u / 4) + u % 4];
+            }
         {
             const int nt0 = wt + (KDA ? 0 : GB * g + 1), per = nb == 1 ? nt0 : 2 * nt0 + (KDA ? 0 : 1);   // tiles of block 0, of the group
 #pragma unroll 1
@@ -636,53 +649,54 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 }
             }
             if constexpr (KDA) {
-                // node pairs, a row per wave at a time, four ancestors at once (16 lanes each)
-                constexpr int CH = D / 16;
-                for (int r = w; r < 16 * nb; r += NW) {
-                    const int n = 16 * GB * g + r;
-                    for (int c = lane; c < 16 * (GB * g + nb); c += 64) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
-                    if (!((here >> n) & 1u)) continue;
-                    const size_t at = ((size_t)n * heads + head) * D + CH * li;
-                    float qn[CH], kn[CH], gn[CH];
+                // the row's ancestors two at a time
 #pragma unroll
-                    for (int u = 0; u < CH; ++u) {
-                        qn[u] = tok_ld<TI>(a.q, at + u);
-                        kn[u] = X::RK ? widen(s.kr[X::RK ? n * D + CH * li + u : 0]) : tok_ld<TI>(a.k, at + u);
-                    }
-                    load_floats<CH>(&s.gk[n * D + CH * li], gn);
-                    const float nbt = -s.beta[n];
-                    uint64_t left = s.t.mask[n] | (1ull << n);
-                    left = ((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(left >> 32)) << 32) |
-                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)left);
-                    while (left) {
-                        int i = -1;
+                for (int p = 0; p < PP; ++p) {
+                    const int r = w + NW * (lg + 4 * p), n = 16 * GB * g + r;
+                    for (int c = li; c < 16 * (GB * g + nb); c += 16) s.s[0][r * SS + WC + c] = s.s[1][r * SS + WC + c] = 0.0f;
+                    auto key = [&](int i, float (&y)[CH]) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            if (left) {
-                                const int f = __builtin_ctzll(left);
-                                left &= left - 1;
-                                if (lg == u) i = f;
-                            }
+                        for (int u = 0; u < CH; ++u) {
+                            const int ch = 64 * (u / 4) + 4 * li + u % 4;
+                            y[u] = X::RK ? widen(s.kr[X::RK ? i * D + ch : 0]) : tok_ld<TI>(a.k, ((size_t)min(i, N - 1) * heads + head) * D + ch);
                         }
-                        float xq = 0.0f, xk2 = 0.0f;
-                        if (i >= 0) {
-                            float gi[CH];
-                            load_floats<CH>(&s.gk[i * D + CH * li], gi);
+                    };
+                    auto decay = [&](int i, float (&y)[CH]) {
+#pragma unroll
+                        for (int u = 0; u < CH; ++u) y[u] = s.gk[i * D + 64 * (u / 4) + 4 * li + u % 4];
+                    };
+                    float kn[CH], gn[CH];
+                    key(n, kn);
+                    decay(n, gn);
+                    const float nbt = -s.beta[n];
+                    uint64_t left = (here >> n) & 1u ? s.t.mask[n] | (1ull << n) : 0;
+                    while (__any(left != 0)) {
+                        int i[2];
+                        float ki[2][CH], gi[2][CH], xq[2] = {0.0f, 0.0f}, xk[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            i[h] = left ? __builtin_ctzll(left) : -1;
+                            left &= left - 1;
+                            key(max(i[h], 0), ki[h]);      // (none left: node 0's, unused)
+                            decay(max(i[h], 0), gi[h]);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
 #pragma unroll
                             for (int u = 0; u < CH; ++u) {
-                                float ki = X::RK ? widen(s.kr[X::RK ? i * D + CH * li + u : 0])
-                                                 : tok_ld<TI>(a.k, ((size_t)i * heads + head) * D + CH * li + u);
-                                if (i != n) ki *= __expf(gn[u] - gi[u]);
-                                xq += qn[u] * ki;
-                                xk2 += kn[u] * ki;
+                                const float y = i[h] == n ? ki[h][u] : ki[h][u] * __expf(gn[u] - gi[h][u]);
+                                xq[h] += widen(qraw[p][u]) * y;
+                                xk[h] += kn[u] * y;
                             }
+                            xq[h] = group_sum<16>(xq[h]);
+                            xk[h] = group_sum<16>(xk[h]);
                         }
-                        xq = group_sum<16>(xq);
-                        xk2 = group_sum<16>(xk2);
-                        if (li == 0 && i >= 0) {
-                            s.s[0][r * SS + WC + i] = xq;
-                            if (i != n) s.s[1][r * SS + WC + i] = nbt * xk2;
-                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (li == 0 && i[h] >= 0) {
+                                s.s[0][r * SS + WC + i[h]] = xq[h];
+                                if (i[h] != n) s.s[1][r * SS + WC + i[h]] = nbt * xk[h];
+                            }
                     }
                 }
             }
