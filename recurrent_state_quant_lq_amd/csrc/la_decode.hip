@@ -12,7 +12,7 @@
 // state and scales at once, the window as soon as pos is known), and a workgroup holds
 // few registers and little LDS, so that ten of them share a CU.  The products with the
 // state run on the vector unit: a lane's column times the query in LDS (broadcast reads).
-#include "lq_internal.h"
+#include "la.h"
 
 namespace lq {
 namespace {

@@ -17,7 +17,7 @@
 // order, so no value of H or V moves between lanes.  Where the heads alone leave most of
 // the GPU idle, a prompt is cut into segments: their states alone, a scan over the
 // segments, then their outputs from the states before them.
-#include "lq_internal.h"
+#include "la.h"
 #include "lq_split.h"
 
 namespace lq {

@@ -1,5 +1,6 @@
 // lq_api.hip -- the C ABI of liblq.so: argument checks, dispatch, status.
 // Every check runs before any HIP call; on an error nothing is enqueued.
+#include "la.h"
 #include "lq_internal.h"
 
 #include <atomic>

@@ -10,7 +10,7 @@
 // once for all N nodes.
 #pragma once
 
-#include "lq_internal.h"
+#include "la.h"
 #include "lq_split.h"
 
 namespace lq {
