@@ -53,23 +53,25 @@ namespace {
 // entry on the way up is valid.  A node is present if its own entry and all its
 // ancestors' are; no index depends on an unchecked value.  sum: of x over the path
 // (the node included), by pointer doubling.
+template <typename F>
 struct TreeNode {
     uint64_t mask;
-    float sum;
+    F sum;
     int parent;               // -1: the last committed token
     bool here;
 };
-__device__ __forceinline__ TreeNode tree_node(int p, int lane, float x) {
+template <typename F>
+__device__ __forceinline__ TreeNode<F> tree_node(int p, int lane, F x) {
     const bool own = p == -1 || (p >= 0 && p < lane);
     int jump = own ? p : -1;
-    TreeNode t;
+    TreeNode<F> t;
     t.parent = jump;
     t.mask = jump >= 0 ? 1ull << jump : 0;
     t.sum = x;
     while (__any(jump >= 0)) {                             // paths of doubling length: at most 6 rounds for 64 nodes
         const int from = jump >= 0 ? jump : lane;
         const uint64_t m = __shfl(t.mask, from, 64);
-        const float y = __shfl(t.sum, from, 64);
+        const F y = __shfl(t.sum, from, 64);
         const int j = __shfl(jump, from, 64);
         if (jump >= 0) {
             t.mask |= m;
@@ -83,7 +85,7 @@ __device__ __forceinline__ TreeNode tree_node(int p, int lane, float x) {
 }
 
 // ---------------------------------------------------------------------------
-// node after node: d = 16, and rows that hold a value that is not finite
+// node after node: rows that hold a value that is not finite
 // ---------------------------------------------------------------------------
 // Lane j = channel j = value column j.  Sums run over a node's own context only, so
 // a value that is not finite reaches its descendants and nothing else.
@@ -193,26 +195,6 @@ struct TreeTables {
     int8_t par[kTreeMax];
     uint64_t here;
 };
-
-template <int D, int RULE, typename TI>
-__global__ __launch_bounds__(64) void tree_kernel(TreeArgs a) {
-    constexpr int NT = 64;
-    static_assert(D <= NT, "a lane per channel");
-    __shared__ TreeTables s_t;
-    __shared__ TreeSimple<D> s_s;
-    const unsigned b = blockIdx.x / (unsigned)a.H;
-    const int pos = a.pos[b];
-    if (pos < 0 || pos > a.W) return;                      // a row outside its window: untouched
-    if (threadIdx.x < 64) {
-        const TreeNode nd = tree_node((int)threadIdx.x < a.N ? a.parent[(size_t)b * a.N + threadIdx.x] : -2, threadIdx.x, 0.0f);
-        s_t.mask[threadIdx.x] = nd.mask;
-        s_t.par[threadIdx.x] = (int8_t)nd.parent;
-        const uint64_t here = __ballot(nd.here);
-        if (threadIdx.x == 0) s_t.here = here;
-    }
-    __syncthreads();
-    tree_simple<D, RULE, TI, NT>(a, pos, s_t.mask, s_t.par, s_t.here, s_s);
-}
 
 // ---------------------------------------------------------------------------
 // d >= 64: blocks of 16 nodes on matrix products
@@ -324,6 +306,309 @@ __device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
 
 __device__ __forceinline__ v4f mfma4(float a, float b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
+// M = (I + A)^{-1} R for a block of 16 rows and CT column tiles, A strictly lower, in place: four
+// rows at a time, lane group p solves its rows; row swaps bring its row 4 p + i to lane group i, the
+// B operand of one k = 4 step with -A's columns 4 p .. 4 p + 3 (rows below them).
+// own[i] = -A[4 lg + 1 + i][4 lg ..], below[p] = -A[li][4 p + lg].
+template <int CT>
+__device__ __forceinline__ void block_solve(const v4f (&own)[3], const float (&below)[3], int lg, v4f (&R)[CT]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        if (lg == p)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                R[ct][1] += own[0][0] * R[ct][0];
+                R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
+                R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
+            }
+        if (p < 3)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const bool on = lg == p;
+                const float x = rows_sum4(on ? R[ct][0] : 0.0f, on ? R[ct][1] : 0.0f, on ? R[ct][2] : 0.0f, on ? R[ct][3] : 0.0f);
+                R[ct] = mfma4(below[p], x, R[ct]);
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// d = 16: one wave a head
+// ---------------------------------------------------------------------------
+// Every product is one 16 x 16 x 16 of the fp32 matrix instruction, its operands loaded in the
+// layout that the instruction takes (lane (lg, li), step v: row or column li, index 4 lg + v).
+// The scores are formed transposed (K Q^T), so that their accumulators are the A operand of S M,
+// and M's are its B operand: only A's diagonal block goes through LDS.  Per-key decay forms the
+// scores of node pairs channel by channel (lane: one node, four ancestors), as the larger kernel
+// does.  Bound by the latency of a wave's phases.
+template <int RULE>
+struct TreeSmall {
+    static constexpr int ND = RULE == TREE_KDA ? 20 * kTreeMax : 4;   // rows of 20 floats (bank spread)
+    __align__(16) float g[ND];                             // per-key decay: g_n
+    __align__(16) float k[ND];                             // per-key decay: the nodes' keys
+    __align__(16) float q[RULE == TREE_KDA ? 20 * 16 : 4]; // per-key decay: the block's queries
+    __align__(16) float a[20 * 16];                        // -A of the block
+};
+
+template <int NB, int RULE, typename TI>
+__global__ __launch_bounds__(64) void tree_small_kernel(TreeArgs a) {
+    constexpr int D = 16, LR = 20;
+    constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
+    __shared__ TreeTables s_t;
+    __shared__ union {
+        TreeSmall<RULE> m;
+        TreeSimple<D> f;
+    } sp;
+    auto& s = sp.m;
+    const int lane = threadIdx.x, li = lane & 15, lg = lane >> 4;
+    const size_t head = blockIdx.x, heads = (size_t)a.heads;
+    const int W = a.W, C = a.C, N = a.N;
+    const unsigned b = blockIdx.x / (unsigned)a.H;
+    auto row4 = [](const void* x, size_t at, float (&y)[4]) {
+        if constexpr (sizeof(TI) == 4) {
+            load_floats<4>(static_cast<const float*>(x) + at, y);
+        } else {
+            const u32x2 z = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(x) + at);
+            y[0] = lo_f32(z[0]), y[1] = hi_f32(z[0]), y[2] = lo_f32(z[1]), y[3] = hi_f32(z[1]);
+        }
+    };
+    // ---- requests (rows past the end: the last node's, zeroed below) ----
+    const int pos = a.pos[b];
+    const int npar = lane < N ? a.parent[(size_t)b * N + lane] : -2;
+    const size_t node = (size_t)min(lane, N - 1);
+    float nal = 1.0f, nbeta = 0.0f;
+    if constexpr (!KDA) nal = a.alpha[a.alpha_tok ? node * a.alpha_tok + head : head % (unsigned)a.H];
+    if constexpr (DELTA) nbeta = a.beta[node * heads + head];
+    float q[NB][4], k[NB][4], vv[NB][4], lal[KDA ? NB : 1][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        if (16 * j >= N) break;
+        const size_t at = ((size_t)min(16 * j + li, N - 1) * heads + head) * D + 4 * lg;
+        row4(a.q, at, q[j]);
+        row4(a.k, at, k[j]);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const size_t to = ((size_t)min(16 * j + 4 * lg + v, N - 1) * heads + head) * D + li;
+            vv[j][v] = tok_ld<TI>(a.v, to);
+            if constexpr (KDA) lal[j][v] = a.alpha[to];
+        }
+    }
+    const uint32_t raw = *reinterpret_cast<const uint32_t*>(a.sq + head * (size_t)(D * D) + sq_off<D>(0, li) + 4 * lg);
+    float rs[4], hb[4];
+    load_floats<4>(a.r + head * D + 4 * lg, rs);
+    const float sj = a.s[head * D + li];
+    if (pos < 0 || pos > W) return;                        // a row outside its window: untouched
+    const int last = max(pos - 1, 0);
+    const float* bk = a.bk + head * (size_t)W * D;
+    const float* bm = a.bm + head * (size_t)W * D;
+    const float* bg = a.bg + head * (size_t)W * (KDA ? D : 1);
+    float wk[2][4], wm[2][4], wg[2][4], gp[4] = {0.f, 0.f, 0.f, 0.f}, gpos = 0.0f;   // gpos: per-key decay: of channel li
+    if (pos > 0) {
+        gpos = bg[(size_t)last * (KDA ? D : 1) + (KDA ? li : 0)];
+        if constexpr (KDA) load_floats<4>(bg + (size_t)last * D + 4 * lg, gp);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (16 * c < pos) {
+                const size_t at = (size_t)min(16 * c + li, last) * D + 4 * lg;
+                load_floats<4>(bk + at, wk[c]);
+                if constexpr (KDA) load_floats<4>(bg + at, wg[c]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int i = min(16 * c + 4 * lg + v, last);
+                    wm[c][v] = bm[(size_t)i * D + li];
+                    if constexpr (!KDA) wg[c][v] = bg[i];
+                }
+            }
+    }
+    // ---- the state: Hb[4 lg + v][li] ----
+#pragma unroll
+    for (int v = 0; v < 4; ++v) hb[v] = sbyte(raw, v) * rs[v] * sj;
+    for (int c = 0; c < C; ++c) {
+        const int ic = a.idx[head * C + c] & (D - 1);
+        const float y = a.cv[(head * C + c) * D + li];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) hb[v] += ic == 4 * lg + v ? y : 0.0f;
+    }
+    // ---- tables: lane n = node n ----
+    // (path sums in 64 bits: differences of strong decays keep fp32's precision)
+    const TreeNode<double> nd = tree_node(npar, lane, KDA ? 0.0 : (double)(DELTA ? logf(nal) : log_decay(nal)));
+    const uint64_t here = __ballot(nd.here);
+    const uint64_t mask = nd.here ? nd.mask : 0;
+    s_t.mask[lane] = mask;                                 // (for rows that are not finite)
+    s_t.par[lane] = (int8_t)nd.parent;
+    const float beta = nd.here ? nbeta : 0.0f;
+    const double G = KDA ? 0.0 : nd.here ? nd.sum + gpos : gpos;
+    if constexpr (!KDA)
+        if (nd.here) a.tg[head * N + lane] = (float)G;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        if (16 * j >= N) break;
+        const bool row = (here >> (16 * j + li)) & 1u;     // absent nodes: zeros
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const bool on = (here >> (16 * j + 4 * lg + v)) & 1u;
+            q[j][v] = row ? q[j][v] : 0.0f;
+            k[j][v] = row ? k[j][v] : 0.0f;
+            vv[j][v] = on ? vv[j][v] : 0.0f;
+            if constexpr (KDA) lal[j][v] = on ? logf(lal[j][v]) : 0.0f;
+        }
+        if constexpr (KDA) {
+            // path sums of the logarithms, rows 4 lg + v, channel li
+            const int n = 16 * j + li;
+            const uint64_t path = __shfl(mask, n, 64) | (1ull << n);
+            v4f y = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c <= j; ++c)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) y = mfma4((path >> (16 * c + 4 * lg + v)) & 1u ? 1.0f : 0.0f, lal[c][v], y);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int m = 16 * j + 4 * lg + v;
+                s.g[m * LR + li] = y[v] + gpos;
+                if ((here >> m) & 1u) a.tg[(head * N + m) * D + li] = y[v] + gpos;
+            }
+            *reinterpret_cast<v4f*>(&s.k[n * LR + 4 * lg]) = v4f{k[j][0], k[j][1], k[j][2], k[j][3]};
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+        if (16 * c < pos)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                if constexpr (KDA) wk[c][v] *= expf(gp[v] - wg[c][v]);
+                wk[c][v] = 16 * c + li < pos ? wk[c][v] : 0.0f;
+                wm[c][v] = 16 * c + 4 * lg + v < pos ? wm[c][v] : 0.0f;
+            }
+
+    v4f M[NB];
+    bool odd = false;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        if (16 * j >= N) break;
+        const int n = 16 * j + li;
+        const uint64_t anc = __shfl(mask, n, 64);
+        const double gn = KDA ? 0.0 : __shfl(G, n, 64);
+        const float bn = DELTA ? __shfl(beta, n, 64) : 0.0f;
+        if constexpr (KDA) {
+            *reinterpret_cast<v4f*>(&s.q[li * LR + 4 * lg]) = v4f{q[j][0], q[j][1], q[j][2], q[j][3]};
+            __syncthreads();
+        }
+        float en[4], ew[4];                                // e^{g_n} of the row's channels; per-key decay: e^{g_n - g_pos}
+        if constexpr (KDA) {
+            float gr[4];
+            load_floats<4>(&s.g[n * LR + 4 * lg], gr);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) en[v] = expf(gr[v]), ew[v] = expf(gr[v] - gp[v]);
+        } else {
+            en[0] = en[1] = en[2] = en[3] = expf((float)gn);
+        }
+        // y += S x context, S^T = K Q^T; x: 0 the queries, 1 the keys
+        v4f O = {0.f, 0.f, 0.f, 0.f}, R = O, dq = O, dk = O;   // dq, dk: the block's own scores, transposed
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            O = mfma4(en[v] * q[j][v], hb[v], O);
+            if constexpr (DELTA) R = mfma4(en[v] * k[j][v], hb[v], R);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            if (16 * c < pos) {
+                v4f sq = {0.f, 0.f, 0.f, 0.f}, sk = sq;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    sq = mfma4(wk[c][v], KDA ? ew[v] * q[j][v] : q[j][v], sq);
+                    if constexpr (DELTA) sk = mfma4(wk[c][v], KDA ? ew[v] * k[j][v] : k[j][v], sk);
+                }
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const float e = KDA ? 1.0f : __expf((float)(gn - wg[c][v]));
+                    O = mfma4(sq[v] * e, wm[c][v], O);
+                    if constexpr (DELTA) R = mfma4(sk[v] * e, wm[c][v], R);
+                }
+            }
+        [[maybe_unused]] float qn[KDA ? D : 1], kn[KDA ? D : 1], gr[KDA ? D : 1];
+        if constexpr (KDA) {
+            load_floats<D>(&s.q[li * LR], qn);
+            load_floats<D>(&s.k[n * LR], kn);
+            load_floats<D>(&s.g[n * LR], gr);
+        }
+#pragma unroll
+        for (int c = 0; c <= j; ++c) {
+            v4f sq = {0.f, 0.f, 0.f, 0.f}, sk = sq;
+            if constexpr (!KDA) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    sq = mfma4(k[c][v], q[j][v], sq);
+                    if constexpr (DELTA) sk = mfma4(k[c][v], k[j][v], sk);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int i = 16 * c + 4 * lg + v;
+                const bool up = (anc >> i) & 1u, on = up || i == n;   // (i = n: <q_n, k_n>; its exponential is 1)
+                if constexpr (KDA) {
+                    if (__any(on)) {
+                        float ki[D], gi[D], xq = 0.0f, xk = 0.0f;
+                        load_floats<D>(&s.k[i * LR], ki);
+                        load_floats<D>(&s.g[i * LR], gi);
+#pragma unroll
+                        for (int u = 0; u < D; ++u) {
+                            const float y = i == n ? ki[u] : ki[u] * __expf(gr[u] - gi[u]);
+                            xq += qn[u] * y;
+                            xk += kn[u] * y;
+                        }
+                        sq[v] = on ? xq : 0.0f;
+                        sk[v] = up ? xk : 0.0f;
+                    }
+                } else {
+                    const float e = __expf((float)(gn - __shfl(G, i, 64)));
+                    sq[v] = on ? sq[v] * (i == n ? 1.0f : e) : 0.0f;
+                    sk[v] = up ? sk[v] * e : 0.0f;
+                }
+            }
+            if (c < j) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    O = mfma4(sq[v], M[c][v], O);
+                    if constexpr (DELTA) R = mfma4(sk[v], M[c][v], R);
+                }
+            } else {
+                dq = sq;
+                dk = sk;
+            }
+        }
+        if constexpr (DELTA) {
+            v4f X[1], own[3];
+            float below[3];
+            *reinterpret_cast<v4f*>(&s.a[li * LR + 4 * lg]) = dk * -bn;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) X[0][v] = __shfl(beta, 16 * j + 4 * lg + v, 64) * (vv[j][v] - R[v]);
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(&s.a[(4 * lg + 1 + i) * LR + 4 * lg]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? s.a[li * LR + 4 * p + lg] : 0.0f;
+            block_solve(own, below, lg, X);
+            M[j] = X[0];
+            __syncthreads();                               // (s.a and s.q are rewritten by the next block)
+        } else {
+            M[j] = v4f{vv[j][0], vv[j][1], vv[j][2], vv[j][3]};
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) O = mfma4(dq[v], M[j][v], O);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int m = 16 * j + 4 * lg + v;
+            odd |= !finite_f32(M[j][v]);
+            if (!((here >> m) & 1u)) continue;
+            tok_st<TI>(a.o, ((size_t)m * heads + head) * D + li, O[v]);
+            a.tm[(head * N + m) * D + li] = M[j][v];
+        }
+    }
+    if (__syncthreads_or(odd)) {
+        all_loads_barrier();                               // (this pass's stores are done: the rows are written again)
+        tree_simple<D, RULE, TI, 64>(a, pos, s_t.mask, s_t.par, here, sp.f);
+    }
+}
+
 template <int D, int NB, int WT, int RULE, typename TI>
 __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE, TI>::WPE)) void tree_mfma_kernel(TreeArgs a) {
     using X = TM<D, NB, WT, RULE, TI>;
@@ -429,7 +714,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     }
     // ---- tables ----
     if (w == 0) {
-        const TreeNode nd = tree_node(lane < N ? npar : -2, lane, KDA ? 0.0f : DELTA ? logf(nal) : log_decay(nal));
+        const TreeNode<float> nd = tree_node(lane < N ? npar : -2, lane, KDA ? 0.0f : DELTA ? logf(nal) : log_decay(nal));
         s.t.mask[lane] = nd.here ? nd.mask : 0;
         s.t.par[lane] = (int8_t)nd.parent;
         const uint64_t here = __ballot(nd.here);
@@ -794,9 +1079,6 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
                     for (int v = 0; v < 4; ++v) R[ct][v] = be[v] * (vv[e][v][ct] - acc[e][NX - 1][ct][v]);
                 context(1, R);
-                // M = (I + A)^{-1} R, four rows at a time: lane group p solves its rows; row swaps bring
-                // its row 4 p + i to lane group i, the B operand of one k = 4 step with -A's columns
-                // 4 p .. 4 p + 3 (rows below them)
                 const float* ab = &s.s[1][16 * e * SS + WC + 16 * j];
                 v4f own[3];                                                               // -A[4 lg + 1 + i][4 lg + v]
 #pragma unroll
@@ -804,23 +1086,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 float below[3];                                                           // -A[li][4 p + lg]
 #pragma unroll
                 for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? ab[li * SS + 4 * p + lg] : 0.0f;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    if (lg == p)
-#pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) {
-                            R[ct][1] += own[0][0] * R[ct][0];
-                            R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
-                            R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
-                        }
-                    if (p < 3)
-#pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) {
-                            const bool on = lg == p;
-                            const float x = rows_sum4(on ? R[ct][0] : 0.0f, on ? R[ct][1] : 0.0f, on ? R[ct][2] : 0.0f, on ? R[ct][3] : 0.0f);
-                            R[ct] = mfma4(below[p], x, R[ct]);
-                        }
-                }
+                block_solve(own, below, lg, R);
                 M[j][0] = R[0];
                 M[j][1] = R[1];
             } else {
@@ -892,7 +1158,9 @@ hipError_t tree_mfma(const lq_dims& d, const TreeArgs& args, hipStream_t s) {
 
 template <int RULE, typename TI>
 hipError_t tree_io(const lq_dims& d, const TreeArgs& args, hipStream_t s) {
-    if (d.dk == 16) return launch_kernel(LQ_KERNEL_TREE, tree_kernel<16, RULE, TI>, dim3((unsigned)args.heads), dim3(64), s, args);
+    if (d.dk == 16)
+        return args.N <= 16 ? launch_kernel(LQ_KERNEL_TREE, tree_small_kernel<1, RULE, TI>, dim3((unsigned)args.heads), dim3(64), s, args)
+                            : launch_kernel(LQ_KERNEL_TREE, tree_small_kernel<4, RULE, TI>, dim3((unsigned)args.heads), dim3(64), s, args);
     return d.dk == 64 ? tree_mfma<64, RULE, TI>(d, args, s) : tree_mfma<128, RULE, TI>(d, args, s);
 }
 
