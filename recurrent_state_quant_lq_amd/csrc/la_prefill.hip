@@ -764,8 +764,10 @@ __global__ __launch_bounds__(256) void la_small_kernel(LaSegArgs a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) H[v] = a.start[soff + (4 * lg + v) * D + li];
     // token li: q, k channels 4 lg + v; tokens 4 lg + v: k, v channel li
-    struct Chunk {
-        float q[4], k[4], kt[4], vt[4], al;
+    struct Chunk {                                                        // (as loaded: widened on use)
+        Row4<TI> q, k;
+        TI kt[4], vt[4];
+        float al;
     };
     auto load = [&](int c0, Chunk& x) {                                   // (past the end: the last token, zeroed on use)
         const int n = min(c0 + li, te - 1);
@@ -773,12 +775,12 @@ __global__ __launch_bounds__(256) void la_small_kernel(LaSegArgs a) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const size_t to = ((size_t)min(c0 + 4 * lg + v, te - 1) * heads + head) * D + li;
-            if (OUT) {
-                x.q[v] = tok_ld<TI>(a.q, at + v);
-                x.k[v] = tok_ld<TI>(a.k, at + v);
-            }
-            x.kt[v] = tok_ld<TI>(a.k, to);
-            x.vt[v] = tok_ld<TI>(a.v, to);
+            x.kt[v] = static_cast<const TI*>(a.k)[to];
+            x.vt[v] = static_cast<const TI*>(a.v)[to];
+        }
+        if (OUT) {
+            x.q.load(a.q, at);
+            x.k.load(a.k, at);
         }
         x.al = a.alpha[a.alpha_tok ? (size_t)n * a.alpha_tok + head : head % (unsigned)a.H];
     };
@@ -798,30 +800,34 @@ __global__ __launch_bounds__(256) void la_small_kernel(LaSegArgs a) {
         double gi[4];                                                     // of tokens 4 lg + v
 #pragma unroll
         for (int v = 0; v < 4; ++v) gi[v] = __shfl(g, 4 * lg + v, 16);
+        // (an exponent is at most 0: off by 2^-24 of it, weighted by its exponential)
         float vt[4], kw[4];
         bool odd = false;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const bool on = 4 * lg + v < L;
-            vt[v] = on ? cur.vt[v] : 0.0f;
-            kw[v] = on ? expf((float)(gl - gi[v])) * cur.kt[v] : 0.0f;
+            vt[v] = on ? widen(cur.vt[v]) : 0.0f;
+            kw[v] = on ? __expf((float)(gl - gi[v])) * widen(cur.kt[v]) : 0.0f;
             odd |= !finite_f32(vt[v]);
         }
         if constexpr (OUT) {
             // P^T[i = 4 lg + v][n = li]
             v4f p = {0.f, 0.f, 0.f, 0.f};
+            float qr[4], kr[4];
+            cur.q.widen4(qr);
+            cur.k.widen4(kr);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const float x = li < L ? cur.k[v] : 0.0f, y = li < L ? cur.q[v] : 0.0f;
+                const float x = li < L ? kr[v] : 0.0f, y = li < L ? qr[v] : 0.0f;
                 p = __builtin_amdgcn_mfma_f32_16x16x4f32(x, y, p, 0, 0, 0);
             }
 #pragma unroll
-            for (int v = 0; v < 4; ++v) p[v] = 4 * lg + v <= li ? expf((float)(g - gi[v])) * p[v] : 0.0f;
+            for (int v = 0; v < 4; ++v) p[v] = 4 * lg + v <= li ? __expf((float)(g - gi[v])) * p[v] : 0.0f;
             const float en = expf((float)g);
             v4f o = {0.f, 0.f, 0.f, 0.f};                                 // o[n = 4 lg + v][li]
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                o = __builtin_amdgcn_mfma_f32_16x16x4f32(li < L ? en * cur.q[v] : 0.0f, H[v], o, 0, 0, 0);
+                o = __builtin_amdgcn_mfma_f32_16x16x4f32(li < L ? en * qr[v] : 0.0f, H[v], o, 0, 0, 0);
                 o = __builtin_amdgcn_mfma_f32_16x16x4f32(p[v], finite_f32(vt[v]) ? vt[v] : 0.0f, o, 0, 0, 0);
             }
             if (__any(odd))                                               // the others, from their own token on

@@ -108,4 +108,19 @@ __device__ __forceinline__ v4f mfma_split(const u32x4 (&a)[3], const u32x4 (&b)[
     return mfma_bf16(a[0], b[0], c);
 }
 
+// A token value as loaded, widened; four consecutive ones.
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
+template <typename TI> struct Row4;
+template <> struct Row4<float> {
+    v4f x;
+    __device__ __forceinline__ void load(const void* p, size_t at) { x = *reinterpret_cast<const v4f*>(static_cast<const float*>(p) + at); }
+    __device__ __forceinline__ void widen4(float (&y)[4]) const { y[0] = x[0], y[1] = x[1], y[2] = x[2], y[3] = x[3]; }
+};
+template <> struct Row4<uint16_t> {
+    u32x2 x;
+    __device__ __forceinline__ void load(const void* p, size_t at) { x = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(p) + at); }
+    __device__ __forceinline__ void widen4(float (&y)[4]) const { y[0] = lo_f32(x[0]), y[1] = hi_f32(x[0]), y[2] = lo_f32(x[1]), y[3] = hi_f32(x[1]); }
+};
+
 }  // namespace lq

@@ -301,8 +301,6 @@ template <> struct Pair<float> { typedef f32x2 T; };
 template <> struct Pair<uint16_t> { typedef uint32_t T; };
 __device__ __forceinline__ f32x2 widen2(f32x2 x) { return x; }
 __device__ __forceinline__ f32x2 widen2(uint32_t x) { return f32x2{lo_f32(x), hi_f32(x)}; }
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(uint16_t x) { return bf16_to_f32(x); }
 
 __device__ __forceinline__ v4f mfma4(float a, float b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
@@ -363,14 +361,6 @@ __global__ __launch_bounds__(64) void tree_small_kernel(TreeArgs a) {
     const size_t head = blockIdx.x, heads = (size_t)a.heads;
     const int W = a.W, C = a.C, N = a.N;
     const unsigned b = blockIdx.x / (unsigned)a.H;
-    auto row4 = [](const void* x, size_t at, float (&y)[4]) {
-        if constexpr (sizeof(TI) == 4) {
-            load_floats<4>(static_cast<const float*>(x) + at, y);
-        } else {
-            const u32x2 z = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(x) + at);
-            y[0] = lo_f32(z[0]), y[1] = hi_f32(z[0]), y[2] = lo_f32(z[1]), y[3] = hi_f32(z[1]);
-        }
-    };
     // ---- requests (rows past the end: the last node's, zeroed below) ----
     const int pos = a.pos[b];
     const int npar = lane < N ? a.parent[(size_t)b * N + lane] : -2;
@@ -383,8 +373,11 @@ __global__ __launch_bounds__(64) void tree_small_kernel(TreeArgs a) {
     for (int j = 0; j < NB; ++j) {
         if (16 * j >= N) break;
         const size_t at = ((size_t)min(16 * j + li, N - 1) * heads + head) * D + 4 * lg;
-        row4(a.q, at, q[j]);
-        row4(a.k, at, k[j]);
+        Row4<TI> rq, rk;
+        rq.load(a.q, at);
+        rk.load(a.k, at);
+        rq.widen4(q[j]);
+        rk.widen4(k[j]);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
             const size_t to = ((size_t)min(16 * j + 4 * lg + v, N - 1) * heads + head) * D + li;
