@@ -903,10 +903,12 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
 // bf16 (fp32), 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192
 // heads 109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
 // (291, 282, 290) for 256, 512 and 768 workgroups.
-// d = 16 (one wave a segment): enough segments for kWantSmall waves, of 8 chunks at least.
-constexpr size_t kWant = 512, kSplitHeads = 128, kWantSmall = 4096, kMinSmall = 128;
+// d = 16 (one wave a segment): up to kSplitSmall heads, enough segments for kWantSmall waves, of 8
+// chunks at least.  bf16 (fp32), 512 tokens: 768 heads 41 us (43) split, 47 (44) whole; 1024 heads
+// 51 (53) split, 48 (45) whole; 2048 heads 87 (94) split, 65 (62) whole, 2.2 (4.4) TB/s.
+constexpr size_t kWant = 512, kSplitHeads = 128, kWantSmall = 4096, kSplitSmall = 768, kMinSmall = 128;
 size_t segments_wanted(size_t heads, int d) {
-    return d == 16 ? (kWantSmall + heads - 1) / heads : heads > kSplitHeads ? 1 : (kWant + heads - 1) / heads;
+    return heads > (d == 16 ? kSplitSmall : kSplitHeads) ? 1 : ((d == 16 ? kWantSmall : kWant) + heads - 1) / heads;
 }
 int chunk_tokens(const lq_dims& d) { return d.dk == 16 ? (int)kMinSmall : d.io_dtype == LQ_IO_BF16 ? BL : FL; }
 int segment_tokens(const lq_dims& d, int T) {
