@@ -899,16 +899,25 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
 
 // Tokens per segment (a multiple of the chunk).  Segments cost a second read of k and v and
 // the states between them, so they pay where the heads alone leave most CUs idle: up to
-// kSplitHeads heads, enough segments for kWant workgroups (two a CU).  Measured at d = 128,
-// bf16 (fp32), 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192
-// heads 109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
-// (291, 282, 290) for 256, 512 and 768 workgroups.
-// d = 16 (one wave a segment): up to kSplitSmall heads, enough segments for kWantSmall waves, of 8
-// chunks at least.  bf16 (fp32), 512 tokens: 768 heads 41 us (43) split, 47 (44) whole; 1024 heads
-// 51 (53) split, 48 (45) whole; 2048 heads 87 (94) split, 65 (62) whole, 2.2 (4.4) TB/s.
-constexpr size_t kWant = 512, kSplitHeads = 128, kWantSmall = 4096, kSplitSmall = 768, kMinSmall = 128;
+// `heads` heads, enough segments for `want` workgroups (as many as fit the GPU: two a CU at
+// d = 128, three at d = 64; d = 16: waves).  Measured, bf16 (fp32):
+//   d = 128, 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192 heads
+//   109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
+//   (291, 282, 290) for 256, 512 and 768 workgroups;
+//   d = 64, 2048 tokens: 128 heads 65 us (87) split, 132 (164) whole; 256 heads 101 us (188)
+//   split, 132 (186) whole, 127 (196) for 512 workgroups; 512 heads, 1024 tokens: 115 us (189)
+//   split, 86 (122) whole;
+//   d = 16, 512 tokens (segments of 8 chunks at least): 768 heads 41 us (43) split, 47 (44)
+//   whole; 1024 heads 51 (53) split, 48 (45) whole; 2048 heads 87 (94) split, 65 (62) whole,
+//   2.2 (4.4) TB/s.
+struct Split {
+    size_t heads, want;
+};
+constexpr Split kSplit128{128, 512}, kSplit64{256, 768}, kSplit16{768, 4096};
+constexpr size_t kMinSmall = 128;
 size_t segments_wanted(size_t heads, int d) {
-    return heads > (d == 16 ? kSplitSmall : kSplitHeads) ? 1 : ((d == 16 ? kWantSmall : kWant) + heads - 1) / heads;
+    const Split x = d == 16 ? kSplit16 : d == 64 ? kSplit64 : kSplit128;
+    return heads > x.heads ? 1 : (x.want + heads - 1) / heads;
 }
 int chunk_tokens(const lq_dims& d) { return d.dk == 16 ? (int)kMinSmall : d.io_dtype == LQ_IO_BF16 ? BL : FL; }
 int segment_tokens(const lq_dims& d, int T) {
