@@ -917,7 +917,7 @@ constexpr Split kSplit128{128, 512}, kSplit64{256, 768}, kSplit16{768, 4096};
 constexpr size_t kMinSmall = 128;
 size_t segments_wanted(size_t heads, int d) {
     const Split x = d == 16 ? kSplit16 : d == 64 ? kSplit64 : kSplit128;
-    return heads > x.heads ? 1 : (x.want + heads - 1) / heads;
+    return heads > x.heads ? 1 : x.want / heads;                  // (one round of workgroups)
 }
 int chunk_tokens(const lq_dims& d) { return d.dk == 16 ? (int)kMinSmall : d.io_dtype == LQ_IO_BF16 ? BL : FL; }
 int segment_tokens(const lq_dims& d, int T) {
