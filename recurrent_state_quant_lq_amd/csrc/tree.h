@@ -233,6 +233,10 @@ struct TM {
     // parts of the window's keys and of the state: three (24 bits); two (16 bits and a rounding,
     // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-8
     static constexpr int NS = !DELTA && sizeof(TI) == 2 ? 2 : 3;
+    // parts of the state: per-key decay keeps the int8 values as they are (exact in bf16) and
+    // writes the rows again after the scores, scaled by r o e^{g_n}: half the products of the
+    // state in three parts, and no splits of it for each block
+    static constexpr int NT8 = KDA ? 1 : NS;
     static constexpr int GB = NP == 1 ? 2 : 1;                     // blocks per group
     static constexpr int KB = KDA ? GB : NB;                       // blocks whose keys stay in LDS
     static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
@@ -277,6 +281,10 @@ struct TM {
 template <int NP, int NQ>
 __device__ __forceinline__ v4f mfma_parts(const u32x4 (&a)[NP], const u32x4 (&b)[NQ], v4f c) {
     if constexpr (NP == 3 && NQ == 3) return mfma_split(a, b, c);
+    if constexpr (NP == 3 && NQ == 1) {
+        c = mfma_bf16(a[2], b[0], c);
+        c = mfma_bf16(a[1], b[0], c);
+    }
     if constexpr (NQ >= 3) c = mfma_bf16(a[0], b[2], c);
     if constexpr (NQ >= 2) c = mfma_bf16(a[0], b[1], c);
     return mfma_bf16(a[0], b[0], c);
@@ -820,6 +828,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
         constexpr size_t QP = sizeof(s.q[0]) / 2, KP = sizeof(s.k[0]) / 2, WP = sizeof(s.wk[0]) / 2;   // shorts per part
         // ---- 1. rows ----
         f32x2 vv[GB][4];
+        [[maybe_unused]] float sc[8];                      // per-key decay: the row's scales
 #pragma unroll
         for (int e = 0; e < GB; ++e) {
             const int r = 16 * e + row, n = 16 * GB * g + r;
@@ -832,7 +841,6 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 *reinterpret_cast<u32x4*>(&s.q[0][r * QS + c8]) = on ? rq[e].x[0] : u32x4{0, 0, 0, 0};
                 *reinterpret_cast<u32x4*>(kbase + r * QS + c8) = on ? rk[e].x[0] : u32x4{0, 0, 0, 0};
             } else {
-                float sc[8];
                 if constexpr (KDA)
 #pragma unroll
                     for (int u = 0; u < 8; ++u) sc[u] = __expf(s.gk[n * D + c8 + u] - s.gp[c8 + u]);
@@ -984,8 +992,45 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 }
             }
         }
+        auto compensators = [&](int e, int x, v4f (&cmp)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float z = 0.0f;
+#pragma unroll
+                for (int m = NP - 1; m >= 0; --m) z += bf16_to_f32((x ? kbase + m * KP : &s.q[m][0])[(16 * e + li) * QS + ci[u]]);
+                if (C > 4 * u) {
+                    cmp[0] = mfma4(z, cb[u][0], cmp[0]);
+                    cmp[1] = mfma4(z, cb[u][1], cmp[1]);
+                }
+            }
+        };
+        [[maybe_unused]] v4f kcmp[NX][2];
+        if constexpr (KDA)
+#pragma unroll
+            for (int x = 0; x < NX; ++x) {
+                kcmp[x][0] = kcmp[x][1] = v4f{0.f, 0.f, 0.f, 0.f};
+                compensators(0, x, kcmp[x]);
+            }
         __syncthreads();
         // ---- 3. products with the state ----
+        if constexpr (KDA) {
+            const bool on = (here >> (16 * g + row)) & 1u;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sc[u] *= s.r[c8 + u];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float y[8];
+                uint32_t p[3][4];
+                widen8<TI>(x ? rk[0] : rq[0], y);
+#pragma unroll
+                for (int u = 0; u < 8; ++u) y[u] = on ? y[u] * sc[u] : 0.0f;
+                split3<8>(y, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m)
+                    *reinterpret_cast<u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + row * QS + c8) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            }
+            __syncthreads();
+        }
         v4f acc[GB][NX][2];
 #pragma unroll
         for (int e = 0; e < GB; ++e)
@@ -997,18 +1042,29 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             for (int hf = 0; hf < 2; ++hf) {
                 // B operands: channels 64 ks + 16 lg + 8 hf .. + 7 of columns col + ct
                 const int ch = 64 * ks + 16 * lg + 8 * hf;
-                float r[8];
-                u32x4 st[2][NS];
-                load_floats<8>(&s.r[ch], r);
+                constexpr int NT8 = X::NT8;
+                u32x4 st[2][NT8];
+                if constexpr (KDA) {
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    float x8[8];
-                    uint32_t p[NS][4];
+                    for (int ct = 0; ct < 2; ++ct)
 #pragma unroll
-                    for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
-                    split<NS, 8>(x8, p);
+                        for (int u = 0; u < 4; ++u) {
+                            const uint32_t y = (uint32_t)raw[ks][ct][2 * hf + u / 2];
+                            st[ct][0][u] = top_halves(sbyte(y, 2 * (u % 2)), sbyte(y, 2 * (u % 2) + 1));
+                        }
+                } else {
+                    float r[8];
+                    load_floats<8>(&s.r[ch], r);
 #pragma unroll
-                    for (int m = 0; m < NS; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                    for (int ct = 0; ct < 2; ++ct) {
+                        float x8[8];
+                        uint32_t p[NT8][4];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
+                        split<NT8, 8>(x8, p);
+#pragma unroll
+                        for (int m = 0; m < NT8; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                    }
                 }
 #pragma unroll
                 for (int e = 0; e < GB; ++e) {
@@ -1020,7 +1076,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                         for (int m = 0; m < NP; ++m)
                             ar[m] = *reinterpret_cast<const u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + (16 * e + li) * QS + ch);
 #pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, NS>(ar, st[ct], acc[e][x][ct]);
+                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, NT8>(ar, st[ct], acc[e][x][ct]);
                     }
                 }
             }
@@ -1030,16 +1086,8 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 v4f cmp[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float z = 0.0f;
-#pragma unroll
-                    for (int m = NP - 1; m >= 0; --m) z += bf16_to_f32((x ? kbase + m * KP : &s.q[m][0])[(16 * e + li) * QS + ci[u]]);
-                    if (C > 4 * u) {
-                        cmp[0] = mfma4(z, cb[u][0], cmp[0]);
-                        cmp[1] = mfma4(z, cb[u][1], cmp[1]);
-                    }
-                }
+                if constexpr (KDA) cmp[0] = kcmp[x][0], cmp[1] = kcmp[x][1];
+                else compensators(e, x, cmp);
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) {
                     acc[e][x][ct] = acc[e][x][ct] * sj[ct] + cmp[ct];
