@@ -208,7 +208,8 @@ struct TreeTables {
 //      k times -beta.  Per-key decay takes the nodes' scores pair by pair, with the
 //      exponential of each channel's difference: a product of two factors could
 //      overflow;
-//   3. the products with the state, r o sq in bf16 parts formed on the way;
+//   3. the products with the state: r o sq in bf16 parts formed on the way, or, for rows in
+//      three parts, the int8 values as they are and the rows formed again, scaled by r;
 //   4. block after block, without barriers: R = beta (v - Hb^T k) - A_ctx M_ctx,
 //      M = (I + A)^{-1} R with A_{n,i} = beta_n <k_n, E k_i> (strictly lower triangular in
 //      node order, solved four rows at a time), O = Hb^T q + S M, on the fp32 matrix
@@ -222,7 +223,7 @@ struct TreeTables {
 // Bound by the issue of these phases and, with two workgroups a CU (per-key decay: LDS), by
 // their latencies.  d = 128, 2048 heads, bf16: delta rule, 32 nodes 50 us (vector unit 23,
 // matrix unit 15; 3.0 TB/s), 64 nodes without it 68 us (3.4 TB/s); 1024 heads, per-key decay,
-// 21 nodes, fp32 51 us.
+// 21 nodes, fp32 46 us.
 // A product of a masked zero with a value that is not finite would spread it: if any
 // m is not finite, the row is computed again node after node.
 template <int D, int NB, int WT, int RULE, typename TI>
@@ -230,13 +231,16 @@ struct TM {
     static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
-    // parts of the window's keys and of the state: three (24 bits); two (16 bits and a rounding,
+    // parts of the window's keys and of the scaled state: three (24 bits); two (16 bits and a rounding,
     // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-8
     static constexpr int NS = !DELTA && sizeof(TI) == 2 ? 2 : 3;
-    // parts of the state: per-key decay keeps the int8 values as they are (exact in bf16) and
-    // writes the rows again after the scores, scaled by r o e^{g_n}: half the products of the
-    // state in three parts, and no splits of it for each block
-    static constexpr int NT8 = KDA ? 1 : NS;
+    // parts of the state: where rows have three parts, the int8 values are kept as they are (exact
+    // in bf16) and the rows are formed again after the scores, scaled by r (per-key decay: by
+    // r o e^{g_n}): half the products of the state in three parts, and no splits of it for each
+    // block (per-key decay, 1024 heads, 21 nodes, fp32: 46 us, not 52; delta rule, 2048 heads,
+    // 32 nodes, fp32: 68 us, not 75)
+    static constexpr bool FOLD = NP == 3;
+    static constexpr int NT8 = FOLD ? 1 : NS;
     static constexpr int GB = NP == 1 ? 2 : 1;                     // blocks per group
     static constexpr int KB = KDA ? GB : NB;                       // blocks whose keys stay in LDS
     static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
@@ -621,7 +625,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
     constexpr int NW = X::NW, NT = X::NT, NP = X::NP, GB = X::GB, KB = X::KB, QS = X::QS, WC = X::WC, SS = X::SS;
     constexpr bool KDA = X::KDA, DELTA = X::DELTA;
     constexpr int NS = X::NS, SB = X::SB;
-    constexpr bool VB = X::VB;
+    constexpr bool VB = X::VB, FOLD = X::FOLD;
     constexpr int NX = DELTA ? 2 : 1, GD = KDA ? D : 1, KS = D / 64, NG = NB / GB;
     __shared__ typename X::Space sp;
     auto& s = sp.m;
@@ -1005,7 +1009,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             }
         };
         [[maybe_unused]] v4f kcmp[NX][2];
-        if constexpr (KDA)
+        if constexpr (FOLD)
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 kcmp[x][0] = kcmp[x][1] = v4f{0.f, 0.f, 0.f, 0.f};
@@ -1013,12 +1017,12 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             }
         __syncthreads();
         // ---- 3. products with the state ----
-        if constexpr (KDA) {
+        // where the keys must stay for the next groups' scores, q and k take turns in the rows of q
+        constexpr bool TURNS = FOLD && DELTA && !KDA;
+        auto scaled_rows = [&](int x0, int x1) {
             const bool on = (here >> (16 * g + row)) & 1u;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sc[u] *= s.r[c8 + u];
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = x0; x < x1; ++x) {
                 float y[8];
                 uint32_t p[3][4];
                 widen8<TI>(x ? rk[0] : rq[0], y);
@@ -1027,9 +1031,14 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                 split3<8>(y, p);
 #pragma unroll
                 for (int m = 0; m < 3; ++m)
-                    *reinterpret_cast<u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + row * QS + c8) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                    *reinterpret_cast<u32x4*>((x && !TURNS ? kbase + m * KP : &s.q[m][0]) + row * QS + c8) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
             __syncthreads();
+        };
+        if constexpr (FOLD) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) sc[u] = KDA ? sc[u] * s.r[c8 + u] : s.r[c8 + u];
+            scaled_rows(0, TURNS ? 1 : NX);
         }
         v4f acc[GB][NX][2];
 #pragma unroll
@@ -1037,56 +1046,65 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
 #pragma unroll
             for (int x = 0; x < NX; ++x) acc[e][x][0] = acc[e][x][1] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int turn = 0; turn < (TURNS ? 2 : 1); ++turn) {
+            if constexpr (TURNS)
+                if (turn) {
+                    __syncthreads();                           // q's rows are read
+                    scaled_rows(1, 2);
+                }
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                // B operands: channels 64 ks + 16 lg + 8 hf .. + 7 of columns col + ct
-                const int ch = 64 * ks + 16 * lg + 8 * hf;
-                constexpr int NT8 = X::NT8;
-                u32x4 st[2][NT8];
-                if constexpr (KDA) {
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
+                for (int hf = 0; hf < 2; ++hf) {
+                    // B operands: channels 64 ks + 16 lg + 8 hf .. + 7 of columns col + ct
+                    const int ch = 64 * ks + 16 * lg + 8 * hf;
+                    constexpr int NT8 = X::NT8;
+                    u32x4 st[2][NT8];
+                    if constexpr (FOLD) {
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const uint32_t y = (uint32_t)raw[ks][ct][2 * hf + u / 2];
-                            st[ct][0][u] = top_halves(sbyte(y, 2 * (u % 2)), sbyte(y, 2 * (u % 2) + 1));
+                        for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const uint32_t y = (uint32_t)raw[ks][ct][2 * hf + u / 2];
+                                st[ct][0][u] = top_halves(sbyte(y, 2 * (u % 2)), sbyte(y, 2 * (u % 2) + 1));
+                            }
+                    } else {
+                        float r[8];
+                        load_floats<8>(&s.r[ch], r);
+#pragma unroll
+                        for (int ct = 0; ct < 2; ++ct) {
+                            float x8[8];
+                            uint32_t p[NT8][4];
+#pragma unroll
+                            for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
+                            split<NT8, 8>(x8, p);
+#pragma unroll
+                            for (int m = 0; m < NT8; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
                         }
-                } else {
-                    float r[8];
-                    load_floats<8>(&s.r[ch], r);
+                    }
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) {
-                        float x8[8];
-                        uint32_t p[NT8][4];
+                    for (int e = 0; e < GB; ++e) {
+                        if (e >= nb) break;
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
-                        split<NT8, 8>(x8, p);
+                        for (int x = 0; x < NX; ++x) {
+                            if (TURNS && x != turn) continue;
+                            u32x4 ar[NP];
 #pragma unroll
-                        for (int m = 0; m < NT8; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                            for (int m = 0; m < NP; ++m)
+                                ar[m] = *reinterpret_cast<const u32x4*>((x && !TURNS ? kbase + m * KP : &s.q[m][0]) + (16 * e + li) * QS + ch);
+#pragma unroll
+                            for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, NT8>(ar, st[ct], acc[e][x][ct]);
+                        }
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < GB; ++e) {
-                    if (e >= nb) break;
-#pragma unroll
-                    for (int x = 0; x < NX; ++x) {
-                        u32x4 ar[NP];
-#pragma unroll
-                        for (int m = 0; m < NP; ++m)
-                            ar[m] = *reinterpret_cast<const u32x4*>((x ? kbase + m * KP : &s.q[m][0]) + (16 * e + li) * QS + ch);
-#pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) acc[e][x][ct] = mfma_parts<NP, NT8>(ar, st[ct], acc[e][x][ct]);
-                    }
-                }
-            }
+        }
 #pragma unroll
         for (int e = 0; e < GB; ++e) {
             if (e >= nb) break;
 #pragma unroll
             for (int x = 0; x < NX; ++x) {
                 v4f cmp[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                if constexpr (KDA) cmp[0] = kcmp[x][0], cmp[1] = kcmp[x][1];
+                if constexpr (FOLD) cmp[0] = kcmp[x][0], cmp[1] = kcmp[x][1];
                 else compensators(e, x, cmp);
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) {
