@@ -395,8 +395,8 @@ int lq_la_decode_step_ragged(const lq_dims *d, const lq_state *st, const int32_t
  *           that the nodes would become (lq_tree_commit).
  * Nodes' depth is not bounded by the window; committed paths are.  A
  * non-finite node reaches itself and its descendants only.  For
- * lq_la_tree_step with bf16 tokens the products with the state and the
- * window, which reach only o, keep 16 bits.
+ * lq_la_tree_step with bf16 tokens the products, which reach only o, keep at
+ * least 16 bits (2^-16 of a sum of absolute values).
  */
 int lq_gdn_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
                      const int32_t *parent, const void *q, const void *k, const void *v,

@@ -258,7 +258,8 @@ class LayerState:
         """The C struct of this state, validated (shapes, dtypes, device) once
         for the tensors the fields hold; a field replaced by another tensor is
         validated again.  In-place writes to the tensors need no revalidation."""
-        key = (tuple(id(getattr(self, n)) for n in _STATE_FIELDS), with_buffer)
+        key = (id(self.sq), id(self.row_scale), id(self.col_scale), id(self.comp_idx), id(self.comp_val),
+               id(self.buf_k), id(self.buf_m), id(self.buf_g), with_buffer)
         c = self.__dict__.get("_ready")
         if c is None or c[0] != key:
             self.check(with_buffer)
@@ -296,8 +297,12 @@ def _token_shapes(d: lq_dims, T=None):
     if sh is None:
         pre = (d.B, d.H) if T is None else (T, d.B, d.H)
         ash = pre + ((d.dk,) if d.decay_mode == LQ_DECAY_PER_KEY else ())
+        gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
+        node = (d.B, d.H, 1 if T is None else T)
         sh = {k: torch.Size(v) for k, v in dict(q=pre + (d.dk,), k=pre + (d.dk,), v=pre + (d.dv,),
-                                                alpha=ash, beta=pre, o=pre + (d.dv,)).items()}
+                                                alpha=ash, beta=pre, o=pre + (d.dv,), row=(d.B,),
+                                                parent=(d.B, node[2]), tree_m=node + (d.dv,),
+                                                tree_g=node + (gd,)).items()}
         _SHAPES[key] = sh
     return sh
 
@@ -450,11 +455,11 @@ def _launch(fn, device, stream, *args):
 def _check_all(device, dtype_io, *items):
     """Items (name, tensor, shape, dtype): dtype None is the token dtype.  Every tensor
     of the shape and dtype, contiguous, on device."""
+    index = device.index
     for name, t, shape, dtype in items:
-        if dtype is None:
-            dtype = dtype_io
-        if t is None or t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-            _check(t, name, shape, dtype)
+        if t is None or t.dtype is not (dtype or dtype_io) or t.shape != shape or t.get_device() != index \
+                or not t.is_contiguous():
+            _check(t, name, shape, dtype or dtype_io)
             raise ValueError(f"{name} on {t.device}, expected {device}")
 
 
@@ -545,11 +550,10 @@ def _tree_items(d, pos, parent, q, k, v, o, tree_m, tree_g):
         raise ValueError("parent: a [B,N] tensor is required")
     N = parent.shape[1]
     sh = _token_shapes(d, N)
-    gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
     f32, i32 = torch.float32, torch.int32
-    return N, sh, (("pos", pos, (d.B,), i32), ("parent", parent, (d.B, N), i32), ("q", q, sh["q"], None),
+    return N, sh, (("pos", pos, sh["row"], i32), ("parent", parent, sh["parent"], i32), ("q", q, sh["q"], None),
                    ("k", k, sh["k"], None), ("v", v, sh["v"], None), ("o", o, sh["o"], None),
-                   ("tree_m", tree_m, (d.B, d.H, N, d.dv), f32), ("tree_g", tree_g, (d.B, d.H, N, gd), f32))
+                   ("tree_m", tree_m, sh["tree_m"], f32), ("tree_g", tree_g, sh["tree_g"], f32))
 
 
 def lq_gdn_tree_step(st: LayerState, pos, parent, q, k, v, alpha, beta, o, tree_m, tree_g, stream=None):
@@ -587,13 +591,13 @@ def lq_tree_commit(st: LayerState, pos, path, n_path, k, tree_m, tree_g, stream=
     if k is None or k.dim() != 4 or path is None or path.dim() != 2:
         raise ValueError("k: the tree's [N,B,H,dk] tensor and path: a [B,P] tensor are required")
     N, P = k.shape[0], path.shape[1]
-    gd = d.dk if d.decay_mode == LQ_DECAY_PER_KEY else 1
+    sh = _token_shapes(d, N)
     cs = st.ready()
     dev = st.sq.device
     f32, i32 = torch.float32, torch.int32
-    _check_all(dev, io_torch_dtype(d), ("pos", pos, (d.B,), i32), ("path", path, (d.B, P), i32),
-               ("n_path", n_path, (d.B,), i32), ("k", k, (N, d.B, d.H, d.dk), None),
-               ("tree_m", tree_m, (d.B, d.H, N, d.dv), f32), ("tree_g", tree_g, (d.B, d.H, N, gd), f32))
+    _check_all(dev, io_torch_dtype(d), ("pos", pos, sh["row"], i32), ("path", path, (d.B, P), i32),
+               ("n_path", n_path, sh["row"], i32), ("k", k, sh["k"], None),
+               ("tree_m", tree_m, sh["tree_m"], f32), ("tree_g", tree_g, sh["tree_g"], f32))
     _launch("lq_tree_commit", dev, stream, ct.byref(d), ct.byref(cs), pos.data_ptr(), N, path.data_ptr(), P,
             n_path.data_ptr(), k.data_ptr(), tree_m.data_ptr(), tree_g.data_ptr())
 
