@@ -108,6 +108,15 @@ def test_prefill_many_heads(B, H, d, T, io):
     check_prefill(o, h, *c, io)
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_prefill_more_heads_than_a_chunk_takes(io):
+    """Above 2^17 heads the recurrence itself runs, whatever the length (two groups of tokens and one token)."""
+    c = prefill_case(6, 1025, 128, 16, 9, io)
+    lens = [(5 * b) % 10 for b in range(1025)]
+    o, h = run_prefill(*c, io, lens=lens)
+    check_prefill(o, h, *c, io, lens=lens)
+
+
 @pytest.mark.parametrize("T", [3, 40, 1300])
 def test_prefill_rows_without_tokens_and_without_a_start(T):
     """A row of length 0 from zeros ends with zeros; its o rows stay."""
