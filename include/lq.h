@@ -332,9 +332,9 @@ enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
  *          16-byte aligned (NULL if that is 0), used until the call's work on
  *          `stream` is done: calls that may run at the same time need their own.
  * T = 0 (or a row with no tokens) copies h0 to h.  T = 1 is the recurrent
- * form over an fp32 state.  With bf16 tokens, products that reach h keep
- * fp32's 24 bits, those that reach only o at least 16 (2^-16 of a sum of
- * absolute values, under the output's own rounding).  A non-finite v reaches
+ * form over an fp32 state.  Sums are in fp32 and operands keep fp32's 24 bits
+ * (with fp32 tokens, d >= 64, a product of two of them is off by at most 2^-21
+ * of itself).  A non-finite v reaches
  * its own column from its own token on.  The result does not depend on
  * earlier calls, on the workspace's content or on other rows.
  * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30; LQ_ERR_DIMS

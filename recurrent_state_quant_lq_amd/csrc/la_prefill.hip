@@ -42,12 +42,13 @@ struct LaPrefillArgs {
 // bf16 tokens, d >= 64: chunks of 64 tokens on bf16 matrix products
 // ---------------------------------------------------------------------------
 // q, k and v enter the products as they are.  Every other operand is an fp32
-// value split into bf16 parts, whose products with a bf16 token are exact and
-// accumulate in fp32:
-//   state update   K^T (w o V), w_t = e^{g_L - g_t}: w v in 3 parts (24 bits);
-//   outputs        Q H with H in 2 parts and (E o Q K^T) V with the scores in 2
-//                  parts: at least 16 bits, 2^-16 of a sum of absolute values,
-//                  under the 2^-8 that the bf16 output keeps.
+// value split into three bf16 parts (all its 24 bits), whose products with a bf16
+// token are exact and accumulate in fp32:
+//   state update   K^T (w o V), w_t = e^{g_L - g_t}: w v in parts;
+//   outputs        Q H with H in parts and (E o Q K^T) V with the scores in parts.
+// (H and the scores in two parts, 16 bits: 303 us, not 332, for 2048 heads of 512 tokens,
+// and 126, not 134, for 16 heads of 16384; but 0.6% of the outputs, not 0.01%, then round to
+// a neighbour of the value that fp32 sums round to.)
 // The wave's D/NW = 32 columns are 2 column tiles; tile ct holds the columns
 // 2 li + ct, so a lane's two columns are one dword of a token row: V is loaded
 // straight into operand order (lane group lg: tokens 8 lg .. 8 lg + 7 of 32),
@@ -56,7 +57,7 @@ struct LaPrefillArgs {
 // order (4 lg + e, 16 + 4 lg + e); Q and K rows are stored in that order.
 // 64 tokens: a chunk's fixed work (the splits of H, three barriers) is shared by as many
 // tokens as the LDS of two workgroups a CU holds.  Measured at d = 128: 2048 heads, 512
-// tokens 304 us (4.0 TB/s); 16 heads, 16384 tokens 42 us for the segments' states and 76 us
+// tokens 332 us (3.7 TB/s); 16 heads, 16384 tokens 42 us for the segments' states and 84 us
 // for the outputs, where the vector unit is busy for 0.57 of the time in both and the matrix
 // unit for 0.38.
 constexpr int BL = 64;        // tokens per chunk
@@ -127,7 +128,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     __shared__ __align__(16) uint16_t sQ[OUT ? pm_shorts<BL>(QP) : 8];
     __shared__ __align__(16) uint16_t sK[OUT ? pm_shorts<BL>(QP) : 8];
     __shared__ __align__(16) uint16_t sT[pm_shorts<D>(TP)];        // K^T: [channel][token]
-    __shared__ __align__(16) uint16_t sP[2][OUT ? pm_shorts<BL>(TP) : 8];   // scores, upper and lower parts
+    __shared__ __align__(16) uint16_t sP[3][OUT ? pm_shorts<BL>(TP) : 8];   // scores in parts
     __shared__ Gates<BL> s_gate[2];                                // of this chunk and the next
 
     const int t = threadIdx.x, lane = t & 63;
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     }
     if constexpr (OUT) {
         // score tiles right of the diagonal inside a 32-token step: zeros, never written again
-        for (int e = t; e < 2 * 2 * 16 * 8; e += NT) {
+        for (int e = t; e < 3 * 2 * 16 * 8; e += NT) {
             const int part = e >> 8, blk = (e >> 7) & 1, row = (e >> 3) & 15, c = e & 7;
             *reinterpret_cast<uint32_t*>(&sP[part][pm<BL>(32 * blk + row, 4 * blk + 2 + (c >> 2)) + 2 * (c & 3)]) = 0;
         }
@@ -278,8 +279,10 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                     float p = __expf((float)(sG[n] - gi)) * acc[v];
                     if (r == c) p = li <= 4 * lg + v ? p : 0.0f;
                     const int to = pm<BL>(n, 2 * c) + pm<BL>(0, li >> 3) + (li & 7);
+                    const float p1 = p - top_f32(p);
                     sP[0][to] = (uint16_t)(__float_as_uint(p) >> 16);
-                    sP[1][to] = (uint16_t)(__float_as_uint(p - top_f32(p)) >> 16);
+                    sP[1][to] = (uint16_t)(__float_as_uint(p1) >> 16);
+                    sP[2][to] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -289,25 +292,24 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
             for (int r = 0; r < 4; ++r) O[r][0] = O[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks) {
-                u32x4 bh[2], bl[2];
+                u32x4 b[2][3];
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
+                for (int ct = 0; ct < 2; ++ct) {
+                    float x[8];
+                    uint32_t p[3][4];
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const v4f x = H[2 * ks + hf][ct];
-                        bh[ct][2 * hf] = top_halves(x[0], x[1]);
-                        bh[ct][2 * hf + 1] = top_halves(x[2], x[3]);
-                        bl[ct][2 * hf] = pack_bf16(x[0] - top_f32(x[0]), x[1] - top_f32(x[1]));
-                        bl[ct][2 * hf + 1] = pack_bf16(x[2] - top_f32(x[2]), x[3] - top_f32(x[3]));
-                    }
+                    for (int e = 0; e < 8; ++e) x[e] = H[2 * ks + e / 4][ct][e % 4];
+                    split3<8>(x, p);
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) b[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+                }
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[at + pm<BL>(16 * r, 4 * ks)]);
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) {
-                        O[r][ct] = mfma_bf16(aq, bh[ct], O[r][ct]);
-                        O[r][ct] = mfma_bf16(aq, bl[ct], O[r][ct]);
-                    }
+                    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+                        for (int m = 2; m >= 0; --m) O[r][ct] = mfma_bf16(aq, b[ct][m], O[r][ct]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -344,7 +346,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 #pragma unroll
                 for (int j = 0; j <= r / 2; ++j)
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
+                    for (int part = 2; part >= 0; --part) {
                         const u32x4 ap = *reinterpret_cast<const u32x4*>(&sP[part][at + pm<BL>(16 * r, 4 * j)]);
 #pragma unroll
                         for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(ap, V[j][ct], O[r][ct]);
@@ -363,7 +365,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
                             for (int v = 0; v < 4; ++v) {
                                 const int n = 16 * r + lq + v;
                                 const int from = pm<BL>(n, i >> 3) + (i & 7);
-                                const float p = n < i ? 0.0f : bf16_to_f32(sP[0][from]) + bf16_to_f32(sP[1][from]);
+                                const float p = n < i ? 0.0f : bf16_to_f32(sP[0][from]) + bf16_to_f32(sP[1][from]) + bf16_to_f32(sP[2][from]);
                                 if (n >= i && (od & 0x8000u)) O[r][0][v] += p * lo_f32(x);
                                 if (n >= i && (od & 0x80000000u)) O[r][1][v] += p * hi_f32(x);
                             }

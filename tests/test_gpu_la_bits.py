@@ -1,0 +1,118 @@
+"""How many bits of their operands linear attention and drafted trees keep.
+
+Queries and keys hold one channel each, no two keys the same one, so that every
+output and every value of a state is a single product of a few operands, whose
+64-bit value and rounding errors are known.  An operand in two bf16 parts is off by
+up to 2^-16 (the second rounded) or 2^-15 (truncated); the bounds below are 2^-18.7
+of a value up to one chunk, 2^-17.9 at most.
+
+Bounds, in units of 2^-23 of the value, |g| <= 0.7 for every exponent:
+  exponential of a difference of log decays: the logarithms 2 ulp each (1.4), a path
+  sum in fp32 at most 8 roundings of g (2.8; prompts: one, 0.4), the product with log2(e)
+  1.1, the function 1 ulp (1);                                            6.3 (prompts 3.9)
+  a product with an operand in exact bf16 parts: the sum of three products  1
+  a product of two fp32 values in three truncated parts: the parts left out are at
+  most 2^-7 2^-15 + 2^-15 2^-7 + 2^-15 2^-15 of it (4.1), the sum of six 2.5  6.6
+  every other product or scaling by an fp32 value                         0.5
+  a chunk's rescaling of the state 0.5, its exponential 1 besides the shares of g above  1.5
+"""
+import math
+
+import pytest
+import torch
+
+from recurrent_state_quant_lq_amd import lq
+
+pytestmark = pytest.mark.gpu
+IO = {"f32": (lq.LQ_IO_F32, torch.float32), "bf16": (lq.LQ_IO_BF16, torch.bfloat16)}
+UNIT = 2.0 ** -23
+# prompt outputs, bf16: 3.9 + 0.5 (e^g) + 1 (scores or state) + 1 (values, or the state's own update);
+# trees 6.3 + 4 x 0.5 + 1 + 1; fp32: two products of split operands in place of the two exact ones
+BITS = {"bf16": 11 * UNIT, "f32": 24 * UNIT}
+
+
+def prompt_bits(io, T):
+    """BITS and the rescalings of at most T/16 + 1 chunks (of 32 and 64 tokens at d >= 64)."""
+    return BITS[io] + 0.75 * math.ceil(T / 16) * UNIT
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    lq.load()
+
+
+def values(g, *s, dtype=torch.float32):
+    """+-[1, 2), every bit of the mantissa in use."""
+    x = 1 + torch.rand(s, generator=g, dtype=torch.float64)
+    return (x * torch.where(torch.rand(s, generator=g) < 0.5, -1.0, 1.0)).to(dtype)
+
+
+def one_hot(at, x, d):
+    """[..., d] with x at channel at."""
+    out = torch.zeros(*x.shape, d, dtype=x.dtype)
+    return out.scatter_(-1, at[..., None].expand(*x.shape, 1), x[..., None])
+
+
+def rounded(got, ref, off, what):
+    """got is the rounding to its type of a value within off of ref."""
+    got = got.cpu()
+    # (the bounds are rounded through fp32: 2^-24 more)
+    lo, hi = ((ref + s * (off + 2.0 ** -24) * ref.abs()).to(got.dtype).double() for s in (-1, 1))
+    bad = (got.double() < lo) | (got.double() > hi)
+    assert not bool(bad.any()), f"{what}: {int(bad.sum())} of {bad.numel()} values off by more than {off / UNIT:.0f} units"
+
+
+def run_prefill(q, k, v, alpha, h0, io):
+    T, B, H, d = q.shape
+    dims = lq.make_dims(B, H, d, d, 16, 4, lq.LQ_DECAY_SCALAR, 1, IO[io][0])
+    o = torch.zeros((T, B, H, d), dtype=IO[io][1], device="cuda")
+    h = torch.zeros((B, H, d, d), device="cuda")
+    lq.lq_la_prefill(dims, None, None if h0 is None else h0.cuda(), h, T, q.cuda(), k.cuda(), v.cuda(), alpha.cuda(), o)
+    torch.cuda.synchronize()
+    return o, h
+
+
+def earlier(g, T, *s):
+    """An index i <= n for every n."""
+    n = torch.arange(T).reshape(T, *[1] * len(s)).expand(T, *s)
+    return torch.minimum((torch.rand((T, *s), generator=g) * (n + 1)).long(), n)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,T", [(16, 16), (64, 64), (128, 64), (128, 128), (128, 4)])
+@pytest.mark.parametrize("B,H", [(2, 6), (3, 50)])
+def test_prompt_scores_and_state_update(B, H, d, T, io):
+    """o_n = e^{g_n - g_i} <q_n, k_i> v_i for one i, h = e^{g_T - g_i} k_i v_i^T."""
+    g = torch.Generator().manual_seed(d + T)
+    t = IO[io][1]
+    at = torch.arange(T)[:, None, None].expand(T, B, H)
+    src = earlier(g, T, B, H)
+    kx, qx, v = values(g, T, B, H, dtype=t), values(g, T, B, H, dtype=t), values(g, T, B, H, d, dtype=t)
+    alpha = 1 - (0.64 / T) * torch.rand((T, B, H), generator=g)
+    o, h = run_prefill(one_hot(src, qx, d), one_hot(at, kx, d), v, alpha, None, io)
+    G = alpha.double().log().cumsum(0)
+    pick = lambda x: x.double().gather(0, src)
+    e = (G - G.gather(0, src)).exp()
+    ref = (e * qx.double() * pick(kx))[..., None] * v.double().gather(0, src[..., None].expand(T, B, H, d))
+    rounded(o, ref, prompt_bits(io, T), "o")
+    rh = ((G[-1] - G).exp() * kx.double())[..., None] * v.double()                # [T,B,H,d]
+    rounded(h[:, :, :T], rh.permute(1, 2, 0, 3), prompt_bits(io, T), "h")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("d,T", [(16, 40), (64, 64), (64, 200), (128, 64), (128, 200), (128, 3)])
+@pytest.mark.parametrize("B,H", [(2, 6), (3, 50)])
+def test_prompt_state(B, H, d, T, io):
+    """o_n = e^{g_n} H0^T q_n for a query of one channel; keys are zero."""
+    g = torch.Generator().manual_seed(d + T)
+    t = IO[io][1]
+    at = torch.randint(0, d, (T, B, H), generator=g)
+    qx, v, h0 = values(g, T, B, H, dtype=t), values(g, T, B, H, d, dtype=t), values(g, B, H, d, d)
+    alpha = 1 - (0.64 / T) * torch.rand((T, B, H), generator=g)
+    o, h = run_prefill(one_hot(at, qx, d), torch.zeros((T, B, H, d), dtype=t), v, alpha, h0, io)
+    G = alpha.double().log().cumsum(0)
+    rows = torch.stack([h0.double().gather(2, at[n][..., None, None].expand(B, H, 1, d))[:, :, 0] for n in range(T)])
+    rounded(o, (G.exp() * qx.double())[..., None] * rows, prompt_bits(io, T), "o")
+    rounded(h, G[-1].exp()[..., None, None] * h0.double(), (4 + 0.75 * math.ceil(T / 16)) * UNIT, "h")
