@@ -394,9 +394,9 @@ int lq_la_decode_step_ragged(const lq_dims *d, const lq_state *st, const int32_t
  *   tree_m  fp32 [B,H,N,dv], tree_g fp32 [B,H,N,gd], out: the window slots
  *           that the nodes would become (lq_tree_commit).
  * Nodes' depth is not bounded by the window; committed paths are.  A
- * non-finite node reaches itself and its descendants only.  For
- * lq_la_tree_step with bf16 tokens the products, which reach only o, keep at
- * least 16 bits (2^-16 of a sum of absolute values).
+ * non-finite node reaches itself and its descendants only.  Sums are in fp32
+ * and operands keep fp32's 24 bits (d >= 64: a product of two fp32 tokens, or
+ * with per-key decay of two decayed rows, is off by at most 2^-21 of itself).
  */
 int lq_gdn_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, int32_t N,
                      const int32_t *parent, const void *q, const void *k, const void *v,

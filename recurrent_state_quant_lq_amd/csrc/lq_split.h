@@ -86,18 +86,6 @@ __device__ __forceinline__ void split3(const float (&x)[N], uint32_t (&p)[3][N /
     }
 }
 
-// The same in two parts (the second rounded to nearest even: 2^-17 of the value is lost) or three.
-template <int P, int N>
-__device__ __forceinline__ void split(const float (&x)[N], uint32_t (&p)[P][N / 2]) {
-    if constexpr (P == 3) split3<N>(x, p);
-    else
-#pragma unroll
-        for (int e = 0; e < N / 2; ++e) {
-            p[0][e] = top_halves(x[2 * e], x[2 * e + 1]);
-            p[1][e] = pack_bf16(x[2 * e] - top_f32(x[2 * e]), x[2 * e + 1] - top_f32(x[2 * e + 1]));
-        }
-}
-
 // c += a b, a and b in three parts each; small products first.
 __device__ __forceinline__ v4f mfma_split(const u32x4 (&a)[3], const u32x4 (&b)[3], v4f c) {
     c = mfma_bf16(a[2], b[0], c);

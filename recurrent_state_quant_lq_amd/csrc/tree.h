@@ -222,7 +222,7 @@ struct TreeTables {
 // exists, so that no load sits behind a branch.
 // Bound by the issue of these phases and, with two workgroups a CU (per-key decay: LDS), by
 // their latencies.  d = 128, 2048 heads, bf16: delta rule, 32 nodes 50 us (vector unit 23,
-// matrix unit 15; 3.0 TB/s), 64 nodes without it 68 us (3.4 TB/s); 1024 heads, per-key decay,
+// matrix unit 15; 3.0 TB/s), 64 nodes without it 74 us (3.1 TB/s); 1024 heads, per-key decay,
 // 21 nodes, fp32 46 us.
 // A product of a masked zero with a value that is not finite would spread it: if any
 // m is not finite, the row is computed again node after node.
@@ -231,9 +231,10 @@ struct TM {
     static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr bool KDA = RULE == TREE_KDA, DELTA = RULE != TREE_LA;
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
-    // parts of the window's keys and of the scaled state: three (24 bits); two (16 bits and a rounding,
-    // 2^-17 of a term) where they reach only bf16 outputs, which keep 2^-8
-    static constexpr int NS = !DELTA && sizeof(TI) == 2 ? 2 : 3;
+    // parts of the window's keys and of the scaled state: three, all 24 bits (plain linear attention, bf16,
+    // 2048 heads: with these and the nodes' scores in two parts 36 us, not 41, for 32 nodes and 68, not 74,
+    // for 64, but 0.3% of the outputs, not 0.01%, then round to a neighbour of what fp32 sums round to)
+    static constexpr int NS = 3;
     // parts of the state: where rows have three parts, the int8 values are kept as they are (exact
     // in bf16) and the rows are formed again after the scores, scaled by r (per-key decay: by
     // r o e^{g_n}): half the products of the state in three parts, and no splits of it for each
@@ -246,9 +247,8 @@ struct TM {
     static constexpr bool RK = KDA && 16 * NB * D * sizeof(TI) <= 16384;   // (else they are read from memory)
     static constexpr int QS = D + 8;                               // shorts per row
     static constexpr int WC = 16 * WT;                             // window columns of the scores
-    // plain linear attention, bf16: m = v is exact in bf16, so the nodes' scores are kept in two
-    // bf16 parts (off by 2^-16 of themselves, against the 2^-8 of the output) and meet the values
-    // of two blocks in one bf16 matrix instruction a part
+    // plain linear attention, bf16: m = v is exact in bf16, so the nodes' scores are kept in three
+    // bf16 parts and meet the values of two blocks in one bf16 matrix instruction a part
     static constexpr bool VB = !DELTA && sizeof(TI) == 2;
     static constexpr int SS = WC + (VB ? 0 : 16 * NB) + 4;         // floats per score row
     static constexpr int SB = VB ? 16 * NB + 8 : 8;                // shorts per row of the nodes' scores in parts
@@ -263,7 +263,7 @@ struct TM {
         __align__(16) uint16_t k[NP][16 * KB * QS];
         __align__(16) uint16_t wk[NS][WC * QS];
         __align__(16) float s[DELTA ? 2 : 1][16 * GB * SS];        // scores of q; -beta times those of k
-        __align__(16) uint16_t sb[2][VB ? 16 * GB * SB : 8];
+        __align__(16) uint16_t sb[3][VB ? 16 * GB * SB : 8];
         __align__(16) float gk[KDA ? 16 * NB * D : 4];             // per-key decay: g_n
         __align__(16) float gp[KDA ? D : 4];                       // per-key decay: g of slot pos - 1
         __align__(16) TI kr[RK ? 16 * NB * D : 8];                 // per-key decay: the nodes' keys as they are
@@ -276,7 +276,7 @@ struct TM {
         } f;
     };
     // waves per SIMD the registers are sized for: the workgroups that fit the LDS of a CU, 3 at
-    // most (2 with 64 nodes, whose registers would spill: 92 us instead of 68, plain rule)
+    // most (2 with 64 nodes, whose registers would spill: a third slower, plain rule)
     static constexpr int FIT = 160 * 1024 / (int)sizeof(Space) * NW / 4;
     static constexpr int WPE = FIT >= 3 && NB == 2 ? 3 : FIT >= 2 ? 2 : 1;
 };
@@ -756,7 +756,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
             if constexpr (KDA) wx[c][u] *= expf(s.gp[c8 + u] - wgc[c][u]);
             wx[c][u] = on ? wx[c][u] : 0.0f;
         }
-        split<NS, 8>(wx[c], p);
+        split3<8>(wx[c], p);
 #pragma unroll
         for (int m = 0; m < NS; ++m)
             *reinterpret_cast<u32x4*>(&s.wk[m][(16 * c + row) * QS + c8]) = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
@@ -935,8 +935,10 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                         const float z = ((anc >> i) & 1u) || (!x && i == n0 + v) ? y : 0.0f;
                         if constexpr (VB) {
                             const int to = (16 * e + 4 * lg + v) * SB + i;
+                            const float z1 = z - top_f32(z);
                             s.sb[0][to] = (uint16_t)(__float_as_uint(z) >> 16);
-                            s.sb[1][to] = (uint16_t)(pack_bf16(z - top_f32(z), 0.0f) & 0xffffu);
+                            s.sb[1][to] = (uint16_t)(__float_as_uint(z1) >> 16);
+                            s.sb[2][to] = (uint16_t)(__float_as_uint(z1 - top_f32(z1)) >> 16);
                         } else {
                             dst[v * SS + WC + 16 * (c - wt)] = z;
                         }
@@ -1077,7 +1079,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                             uint32_t p[NT8][4];
 #pragma unroll
                             for (int u = 0; u < 8; ++u) x8[u] = sbyte((uint32_t)raw[ks][ct][2 * hf + u / 4], u % 4) * r[u];
-                            split<NT8, 8>(x8, p);
+                            split3<8>(x8, p);
 #pragma unroll
                             for (int m = 0; m < NT8; ++m) st[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
                         }
@@ -1175,7 +1177,7 @@ __global__ __launch_bounds__((TM<D, NB, WT, RULE, TI>::NT), (TM<D, NB, WT, RULE,
                         vb[ct] = u32x4{lo[0], lo[1], hi[0], hi[1]};
                     }
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
+                    for (int part = 2; part >= 0; --part) {
                         const uint16_t* sr = &s.sb[part][(16 * e + li) * SB + 32 * c + 4 * lg];
                         const u32x2 lo = *reinterpret_cast<const u32x2*>(sr), hi = two ? *reinterpret_cast<const u32x2*>(sr + 16) : u32x2{0, 0};
 #pragma unroll

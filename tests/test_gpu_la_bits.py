@@ -36,6 +36,11 @@ def prompt_bits(io, T):
     return BITS[io] + 0.75 * math.ceil(T / 16) * UNIT
 
 
+def tree_bits(io, rule):
+    """Rows scaled by a decay per key have 24 bits, whatever the tokens' type."""
+    return BITS["f32" if rule == "kda" else io]
+
+
 @pytest.fixture(scope="module", autouse=True)
 def _gpu():
     if not torch.cuda.is_available():
@@ -116,3 +121,97 @@ def test_prompt_state(B, H, d, T, io):
     rows = torch.stack([h0.double().gather(2, at[n][..., None, None].expand(B, H, 1, d))[:, :, 0] for n in range(T)])
     rounded(o, (G.exp() * qx.double())[..., None] * rows, prompt_bits(io, T), "o")
     rounded(h, G[-1].exp()[..., None, None] * h0.double(), (4 + 0.75 * math.ceil(T / 16)) * UNIT, "h")
+
+
+def tree_state(g, B, H, d, W, C, io, per_key, codec):
+    dims = lq.make_dims(B, H, d, d, W, C, lq.LQ_DECAY_PER_KEY if per_key else lq.LQ_DECAY_SCALAR, 1, IO[io][0])
+    st = lq.LayerState.allocate(dims)
+    sq = torch.randint(-127, 128, (B, H, d, d), generator=g, dtype=torch.int8) if codec else torch.zeros((B, H, d, d), dtype=torch.int8)
+    r, s = values(g, B, H, d).abs() / 128, values(g, B, H, d).abs()
+    idx = torch.stack([torch.randperm(d, generator=g)[:C].sort().values for _ in range(B * H)]).reshape(B, H, C)
+    sq.scatter_(2, idx[..., None].expand(B, H, C, d), 0)
+    cv = values(g, B, H, C, d) if codec else torch.zeros(B, H, C, d)
+    st.load_codec(dict(sq=sq.numpy(), r=r.numpy(), s=s.numpy(), idx=idx.to(torch.int32).numpy(), cv=cv.numpy()))
+    hb = sq.double() * r.double()[..., None] * s.double()[..., None, :]
+    return st, hb.scatter_add(2, idx[..., None].expand(B, H, C, d), cv.double())
+
+
+def run_tree(st, rule, pos, parent, q, k, v, alpha, beta):
+    N, B, H, d = q.shape
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    o = torch.zeros((N, B, H, d), dtype=q.dtype, device="cuda")
+    tm, tg = torch.zeros((B, H, N, d), device="cuda"), torch.zeros((B, H, N, st.buf_g.shape[-1]), device="cuda")
+    args = [x.cuda() for x in (q, k, v, alpha)]
+    if rule == "la":
+        lq.lq_la_tree_step(st, i32([pos] * B), i32([parent] * B), *args, o, tm, tg)
+    else:
+        lq.lq_gdn_tree_step(st, i32([pos] * B), i32([parent] * B), *args, beta.cuda(), o, tm, tg)
+    torch.cuda.synchronize()
+    return o, tm
+
+
+RULES = [(rule, io, d) for rule in ("la", "gdn", "kda") for io in ("f32", "bf16") for d in (16, 64, 128)]
+
+
+@pytest.mark.parametrize("N", [13, 32, 64])
+@pytest.mark.parametrize("rule,io,d", RULES)
+def test_tree_state_and_window(rule, io, d, N):
+    """o_n = e^{g_n} Hb^T q_n (no slots), then o_n = e^{g_n - g_c} <q_n, k_c> m_c for one slot c (no state).
+    The drafted keys are zero; a chain."""
+    B, H, W, C = 2, 4, 16, 3
+    g = torch.Generator().manual_seed(N + d)
+    t, per_key = IO[io][1], rule == "kda"
+    lead = (N, B, H, d) if per_key else (N, B, H)
+    qx, v = values(g, N, B, H, dtype=t), values(g, N, B, H, d, dtype=t)
+    alpha, beta = 1 - (0.3 / N) * torch.rand(lead, generator=g), 0.1 + 0.8 * torch.rand((N, B, H), generator=g)
+    parent, zero = list(range(-1, N - 1)), torch.zeros((N, B, H, d), dtype=t)
+    G = alpha.double().log().cumsum(0)
+    of = lambda x, at: x.gather(-1, at[..., None])[..., 0] if per_key else x      # the query's channel of a log decay
+
+    st, hb = tree_state(g, B, H, d, W, C, io, per_key, True)
+    at = torch.randint(0, d, (N, B, H), generator=g)
+    o, _ = run_tree(st, rule, 0, parent, one_hot(at, qx, d), zero, v, alpha, beta)
+    rows = torch.stack([hb.gather(2, at[n][..., None, None].expand(B, H, 1, d))[:, :, 0] for n in range(N)])
+    rounded(o, (of(G, at).exp() * qx.double())[..., None] * rows, tree_bits(io, rule), "o of the state")
+
+    st, _ = tree_state(g, B, H, d, W, 0, io, per_key, False)
+    slot = torch.randint(0, W, (N, B, H), generator=g)
+    ch = torch.stack([torch.randperm(d, generator=g)[:W] for _ in range(B * H)]).reshape(B, H, W)
+    kx, m = values(g, B, H, W), values(g, B, H, W, d)
+    bg = -(0.3 / W) * torch.rand((B, H, W, st.buf_g.shape[-1]), generator=g)
+    bg = bg.cumsum(2)
+    st.buf_k.copy_(one_hot(ch, kx, d)), st.buf_m.copy_(m), st.buf_g.copy_(bg)
+    at = torch.stack([ch.gather(2, slot[n][..., None])[..., 0] for n in range(N)])
+    o, _ = run_tree(st, rule, W, parent, one_hot(at, qx, d), zero, v, alpha, beta)
+    pick = lambda x, n: x.double().gather(2, slot[n][..., None, None].expand(B, H, 1, x.shape[-1]))[:, :, 0]
+    gc = torch.stack([pick(bg, n) for n in range(N)])                             # [N,B,H,gd]
+    gn = bg[:, :, -1].double() + (G if per_key else G[..., None])
+    e = (gn - gc).exp()
+    e = e.gather(-1, at[..., None])[..., 0] if per_key else e[..., 0]
+    ks = torch.stack([kx.double().gather(2, slot[n][..., None])[..., 0] for n in range(N)])
+    rounded(o, (e * qx.double() * ks)[..., None] * torch.stack([pick(m, n) for n in range(N)]),
+            tree_bits(io, rule), "o of the window")
+
+
+@pytest.mark.parametrize("rule,io,d", RULES)
+def test_tree_scores(rule, io, d):
+    """o_n = e^{g_n - g_i} <q_n, k_i> m_i for one ancestor i, m_i = beta_i v_i: no key meets another; a chain."""
+    B, H, W, N = 2, 4, 16, min(64, d)
+    g = torch.Generator().manual_seed(d)
+    t, per_key = IO[io][1], rule == "kda"
+    st, _ = tree_state(g, B, H, d, W, 0, io, per_key, False)
+    at = torch.arange(N)[:, None, None].expand(N, B, H)
+    src = earlier(g, N, B, H)
+    qx, kx, v = values(g, N, B, H, dtype=t), values(g, N, B, H, dtype=t), values(g, N, B, H, d, dtype=t)
+    alpha = 1 - (0.6 / N) * torch.rand((N, B, H, d) if per_key else (N, B, H), generator=g)
+    beta = 0.1 + 0.8 * torch.rand((N, B, H), generator=g)
+    o, tm = run_tree(st, rule, 0, list(range(-1, N - 1)), one_hot(src, qx, d), one_hot(at, kx, d), v, alpha, beta)
+    G = alpha.double().log().cumsum(0)
+    if per_key:                                                                   # of the channel of the key
+        gn, gi = G.gather(-1, src[..., None])[..., 0], G.gather(0, src[..., None].expand(N, B, H, d)).gather(-1, src[..., None])[..., 0]
+    else:
+        gn, gi = G, G.gather(0, src)
+    m = v.double() if rule == "la" else beta.double()[..., None] * v.double()
+    rounded(tm, m.permute(1, 2, 0, 3), UNIT, "m")
+    ref = ((gn - gi).exp() * qx.double() * kx.double().gather(0, src))[..., None] * m.gather(0, src[..., None].expand(N, B, H, d))
+    rounded(o, ref, tree_bits(io, rule), "o")
