@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes as ct
 import os
 from dataclasses import dataclass
+from operator import is_
 
 import numpy as np
 import torch
@@ -256,16 +257,23 @@ class LayerState:
 
     def ready(self, with_buffer=True) -> lq_state:
         """The C struct of this state, validated (shapes, dtypes, device) once
-        for the tensors the fields hold; a field replaced by another tensor is
-        validated again.  In-place writes to the tensors need no revalidation."""
-        key = (id(self.sq), id(self.row_scale), id(self.col_scale), id(self.comp_idx), id(self.comp_val),
-               id(self.buf_k), id(self.buf_m), id(self.buf_g), with_buffer)
+        for the dims and the tensors the fields hold; dims changed, a field
+        replaced by another tensor or a tensor whose memory was exchanged
+        (set_, .data) are validated again.  In-place writes to the tensors need
+        no revalidation.  The entry holds the tensors it was formed from, so
+        that another tensor cannot pass for one of them."""
+        fields = (self.sq, self.row_scale, self.col_scale, self.comp_idx, self.comp_val, self.buf_k, self.buf_m,
+                  self.buf_g)
+        try:
+            key = (with_buffer, bytes(self.dims), *map(torch.Tensor.data_ptr, fields))
+        except TypeError:                                # a codec without a window buffer
+            key = (with_buffer, bytes(self.dims), *map(_ptr, fields))
         c = self.__dict__.get("_ready")
-        if c is None or c[0] != key:
+        if c is None or c[0] != key or not all(map(is_, c[1], fields)):
             self.check(with_buffer)
-            c = (key, self.c_state())
+            c = (key, fields, self.c_state())
             self.__dict__["_ready"] = c
-        return c[1]
+        return c[2]
 
     def codec(self) -> dict:
         """Host copies of the codec arrays, int8 matrix row-major [B,H,dk,dv]
