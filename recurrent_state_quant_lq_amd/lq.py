@@ -241,6 +241,10 @@ class LayerState:
             _check(self.buf_k, "buf_k", (B, H, W, dk), torch.float32)
             _check(self.buf_m, "buf_m", (B, H, W, dv), torch.float32)
             _check(self.buf_g, "buf_g", (B, H, W, gd), torch.float32)
+        for n in _STATE_FIELDS if with_buffer else _STATE_FIELDS[:5]:
+            t = getattr(self, n)
+            if t.device != self.sq.device:
+                raise ValueError(f"{n} on {t.device}, sq on {self.sq.device}")
 
     def c_state(self) -> lq_state:
         return lq_state(*[_ptr(getattr(self, n)) for n in _STATE_FIELDS])

@@ -96,3 +96,11 @@ def test_a_codec_without_a_buffer(seen):
 
 def pointers_of_codec(st):
     return [getattr(st, n).data_ptr() for n in lq._STATE_FIELDS[:5]]
+
+
+@pytest.mark.parametrize("name", lq._STATE_FIELDS[1:])
+def test_a_state_on_two_devices_is_refused(seen, name):
+    st = state()
+    setattr(st, name, torch.zeros_like(getattr(st, name), device="meta"))
+    with pytest.raises(ValueError, match=name):
+        st.ready()
