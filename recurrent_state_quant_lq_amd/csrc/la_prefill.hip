@@ -167,7 +167,7 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
     // (each phase of the chunk loop forms its lane indices anew: addresses kept across the
     // phases would spill, and a reload waits for the loads in flight)
     constexpr int OPW = 128 / D;                                   // octets per wave and pass (D = 64: 2)
-    const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= kChunkHeads)
+    const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= chunk_heads(D))
     uint32_t kd[2][8], vd[2][8];
     u32x4 qd[4];
     auto rows = [&](const void* x, int c0) {                       // tokens c0 .. min(c0 + BL, te) - 1 of this head
@@ -496,7 +496,7 @@ __global__ __launch_bounds__(LF<D>::NT, 2) void la_chunk32_kernel(LaSegArgs a) {
     // chunk loads, one chunk ahead; tokens past the end read as zeros
     constexpr int CPR = D / 8;                                     // 8-channel pieces per row
     static_assert(NT / CPR == FL && NT / D == FL / 8, "one piece and one octet per thread");
-    const uint32_t rb = (uint32_t)heads * (4 * D);                 // bytes between tokens (heads <= kChunkHeads)
+    const uint32_t rb = (uint32_t)heads * (4 * D);                 // bytes between tokens (heads <= chunk_heads(D))
     uint32_t kt[8], vr[8];
     u32x4 qr[2], kr[2];
     auto rows = [&](const void* x, int c0) {                       // tokens c0 .. min(c0 + FL, te) - 1 of this head
@@ -776,7 +776,10 @@ __global__ __launch_bounds__(256) void la_step_kernel(LaPrefillArgs a) {
     for (int p = 0; p < NP; ++p)
         __builtin_nontemporal_store(H[p], reinterpret_cast<v4f*>(a.h + head * (size_t)(D * D) + (size_t)(p * RPP + rg) * D + c0));
 }
-constexpr int kChunkHeads = 1 << 17;   // a chunk's rows lie within 32-bit byte offsets (64 rows of 256 B, 32 of 512 B)
+// Heads that the chunk kernels take: at d >= 64 a chunk's rows lie within 32-bit byte offsets (64 rows of
+// 2 d bytes a head, 32 of 4 d); d = 16 has offsets in 64 bits.  More heads take the recurrence itself:
+// 131200 heads of 64 (512) tokens, bf16, 1.6 (5.7) ms by chunks, 5.9 (13.4) ms token after token at d = 64 (16).
+constexpr size_t chunk_heads(int d) { return d == 16 ? (size_t)INT32_MAX : (size_t)(1 << 24) / d; }
 
 // ---------------------------------------------------------------------------
 // d = 16: chunks of 16 tokens, one wave a segment, no LDS
@@ -1002,7 +1005,7 @@ hipError_t la_chunks(const lq_dims& d, const LaPrefillArgs& args, void* workspac
 template <int D, typename TI>
 hipError_t la_prefill_t(const lq_dims& d, const LaPrefillArgs& args, void* workspace, hipStream_t s) {
     const dim3 grid((unsigned)args.heads);
-    if (args.T <= kStepTokens || args.heads > kChunkHeads)
+    if (args.T <= kStepTokens || (size_t)args.heads > chunk_heads(D))
         return launch_kernel(LQ_KERNEL_LA_PREFILL, la_step_kernel<D, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
     return la_chunks<D, TI>(d, args, workspace, s);
 }
@@ -1017,7 +1020,7 @@ hipError_t la_prefill_d(const lq_dims& d, const LaPrefillArgs& args, void* works
 
 size_t la_workspace_bytes(const lq_dims& d, int T) {
     const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d);
-    if (T <= kStepTokens || heads > (size_t)kChunkHeads) return 0;
+    if (T <= kStepTokens || heads > chunk_heads(d.dk)) return 0;
     // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
     const size_t segs = min(segments_wanted(heads, d.dk), ((size_t)T + chunk - 1) / chunk);
     return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
