@@ -56,7 +56,8 @@
  *     their own (every pointer advanced by b0 rows, lq_dims.B = b1 - b0), and
  *     calls on disjoint row ranges may run at the same time on different
  *     streams.  Each (row, head) is computed the same way whatever the batch
- *     of its call, so the results do not depend on the split.
+ *     of its call, so the results do not depend on the split, except for the
+ *     order of sums in lq_la_prefill's longer prompts of few heads (see there).
  */
 #ifndef LQ_H
 #define LQ_H
@@ -335,8 +336,15 @@ enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
  * form over an fp32 state.  Sums are in fp32 and operands keep fp32's 24 bits
  * (with fp32 tokens, d >= 64, a product of two of them is off by at most 2^-21
  * of itself).  A non-finite v reaches
- * its own column from its own token on.  The result does not depend on
- * earlier calls, on the workspace's content or on other rows.
+ * its own column from its own token on.  The result of a row does not depend
+ * on earlier calls, on the workspace's content or on what other rows hold.
+ * The order of its sums depends on B*H and T: where the heads of a batch
+ * leave most of the GPU idle, a prompt is cut into segments whose number
+ * follows from both, and such a prompt in a batch of another size, or padded
+ * to another T, agrees to rounding, not bit for bit.  Every call with T > 4
+ * (and at most 2^17 heads at d = 128, 2^18 at d = 64) that needs no workspace
+ * (lq_la_workspace_bytes = 0) computes a row in the same order, so that there
+ * its bits are the same whatever B and T.
  * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30; LQ_ERR_DIMS
  * for a bad alpha_kind; LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
