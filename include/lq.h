@@ -310,8 +310,10 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  * alpha = 0 forgets everything before the token (the log decay kept for it,
  * in buf_g and in sums, is -110: exp(-110) is 0 in fp32).  Values outside
  * [0, 1] are not checked.  A window's and a tree's log decays are sums in
- * fp32, so what follows a sum g of strong decays there is off by up to
- * 2^-23 |g| of itself; the prompt's sums are in 64 bits.
+ * fp32 of one logarithm a token: a sum g over n window slots and nodes of a
+ * path is off by at most (n + 4) 2^-23 |g|, and the exponential of the
+ * difference of two by as much of itself as both together.  The prompt's sums
+ * are in 64 bits.
  */
 enum lq_alpha_kind { LQ_ALPHA_TOKENS = 0, LQ_ALPHA_HEADS = 1 };
 

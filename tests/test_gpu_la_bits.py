@@ -215,3 +215,94 @@ def test_tree_scores(rule, io, d):
     rounded(tm, m.permute(1, 2, 0, 3), UNIT, "m")
     ref = ((gn - gi).exp() * qx.double() * kx.double().gather(0, src))[..., None] * m.gather(0, src[..., None].expand(N, B, H, d))
     rounded(o, ref, tree_bits(io, rule), "o")
+
+
+# ---------------------------------------------------------------------------
+# log decays as sums in fp32
+# ---------------------------------------------------------------------------
+
+def sum_off(n):
+    """A sum of n logarithms in fp32, relative: 2 ulp each, n additions (2^-24 each if they are rounded, 2^-23 if
+    cut as a matrix instruction may)."""
+    return (n + 4) * UNIT
+
+
+@pytest.mark.parametrize("rule,io,d", [(r, "f32", d) for r in ("la", "gdn", "kda") for d in (16, 64, 128)])
+@pytest.mark.parametrize("shape", ["chain", "binary"])
+def test_tree_sums_of_strong_decays(rule, io, d, shape):
+    """Log decays of 0 to -3 a token over 32 window slots and 64 nodes: the sums, and outputs that are one
+    exponential of their difference each (to a window slot, then to an ancestor)."""
+    B, H, W, N = 2, 3, 32, 64
+    g = torch.Generator().manual_seed(d)
+    per_key = rule == "kda"
+    gd = d if per_key else 1
+    # the window as decode steps leave it: sums in fp32, slot after slot
+    steps = -3 * torch.rand((B, H, W, gd), generator=g) ** 4
+    bg = steps.clone()
+    for i in range(1, W):
+        bg[:, :, i] = bg[:, :, i - 1] + steps[:, :, i]
+    alpha = torch.exp(-3 * torch.rand((N, B, H, d) if per_key else (N, B, H), generator=g) ** 4)
+    la = (alpha if per_key else alpha[..., None]).double().log()                  # [N,B,H,gd]
+    parent = [n - 1 if shape == "chain" else (n - 1) // 2 if n else -1 for n in range(N)]
+    path, depth = [], []
+    for n, p in enumerate(parent):
+        path.append(la[n] + (path[p] if p >= 0 else 0))
+        depth.append(1 + (depth[p] if p >= 0 else 0))
+    G = torch.stack(path) + bg[:, :, -1].double()
+    off = torch.tensor([sum_off(W + x) for x in depth], dtype=torch.float64)[:, None, None, None]
+    st, _ = tree_state(g, B, H, d, W, 0, io, per_key, False)
+    slots = min(W, d)
+    at = torch.arange(W) % d
+    kx, m = values(g, B, H, W), values(g, B, H, W, d)
+    kx[:, :, slots:] = 0.0                                                        # (no two keys of one channel)
+    st.buf_k.copy_(one_hot(at[None, None].expand(B, H, W), kx, d)), st.buf_m.copy_(m), st.buf_g.copy_(bg)
+    src = torch.randint(0, slots, (N, B, H), generator=g)
+    qx, v = values(g, N, B, H), values(g, N, B, H, d)
+    beta = torch.ones(N, B, H)
+    zero = torch.zeros(N, B, H, d)
+    o, _ = run_tree(st, rule, W, parent, one_hot(src, qx, d), zero, v, alpha, beta)
+    pick = lambda x: torch.stack([x.double().gather(2, src[n][..., None, None].expand(B, H, 1, x.shape[-1]))[:, :, 0] for n in range(N)])
+    last = lambda x: x.gather(-1, src[..., None])[..., 0] if per_key else x[..., 0]
+    gn, gc = last(G), last(pick(bg))
+    # (the window's own sums are inputs here; g_n's error and the difference's rounding, absolute in the exponent)
+    lim = (off[..., 0] * gn.abs() + UNIT * (gn - gc).abs()) + BITS["f32"]
+    ref = ((gn - gc).exp() * qx.double() * pick(kx[..., None])[..., 0])[..., None] * pick(m)
+    near = ((o.cpu().double() - ref).abs() <= lim[..., None] * ref.abs() + 1e-30)
+    assert bool(near.all()), f"{int((~near).sum())} outputs of the window"
+    # nodes: ancestor or self i, a channel of its own
+    if N <= d:
+        chan = torch.arange(N)[:, None, None].expand(N, B, H)
+        up = []
+        for n in range(N):
+            a = [n]
+            while parent[a[-1]] >= 0:
+                a.append(parent[a[-1]])
+            up.append(a[int(torch.randint(0, len(a), (1,), generator=g))])
+        up = torch.tensor(up)
+        kx = values(g, N, B, H)
+        st.buf_k.zero_()
+        o, tm = run_tree(st, rule, W, parent, one_hot(up[:, None, None].expand(N, B, H), qx, d), one_hot(chan, kx, d), v, alpha, beta)
+        pickc = lambda x: x.gather(-1, up[:, None, None, None].expand(N, B, H, 1))[..., 0] if per_key else x[..., 0]
+        gn, gi = pickc(G), pickc(G[up])
+        lim = (off[..., 0] * gn.abs() + off[up][..., 0] * gi.abs() + UNIT * (gn - gi).abs()) + BITS["f32"]
+        ref = ((gn - gi).exp() * qx.double() * kx[up].double())[..., None] * v[up].double()
+        near = ((o.cpu().double() - ref).abs() <= lim[..., None] * ref.abs() + 1e-30)
+        assert bool(near.all()), f"{int((~near).sum())} outputs of the nodes"
+
+
+def test_window_sums_of_strong_decays():
+    """buf_g of 32 decode steps, alpha 0 (log decay -110) among them."""
+    B, H, d, W = 2, 3, 64, 32
+    g = torch.Generator().manual_seed(1)
+    dims = lq.make_dims(B, H, d, d, W, 0)
+    st = lq.LayerState.allocate(dims)
+    z = torch.zeros(B, H, d, device="cuda")
+    o = torch.zeros_like(z)
+    total = torch.zeros(B, H, dtype=torch.float64)
+    for n in range(W):
+        alpha = torch.exp(-5 * torch.rand((B, H), generator=g) ** 4)
+        alpha[1, 1] = 0.0 if n in (4, 20) else alpha[1, 1]
+        lq.lq_la_decode_step(st, n, z, z, z, alpha.cuda(), o)
+        total += torch.where(alpha == 0, torch.tensor(-110.0, dtype=torch.float64), alpha.double().log())
+        got = st.buf_g[:, :, n, 0].cpu().double()
+        assert bool(((got - total).abs() <= sum_off(n + 1) * total.abs() + 1e-30).all()), n
