@@ -45,7 +45,9 @@
  *   - Return value: LQ_OK or an LQ_ERR_* code.  Argument checks run first and
  *     make no HIP call; on any error nothing is enqueued.  LQ_ERR_HIP means a
  *     launch failed; lq_last_hip_error() gives the hipError_t.
- *   - Non-finite inputs are not checked; they propagate.
+ *   - Non-finite inputs are not checked; they propagate.  (lq_la_* and tree
+ *     calls: an infinity may arrive as NaN, where its operand enters a product
+ *     in parts.)
  *   - Supported: dk = dv in {16, 64, 128}; 1 <= W <= 32; 0 <= C <= 8.  The
  *     plain calls take one window position for the whole batch (lockstep);
  *     the *_ragged calls take one per batch row from a device array.
