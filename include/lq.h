@@ -422,9 +422,10 @@ int lq_la_tree_step(const lq_dims *d, const lq_state *st, const int32_t *pos, in
 /*
  * Appends accepted nodes of a tree step to the windows: for row b, slots
  * pos[b] .. pos[b] + n_path[b] - 1 become the nodes path[b][0..n_path[b]-1]
- * (k of that node widened to fp32, its tree_m and tree_g rows), exactly the
- * slots that decoding those tokens would have left.  The caller then advances
- * pos[b] by n_path[b].
+ * (k of that node widened to fp32, its tree_m and tree_g rows, copied as they
+ * are).  They are the slots that decoding those tokens would have left, to
+ * rounding: a tree step forms m and the sums g in another order.  The caller
+ * then advances pos[b] by n_path[b].
  *   path    int32 [B,P] (device, 4-byte aligned), the path from its root node
  *           on; n_path int32 [B] (device, 4-byte aligned);
  *   N, k, tree_m, tree_g  those of the tree step;
