@@ -941,13 +941,19 @@ __global__ __launch_bounds__(256) void la_scan_kernel(LaScanArgs a) {
 // Tokens per segment (a multiple of the chunk).  Segments cost a second read of k and v and
 // the states between them, so they pay where the heads alone leave most CUs idle: up to
 // `heads` heads, enough segments for `want` workgroups (as many as fit the GPU: two a CU at
-// d = 128, three at d = 64; d = 16: waves).  Measured, bf16 (fp32):
-//   d = 128, 2048 tokens: 96 heads 97 us (249) split, 168 (307) whole; 1024 tokens: 192 heads
-//   109 us (247) split, 91 (177) whole; 16 heads and 16384 tokens: 145, 117, 129 us
-//   (291, 282, 290) for 256, 512 and 768 workgroups;
-//   d = 64, 2048 tokens: 128 heads 65 us (87) split, 132 (164) whole; 256 heads 101 us (188)
-//   split, 132 (186) whole, 127 (196) for 512 workgroups; 512 heads, 1024 tokens: 115 us (189)
-//   split, 86 (122) whole;
+// d = 128, three at d = 64; d = 16: waves), and from three chunks on (the whole prompt is one
+// launch, segments are three).  Measured, bf16 (fp32), replayed in a graph:
+//   d = 128, 2048 tokens: 96 heads 109 us (187) split, 181 (271) whole; 1024 tokens: 192 heads
+//   110 us (210) split, 101 (148) whole; 16 heads and 16384 tokens: 161, 131, 139 us
+//   (253, 252, 272) for 256, 512 and 768 workgroups;
+//   d = 64, 2048 tokens: 128 heads 67 us (92) split, 146 (161) whole; 256 heads 107 us (186)
+//   split, 147 (177) whole, 134 (192) for 512 workgroups; 512 heads, 1024 tokens: 96 us (127)
+//   in two segments, 104 (127) whole;
+//   two chunks (65 tokens): 16 heads at d = 128 16.4 us (16.1) split, 14.3 (15.7) whole, 128
+//   heads 27 (33) split, 16 (17) whole; 16 heads at d = 64 13.2 (11.4) split, 12.0 (10.7) whole;
+//   three chunks (130 tokens) of 16 heads: 17.6 us (18.3) split, 19.8 (23.6) whole;
+//   (many heads lose by it: 128 heads of 130 tokens 31 us (40) split, 21 (25) whole, 512
+//   tokens 50 (80) split, 51 (72) whole; 256 heads of 130 tokens at d = 64 28 (26), 18 (17))
 //   d = 16, 512 tokens (segments of 8 chunks at least): 768 heads 41 us (43) split, 47 (44)
 //   whole; 1024 heads 51 (53) split, 48 (45) whole; 2048 heads 87 (94) split, 65 (62) whole,
 //   2.2 (4.4) TB/s.
@@ -956,14 +962,15 @@ struct Split {
 };
 constexpr Split kSplit128{128, 512}, kSplit64{256, 768}, kSplit16{768, 4096};
 constexpr size_t kMinSmall = 128;
-size_t segments_wanted(size_t heads, int d) {
+size_t segments_wanted(size_t heads, size_t chunks, int d) {
     const Split x = d == 16 ? kSplit16 : d == 64 ? kSplit64 : kSplit128;
-    return heads > x.heads ? 1 : x.want / heads;                  // (one round of workgroups)
+    if (heads > x.heads || (d >= 64 && chunks <= 2)) return 1;
+    return x.want / heads;                                        // (one round of workgroups)
 }
 int chunk_tokens(const lq_dims& d) { return d.dk == 16 ? (int)kMinSmall : d.io_dtype == LQ_IO_BF16 ? BL : FL; }
 int segment_tokens(const lq_dims& d, int T) {
     const size_t chunk = chunk_tokens(d), chunks = ((size_t)T + chunk - 1) / chunk;
-    const size_t want = segments_wanted((size_t)d.B * d.H, d.dk);
+    const size_t want = segments_wanted((size_t)d.B * d.H, chunks, d.dk);
     return (int)((chunks + want - 1) / want * chunk);
 }
 
@@ -1019,10 +1026,10 @@ hipError_t la_prefill_d(const lq_dims& d, const LaPrefillArgs& args, void* works
 }  // namespace
 
 size_t la_workspace_bytes(const lq_dims& d, int T) {
-    const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d);
+    const size_t heads = (size_t)d.B * d.H, chunk = chunk_tokens(d), chunks = ((size_t)T + chunk - 1) / chunk;
     if (T <= kStepTokens || heads > chunk_heads(d.dk)) return 0;
     // segment_tokens gives at most min(want, chunks) segments; that bound grows with T
-    const size_t segs = min(segments_wanted(heads, d.dk), ((size_t)T + chunk - 1) / chunk);
+    const size_t segs = min(segments_wanted(heads, chunks, d.dk), chunks);
     return segs <= 1 ? 0 : segs * heads * ((size_t)d.dk * d.dv + 4) * sizeof(float);
 }
 
