@@ -12,7 +12,6 @@ from __future__ import annotations
 import ctypes as ct
 import os
 from dataclasses import dataclass
-from operator import is_
 
 import numpy as np
 import torch
@@ -217,6 +216,11 @@ class LayerState:
     buf_m: torch.Tensor
     buf_g: torch.Tensor
 
+    def __setattr__(self, name, value):
+        """A field set anew drops what ready() keeps."""
+        self.__dict__[name] = value
+        self.__dict__["_ready"] = None
+
     @staticmethod
     def allocate(d: lq_dims, device="cuda") -> "LayerState":
         B, H, dk, dv, W, C = d.B, d.H, d.dk, d.dv, d.W, d.C
@@ -264,20 +268,19 @@ class LayerState:
         for the dims and the tensors the fields hold; dims changed, a field
         replaced by another tensor or a tensor whose memory was exchanged
         (set_, .data) are validated again.  In-place writes to the tensors need
-        no revalidation.  The entry holds the tensors it was formed from, so
-        that another tensor cannot pass for one of them."""
-        fields = (self.sq, self.row_scale, self.col_scale, self.comp_idx, self.comp_val, self.buf_k, self.buf_m,
-                  self.buf_g)
+        no revalidation."""
         try:
-            key = (with_buffer, bytes(self.dims), *map(torch.Tensor.data_ptr, fields))
-        except TypeError:                                # a codec without a window buffer
-            key = (with_buffer, bytes(self.dims), *map(_ptr, fields))
-        c = self.__dict__.get("_ready")
-        if c is None or c[0] != key or not all(map(is_, c[1], fields)):
+            key = (with_buffer, bytes(self.dims), self.sq.data_ptr(), self.row_scale.data_ptr(),
+                   self.col_scale.data_ptr(), self.comp_idx.data_ptr(), self.comp_val.data_ptr(),
+                   self.buf_k.data_ptr(), self.buf_m.data_ptr(), self.buf_g.data_ptr())
+        except AttributeError:                           # a codec without a window buffer
+            key = (with_buffer, bytes(self.dims), *(_ptr(getattr(self, n)) for n in _STATE_FIELDS))
+        c = self._ready
+        if c is None or c[0] != key:
             self.check(with_buffer)
-            c = (key, fields, self.c_state())
+            c = (key, self.c_state())
             self.__dict__["_ready"] = c
-        return c[2]
+        return c[1]
 
     def codec(self) -> dict:
         """Host copies of the codec arrays, int8 matrix row-major [B,H,dk,dv]
