@@ -46,8 +46,8 @@ struct LaPrefillArgs {
 // token are exact and accumulate in fp32:
 //   state update   K^T (w o V), w_t = e^{g_L - g_t}: w v in parts;
 //   outputs        Q H with H in parts and (E o Q K^T) V with the scores in parts.
-// (H and the scores in two parts, 16 bits: 303 us, not 332, for 2048 heads of 512 tokens,
-// and 126, not 134, for 16 heads of 16384; but 0.6% of the outputs, not 0.01%, then round to
+// (H and the scores in two parts, 16 bits: 302 us, not 331, for 2048 heads of 512 tokens,
+// and 124, not 132, for 16 heads of 16384; but 0.6% of the outputs, not 0.02%, then round to
 // a neighbour of the value that fp32 sums round to.)
 // The wave's D/NW = 32 columns are 2 column tiles; tile ct holds the columns
 // 2 li + ct, so a lane's two columns are one dword of a token row: V is loaded
@@ -57,9 +57,9 @@ struct LaPrefillArgs {
 // order (4 lg + e, 16 + 4 lg + e); Q and K rows are stored in that order.
 // 64 tokens: a chunk's fixed work (the splits of H, three barriers) is shared by as many
 // tokens as the LDS of two workgroups a CU holds.  Measured at d = 128: 2048 heads, 512
-// tokens 332 us (3.7 TB/s); 16 heads, 16384 tokens 42 us for the segments' states and 84 us
-// for the outputs, where the vector unit is busy for 0.57 of the time in both and the matrix
-// unit for 0.38.
+// tokens 331 us (3.7 TB/s; vector unit busy for 0.62 of the time, matrix unit for 0.43); 16
+// heads, 16384 tokens 132 us, of it 43 for the segments' states (0.54, 0.36) and about 80 for the
+// outputs (0.60, 0.41).
 constexpr int BL = 64;        // tokens per chunk
 
 struct LaSegArgs {
@@ -445,12 +445,15 @@ __global__ __launch_bounds__(LB<D>::NT, 2) void la_chunk_kernel(LaSegArgs a) {
 // fp32 tokens, d >= 64: chunks of 32 tokens, every operand in three bf16 parts
 // ---------------------------------------------------------------------------
 // An fp32 value is the exact sum of three bf16 parts (its 24 bits cut in three), so a
-// product is six bf16 products (the three below 2^-24 of it are left out) summed in
-// fp32: 6 x 16 cycles for 16x16x32 against 8 x 32 on the fp32 matrix instruction.
+// product is six bf16 products (of nine: the three left out are at most 2^-21 of it, 2^-24.7
+// on average) summed in fp32: 6 x 16 cycles for 16x16x32 against 8 x 32 on the fp32 matrix
+// instruction.
 // Wave w owns the 16 columns 16 w + li; otherwise as la_chunk_kernel.  32 tokens: three parts
-// of three operands fill half a CU's LDS.  Bound by the issue of the splits and products:
-// d = 128, 192 heads of up to 1021 tokens 140 us (4.4 us a chunk), 512 heads of 512 tokens
-// 177 us (3.2 TB/s).  Workgroups of half the columns fill more CUs but form the rows' parts
+// of three operands fill half a CU's LDS.  Bound by phases that take turns on the vector unit (splits)
+// and the matrix unit, two waves a SIMD:
+// d = 128, 192 heads of up to 1021 tokens 140 us (4.4 us a chunk; vector unit busy for
+// 0.50 of the waves' time, matrix unit for 0.35), 512 heads of 512 tokens 200 us (2.9 TB/s).
+// Workgroups of half the columns fill more CUs but form the rows' parts
 // twice: 512 heads of 512 tokens 213 us, not 198; 1024 heads of 300 tokens 296 us, not 261.
 constexpr int FL = 32;        // tokens per chunk
 
@@ -786,8 +789,9 @@ constexpr size_t chunk_heads(int d) { return d == 16 ? (size_t)INT32_MAX : (size
 // ---------------------------------------------------------------------------
 // With d = 16 every product is one 16 x 16 x 16 of the fp32 matrix instruction, and each
 // operand is loaded in the layout that the instruction takes (lane (lg, li), step v: row or
-// column li, index 4 lg + v): 65 us for 2048 heads of 512 tokens, bf16 (2.2 TB/s), 62 us in
-// fp32 (4.4 TB/s), bound by the waves' issue (gates and products of 16 tokens).  The scores are formed transposed (K Q^T): their accumulators
+// column li, index 4 lg + v): 80 us for 2048 heads of 512 tokens, bf16 (1.8 TB/s) or fp32
+// (3.5 TB/s); 65 and 62 with the tokens in the Infinity Cache.  Bound by the waves' issue (two
+// waves a SIMD: vector unit busy for 0.53 of the time, matrix unit for 0.22).  The scores are formed transposed (K Q^T): their accumulators
 // are then the A operand of P V as they are.  Everything stays in registers, so waves need
 // no barrier and many fit; the next chunk's loads are in flight during a chunk.
 template <typename TI, bool OUT>
@@ -900,8 +904,8 @@ __global__ __launch_bounds__(256) void la_small_kernel(LaSegArgs a) {
 
 // States before each segment from the states of each segment alone, in place, and the
 // state after the last one: S_s = X, X <- decay_s X + S_s.  Four values per lane; bound by
-// memory and, with few heads, by the latency of one group of loads (16 heads at d = 128: 4.8 us
-// for 8 segments, 12 us for 32, 5.6 TB/s).
+// memory and, with few heads, by the latency of one group of loads (16 heads at d = 128: 5.1 us
+// for 8 segments, 12.5 us for 32, 5.4 TB/s).
 struct LaScanArgs {
     const float* h0;          // or null: zeros
     float* h;

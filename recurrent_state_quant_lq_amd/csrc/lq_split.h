@@ -3,7 +3,7 @@
 // An fp32 value is the exact sum of three bf16 values (its 24 bits cut in three).
 // Products of bf16 values are exact in the fp32 accumulator, so a product of a bf16
 // value and an fp32 value is three matrix instructions, one of two fp32 values six
-// (the part products below 2^-24 of it are left out).
+// (the other three of the nine are left out: at most 2^-21 of it, 2^-24.7 on average).
 #pragma once
 
 #include "lq_internal.h"

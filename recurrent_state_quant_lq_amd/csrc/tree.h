@@ -221,9 +221,10 @@ struct TreeTables {
 // group's rows while a group is computed; rows past the end are read from a row that
 // exists, so that no load sits behind a branch.
 // Bound by the issue of these phases and, with two workgroups a CU (per-key decay: LDS), by
-// their latencies.  d = 128, 2048 heads, bf16: delta rule, 32 nodes 50 us (vector unit 23,
-// matrix unit 15; 3.0 TB/s), 64 nodes without it 74 us (3.1 TB/s); 1024 heads, per-key decay,
-// 21 nodes, fp32 46 us.
+// their latencies; 64 nodes of the delta rule in fp32 and of per-key decay leave room in LDS for one
+// workgroup a CU.  d = 128, 2048 heads, bf16 (fp32): delta rule, 32 nodes 52 us (73; bf16: vector
+// unit 23, matrix unit 15; 3.0 TB/s), 64 nodes 114 us (205), without it 74 us (136); 1024 heads,
+// per-key decay, 21 nodes, fp32 48 us, 64 nodes 145 us (148).
 // A product of a masked zero with a value that is not finite would spread it: if any
 // m is not finite, the row is computed again node after node.
 template <int D, int NB, int WT, int RULE, typename TI>
@@ -233,7 +234,7 @@ struct TM {
     static constexpr int NP = sizeof(TI) == 2 && !KDA ? 1 : 3;     // parts of a token row
     // parts of the window's keys and of the scaled state: three, all 24 bits (plain linear attention, bf16,
     // 2048 heads: with these and the nodes' scores in two parts 36 us, not 41, for 32 nodes and 68, not 74,
-    // for 64, but 0.3% of the outputs, not 0.01%, then round to a neighbour of what fp32 sums round to)
+    // for 64, but 0.3% of the outputs, not 0.02%, then round to a neighbour of what fp32 sums round to)
     static constexpr int NS = 3;
     // parts of the state: where rows have three parts, the int8 values are kept as they are (exact
     // in bf16) and the rows are formed again after the scores, scaled by r (per-key decay: by

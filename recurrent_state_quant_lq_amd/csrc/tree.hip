@@ -20,7 +20,7 @@ struct CommitArgs {
 
 // One workgroup per (b, h): the path's slots, copied; D/4 lanes per slot (four values
 // of each row a lane), all slots of up to 1024/D nodes at once.  A copy of a few rows, bound
-// by the latency of path, then rows: 4 us for 16 heads, 7.5 us for 2048 heads (12-node paths).
+// by the latency of path, then rows: 3 us for 16 heads, 7.7 us for 2048 heads (12-node paths).
 template <int D, typename TI>
 __global__ __launch_bounds__(256) void commit_kernel(CommitArgs a) {
     constexpr int LPS = D / 4, SPP = 256 / LPS;            // lanes per slot, slots per pass
