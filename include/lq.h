@@ -80,7 +80,8 @@ enum lq_status {
     LQ_ERR_POS = 5,           /* pos < 0, n_buffered outside [0, W], T < 0 */
     LQ_ERR_ALIGN = 6,         /* a pointer is misaligned (see conventions) */
     LQ_ERR_HIP = 7,           /* kernel launch failed, see lq_last_hip_error() */
-    LQ_ERR_WORKSPACE = 8      /* workspace smaller than lq_la_workspace_bytes() */
+    LQ_ERR_WORKSPACE = 8,     /* workspace smaller than the call's lq_*_workspace_bytes() */
+    LQ_ERR_OVERLAP = 9        /* lq_state_gather: arrays overlap other than as the same state */
 };
 
 enum lq_decay_mode { LQ_DECAY_SCALAR = 0, LQ_DECAY_PER_KEY = 1 };
@@ -299,6 +300,39 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
                    const float *alpha, const float *beta, void *o, void *stream);
 
 /*
+ * The gated delta rule over a padded batch of prompts: outputs of up to T tokens
+ * a row and the states after them, from any starting states.  The recurrence of
+ * lq_gdn_decode_step, in chunks (T <= 4: token after token), accumulated in fp32.
+ *   h0     nullable fp32 [B,H,dk,dv]: the state before the prompt (NULL: zeros);
+ *   h      fp32 [B,H,dk,dv], out: the state after it; h == h0 is allowed,
+ *          any other overlap is not;
+ *   q..beta  as lq_gdn_fp32_recurrence, [T,B,H,...]; alpha in [0, 1], and alpha = 0
+ *          forgets everything before the token (of the key channel, per key);
+ *   o      nullable [T,B,H,dv] (fp32 or bf16 per d->io_dtype);
+ *   lens   nullable int32 [B] (device, 4-byte aligned): row b has
+ *          min(max(lens[b], 0), T) tokens.  Its later tokens are not used
+ *          (they may hold anything) and its later o rows are left as they were;
+ *   st     nullable: the codec of h is written (as lq_gdn_prefill);
+ *   workspace  device memory of at least lq_gdn_workspace_bytes(d, T) bytes,
+ *          16-byte aligned (NULL if that is 0), used until the call's work on
+ *          `stream` is done: calls that may run at the same time need their own.
+ * T = 0 (or a row with no tokens) copies h0 to h.  A token that is not finite
+ * reaches its own and later tokens only (a v its own column only).  The result of
+ * a row does not depend on earlier calls, on the workspace's content or on what
+ * other rows hold.
+ * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30;
+ * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ */
+int lq_gdn_prefill_ragged(const lq_dims *d, const lq_state *st, const float *h0, float *h, int32_t T,
+                          const void *q, const void *k, const void *v, const float *alpha,
+                          const float *beta, const int32_t *lens, void *o, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* Bytes of lq_gdn_prefill_ragged's workspace for prompts of up to T tokens of these
+ * dims (0: none; also 0 if d is invalid or T <= 0).  Never less for a larger T. */
+size_t lq_gdn_workspace_bytes(const lq_dims *d, int32_t T);
+
+/*
  * Linear attention with a decay for each head (no delta rule):
  *     H <- alpha H + k v^T,   o = H^T q  (after the update).
  * The state has the shape of the delta rule's, so the codec, the window
@@ -439,6 +473,90 @@ int lq_tree_commit(const lq_dims *d, const lq_state *st, const int32_t *pos, int
                    const int32_t *path, int32_t P, const int32_t *n_path, const void *k,
                    const float *tree_m, const float *tree_g, void *stream);
 
+/*
+ * Decides, between a tree step and its commit, which drafted tokens are accepted,
+ * and draws the token after them, so that both are distributed as the target's own
+ * samples.  For row b the walk starts at the last committed token; the children
+ * of the current node are tested in the order of their indices with the row's
+ * random numbers, an accepted child becomes the current node, and where no child
+ * is left the next token is drawn.  With p and q the target's and the draft's
+ * probabilities after the current node, c = 0 and S = Z = 1 at first, a child n
+ * with token t is accepted if
+ *     u_n q(t) S < max(p(t) - c q(t), 0) Z,
+ * and a rejection sets c <- c + S / Z, S <- sum_i max(p(i) - c q(i), 0) and, if the
+ * draft drew a node's children without replacement, Z <- Z - q(t) (once a token).
+ * The next token is the first t with sum_{i<=t} w_i > u_N sum_i w_i,
+ * w = max(p - c q, 0).  Without a draft (draft NULL: its tokens were certain, e.g.
+ * looked up) a child is accepted if u_n S < p(t), and a rejection takes p(t) out of
+ * p and of S.  Where nothing is left (S <= 0) the node's other children are not
+ * tested and the next token is drawn from p itself; where Z <= 0 it is drawn
+ * from what is left.  All of it is computed in 64 bits.
+ *   d       B (rows) and W (window) only;
+ *   pos     int32 [B], buffered tokens of row b, 0..W; a row outside is left
+ *           untouched.  At most min(P, W - pos[b]) nodes are accepted, as many as
+ *           lq_tree_commit takes;
+ *   N, parent  those of the tree step (N 1..64, parent int32 [B,N], absent nodes too);
+ *   token   int32 [B,N], the nodes' tokens; a node with a token outside [0, V)
+ *           is absent;
+ *   V       size of the vocabulary, 1..2^30;
+ *   target  fp32 [N,B,V], the target's probabilities after each node (>= 0, summing to
+ *           1 up to rounding; 0 for tokens that are masked).  Only rows of
+ *           accepted nodes, and their values at drafted tokens, are read;
+ *   target0 fp32 [B,V], after the last committed token.  NULL: the row's first node
+ *           with parent -1 is a token that is already chosen (e.g. the one drawn
+ *           last) and is accepted without a test;
+ *   draft   nullable fp32 [N,B,V], the distribution that the children of each node
+ *           were drawn from; draft0 fp32 [B,V], those of the nodes with parent -1
+ *           (required with both draft and target0);
+ *   replace 1: a node's children were drawn with replacement, 0: without;
+ *   u       fp32 [N+1,B] in [0, 1): u[n] for the test of node n, u[N] for the draw;
+ *   path    int32 [B,P], out: the accepted nodes from the root on, then -1;
+ *   n_path  int32 [B], out;   next  int32 [B], out: the token after them (-1 if no
+ *           value after the path is positive, or if target0 is NULL and nothing was
+ *           accepted).
+ * Probabilities that are NaN count as 0.  All arrays 4-byte aligned (the workspace
+ * 16); outputs may not overlap inputs.  workspace: at least
+ * lq_verify_workspace_bytes(d, N, V) bytes, as lq_gdn_prefill_ragged's.
+ * Errors: LQ_ERR_DIMS if N, P or V < 1, P > N or replace is not 0 or 1;
+ * LQ_ERR_UNSUPPORTED if N > 64, V > 2^30 or B V > 2^40; LQ_ERR_NULL, LQ_ERR_ALIGN,
+ * LQ_ERR_WORKSPACE.
+ */
+int lq_tree_verify(const lq_dims *d, const int32_t *pos, int32_t N, const int32_t *parent,
+                   const int32_t *token, int32_t V, const float *target, const float *target0,
+                   const float *draft, const float *draft0, int32_t replace, const float *u,
+                   int32_t *path, int32_t P, int32_t *n_path, int32_t *next, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Bytes of lq_tree_verify's workspace (0 if d, N or V is invalid). */
+size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
+
+/*
+ * Moves rows (sequences) of the layers' states: dst row b becomes src row index[b],
+ * for all d->B rows of every layer at once, as if every row were read before any is
+ * written.  It admits prompts into a serving batch, forks a sequence into several,
+ * reorders beams, closes gaps and clears rows.
+ *   dst, src  host arrays of n_layers states (n_layers >= 1; d holds for all of them,
+ *           except that src's have src_rows rows).  A layer's dst and src are the
+ *           same arrays (in place: src_rows = d->B, at most 4096) or do not
+ *           overlap; different layers' arrays do not overlap;
+ *   index   int32 [B] (device, 4-byte aligned): a row of src; LQ_ROW_CLEAR: an empty
+ *           state (the codec of a zero state, no window); any other value, e.g.
+ *           LQ_ROW_KEEP: the row is left as it was;
+ *   pos     int32 [src_rows] (device, 4-byte aligned): buffered tokens of the source
+ *           rows; the window's slots before them move, later slots of dst stay.
+ *           NULL: the windows are empty (after a prompt or a flush), and the
+ *           states' buffers may be NULL;
+ *   pos_out nullable int32 [B] (device, 4-byte aligned), not overlapping pos or
+ *           index: the positions of the rows that moved (0: cleared; pos NULL:
+ *           0), the others are left as they were.
+ * Errors: LQ_ERR_DIMS if n_layers or src_rows < 1; LQ_ERR_UNSUPPORTED in place with
+ * B > 4096, or H > 2^17; LQ_ERR_OVERLAP; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ */
+enum { LQ_ROW_KEEP = -1, LQ_ROW_CLEAR = -2 };
+int lq_state_gather(const lq_dims *d, int32_t n_layers, const lq_state *dst, const lq_state *src,
+                    int32_t src_rows, const int32_t *index, const int32_t *pos, int32_t *pos_out,
+                    void *stream);
+
 /* Bytes of one layer's codec arrays (sq, scales, compensators), i.e.
  * B*H*(dk*dv + 4dk + 4dv + C*(4dv + 4)); 0 if d is NULL or invalid. */
 size_t lq_state_bytes(const lq_dims *d);
@@ -471,12 +589,14 @@ enum {
     LQ_KERNEL_FP32_RECURRENCE = 4,
     LQ_KERNEL_CHECKPOINT = 5,   /* lq_gdn_state_pack / lq_gdn_state_unpack */
     LQ_KERNEL_DECODE_FLUSH = 6, /* lq_gdn_decode_step_flush */
-    LQ_KERNEL_PREFILL = 7,      /* lq_gdn_prefill (its quantization: LQ_KERNEL_QUANTIZE) */
+    LQ_KERNEL_PREFILL = 7,      /* lq_gdn_prefill(_ragged) (its quantization: LQ_KERNEL_QUANTIZE) */
     LQ_KERNEL_MEASURE = 8,      /* lq_measure_stream_read */
     LQ_KERNEL_LA_PREFILL = 9,   /* lq_la_prefill (its quantization: LQ_KERNEL_QUANTIZE) */
     LQ_KERNEL_LA_DECODE = 10,   /* lq_la_decode_step */
     LQ_KERNEL_TREE = 11,        /* lq_gdn_tree_step / lq_la_tree_step */
-    LQ_KERNEL_COMMIT = 12       /* lq_tree_commit */
+    LQ_KERNEL_COMMIT = 12,      /* lq_tree_commit */
+    LQ_KERNEL_VERIFY = 13,      /* lq_tree_verify */
+    LQ_KERNEL_GATHER = 14       /* lq_state_gather */
 };
 
 /* on = 1: drop earlier records and start recording (at most 65536 launches;

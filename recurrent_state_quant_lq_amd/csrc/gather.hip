@@ -1,0 +1,155 @@
+// gather.hip -- rows of the layers' states moved by an index per row (gfx950): sequences that
+// are admitted, fork, move together or end.
+//
+// Row b of dst becomes row index[b] of src: the codec, and the window's slots before that row's
+// position.  In place the rows may depend on each other in any way (chains, swaps, one row read
+// by many): the columns of a state's rows are independent of each other, so a workgroup takes a
+// slab of columns for every row, and per step loads the pieces of all the moved rows into
+// registers, passes a barrier, and only then stores.  The step's width follows from the number
+// of moved rows, which only the device knows: as many columns as the registers take.
+#include "gdn.h"
+
+namespace lq {
+namespace {
+
+constexpr int GT = 256;                  // threads
+constexpr int GP = 16;                   // pieces of 16 bytes per thread and step
+constexpr int kCap = GT * GP;            // pieces per step
+static_assert(kGatherInPlace == kCap, "an in-place gather holds a piece of every row");
+constexpr int kLayers = 24;              // layers per launch (their pointers are kernel arguments: 3 KB)
+constexpr int kFields = 8;
+
+struct GatherArgs {
+    void* dst[kLayers][kFields];
+    const void* src[kLayers][kFields];
+    const int32_t* index;
+    const int32_t* pos;       // or null: no window slots
+    int32_t* pos_out;         // or null
+    uint32_t units[kFields];  // per row: pieces of 16 bytes (numbers of 4: comp_idx, one log decay a slot)
+    uint32_t slab0[kFields + 1];         // first slab of each field
+    int B, src_rows, W, C;
+    uint32_t slot[kFields];   // units per window slot, 0: codec
+    bool small[kFields];      // units of 4 bytes
+};
+
+enum Field { F_SQ, F_ROW, F_COL, F_IDX, F_VAL, F_K, F_M, F_G };
+
+template <typename U>
+__device__ __forceinline__ void move_rows(const GatherArgs& a, int layer, int f, uint32_t slab, const int2* list, int n) {
+    const U* src = static_cast<const U*>(a.src[layer][f]);
+    U* dst = static_cast<U*>(a.dst[layer][f]);
+    const uint32_t units = a.units[f], slot = a.slot[f], W = a.W;
+    const uint32_t first = slab * GT, width = min((uint32_t)GT, units - first);
+    // columns per step: a power of two, so that a step's pieces divide among the threads by shifts
+    int shift = 8;
+    while (shift > 0 && (n << shift) > kCap) --shift;
+    for (uint32_t c0 = 0; c0 < width; c0 += 1u << shift) {
+        U x[GP];
+        uint32_t to[GP];      // (row << 8 | column) + 1, 0: nothing to store
+#pragma unroll
+        for (int u = 0; u < GP; ++u) {
+            const int e = threadIdx.x + GT * u;
+            to[u] = 0;
+            if ((e >> shift) >= n) continue;
+            const int2 m = list[e >> shift];               // (dst row, src row; -2: cleared)
+            const uint32_t col = c0 + (e & ((1 << shift) - 1));
+            if (col >= width) continue;
+            const uint32_t at = first + col;
+            if (slot && (m.y < 0 || (int)(at / slot % W) >= a.pos[m.y])) continue;
+            to[u] = ((uint32_t)(e >> shift) << 8 | col) + 1;
+            if (m.y >= 0) {
+                x[u] = src[(size_t)m.y * units + at];
+            } else {
+                // an empty state: zeros, column factors of 1, the first C rows as compensators
+                const uint32_t z = f == F_COL ? 0x3f800000u : f == F_IDX ? at % (uint32_t)a.C : 0u;
+                if constexpr (sizeof(U) == 4) x[u] = z;
+                else x[u] = U{z, z, z, z};
+            }
+        }
+        __syncthreads();                                   // every row's columns are read
+#pragma unroll
+        for (int u = 0; u < GP; ++u)
+            if (to[u]) {
+                const uint32_t y = to[u] - 1;
+                dst[(size_t)list[y >> 8].x * units + first + (y & 255)] = x[u];
+            }
+    }
+}
+
+typedef uint32_t piece __attribute__((ext_vector_type(4)));
+
+__global__ __launch_bounds__(GT) void gather_kernel(GatherArgs a) {
+    __shared__ int2 s_list[kCap];
+    __shared__ int s_n;
+    const int t = threadIdx.x, layer = blockIdx.y;
+    int f = 0;
+    while (f + 1 < kFields && blockIdx.x >= a.slab0[f + 1]) ++f;
+    const uint32_t slab = blockIdx.x - a.slab0[f];
+    const bool same = a.dst[layer][F_SQ] == a.src[layer][F_SQ];
+    const bool window = a.slot[f] != 0;
+    // (more rows than a step holds: out of place only, in groups)
+    for (int b0 = 0; b0 < a.B; b0 += kCap) {
+        if (t == 0) s_n = 0;
+        __syncthreads();
+        for (int b = b0 + t; b < min(a.B, b0 + kCap); b += GT) {
+            const int i = a.index[b];
+            const bool clear = i == -2 && !window;
+            const bool move = i >= 0 && i < a.src_rows && !(same && i == b) && !(window && a.pos[i] <= 0);
+            if (clear || move) s_list[atomicAdd(&s_n, 1)] = make_int2(b, i);
+            if (a.pos_out && blockIdx.x == 0 && layer == 0) {
+                if (i == -2) a.pos_out[b] = 0;
+                else if (i >= 0 && i < a.src_rows) a.pos_out[b] = a.pos ? a.pos[i] : 0;
+            }
+        }
+        __syncthreads();
+        const int n = s_n;
+        if (n) {
+            if (a.small[f]) move_rows<uint32_t>(a, layer, f, slab, s_list, n);
+            else move_rows<piece>(a, layer, f, slab, s_list, n);
+        }
+        __syncthreads();                                   // the list is rewritten
+    }
+}
+
+}  // namespace
+
+hipError_t launch_gather(const lq_dims& d, int n_layers, const lq_state* dst, const lq_state* src, int src_rows,
+                         const int32_t* index, const int32_t* pos, int32_t* pos_out, hipStream_t s) {
+    GatherArgs a;
+    const uint32_t H = d.H, dk = d.dk, C = d.C, W = d.W;
+    const bool per_key = d.decay_mode == LQ_DECAY_PER_KEY;
+    const uint32_t units[kFields] = {H * dk * dk / 16, H * dk / 4, H * dk / 4, H * C, H * C * dk / 4,
+                                     H * W * dk / 4, H * W * dk / 4, per_key ? H * W * dk / 4 : H * W};
+    a.slab0[0] = 0;
+    for (int f = 0; f < kFields; ++f) {
+        const bool window = f >= F_K;
+        a.units[f] = window && !pos ? 0 : units[f];
+        a.slot[f] = !window ? 0 : f == F_G && !per_key ? 1 : dk / 4;
+        a.small[f] = f == F_IDX || (f == F_G && !per_key);
+        a.slab0[f + 1] = a.slab0[f] + (a.units[f] + GT - 1) / GT;
+    }
+    a.index = index;
+    a.pos = pos;
+    a.B = d.B;
+    a.src_rows = src_rows;
+    a.W = d.W;
+    a.C = d.C;
+    for (int l0 = 0; l0 < n_layers; l0 += kLayers) {
+        const int n = n_layers - l0 < kLayers ? n_layers - l0 : kLayers;
+        a.pos_out = l0 == 0 ? pos_out : nullptr;
+        for (int l = 0; l < n; ++l) {
+            const lq_state &x = dst[l0 + l], &y = src[l0 + l];
+            void* const px[kFields] = {x.sq, x.row_scale, x.col_scale, x.comp_idx, x.comp_val, x.buf_k, x.buf_m, x.buf_g};
+            const void* const py[kFields] = {y.sq, y.row_scale, y.col_scale, y.comp_idx, y.comp_val, y.buf_k, y.buf_m, y.buf_g};
+            for (int f = 0; f < kFields; ++f) {
+                a.dst[l][f] = px[f];
+                a.src[l][f] = py[f];
+            }
+        }
+        const hipError_t e = launch_kernel(LQ_KERNEL_GATHER, gather_kernel, dim3(a.slab0[kFields], n), dim3(GT), s, a);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace lq

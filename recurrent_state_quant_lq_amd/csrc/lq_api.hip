@@ -1,5 +1,6 @@
 // lq_api.hip -- the C ABI of liblq.so: argument checks, dispatch, status.
 // Every check runs before any HIP call; on an error nothing is enqueued.
+#include "gdn.h"
 #include "la.h"
 #include "lq_internal.h"
 
@@ -93,6 +94,59 @@ int check_tree(int32_t N, const int32_t* pos, const int32_t* parent, const float
     if (rc) return rc;
     if (!tree_m || !tree_g) return LQ_ERR_NULL;
     if (!aligned16(tree_m) || (per_key ? !aligned16(tree_g) : !aligned4(tree_g))) return LQ_ERR_ALIGN;
+    return LQ_OK;
+}
+
+int check_workspace(size_t need, const void* workspace, size_t bytes) {
+    if (need == 0) return LQ_OK;
+    if (!workspace) return LQ_ERR_NULL;
+    if (!aligned16(workspace)) return LQ_ERR_ALIGN;
+    return bytes < need ? LQ_ERR_WORKSPACE : LQ_OK;
+}
+
+// Sizes of a verification; of d only the rows and the window count.
+int check_verify(const lq_dims* d, int32_t N, int32_t V) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if (N < 1 || V < 1) return LQ_ERR_DIMS;
+    if (N > lq::kTreeMax || V > (1 << 30) || (int64_t)d->B * V > (int64_t)1 << 40) return LQ_ERR_UNSUPPORTED;
+    return LQ_OK;
+}
+
+// Whether [a, a + n) and [b, b + m) share a byte.
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + m && y < x + n;
+}
+
+// A gather's layers: the same arrays in place, or apart; and apart from one another (the int8
+// states stand for their layers there).
+int check_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const lq_state* src, int32_t src_rows,
+                 const int32_t* index, const int32_t* pos, int32_t* pos_out) {
+    const size_t H = d->H, dk = d->dk, C = d->C, W = d->W, gd = d->decay_mode == LQ_DECAY_PER_KEY ? dk : 1;
+    const size_t row[8] = {H * dk * dk, H * dk * 4, H * dk * 4, H * C * 4, H * C * dk * 4,
+                           H * W * dk * 4, H * W * dk * 4, H * W * gd * 4};
+    const size_t B = d->B, S = src_rows;
+    const int fields = pos ? 8 : 5;
+    for (int32_t l = 0; l < n_layers; ++l) {
+        const void* x[8] = {dst[l].sq, dst[l].row_scale, dst[l].col_scale, dst[l].comp_idx, dst[l].comp_val,
+                            dst[l].buf_k, dst[l].buf_m, dst[l].buf_g};
+        const void* y[8] = {src[l].sq, src[l].row_scale, src[l].col_scale, src[l].comp_idx, src[l].comp_val,
+                            src[l].buf_k, src[l].buf_m, src[l].buf_g};
+        const bool same = x[0] == y[0];
+        if (same && B > lq::kGatherInPlace) return LQ_ERR_UNSUPPORTED;
+        for (int f = 0; f < fields; ++f) {
+            if (row[f] == 0) continue;
+            if (same ? x[f] != y[f] || S != B : overlap(x[f], B * row[f], y[f], S * row[f])) return LQ_ERR_OVERLAP;
+            if (overlap(x[f], B * row[f], index, B * 4) || overlap(x[f], B * row[f], pos, S * 4)) return LQ_ERR_OVERLAP;
+        }
+        for (int32_t m = 0; m < l; ++m)
+            if (overlap(dst[l].sq, B * row[0], dst[m].sq, B * row[0]) ||
+                overlap(dst[l].sq, B * row[0], src[m].sq, S * row[0]) ||
+                overlap(src[l].sq, S * row[0], dst[m].sq, B * row[0]))
+                return LQ_ERR_OVERLAP;
+    }
+    if (overlap(pos_out, B * 4, index, B * 4) || overlap(pos_out, B * 4, pos, S * 4)) return LQ_ERR_OVERLAP;
     return LQ_OK;
 }
 
@@ -380,6 +434,65 @@ int lq_tree_commit(const lq_dims* d, const lq_state* st, const int32_t* pos, int
     return finish(lq::launch_tree_commit(*d, *st, pos, N, path, P, n_path, k, tree_m, tree_g, (hipStream_t)stream));
 }
 
+int lq_gdn_prefill_ragged(const lq_dims* d, const lq_state* st, const float* h0, float* h, int32_t T,
+                          const void* q, const void* k, const void* v, const float* alpha, const float* beta,
+                          const int32_t* lens, void* o, void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if (st && (rc = check_state(d, st, false))) return rc;
+    if ((rc = check_ptrs({h}))) return rc;
+    if (h0 && !aligned16(h0)) return LQ_ERR_ALIGN;
+    if (lens && !aligned4(lens)) return LQ_ERR_ALIGN;
+    if (T < 0) return LQ_ERR_POS;
+    if (T > lq::kGdnMaxTokens) return LQ_ERR_UNSUPPORTED;
+    if (T > 0 && (rc = check_tokens(d, q, k, v, alpha, beta, o, false))) return rc;
+    if ((rc = check_workspace(lq_gdn_workspace_bytes(d, T), workspace, workspace_bytes))) return rc;
+    const hipStream_t s = (hipStream_t)stream;
+    if ((rc = finish(lq::launch_gdn_prefill(*d, h0, h, T, q, k, v, alpha, beta, lens, o, workspace, s)))) return rc;
+    return st ? finish(lq::launch_quantize(*d, h, *st, s)) : LQ_OK;
+}
+
+size_t lq_gdn_workspace_bytes(const lq_dims* d, int32_t T) {
+    return check_dims(d) == LQ_OK && T > 0 && T <= lq::kGdnMaxTokens ? lq::gdn_workspace_bytes(*d, T) : 0;
+}
+
+int lq_tree_verify(const lq_dims* d, const int32_t* pos, int32_t N, const int32_t* parent, const int32_t* token,
+                   int32_t V, const float* target, const float* target0, const float* draft, const float* draft0,
+                   int32_t replace, const float* u, int32_t* path, int32_t P, int32_t* n_path, int32_t* next,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+    int rc = check_verify(d, N, V);
+    if (rc) return rc;
+    if (P < 1 || P > N || (replace != 0 && replace != 1)) return LQ_ERR_DIMS;
+    if ((rc = check_indices({pos, parent, token, target, u, path, n_path, next}))) return rc;
+    if (draft && target0 && !draft0) return LQ_ERR_NULL;
+    if (!aligned4(target0) || !aligned4(draft) || !aligned4(draft0)) return LQ_ERR_ALIGN;
+    if ((rc = check_workspace(lq_verify_workspace_bytes(d, N, V), workspace, workspace_bytes))) return rc;
+    const lq::VerifyArgs a{pos, parent, token, target, target0, draft, draft0, u, path, n_path, next,
+                           static_cast<double*>(workspace), d->B, d->W, N, V, P, replace};
+    return finish(lq::launch_verify(a, (hipStream_t)stream));
+}
+
+size_t lq_verify_workspace_bytes(const lq_dims* d, int32_t N, int32_t V) {
+    return check_verify(d, N, V) == LQ_OK ? lq::verify_workspace_bytes(d->B, N, V) : 0;
+}
+
+int lq_state_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const lq_state* src, int32_t src_rows,
+                    const int32_t* index, const int32_t* pos, int32_t* pos_out, void* stream) {
+    int rc = check_dims(d);
+    if (rc) return rc;
+    if (n_layers < 1 || src_rows < 1) return LQ_ERR_DIMS;
+    if (!dst || !src) return LQ_ERR_NULL;
+    if (d->H > (1 << 17)) return LQ_ERR_UNSUPPORTED;
+    if ((rc = check_indices({index}))) return rc;
+    if (!aligned4(pos) || !aligned4(pos_out)) return LQ_ERR_ALIGN;
+    for (int32_t l = 0; l < n_layers; ++l) {
+        if ((rc = check_state(d, dst + l, pos != nullptr))) return rc;
+        if ((rc = check_state(d, src + l, pos != nullptr))) return rc;
+    }
+    if ((rc = check_gather(d, n_layers, dst, src, src_rows, index, pos, pos_out))) return rc;
+    return finish(lq::launch_gather(*d, n_layers, dst, src, src_rows, index, pos, pos_out, (hipStream_t)stream));
+}
+
 size_t lq_checkpoint_bytes(const lq_dims* d) {
     if (check_dims(d) != LQ_OK) return 0;
     return (size_t)d->B * d->H * lq::checkpoint_head_bytes(*d);
@@ -425,7 +538,8 @@ const char* lq_status_str(int status) {
         case LQ_ERR_POS: return "window position or token count out of range";
         case LQ_ERR_ALIGN: return "misaligned pointer (16 bytes; 4 for beta and scalar alpha)";
         case LQ_ERR_HIP: return "HIP launch failed";
-        case LQ_ERR_WORKSPACE: return "workspace smaller than lq_la_workspace_bytes()";
+        case LQ_ERR_WORKSPACE: return "workspace smaller than the call's workspace_bytes()";
+        case LQ_ERR_OVERLAP: return "overlapping arrays";
         default: return "unknown status";
     }
 }

@@ -21,10 +21,11 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("LQ_LIB") or os.path.join(_PKG, "liblq.so")
 
 LQ_OK, LQ_ERR_NULL, LQ_ERR_DIMS, LQ_ERR_UNSUPPORTED, LQ_ERR_WINDOW_FULL, LQ_ERR_POS, \
-    LQ_ERR_ALIGN, LQ_ERR_HIP, LQ_ERR_WORKSPACE = range(9)
+    LQ_ERR_ALIGN, LQ_ERR_HIP, LQ_ERR_WORKSPACE, LQ_ERR_OVERLAP = range(10)
 LQ_DECAY_SCALAR, LQ_DECAY_PER_KEY = 0, 1
 LQ_IO_F32, LQ_IO_BF16 = 0, 1
 LQ_ALPHA_TOKENS, LQ_ALPHA_HEADS = 0, 1
+LQ_ROW_KEEP, LQ_ROW_CLEAR = -1, -2
 
 # every symbol include/lq.h declares
 EXPORTS = ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_ragged",
@@ -35,11 +36,12 @@ EXPORTS = ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_ragg
            "lq_gdn_state_unpack", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
            "lq_gdn_decode_step_flush_ragged", "lq_measure_stream_read", "lq_la_prefill",
            "lq_la_workspace_bytes", "lq_la_decode_step", "lq_la_decode_step_ragged",
-           "lq_gdn_tree_step", "lq_la_tree_step", "lq_tree_commit")
+           "lq_gdn_tree_step", "lq_la_tree_step", "lq_tree_commit", "lq_gdn_prefill_ragged",
+           "lq_gdn_workspace_bytes", "lq_tree_verify", "lq_verify_workspace_bytes", "lq_state_gather")
 LQ_KERNEL_DECODE, LQ_KERNEL_FLUSH, LQ_KERNEL_QUANTIZE, LQ_KERNEL_DEQUANTIZE, \
     LQ_KERNEL_FP32_RECURRENCE, LQ_KERNEL_CHECKPOINT, LQ_KERNEL_DECODE_FLUSH, \
     LQ_KERNEL_PREFILL, LQ_KERNEL_MEASURE, LQ_KERNEL_LA_PREFILL, LQ_KERNEL_LA_DECODE, \
-    LQ_KERNEL_TREE, LQ_KERNEL_COMMIT = range(13)
+    LQ_KERNEL_TREE, LQ_KERNEL_COMMIT, LQ_KERNEL_VERIFY, LQ_KERNEL_GATHER = range(15)
 
 
 class lq_dims(ct.Structure):
@@ -90,7 +92,14 @@ def load() -> ct.CDLL:
         L.lq_gdn_tree_step.argtypes = [D, S, P, I, P, P, P, P, P, P, P, P, P, P]
         L.lq_la_tree_step.argtypes = [D, S, P, I, P, P, P, P, P, I, P, P, P, P]
         L.lq_tree_commit.argtypes = [D, S, P, I, P, I, P, P, P, P, P]
-        for f in ("lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
+        L.lq_gdn_prefill_ragged.argtypes = [D, S, P, P, I, P, P, P, P, P, P, P, P, ct.c_size_t, P]
+        L.lq_gdn_workspace_bytes.argtypes = [D, I]
+        L.lq_gdn_workspace_bytes.restype = ct.c_size_t
+        L.lq_tree_verify.argtypes = [D, P, I, P, P, I, P, P, P, P, I, P, P, I, P, P, P, ct.c_size_t, P]
+        L.lq_verify_workspace_bytes.argtypes = [D, I, I]
+        L.lq_verify_workspace_bytes.restype = ct.c_size_t
+        L.lq_state_gather.argtypes = [D, I, S, S, I, P, P, P, P]
+        for f in ("lq_gdn_prefill_ragged", "lq_tree_verify", "lq_state_gather", "lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
                   "lq_la_prefill", "lq_la_decode_step", "lq_la_decode_step_ragged", "lq_gdn_tree_step",
                   "lq_la_tree_step", "lq_tree_commit",
                   "lq_gdn_decode_step_flush_ragged", "lq_gdn_decode_step_ragged",
@@ -615,6 +624,125 @@ def lq_tree_commit(st: LayerState, pos, path, n_path, k, tree_m, tree_g, stream=
                ("tree_m", tree_m, sh["tree_m"], f32), ("tree_g", tree_g, sh["tree_g"], f32))
     _launch("lq_tree_commit", dev, stream, ct.byref(d), ct.byref(cs), pos.data_ptr(), N, path.data_ptr(), P,
             n_path.data_ptr(), k.data_ptr(), tree_m.data_ptr(), tree_g.data_ptr())
+
+
+def _workspace(given, need, device, stream):
+    """The caller's workspace, or memory of the stream that uses it; and its size."""
+    if given is None and need:
+        with torch.cuda.stream(stream):
+            given = torch.empty(need, dtype=torch.uint8, device=device)
+    return given, 0 if given is None else given.numel()
+
+
+def lq_gdn_workspace_bytes(d: lq_dims, T: int) -> int:
+    """Bytes of lq_gdn_prefill_ragged's workspace for prompts of up to T tokens."""
+    return int(load().lq_gdn_workspace_bytes(ct.byref(d), int(T)))
+
+
+def lq_gdn_prefill_ragged(d: lq_dims, st, h0, h, T: int, q, k, v, alpha, beta, o=None, lens=None, workspace=None,
+                          stream=None):
+    """The gated delta rule over a padded batch of prompts: o (or None) and the state h
+    after T tokens from h0 (None: zeros; h0 may be h), then the codec of h into st (or
+    None).  lens: device int32 [B] tokens per row, or None.  workspace: device uint8
+    tensor of at least lq_gdn_workspace_bytes(d, T) bytes (None: allocated for this call)."""
+    T = int(T)
+    f32 = torch.float32
+    hs = (d.B, d.H, d.dk, d.dv)
+    _check(h, "h", hs, f32)
+    dev = h.device
+    items = []
+    if h0 is not None:
+        items.append(("h0", h0, hs, f32))
+        off = abs(h0.data_ptr() - h.data_ptr())
+        if 0 < off < h.numel() * 4:
+            raise ValueError("h0 and h overlap")
+    if T > 0:
+        sh = _token_shapes(d, T)
+        items += [("q", q, sh["q"], None), ("k", k, sh["k"], None), ("v", v, sh["v"], None),
+                  ("alpha", alpha, sh["alpha"], f32), ("beta", beta, sh["beta"], f32)]
+        if o is not None:
+            items.append(("o", o, sh["o"], None))
+    if lens is not None:
+        items.append(("lens", lens, (d.B,), torch.int32))
+    cs = None
+    if st is not None:
+        cs = ct.byref(st.ready(with_buffer=False))
+        items.append(("the state", st.sq, st.sq.shape, torch.int8))
+        if any(getattr(st.dims, n) != getattr(d, n) for n in ("B", "H", "dk", "dv", "C")):
+            raise ValueError("the state's dims are not d")
+    workspace, size = _workspace(workspace, lq_gdn_workspace_bytes(d, T), dev, stream)
+    if workspace is not None:
+        items.append(("workspace", workspace, (size,), torch.uint8))
+    _check_all(dev, io_torch_dtype(d), *items)
+    _launch("lq_gdn_prefill_ragged", dev, stream, ct.byref(d), cs, _ptr(h0), h.data_ptr(), T, _ptr(q), _ptr(k),
+            _ptr(v), _ptr(alpha), _ptr(beta), _ptr(lens), _ptr(o), _ptr(workspace) if size else None, size)
+
+
+def lq_verify_workspace_bytes(d: lq_dims, N: int, V: int) -> int:
+    """Bytes of lq_tree_verify's workspace for N nodes and a vocabulary of V tokens."""
+    return int(load().lq_verify_workspace_bytes(ct.byref(d), int(N), int(V)))
+
+
+def lq_tree_verify(d: lq_dims, pos, parent, token, target, u, path, n_path, next, target0=None, draft=None,
+                   draft0=None, replace=True, workspace=None, stream=None):
+    """Accepted path and next token of every row's drafted tree (parent, token: device int32
+    [B,N]) from the target's probabilities (target fp32 [N,B,V] after each node, target0 [B,V]
+    before the first, or None: the first node is already chosen), the draft's (draft, draft0,
+    or None) and the random numbers u fp32 [N+1,B].  path int32 [B,P], n_path and next int32
+    [B] are written.  replace: a node's children were drawn with replacement."""
+    if parent is None or parent.dim() != 2 or target is None or target.dim() != 3 or path is None or path.dim() != 2:
+        raise ValueError("parent: a [B,N], target: a [N,B,V] and path: a [B,P] tensor are required")
+    N, V, P = parent.shape[1], target.shape[2], path.shape[1]
+    if draft is None and draft0 is not None or target0 is None and draft0 is not None:
+        raise ValueError("draft0 goes with draft and target0")
+    f32, i32, B = torch.float32, torch.int32, d.B
+    dev = pos.device if pos is not None else None
+    items = [("parent", parent, (B, N), i32), ("token", token, (B, N), i32), ("target", target, (N, B, V), f32),
+             ("u", u, (N + 1, B), f32), ("path", path, (B, P), i32), ("n_path", n_path, (B,), i32),
+             ("next", next, (B,), i32)]
+    if target0 is not None:
+        items.append(("target0", target0, (B, V), f32))
+    if draft is not None:
+        items.append(("draft", draft, (N, B, V), f32))
+        if target0 is not None:
+            items.append(("draft0", draft0, (B, V), f32))
+    _check(pos, "pos", (B,), i32)
+    _check_all(dev, f32, *items)
+    workspace, size = _workspace(workspace, lq_verify_workspace_bytes(d, N, V), dev, stream)
+    if workspace is not None:
+        _check_all(dev, f32, ("workspace", workspace, (size,), torch.uint8))
+    _launch("lq_tree_verify", dev, stream, ct.byref(d), pos.data_ptr(), N, parent.data_ptr(), token.data_ptr(), V,
+            target.data_ptr(), _ptr(target0), _ptr(draft), _ptr(draft0), 1 if replace else 0, u.data_ptr(),
+            path.data_ptr(), P, n_path.data_ptr(), next.data_ptr(), _ptr(workspace) if size else None, size)
+
+
+def lq_state_gather(dst, src, index, pos=None, pos_out=None, stream=None):
+    """Row b of every state in dst (a LayerState or a list, one a layer) becomes row index[b]
+    (device int32 [B]; LQ_ROW_KEEP, LQ_ROW_CLEAR) of the state in src, which may be the same
+    ones.  pos: device int32, buffered tokens of src's rows (None: the windows are empty);
+    pos_out: device int32 [B], receives those of the rows that moved."""
+    dst, src = ([x] if isinstance(x, LayerState) else list(x) for x in (dst, src))
+    if not dst or len(dst) != len(src):
+        raise ValueError("dst and src: as many states each, one at least")
+    d, rows = dst[0].dims, src[0].dims.B
+    dev = dst[0].sq.device
+    same = ("H", "dk", "dv", "W", "C", "decay_mode")
+    for x in (*dst, *src):
+        if any(getattr(x.dims, n) != getattr(d, n) for n in same) or x.sq.device != dev:
+            raise ValueError("the states differ in their dims or devices")
+    if any(x.dims.B != d.B for x in dst) or any(x.dims.B != rows for x in src):
+        raise ValueError("the states of a side differ in their rows")
+    buf = pos is not None
+    n = len(dst)
+    cd = (lq_state * n)(*[x.ready(buf) for x in dst])
+    cs = (lq_state * n)(*[x.ready(buf) for x in src])
+    items = [("index", index, (d.B,), torch.int32)]
+    if pos is not None:
+        items.append(("pos", pos, (rows,), torch.int32))
+    if pos_out is not None:
+        items.append(("pos_out", pos_out, (d.B,), torch.int32))
+    _check_all(dev, torch.float32, *items)
+    _launch("lq_state_gather", dev, stream, ct.byref(d), n, cd, cs, rows, index.data_ptr(), _ptr(pos), _ptr(pos_out))
 
 
 def lq_checkpoint_bytes(d: lq_dims) -> int:
