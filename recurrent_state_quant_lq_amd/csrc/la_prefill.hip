@@ -77,24 +77,6 @@ struct LaSegArgs {
     int seg;                  // tokens per segment (a multiple of BL)
 };
 
-// Inclusive prefix sum over the 64 lanes: lane shifts within 16 lanes, then the last lane
-// of a row to the rows above it (data-parallel moves, no LDS).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ double scan_step(double x) {
-    const uint64_t u = __double_as_longlong(x);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
-    return x + __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
-}
-__device__ __forceinline__ double wave_scan(double x) {
-    x = scan_step<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
-    x = scan_step<0x112, 0xf>(x);
-    x = scan_step<0x114, 0xf>(x);
-    x = scan_step<0x118, 0xf>(x);
-    x = scan_step<0x142, 0xa>(x);      // row_bcast 15 into rows 1, 3
-    return scan_step<0x143, 0xc>(x);   // row_bcast 31 into rows 2, 3
-}
-
 template <int D>
 struct LB {
     static constexpr int NW = D / 32, NT = 64 * NW;

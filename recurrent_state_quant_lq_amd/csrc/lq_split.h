@@ -111,4 +111,49 @@ template <> struct Row4<uint16_t> {
     __device__ __forceinline__ void widen4(float (&y)[4]) const { y[0] = lo_f32(x[0]), y[1] = hi_f32(x[0]), y[2] = lo_f32(x[1]), y[3] = hi_f32(x[1]); }
 };
 
+// Inclusive prefix sum over the 64 lanes: lane shifts within 16 lanes, then the last lane
+// of a row to the rows above it (data-parallel moves, no LDS).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double scan_step(double x) {
+    const uint64_t u = __double_as_longlong(x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, false);
+    return x + __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double wave_scan(double x) {
+    x = scan_step<0x111, 0xf>(x);      // row_shr 1, 2, 4, 8
+    x = scan_step<0x112, 0xf>(x);
+    x = scan_step<0x114, 0xf>(x);
+    x = scan_step<0x118, 0xf>(x);
+    x = scan_step<0x142, 0xa>(x);      // row_bcast 15 into rows 1, 3
+    return scan_step<0x143, 0xc>(x);   // row_bcast 31 into rows 2, 3
+}
+
+__device__ __forceinline__ v4f mfma4(float a, float b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
+// M = (I + A)^{-1} R for a block of 16 rows and CT column tiles, A strictly lower, in place: four
+// rows at a time, lane group p solves its rows; row swaps bring its row 4 p + i to lane group i, the
+// B operand of one k = 4 step with -A's columns 4 p .. 4 p + 3 (rows below them).
+// own[i] = -A[4 lg + 1 + i][4 lg ..], below[p] = -A[li][4 p + lg].
+template <int CT>
+__device__ __forceinline__ void block_solve(const v4f (&own)[3], const float (&below)[3], int lg, v4f (&R)[CT]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        if (lg == p)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                R[ct][1] += own[0][0] * R[ct][0];
+                R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
+                R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
+            }
+        if (p < 3)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                const bool on = lg == p;
+                const float x = rows_sum4(on ? R[ct][0] : 0.0f, on ? R[ct][1] : 0.0f, on ? R[ct][2] : 0.0f, on ? R[ct][3] : 0.0f);
+                R[ct] = mfma4(below[p], x, R[ct]);
+            }
+    }
+}
+
 }  // namespace lq

@@ -319,33 +319,6 @@ template <> struct Pair<uint16_t> { typedef uint32_t T; };
 __device__ __forceinline__ f32x2 widen2(f32x2 x) { return x; }
 __device__ __forceinline__ f32x2 widen2(uint32_t x) { return f32x2{lo_f32(x), hi_f32(x)}; }
 
-__device__ __forceinline__ v4f mfma4(float a, float b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
-
-// M = (I + A)^{-1} R for a block of 16 rows and CT column tiles, A strictly lower, in place: four
-// rows at a time, lane group p solves its rows; row swaps bring its row 4 p + i to lane group i, the
-// B operand of one k = 4 step with -A's columns 4 p .. 4 p + 3 (rows below them).
-// own[i] = -A[4 lg + 1 + i][4 lg ..], below[p] = -A[li][4 p + lg].
-template <int CT>
-__device__ __forceinline__ void block_solve(const v4f (&own)[3], const float (&below)[3], int lg, v4f (&R)[CT]) {
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        if (lg == p)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                R[ct][1] += own[0][0] * R[ct][0];
-                R[ct][2] += own[1][0] * R[ct][0] + own[1][1] * R[ct][1];
-                R[ct][3] += own[2][0] * R[ct][0] + own[2][1] * R[ct][1] + own[2][2] * R[ct][2];
-            }
-        if (p < 3)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                const bool on = lg == p;
-                const float x = rows_sum4(on ? R[ct][0] : 0.0f, on ? R[ct][1] : 0.0f, on ? R[ct][2] : 0.0f, on ? R[ct][3] : 0.0f);
-                R[ct] = mfma4(below[p], x, R[ct]);
-            }
-    }
-}
-
 // ---------------------------------------------------------------------------
 // d = 16: one wave a head
 // ---------------------------------------------------------------------------
