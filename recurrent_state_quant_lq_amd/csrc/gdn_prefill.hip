@@ -143,11 +143,12 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
 //     A_{n,i} = beta_n e^{g_n - g_i} <k_n, k_i> (i < n),   P_{n,i} = e^{g_n - g_i} <q_n, k_i> (i <= n),
 //     R = beta (V - e^g o (K H)),   (I + A) M = R,   O = e^g o (Q H) + P M,
 //     H = e^{g_L} H + K^T (e^{g_L - g} o M).
-// Tokens enter the products as they are; H, M, A and P are split into three bf16 parts (all
+// Tokens enter the products as they are (K^T by transposed LDS reads); H, M, A and P are split into three bf16 parts (all
 // their 24 bits).  The accumulator layout is the B operand of the next products, with the rows of
-// a 32-block in the order (4 lg + e, 16 + 4 lg + e): K, Q, K^T, A and P are stored in that order,
+// a 32-block in the order (4 lg + e, 16 + 4 lg + e): K, Q, A and P are stored in that order,
 // and H, R and M never leave the registers.  (I + A) M = R runs block after block of 16 tokens:
-// the blocks before it on bf16 products, the block itself four rows at a time (block_solve).
+// the blocks before it on bf16 products, then the inverse of the block itself, which one wave
+// forms for all columns (block_solve against the identity), on the fp32 instruction.
 // A product of a masked zero with a value that is not finite would spread it to earlier tokens: a
 // chunk ends before such a token, which is then the first of its chunk.
 constexpr int GL = 64;        // tokens per chunk
@@ -182,11 +183,14 @@ __device__ __forceinline__ void make_gates(float alpha, float beta, int left, in
     const uint64_t odd = __ballot(lane > 0 && (!finite_f32(la) || !finite_f32(be)));
     if (lane == 0) *cut = odd ? __ffsll((unsigned long long)odd) - 1 : L;
     const double g = wave_scan((double)la);
-    const double gl = __shfl(g, 63, 64);
+    const uint64_t bits = __double_as_longlong(g);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)bits, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(bits >> 32), 63);
+    const double gl = __longlong_as_double((int64_t)(((uint64_t)hi << 32) | lo));
+    // (an exponent is at most 0: off by 2^-24 of it, weighted by its exponential)
     if (lane < L) {
         s.g[lane] = g;
-        s.e[lane] = expf((float)g);
-        s.w[lane] = expf((float)(gl - g));
+        s.e[lane] = __expf((float)g);
+        s.w[lane] = __expf((float)(gl - g));
         s.b[lane] = be;
     }
 }
@@ -196,25 +200,26 @@ __device__ __forceinline__ constexpr int blk(int row, int i) { return pm<16>(row
 constexpr int kBlk = pm_shorts<16>(4);
 __device__ __forceinline__ constexpr int p_blk(int r, int j) { return r < 2 ? r : 2 * r - 2 + j; }
 __device__ __forceinline__ constexpr int a_blk(int r, int j) { return r - 1 + j; }
-__device__ __forceinline__ constexpr int tile_row(int x) { return x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3; }
+__device__ __forceinline__ constexpr int tile_row(int x) { return x < 1 ? 0 : x < 3 ? 1 : x < 6 ? 2 : 3; }   // r of x = r (r + 1) / 2 + c
 
 template <int D>
 struct GB {
     static constexpr int NW = D / 32, NT = 64 * NW;
     static constexpr int RT = D / 16;
-    static constexpr int QP = D / 8, TP = GL / 8;   // pieces per Q / K row, per K^T row
+    static constexpr int QP = D / 8;                // pieces per Q / K row
+    static constexpr int VS = D / 2 + 4;            // dwords per V row: four rows' columns 16 banks apart
     static constexpr int QROWS = pm_shorts<GL>(QP), PALL = 3 * 6 * kBlk;
 };
 
 template <int D, bool OUT>
 __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     using P = GB<D>;
-    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, TP = P::TP;
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP;
     constexpr int LA = 20;                                         // floats per row of A's diagonal blocks
     __shared__ __align__(16) uint16_t sK[pm_shorts<GL>(QP)];
-    __shared__ __align__(16) uint16_t sT[pm_shorts<D>(TP)];        // K^T: [channel][token]
+    __shared__ __align__(16) uint32_t sV[GL * P::VS];
     __shared__ __align__(16) uint16_t sA[3][4 * kBlk];             // -A left of the diagonal blocks, in parts
-    __shared__ __align__(16) float sD[4][16 * LA];                 // -A's diagonal blocks
+    __shared__ __align__(16) float sD[4][16 * LA];                 // inverses of the diagonal blocks of I + A
     __shared__ __align__(16) uint16_t sQ[OUT ? (P::QROWS > P::PALL ? P::QROWS : P::PALL) : 8];   // Q, then P in parts
     __shared__ GdnGates<GL> s_gate[2];                             // of this chunk and the next
     __shared__ int s_cut[2];
@@ -253,41 +258,23 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     // columns of A's blocks (1, 0) and (3, 1) that belong to the diagonal blocks: zeros, never written again
     for (int e = t; e < 3 * 2 * 16 * 16; e += NT) sA[e >> 9][((e >> 8) & 1) * (a_blk(3, 1) - a_blk(1, 0)) * kBlk + blk((e >> 4) & 15, 16 + (e & 15))] = 0;
 
-    // chunk loads in registers, one chunk ahead; tokens past `end` read as zeros
-    constexpr int OPW = 128 / D;                                   // token groups per wave and pass (D = 64: 2)
+    // chunk loads in registers, one chunk ahead; tokens past `end` read as zeros: pieces of 16 bytes
+    constexpr int CPR = D / 8, RPP = NT / CPR;                     // pieces per row, rows per pass
+    static_assert(4 * RPP == GL, "four pieces of each kind per thread");
     const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= chunk_heads(D))
-    uint32_t kd[2][8], vd[4][4];
-    u32x4 qd[4];
+    u32x4 kd[4], vd[4], qd[4];
     auto rows = [&](const void* x, int c0, int end) {              // tokens c0 .. min(c0 + GL, end) - 1 of this head
         return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (2 * D),
-                         (uint32_t)(min(end - c0, GL) - 1) * rb + 2 * D);
+                         end > c0 ? (uint32_t)(min(end - c0, GL) - 1) * rb + 2 * D : 0);
     };
-    auto load_v = [&](int c0, int end) {
-        if (map) return;
-        const rsrc_t rv = rows(a.v, c0, end);
-        const uint32_t ln = fresh(lane), voff = 4 * (ln >> 4) * rb + 4 * (16 * w + (ln & 15));
+    auto load = [&](int c0, int end) {
+        const uint32_t tt = fresh(t), off = (tt / CPR) * rb + 16 * (tt % CPR);
+        const rsrc_t rk = rows(a.k, c0, end), rv = rows(a.v, c0, end), rq = rows(OUT ? a.q : a.k, c0, end);
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) vd[r][v] = row_ld(rv, voff + (16 * r + v) * rb);
-    };
-    // K: eight tokens of a channel pair, in operand order (group u of a 32-block: 4 u + e, 16 + 4 u + e)
-    auto k_token = [&](uint32_t grp, int e) { return 32 * (grp >> 2) + 4 * (grp & 3) + (e & 3) + 16 * (e >> 2); };
-    auto load_kq = [&](int c0, int end) {
-        const rsrc_t rk = rows(a.k, c0, end);
-        const uint32_t ln = fresh(lane);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint32_t grp = (2 * w + j) * OPW + ln / (D / 2);
-            const uint32_t koff = k_token(grp, 0) * rb + 4 * (ln % (D / 2));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) kd[j][e] = row_ld(rk, koff + ((e & 3) + 16 * (e >> 2)) * rb);
-        }
-        if constexpr (OUT) {
-            const rsrc_t rq = rows(a.q, c0, end);
-            const uint32_t tt = 64 * w + ln, qoff = (tt / (D / 8)) * rb + 16 * (tt % (D / 8));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) qd[j] = row_ld4(rq, qoff + (j * (NT / (D / 8))) * rb);
+        for (int j = 0; j < 4; ++j) {
+            kd[j] = row_ld4(rk, off + j * RPP * rb);
+            if constexpr (OUT) qd[j] = row_ld4(rq, off + j * RPP * rb);
+            vd[j] = map ? u32x4{0, 0, 0, 0} : row_ld4(rv, off + j * RPP * rb);
         }
     };
     float al = 1.0f, be = 0.0f;                                    // gates of the next chunk: the last wave's
@@ -296,71 +283,41 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         al = a.alpha[at];
         be = a.beta[at];
     };
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) vd[r][v] = 0;
     if (t0 < te) {
-        load_kq(t0, te);
-        load_v(t0, te);
+        load(t0, te);
         if (w == NW - 1) {
             load_gates(t0);
             make_gates<GL>(al, be, te - t0, lane, s_gate[0], &s_cut[0]);
         }
     }
     // registers -> LDS; cut: the first token after the chunk's first one with a value that is not finite
-    auto store = [&](int cur, int L) {
-        const int ln = fresh(lane), kpair = ln % (D / 2), ksub = ln / (D / 2);
+    auto store = [&](int cur) {
+        const uint32_t tt = fresh(t), row = tt / CPR, c = 8 * (tt % CPR);
+        const int u = (c & 31) >> 2, p0 = (c >> 5) * 4;            // two groups of 4 channels, in operand order
+        const int at0 = pm<GL>(row, p0 + (u & 3)) + 4 * (u >> 2), at1 = pm<GL>(row, p0 + ((u + 1) & 3)) + 4 * (u >> 2);
         uint32_t odd = 0;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int grp = (2 * w + j) * OPW + ksub;
-            u32x4 x0, x1;                                          // 8 tokens of the pair's two channels
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x0[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x05040100u);
-                x1[e] = __builtin_amdgcn_perm(kd[j][2 * e + 1], kd[j][2 * e], 0x07060302u);
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<u32x2*>(&sK[at0 + pm<GL>(j * RPP, 0)]) = u32x2{kd[j][0], kd[j][1]};
+            *reinterpret_cast<u32x2*>(&sK[at1 + pm<GL>(j * RPP, 0)]) = u32x2{kd[j][2], kd[j][3]};
+            if constexpr (OUT) {
+                *reinterpret_cast<u32x2*>(&sQ[at0 + pm<GL>(j * RPP, 0)]) = u32x2{qd[j][0], qd[j][1]};
+                *reinterpret_cast<u32x2*>(&sQ[at1 + pm<GL>(j * RPP, 0)]) = u32x2{qd[j][2], qd[j][3]};
             }
-            *reinterpret_cast<u32x4*>(&sT[pm<D>(2 * kpair, grp)]) = x0;
-            *reinterpret_cast<u32x4*>(&sT[pm<D>(2 * kpair + 1, grp)]) = x1;
-            // channels (c, c + 1), c = 2 kpair, in the operand order of their 32-block
-            const int u = (2 * kpair & 31) >> 2;
-            const int piece = (kpair >> 4) * 4 + (u & 3), in = 4 * (u >> 2) + (2 * kpair & 3);
+            *reinterpret_cast<u32x4*>(&sV[(row + j * RPP) * P::VS + c / 2]) = vd[j];
+            if (j > 0 || row > 0)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                *reinterpret_cast<uint32_t*>(&sK[pm<GL>(k_token(grp, e), piece) + in]) = kd[j][e];
-                odd |= odd_bf16(kd[j][e]);
-            }
+                for (int e = 0; e < 4; ++e) odd |= odd_bf16(kd[j][e]) | odd_bf16(vd[j][e]);
         }
-        if constexpr (OUT)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int e = 64 * w + ln + NT * j, row = e / (D / 8), c = 8 * (e % (D / 8));
-                const int u = (c & 31) >> 2;                       // two groups of 4 channels: u, u + 1
-                const int p0 = (c >> 5) * 4, in = 4 * (u >> 2);
-                *reinterpret_cast<u32x2*>(&sQ[pm<GL>(row, p0 + (u & 3)) + in]) = u32x2{qd[j][0], qd[j][1]};
-                *reinterpret_cast<u32x2*>(&sQ[pm<GL>(row, p0 + ((u + 1) & 3)) + in]) = u32x2{qd[j][2], qd[j][3]};
-            }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) odd |= odd_bf16(vd[r][v]);
         if (odd) {
             int first = GL;
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 3; j >= 0; --j) {
+                uint32_t x = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int n = k_token((2 * w + j) * OPW + ksub, e);
-                    if (n > 0 && odd_bf16(kd[j][e])) first = min(first, n);
-                }
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int n = 16 * r + 4 * (ln >> 4) + v;
-                    if (n > 0 && odd_bf16(vd[r][v])) first = min(first, n);
-                }
+                for (int e = 0; e < 4; ++e) x |= odd_bf16(kd[j][e]) | odd_bf16(vd[j][e]);
+                if (x && (j > 0 || row > 0)) first = row + j * RPP;
+            }
             atomicMin(&s_cut[cur], first);
         }
     };
@@ -370,21 +327,20 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     for (int c0 = t0; c0 < te; c0 = next, cur ^= 1) {
         int ce = min(c0 + GL, te);
         if (w == NW - 1 && ce < te) load_gates(ce);
-        store(cur, ce - c0);
+        store(cur);
         __syncthreads();
         const int cut = s_cut[cur];
         if (cut < ce - c0) {                                       // the chunk again, up to that token
             ce = c0 + cut;
             __syncthreads();
-            load_kq(c0, ce);
-            load_v(c0, ce);
+            load(c0, ce);
             if (w == NW - 1) {
                 int dummy;
                 load_gates(c0);
                 make_gates<GL>(al, be, cut, lane, s_gate[cur], &dummy);
                 load_gates(ce);
             }
-            store(cur, cut);
+            store(cur);
             __syncthreads();
         }
         next = ce;
@@ -395,15 +351,15 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 
         // ---- scores: the 10 tiles on and below the diagonal of K K^T and of Q K^T, over the waves ----
         // (tile x = r (r + 1) / 2 + c; its indices are scalars of the wave, so that no code is repeated per tile)
-        constexpr int KT = (10 + NW - 1) / NW, QT = 12 / NW;       // (tiles 10 and 11: zeros right of the diagonal)
+        constexpr int KD = 4 / NW, KT = KD + (6 + NW - 1) / NW, QT = 12 / NW;   // (tiles 10, 11 of Q K^T: zeros right of the diagonal)
         v4f pr[OUT ? QT : 1];
         const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
         const int at = pm<GL>(li, lg);                             // operand reads: row li, piece lg
 #pragma unroll
         for (int y = 0; y < KT; ++y) {
-            const int x = w + NW * y;
-            if (x >= 10) break;
-            const int r = tile_row(x), c = x - r * (r + 1) / 2;
+            const bool diag = y < KD;
+            const int x = diag ? w + NW * y : min(w + NW * (y - KD), 5);   // block, or tile x = r (r - 1) / 2 + c
+            const int r = diag ? x : tile_row(x) + 1, c = diag ? x : x - r * (r - 1) / 2;
             const int ar = at + pm<GL>(16 * r, 0), ac = at + pm<GL>(16 * c, 0);
             const double gi = sG[16 * c + li];
             v4f acc = {0.f, 0.f, 0.f, 0.f};
@@ -413,9 +369,24 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
                                 *reinterpret_cast<const u32x4*>(&sK[ac + pm<GL>(0, 4 * ks)]), acc);
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[v] *= -sB[16 * r + 4 * lg + v] * __expf((float)(sG[16 * r + 4 * lg + v] - gi));
-            if (r == c) {
+            if (diag) {
+                // the block's inverse (I + A)^{-1}: solved against the identity, then an A operand of k = 4 steps
+                float* sd = sD[r];
 #pragma unroll
-                for (int v = 0; v < 4; ++v) sD[r][(4 * lg + v) * LA + li] = li < 4 * lg + v ? acc[v] : 0.0f;
+                for (int v = 0; v < 4; ++v) sd[(4 * lg + v) * LA + li] = li < 4 * lg + v ? acc[v] : 0.0f;
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                v4f own[3], inv[1];
+                float below[3];
+#pragma unroll
+                for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(&sd[(4 * lg + 1 + i) * LA + 4 * lg]);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? sd[li * LA + 4 * p + lg] : 0.0f;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) inv[0][v] = 4 * lg + v == li ? 1.0f : 0.0f;
+                block_solve<1>(own, below, lg, inv);
+                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+                for (int v = 0; v < 4; ++v) sd[(4 * lg + v) * LA + li] = inv[0][v];
             } else {
                 const int to = a_blk(r, c >> 1) * kBlk + 4 * (c & 1) + blk(4 * lg, li);
 #pragma unroll
@@ -431,23 +402,20 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         if constexpr (OUT)
 #pragma unroll
             for (int y = 0; y < QT; ++y) {
-                const int x = ((w + 2) & (NW - 1)) + NW * y;
+                const int x = w + NW * y;
+                const int r = x < 10 ? tile_row(x) : 2 * (x - 10), c = x < 10 ? x - r * (r + 1) / 2 : r + 1;
+                const int ar = at + pm<GL>(16 * r, 0), ac = at + pm<GL>(16 * c, 0);
+                const double gi = sG[16 * c + li];
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
-                if (x < 10) {
-                    const int r = tile_row(x), c = x - r * (r + 1) / 2;
-                    const int ar = at + pm<GL>(16 * r, 0), ac = at + pm<GL>(16 * c, 0);
-                    const double gi = sG[16 * c + li];
 #pragma unroll
-                    for (int ks = 0; ks < D / 32; ++ks)
-                        acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[ar + pm<GL>(0, 4 * ks)]),
-                                        *reinterpret_cast<const u32x4*>(&sK[ac + pm<GL>(0, 4 * ks)]), acc);
+                for (int ks = 0; ks < D / 32; ++ks)
+                    acc = mfma_bf16(*reinterpret_cast<const u32x4*>(&sQ[ar + pm<GL>(0, 4 * ks)]),
+                                    *reinterpret_cast<const u32x4*>(&sK[ac + pm<GL>(0, 4 * ks)]), acc);
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        const float p = __expf((float)(sG[16 * r + 4 * lg + v] - gi)) * acc[v];
-                        acc[v] = 16 * (r - c) + 4 * lg + v >= li ? p : 0.0f;
-                    }
+                for (int v = 0; v < 4; ++v) {
+                    const float p = __expf((float)(sG[16 * r + 4 * lg + v] - gi)) * acc[v];
+                    pr[y][v] = 16 * (r - c) + 4 * lg + v >= li ? p : 0.0f;
                 }
-                pr[y] = acc;
                 __builtin_amdgcn_sched_barrier(0);
             }
         // ---- K H and Q H ----
@@ -457,9 +425,7 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
             R[r][0] = R[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
             if constexpr (OUT) O[r][0] = O[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
         }
-#pragma unroll
-        for (int ks = 0; ks < D / 32; ++ks) {
-            u32x4 b[2][3];
+        auto split_h = [&](int ks, u32x4 (&b)[2][3]) {
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 float x[8];
@@ -470,31 +436,40 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int m = 0; m < 3; ++m) b[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
+        };
+        u32x4 hb[2][2][3];                                         // (the next step's parts are formed during a step)
+        split_h(0, hb[0]);
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks) {
+            const u32x4 (&b)[2][3] = hb[ks & 1];
+            if (ks + 1 < D / 32) split_h(ks + 1, hb[(ks + 1) & 1]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const u32x4 ak = *reinterpret_cast<const u32x4*>(&sK[at + pm<GL>(16 * r, 4 * ks)]);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct)
+                for (int m = 2; m >= 0; --m)
 #pragma unroll
-                    for (int m = 2; m >= 0; --m) R[r][ct] = mfma_bf16(ak, b[ct][m], R[r][ct]);
+                    for (int ct = 0; ct < 2; ++ct) R[r][ct] = mfma_bf16(ak, b[ct][m], R[r][ct]);
                 if constexpr (OUT) {
                     const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[at + pm<GL>(16 * r, 4 * ks)]);
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
+                    for (int m = 2; m >= 0; --m)
 #pragma unroll
-                        for (int m = 2; m >= 0; --m) O[r][ct] = mfma_bf16(aq, b[ct][m], O[r][ct]);
+                        for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(aq, b[ct][m], O[r][ct]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const v4f e = *reinterpret_cast<const v4f*>(&sE[16 * r + 4 * lg]);
             const v4f bt = *reinterpret_cast<const v4f*>(&sB[16 * r + 4 * lg]);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                R[r][0][v] = bt[v] * (lo_f32(vd[r][v]) - e[v] * R[r][0][v]);
-                R[r][1][v] = bt[v] * (hi_f32(vd[r][v]) - e[v] * R[r][1][v]);
+                const uint32_t x = sV[(16 * r + 4 * lg + v) * P::VS + 16 * w + li];
+                R[r][0][v] = bt[v] * (lo_f32(x) - e[v] * R[r][0][v]);
+                R[r][1][v] = bt[v] * (hi_f32(x) - e[v] * R[r][1][v]);
             }
             if constexpr (OUT) {
                 O[r][0] *= e;
@@ -507,7 +482,7 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
             // P in parts, in Q's place; right of the diagonal zeros
 #pragma unroll
             for (int y = 0; y < QT; ++y) {
-                const int x = ((w + 2) & (NW - 1)) + NW * y;
+                const int x = w + NW * y;
                 const int r = x < 10 ? tile_row(x) : 2 * (x - 10), c = x < 10 ? x - r * (r + 1) / 2 : r + 1;
                 const int to = p_blk(r, c >> 1) * kBlk + 4 * (c & 1) + blk(4 * lg, li);
 #pragma unroll
@@ -532,13 +507,14 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int ct = 0; ct < 2; ++ct) R[r][ct] = mfma_split(x, mp[j][ct], R[r][ct]);
             }
-            v4f own[3];
-            float below[3];
+            const v4f ti = *reinterpret_cast<const v4f*>(&sD[r][li * LA + 4 * lg]);
+            v4f m[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-            for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(&sD[r][min(4 * lg + 1 + i, 15) * LA + 4 * lg]);
+            for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? sD[r][li * LA + 4 * p + lg] : 0.0f;
-            block_solve<2>(own, below, lg, R[r]);
+                for (int ct = 0; ct < 2; ++ct) m[ct] = mfma4(ti[v], R[r][ct][v], m[ct]);
+            R[r][0] = m[0];
+            R[r][1] = m[1];
 #pragma unroll
             for (int ct = 0; ct < 2; ++ct) {
                 const float y[4] = {R[r][ct][0], R[r][ct][1], R[r][ct][2], R[r][ct][3]};
@@ -574,42 +550,40 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, pack_bf16(O[r][0][v], O[r][1][v]));
         }
-        if (more) {
-            load_kq(ce, te);
-            load_v(ce, te);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(ce, te);                                              // (none left: zeros; a branch would keep the old rows alive)
         __builtin_amdgcn_sched_barrier(0);
         // ---- H = e^{g_L} H + K^T (w o M) ----
-        if (a.end || more) {
+        const int kt = pm<GL>(4 * lg + (li >> 2), li & 3);         // transposed reads: 4 tokens of 16 channels a lane group
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                H[rt][0] *= egl;
-                H[rt][1] *= egl;
+        for (int j = 0; j < 2; ++j) {
+            const v4f w0 = *reinterpret_cast<const v4f*>(&sW[32 * j + 4 * lg]);
+            const v4f w1 = *reinterpret_cast<const v4f*>(&sW[32 * j + 16 + 4 * lg]);
+            u32x4 b[2][3];
+#pragma unroll
+            for (int ct = 0; ct < 2; ++ct) {
+                float x[8];
+                uint32_t p[3][4];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = (e < 4 ? w0[e & 3] : w1[e & 3]) * R[2 * j + e / 4][ct][e % 4];
+                split3<8>(x, p);
+#pragma unroll
+                for (int m = 0; m < 3; ++m) b[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const v4f w0 = *reinterpret_cast<const v4f*>(&sW[32 * j + 4 * lg]);
-                const v4f w1 = *reinterpret_cast<const v4f*>(&sW[32 * j + 16 + 4 * lg]);
-                u32x4 b[2][3];
-#pragma unroll
-                for (int ct = 0; ct < 2; ++ct) {
-                    float x[8];
-                    uint32_t p[3][4];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = (e < 4 ? w0[e & 3] : w1[e & 3]) * R[2 * j + e / 4][ct][e % 4];
-                    split3<8>(x, p);
-#pragma unroll
-                    for (int m = 0; m < 3; ++m) b[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+            for (int rt = 0; rt < RT; ++rt) {
+                const uint16_t* from = &sK[kt + pm<GL>(32 * j, 4 * (rt >> 1)) + 4 * (rt & 1)];
+                const u32x2 k0 = lds_tr(from), k1 = lds_tr(from + pm<GL>(16, 0));
+                const u32x4 ak = {k0[0], k0[1], k1[0], k1[1]};
+                if (j == 0) {
+                    H[rt][0] *= egl;
+                    H[rt][1] *= egl;
                 }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const u32x4 ak = *reinterpret_cast<const u32x4*>(&sT[pm<D>(li, lg) + pm<D>(16 * rt, 4 * j)]);
+                for (int m = 2; m >= 0; --m)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-                        for (int m = 2; m >= 0; --m) H[rt][ct] = mfma_bf16(ak, b[ct][m], H[rt][ct]);
-                    if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
-                }
+                    for (int ct = 0; ct < 2; ++ct) H[rt][ct] = mfma_bf16(ak, b[ct][m], H[rt][ct]);
+                if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk

@@ -73,6 +73,14 @@ __device__ __forceinline__ v4f mfma_bf16(u32x4 a, u32x4 b, v4f c) {
                                                    0, 0, 0);
 }
 
+// Transposed LDS read (every lane of a group of 16: 8 bytes, four columns of row lane / 4): lane i
+// receives column i of the group's four rows.
+__device__ __forceinline__ u32x2 lds_tr(const uint16_t* p) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)const_cast<uint16_t*>(p)));
+}
+
 // N values in three bf16 parts, packed.
 template <int N>
 __device__ __forceinline__ void split3(const float (&x)[N], uint32_t (&p)[3][N / 2]) {
