@@ -6,6 +6,8 @@
 #include "la.h"
 #include "lq_split.h"
 
+#include <type_traits>
+
 namespace lq {
 namespace {
 
@@ -154,9 +156,11 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
 constexpr int GL = 64;        // tokens per chunk
 
 struct GdnSegArgs {
-    const float* start;       // states before each segment, or null: zeros
+    const float* first;       // state before the first segment, or null: zeros
+    const float* start;       // states before the segments after it, or null: zeros (their own parts alone)
     float* end;               // states after each segment, or null: not needed
-    float* map;               // maps of each segment, or null (grid.z = 2: the second computes them)
+    float* map;               // maps of the segments after the first (grid.z = 2: the second computes them)
+    float* fin;               // state after the last segment, or null: not needed
     const void* q;
     const void* k;
     const void* v;
@@ -173,6 +177,10 @@ template <int L>
 struct GdnGates {
     double g[L];
     __align__(16) float e[L], w[L], b[L];
+};
+template <int L>
+struct GdnSteps {             // per key: the decays are in the rows
+    __align__(16) float b[L];
 };
 // Formed by one wave, lane n = token n; tokens from `left` on decay nothing and change nothing.
 // *cut: the first token after the chunk's first one whose gates are not finite.
@@ -232,16 +240,19 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     const int te = min(len, t0 + a.seg);
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
     const bool map = !OUT && blockIdx.z;                           // the segment's map: from the identity, without values
+    if (map && blockIdx.y == 0) return;
+    const float* start = blockIdx.y == 0 ? a.first : a.start;
+    const size_t from = blockIdx.y == 0 ? head * (size_t)(D * D) : soff;
 
     // H[rt][ct][v] = H[16 rt + 4 lg + v][32 w + 2 li + ct]
     v4f H[RT][2];
-    if (!map && a.start) {
+    if (!map && start) {
         const int lg = lane >> 4, band = 16 * w + (lane & 15);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const f32x2 x = *reinterpret_cast<const f32x2*>(a.start + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
+                const f32x2 x = *reinterpret_cast<const f32x2*>(start + from + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
                 H[rt][0][v] = x[0];
                 H[rt][1][v] = x[1];
             }
@@ -588,28 +599,513 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk
     }
-    float* end = map ? a.map : a.end;
+    float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
+    if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
     if (!end) return;
     const int lf = fresh(lane), lg = lf >> 4, band = 16 * w + (lf & 15);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            *reinterpret_cast<f32x2*>(end + soff + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band) = f32x2{H[rt][0][v], H[rt][1][v]};
+            *reinterpret_cast<f32x2*>(end + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band) = f32x2{H[rt][0][v], H[rt][1][v]};
+}
+
+// ---------------------------------------------------------------------------
+// fp32 tokens, or a decay per key channel, d >= 64: chunks of 32 tokens, every operand in parts
+// ---------------------------------------------------------------------------
+// The same algebra with all operands in three bf16 parts (six products of nine: the others are at
+// most 2^-21 of a product, 2^-24.7 on average).  Wave w owns the 16 columns 16 w + li.
+// A decay per key channel: with g the prefix sums (64 bits, per channel) of the log decays after
+// the chunk's first token,
+//     H' = diag(e^{g_0}) H,  x_n = e^{g_n} o k_n (and q_n),  y_i = e^{-g_i} o k_i,
+//     A_{n,i} = beta_n <x_n, y_i>,  P_{n,i} = <e^{g_n} o q_n, y_i>,  R = beta (V - X H'),
+//     O = (e^g o Q) H' + P M,  H = diag(e^{g_L}) (H' + Y^T M),
+// so no exponential of a pair of tokens is formed.  e^{-g} grows: a chunk ends before a token
+// whose g passes kMaxDecay in a channel (e^{+-64} and its parts are in range), which is then the
+// first of the next chunk, and whose own decay goes to H as a factor of at most 1.
+constexpr int GF = 32;        // tokens per chunk
+constexpr double kMaxDecay = 64.0;
+
+// e^x and e^{-x}, x in 64 bits: an exponent off by 2^-24 of itself would count at |x| up to kMaxDecay.
+__device__ __forceinline__ void exp_both(double x, float& e, float& inv) {
+    const double y = x * 1.4426950408889634;
+    const float hi = (float)y, lo = (float)(y - (double)hi) * 0.6931472f;
+    e = __builtin_amdgcn_exp2f(hi);
+    e += e * lo;
+    inv = __builtin_amdgcn_exp2f(-hi);
+    inv -= inv * lo;
+}
+
+template <typename TI> struct Two;                                 // two neighbouring channels of a token
+template <> struct Two<float> { typedef u32x2 T; };
+template <> struct Two<uint16_t> { typedef uint32_t T; };
+__device__ __forceinline__ f32x2 two(u32x2 x) { return f32x2{__uint_as_float(x[0]), __uint_as_float(x[1])}; }
+__device__ __forceinline__ f32x2 two(uint32_t x) { return f32x2{lo_f32(x), hi_f32(x)}; }
+__device__ __forceinline__ u32x2 row_ld2(rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+
+template <int D, bool KDA>
+struct GF32 {
+    static constexpr int NW = D / 16, NT = 64 * NW;
+    static constexpr int RT = D / 16, QP = D / 8;
+    static constexpr int ROWS = pm_shorts<GF>(QP);  // shorts of one part of 32 rows
+};
+
+template <int D, bool KDA, typename TI, bool OUT>
+__global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnSegArgs a) {
+    using P = GF32<D, KDA>;
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, ROWS = P::ROWS;
+    constexpr int LA = 20, ES = sizeof(TI);
+    __shared__ __align__(16) uint16_t sK[3][ROWS];                 // K (per key: e^g o K) in parts
+    __shared__ __align__(16) uint16_t sY[3][KDA ? ROWS : 8];       // per key: e^{-g} o K in parts
+    __shared__ __align__(16) uint16_t sQ[3 * (OUT ? ROWS : 8)];    // Q (per key: e^g o Q), then P, in parts
+    __shared__ __align__(16) uint16_t sA[3][kBlk];                 // -A left of the second diagonal block, in parts
+    __shared__ __align__(16) float sD[2][16 * LA];                 // inverses of the diagonal blocks of I + A
+    __shared__ std::conditional_t<KDA, GdnSteps<GF>, GdnGates<GF>> s_gate[KDA ? 1 : 2];   // of this chunk (and the next)
+    __shared__ __align__(16) float s_first[KDA ? D : 4], s_last[KDA ? D : 4];   // per key: e^{g_0}, e^{g_L}
+    __shared__ int s_cut[2];
+
+    const int t = threadIdx.x, lane = t & 63;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const size_t head = blockIdx.x, heads = (size_t)a.heads;
+    const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int t0 = (int)blockIdx.y * a.seg;
+    const int te = min(len, t0 + a.seg);
+    const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
+    const bool map = !OUT && blockIdx.z;
+    if (map && blockIdx.y == 0) return;
+    const float* start = blockIdx.y == 0 ? a.first : a.start;
+
+    v4f H[RT];                                                     // H[rt][v] = H[16 rt + 4 lg + v][16 w + li]
+    if (!map && start) {
+        const float* from = start + (blockIdx.y == 0 ? head * (size_t)(D * D) : soff) + (size_t)(4 * (lane >> 4)) * D + 16 * w + (lane & 15);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) H[rt][v] = from[(size_t)(16 * rt + v) * D];
+    } else {
+        const int diag = map ? 16 * w + (lane & 15) - 4 * (lane >> 4) : -(1 << 20);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) H[rt][v] = 16 * rt + v == diag ? 1.0f : 0.0f;
+    }
+    // columns of A's block that belong to the diagonal block: zeros, never written again
+    for (int e = t; e < 3 * 16 * 16; e += NT) sA[e >> 8][blk((e >> 4) & 15, 16 + (e & 15))] = 0;
+
+    // chunk loads in registers, one chunk ahead; tokens past `end` read as zeros.  Thread: two channels
+    // of four tokens; the values' columns as accumulators hold them
+    constexpr int PR = D / 2;                                      // channel pairs
+    static_assert(NT == 8 * PR, "four tokens per thread");
+    const uint32_t rb = (uint32_t)heads * (ES * D);                // bytes between tokens (heads <= chunk_heads(D))
+    typename Two<TI>::T kd[4], qd[4];
+    f32x2 ad[KDA ? 4 : 1];
+    float vd[8];
+    auto rows = [&](const void* x, int c0, int end, uint32_t es) { // tokens c0 .. min(c0 + GF, end) - 1 of this head
+        return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (es * D),
+                         end > c0 ? (uint32_t)(min(end - c0, GF) - 1) * (uint32_t)heads * (es * D) + es * D : 0);
+    };
+    auto load = [&](int c0, int end) {
+        const uint32_t tt = fresh(t), pair = tt % PR, n0 = 4 * (tt / PR), off = n0 * rb + 2 * ES * pair;
+        const rsrc_t rk = rows(a.k, c0, end, ES), rv = rows(a.v, c0, end, ES), rq = rows(OUT ? a.q : a.k, c0, end, ES);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (ES == 4) {
+                kd[e] = row_ld2(rk, off + e * rb);
+                if constexpr (OUT) qd[e] = row_ld2(rq, off + e * rb);
+            } else {
+                kd[e] = row_ld(rk, off + e * rb);
+                if constexpr (OUT) qd[e] = row_ld(rq, off + e * rb);
+            }
+        }
+        if constexpr (KDA) {
+            const rsrc_t ra = rows(a.alpha, c0, end, 4);
+            const uint32_t rba = (uint32_t)heads * (4 * D);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ad[e] = __builtin_bit_cast(f32x2, row_ld2(ra, (n0 + e) * rba + 8 * pair));
+        }
+        const uint32_t ln = tt & 63, voff = 4 * (ln >> 4) * rb + ES * (16 * w + (ln & 15));
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                if (map) vd[4 * r + v] = 0.0f;
+                else if constexpr (ES == 4) vd[4 * r + v] = __uint_as_float(row_ld(rv, voff + (16 * r + v) * rb));
+                else vd[4 * r + v] = bf16_to_f32(__builtin_bit_cast(uint16_t, __builtin_amdgcn_raw_buffer_load_b16(rv, voff + (16 * r + v) * rb, 0, 0)));
+            }
+    };
+    float al = 1.0f, be = 0.0f;                                    // gates of the next chunk: the last wave's
+    auto load_gates = [&](int c0) {
+        const size_t at = (size_t)min(c0 + (lane & (GF - 1)), te - 1) * heads + head;
+        if constexpr (!KDA) al = a.alpha[at];
+        be = a.beta[at];
+    };
+    if (t0 < te) {
+        load(t0, te);
+        if (w == NW - 1) {
+            load_gates(t0);
+            if constexpr (!KDA) make_gates<GF>(al, be, te - t0, lane, s_gate[0], &s_cut[0]);
+        }
+    }
+    if (KDA && t == 0) s_cut[0] = s_cut[1] = GF;
+    // registers -> LDS, in parts.  s_cut: the first token after the chunk's first one with a value that
+    // is not finite, or past which a channel decays too far
+    auto store = [&](int cur, int L) {
+        const uint32_t tt = fresh(t), pair = tt % PR, quad = tt / PR, n0 = 4 * quad;
+        const int c = 2 * pair, u = (c & 31) >> 2;                 // operand order of the channel's 32-block
+        const int at = pm<GF>(n0, (c >> 5) * 4 + (u & 3)) + 4 * (u >> 2) + (c & 3);
+        int first = GF;
+        [[maybe_unused]] double g[4][2];
+        if constexpr (KDA) {
+            double s0 = 0.0, s1 = 0.0, mine0 = 0.0, mine1 = 0.0;
+            float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool on = (int)n0 + e < L;
+                const float x0 = on ? log_decay(ad[e][0]) : 0.0f, x1 = on ? log_decay(ad[e][1]) : 0.0f;
+                if (n0 + e > 0) {                                  // (the first token's own decay is H's)
+                    s0 += (double)x0;
+                    s1 += (double)x1;
+                    if (!finite_f32(x0) || !finite_f32(x1)) first = min(first, (int)n0 + e);
+                } else {
+                    l0 = x0;
+                    l1 = x1;
+                }
+                g[e][0] = s0;
+                g[e][1] = s1;
+            }
+            double* s_tot = reinterpret_cast<double*>(sY[0]);      // log decays of four tokens, in Y's place
+            static_assert(sizeof(sY) >= 8 * D * sizeof(double) || !KDA, "a total per channel and four tokens");
+            s_tot[quad * D + c] = s0;
+            s_tot[quad * D + c + 1] = s1;
+            if (quad == 0) {
+                s_first[c] = __expf(l0);
+                s_first[c + 1] = __expf(l1);
+            }
+            if (w == NW - 1 && lane < GF) {
+                const float b = lane < L ? be : 0.0f;
+                s_gate[0].b[lane] = b;
+                if (lane > 0 && !finite_f32(b)) atomicMin(&s_cut[cur], lane);
+            }
+            __syncthreads();
+            double gl0 = 0.0, gl1 = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i == (int)quad) {
+                    mine0 = gl0;
+                    mine1 = gl1;
+                }
+                gl0 += s_tot[i * D + c];
+                gl1 += s_tot[i * D + c + 1];
+            }
+            __syncthreads();                                       // the totals are read
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g[e][0] += mine0;
+                g[e][1] += mine1;
+                if (n0 + e > 0 && (g[e][0] < -kMaxDecay || g[e][1] < -kMaxDecay)) first = min(first, (int)n0 + e);
+            }
+            if (quad == 0) {
+                s_last[c] = __expf((float)gl0);
+                s_last[c + 1] = __expf((float)gl1);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const f32x2 k = two(kd[e]), q = OUT ? two(qd[e]) : f32x2{0.f, 0.f};
+            if (n0 + e > 0 && (!finite_f32(k[0]) || !finite_f32(k[1]))) first = min(first, (int)n0 + e);
+            float x[6] = {k[0], k[1], q[0], q[1], 0.f, 0.f};
+            if constexpr (KDA) {
+                float e0, e1, i0, i1;
+                exp_both(g[e][0], e0, i0);
+                exp_both(g[e][1], e1, i1);
+                x[0] *= e0, x[1] *= e1, x[2] *= e0, x[3] *= e1;
+                x[4] = i0 * k[0], x[5] = i1 * k[1];
+            }
+            uint32_t p[3][3];
+            split3<6>(x, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                *reinterpret_cast<uint32_t*>(&sK[m][at + 8 * e]) = p[m][0];
+                if constexpr (OUT) *reinterpret_cast<uint32_t*>(&sQ[m * ROWS + at + 8 * e]) = p[m][1];
+                if constexpr (KDA) *reinterpret_cast<uint32_t*>(&sY[m][at + 8 * e]) = p[m][2];
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int n = 16 * r + 4 * ((int)(tt & 63) >> 4) + v;
+                if (n > 0 && !finite_f32(vd[4 * r + v])) first = min(first, n);
+            }
+        if (first < GF) atomicMin(&s_cut[cur], first);
+    };
+    __syncthreads();                                               // the first gates (and s_cut) are written
+
+    int cur = 0, next;
+    for (int c0 = t0; c0 < te; c0 = next, cur ^= 1) {
+        int ce = min(c0 + GF, te);
+        if (!KDA && w == NW - 1) load_gates(ce);                   // (none left: the last token's again)
+        store(cur, ce - c0);
+        __syncthreads();
+        const int cut = s_cut[cur];
+        if (cut < ce - c0) {                                       // the chunk again, up to that token
+            ce = c0 + cut;
+            __syncthreads();
+            load(c0, ce);
+            if (w == NW - 1) {
+                load_gates(c0);
+                if constexpr (!KDA) {
+                    int dummy;
+                    make_gates<GF>(al, be, cut, lane, s_gate[cur], &dummy);
+                    load_gates(ce);
+                }
+            }
+            store(cur, cut);
+            __syncthreads();
+        }
+        if (KDA && t == 0) s_cut[cur] = GF;                        // (read by all; for the chunk after the next)
+        next = ce;
+        const auto& G = s_gate[KDA ? 0 : cur];
+
+        const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
+        const int at = pm<GF>(li, lg);                             // operand reads: row li, piece lg
+        if constexpr (KDA)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) H[rt] *= *reinterpret_cast<const v4f*>(&s_first[16 * rt + 4 * lg]);
+        // ---- scores: the three tiles on and below the diagonal, of K K^T and of Q K^T, a wave each ----
+        const uint16_t(*sC)[ROWS] = reinterpret_cast<const uint16_t(*)[ROWS]>(KDA ? &sY[0][0] : &sK[0][0]);
+        auto scores = [&](const uint16_t* x, int r, int c) {
+            v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                u32x4 y[3], z[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) {
+                    y[m] = *reinterpret_cast<const u32x4*>(&x[m * ROWS + at + pm<GF>(16 * r, 4 * ks)]);
+                    z[m] = *reinterpret_cast<const u32x4*>(&sC[m][at + pm<GF>(16 * c, 4 * ks)]);
+                }
+                acc = mfma_split(y, z, acc);
+            }
+            if constexpr (!KDA) {
+                const double gi = G.g[16 * c + li];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[v] *= __expf((float)(G.g[16 * r + 4 * lg + v] - gi));
+            }
+            return acc;
+        };
+        auto put = [&](uint16_t* p0, int part, int to, const v4f& x) {   // a tile in parts
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const float p = x[v], p1 = p - top_f32(p);
+                p0[to + 8 * v] = (uint16_t)(__float_as_uint(p) >> 16);
+                p0[part + to + 8 * v] = (uint16_t)(__float_as_uint(p1) >> 16);
+                p0[2 * part + to + 8 * v] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
+            }
+        };
+        auto invert = [&](int r) {
+            const v4f x = scores(sK[0], r, r);
+            float* sd = sD[r];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sd[(4 * lg + v) * LA + li] = li < 4 * lg + v ? -G.b[16 * r + 4 * lg + v] * x[v] : 0.0f;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            v4f own[3], inv[1];
+            float below[3];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(&sd[(4 * lg + 1 + i) * LA + 4 * lg]);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) below[p] = (li >> 2) > p ? sd[li * LA + 4 * p + lg] : 0.0f;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) inv[0][v] = 4 * lg + v == li ? 1.0f : 0.0f;
+            block_solve<1>(own, below, lg, inv);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int v = 0; v < 4; ++v) sd[(4 * lg + v) * LA + li] = inv[0][v];
+        };
+        // tiles of P: (0, 0), (1, 0), (1, 1), by the last three waves (eight waves; of four: by waves 1 to 3)
+        constexpr int PW = NW - 3;
+        v4f pr = {0.f, 0.f, 0.f, 0.f};
+        if (w < 2) invert(w);
+        if (w == (NW == 8 ? 2 : 0)) {
+            v4f y = scores(sK[0], 1, 0);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] *= -G.b[16 + 4 * lg + v];
+            put(sA[0], kBlk, blk(4 * lg, li), y);
+        }
+        if (OUT && w >= PW) {
+            const int r = (w - PW + 1) >> 1, c = (w - PW) >> 1;
+            pr = scores(sQ, r, c);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) pr[v] = 16 * (r - c) + 4 * lg + v >= li ? pr[v] : 0.0f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- K H and Q H ----
+        v4f R[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, O[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int ks = 0; ks < D / 32; ++ks) {
+            float x[8];
+            uint32_t p[3][4];
+            u32x4 b[3];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = H[2 * ks + e / 4][e % 4];
+            split3<8>(x, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                u32x4 y[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) y[m] = *reinterpret_cast<const u32x4*>(&sK[m][at + pm<GF>(16 * r, 4 * ks)]);
+                R[r] = mfma_split(y, b, R[r]);
+                if constexpr (OUT) {
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) y[m] = *reinterpret_cast<const u32x4*>(&sQ[m * ROWS + at + pm<GF>(16 * r, 4 * ks)]);
+                    O[r] = mfma_split(y, b, O[r]);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const v4f bt = *reinterpret_cast<const v4f*>(&G.b[16 * r + 4 * lg]);
+            if constexpr (!KDA) {
+                const v4f e = *reinterpret_cast<const v4f*>(&G.e[16 * r + 4 * lg]);
+                R[r] *= e;
+                O[r] *= e;
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) R[r][v] = bt[v] * (vd[4 * r + v] - R[r][v]);
+        }
+        if (w == NW - 1) {
+            if constexpr (KDA) load_gates(ce);
+            else make_gates<GF>(al, be, te - ce, lane, s_gate[cur ^ 1], &s_cut[cur ^ 1]);
+        }
+        __syncthreads();                                           // A is written, Q is read
+        if (OUT && w >= PW) {                                      // P in parts, in Q's place; right of the diagonal zeros
+            const int r = (w - PW + 1) >> 1, c = (w - PW) >> 1;
+            put(sQ, 2 * kBlk, r * kBlk + 4 * c + blk(4 * lg, li), pr);
+            if (w == PW) put(sQ, 2 * kBlk, 4 + blk(4 * lg, li), v4f{0.f, 0.f, 0.f, 0.f});
+        }
+        // ---- (I + A) M = R ----
+        u32x4 mp[3];                                               // M in parts
+        const int ab = blk(li, 4 * lg);                            // operand reads: row li, piece lg
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (r == 1) {
+                u32x4 x[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) x[m] = *reinterpret_cast<const u32x4*>(&sA[m][ab]);
+                R[1] = mfma_split(x, mp, R[1]);
+            }
+            const v4f ti = *reinterpret_cast<const v4f*>(&sD[r][li * LA + 4 * lg]);
+            v4f m = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int v = 0; v < 4; ++v) m = mfma4(ti[v], R[r][v], m);
+            R[r] = m;
+            const float y[4] = {m[0], m[1], m[2], m[3]};
+            uint32_t p[3][2];
+            split3<4>(y, p);
+#pragma unroll
+            for (int u = 0; u < 3; ++u) {
+                mp[u][2 * r] = p[u][0];
+                mp[u][2 * r + 1] = p[u][1];
+                if (r == 0) mp[u][2] = mp[u][3] = 0;
+            }
+        }
+        if constexpr (OUT) {
+            __syncthreads();                                       // P is written
+            // ---- O += P M ----
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                u32x4 x[3];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) x[m] = *reinterpret_cast<const u32x4*>(&sQ[(2 * m + r) * kBlk + ab]);
+                O[r] = mfma_split(x, mp, O[r]);
+            }
+            const rsrc_t ro = rows(a.o, c0, ce, ES);               // rows past the end are left as they were
+            if constexpr (ES == 4) {
+                const uint32_t ooff = 4 * lg * rb + 4 * (16 * w + li);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, __float_as_uint(O[r][v]));
+            } else {
+                // lanes in pairs: the even one stores both columns of the rows v, the odd one those of v + 1
+                const bool up = li & 1;
+                const uint32_t ooff = (4 * lg + (li & 1)) * rb + 2 * (16 * w + (li & 14));
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; v += 2) {
+                        const float x = dpp<DPP_XOR1>(up ? O[r][v] : O[r][v + 1]);
+                        row_st(ro, ooff + (16 * r + v) * rb, up ? pack_bf16(x, O[r][v + 1]) : pack_bf16(O[r][v], x));
+                    }
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        load(ce, te);                                              // (none left: zeros)
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- H = e^{g_L} H + K^T (w o M); per key: e^{g_L} o (H + Y^T M) ----
+        const int kt = pm<GF>(4 * lg + (li >> 2), li & 3);         // transposed reads: 4 tokens of 16 channels a lane group
+        if constexpr (!KDA) {
+            const v4f w0 = *reinterpret_cast<const v4f*>(&G.w[4 * lg]), w1 = *reinterpret_cast<const v4f*>(&G.w[16 + 4 * lg]);
+            float x[8];
+            uint32_t p[3][4];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (e < 4 ? w0[e & 3] : w1[e & 3]) * R[e / 4][e % 4];
+            split3<8>(x, p);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) mp[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
+        }
+        float egl = 1.0f;
+        if constexpr (!KDA) egl = G.e[GF - 1];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            u32x4 y[3];
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                const uint16_t* from = &sC[m][kt + pm<GF>(0, 4 * (rt >> 1)) + 4 * (rt & 1)];
+                const u32x2 k0 = lds_tr(from), k1 = lds_tr(from + pm<GF>(16, 0));
+                y[m] = u32x4{k0[0], k0[1], k1[0], k1[1]};
+            }
+            if constexpr (!KDA) H[rt] *= egl;
+            H[rt] = mfma_split(y, mp, H[rt]);
+            if constexpr (KDA) H[rt] *= *reinterpret_cast<const v4f*>(&s_last[16 * rt + 4 * lg]);
+            if (rt % 2 == 1) __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();                                           // LDS is rewritten by the next chunk
+    }
+    float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
+    if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
+    if (!end) return;
+    const int lf = fresh(lane);
+    end += (size_t)(4 * (lf >> 4)) * D + 16 * w + (lf & 15);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) end[(size_t)(16 * rt + v) * D] = H[rt][v];
 }
 
 // Heads that the chunk kernels take: a chunk's rows lie within 32-bit byte offsets.
 constexpr size_t chunk_heads(int d) { return (size_t)(1 << 24) / d; }
 
+template <int D, bool KDA, typename TI, bool OUT>
+hipError_t chunk_launch(dim3 grid, const GdnSegArgs& sa, hipStream_t s) {
+    if constexpr (!KDA && sizeof(TI) == 2)
+        return launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk_kernel<D, OUT>, grid, dim3(GB<D>::NT), s, sa);
+    else
+        return launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk32_kernel<D, KDA, TI, OUT>, grid, dim3(GF32<D, KDA>::NT), s, sa);
+}
+
 template <int D, bool KDA, typename TI>
 hipError_t gdn_prefill_t(const lq_dims& d, const GdnPrefillArgs& args, void* workspace, hipStream_t s) {
     const dim3 grid((unsigned)args.heads);
-    if constexpr (D >= 64 && !KDA && sizeof(TI) == 2)
+    if constexpr (D >= 64)
         if (args.T > kGdnStepTokens && (size_t)args.heads <= chunk_heads(D)) {
-            GdnSegArgs sa{args.h0, args.h, nullptr, args.q, args.k, args.v, args.alpha, args.beta, args.lens, args.o, 0,
-                          args.T, args.H, args.heads, args.T};
-            return args.o ? launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk_kernel<D, true>, grid, dim3(GB<D>::NT), s, sa)
-                          : launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk_kernel<D, false>, grid, dim3(GB<D>::NT), s, sa);
+            GdnSegArgs sa{args.h0, nullptr, nullptr, nullptr, args.h, args.q, args.k, args.v, args.alpha, args.beta,
+                          args.lens, args.o, 0, args.T, args.H, args.heads, args.T};
+            return args.o ? chunk_launch<D, KDA, TI, true>(grid, sa, s) : chunk_launch<D, KDA, TI, false>(grid, sa, s);
         }
     return launch_kernel(LQ_KERNEL_PREFILL, gdn_step_kernel<D, KDA, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
 }
