@@ -6,6 +6,7 @@
 #include "la.h"
 #include "lq_split.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace lq {
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
 // bf16 tokens, one decay per head, d >= 64: chunks of 64 tokens on bf16 matrix products
 // ---------------------------------------------------------------------------
 // A workgroup owns a head's state in matrix-instruction accumulators (tile (rt, ct): rows
-// 16 rt + 4 (lane / 16) + v, columns 32 w + 2 (lane % 16) + ct of wave w) from the first load
+// 16 rt + 4 (lane / 16) + v, columns CT (16 w + lane % 16) + ct of wave w, CT = d / 64) from the first load
 // to the final store.  Per chunk, with g the prefix sums of log alpha (64 bits),
 //     A_{n,i} = beta_n e^{g_n - g_i} <k_n, k_i> (i < n),   P_{n,i} = e^{g_n - g_i} <q_n, k_i> (i <= n),
 //     R = beta (V - e^g o (K H)),   (I + A) M = R,   O = e^g o (Q H) + P M,
@@ -161,6 +162,7 @@ struct GdnSegArgs {
     float* end;               // states after each segment, or null: not needed
     float* map;               // maps of the segments after the first (grid.z = 2: the second computes them)
     float* fin;               // state after the last segment, or null: not needed
+    float* keep;              // null, or where the state before the first segment is copied (h0 is h)
     const void* q;
     const void* k;
     const void* v;
@@ -212,23 +214,26 @@ __device__ __forceinline__ constexpr int tile_row(int x) { return x < 1 ? 0 : x 
 
 template <int D>
 struct GB {
-    static constexpr int NW = D / 32, NT = 64 * NW;
+    static constexpr int NW = 4, NT = 64 * NW;
+    static constexpr int CT = D / 64;               // column tiles per wave
     static constexpr int RT = D / 16;
     static constexpr int QP = D / 8;                // pieces per Q / K row
-    static constexpr int VS = D / 2 + 4;            // dwords per V row: four rows' columns 16 banks apart
+    static constexpr int VS = D + 8;                // values per V row: four rows' columns 16 banks apart
     static constexpr int QROWS = pm_shorts<GL>(QP), PALL = 3 * 6 * kBlk;
+    static constexpr int QV(bool out) { return !out ? GL * VS : QROWS + GL * VS > PALL ? QROWS + GL * VS : PALL; }
+    static constexpr int WPE = CT == 1 ? 3 : 2;     // workgroups per CU: registers at d = 128, LDS at d = 64
 };
 
 template <int D, bool OUT>
-__global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
+__global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSegArgs a) {
     using P = GB<D>;
-    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP;
+    constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, CT = P::CT;
     constexpr int LA = 20;                                         // floats per row of A's diagonal blocks
     __shared__ __align__(16) uint16_t sK[pm_shorts<GL>(QP)];
-    __shared__ __align__(16) uint32_t sV[GL * P::VS];
     __shared__ __align__(16) uint16_t sA[3][4 * kBlk];             // -A left of the diagonal blocks, in parts
     __shared__ __align__(16) float sD[4][16 * LA];                 // inverses of the diagonal blocks of I + A
-    __shared__ __align__(16) uint16_t sQ[OUT ? (P::QROWS > P::PALL ? P::QROWS : P::PALL) : 8];   // Q, then P in parts
+    __shared__ __align__(16) uint16_t sQV[P::QV(OUT)];             // V and Q, then P in parts
+    uint16_t *sV = sQV, *sQ = sQV + GL * P::VS;
     __shared__ GdnGates<GL> s_gate[2];                             // of this chunk and the next
     __shared__ int s_cut[2];
 
@@ -244,36 +249,49 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     const float* start = blockIdx.y == 0 ? a.first : a.start;
     const size_t from = blockIdx.y == 0 ? head * (size_t)(D * D) : soff;
 
-    // H[rt][ct][v] = H[16 rt + 4 lg + v][32 w + 2 li + ct]
-    v4f H[RT][2];
+    // H[rt][ct][v] = H[16 rt + 4 lg + v][CT (16 w + li) + ct]
+    typedef float cols __attribute__((ext_vector_type(CT)));
+    v4f H[RT][CT];
     if (!map && start) {
-        const int lg = lane >> 4, band = 16 * w + (lane & 15);
+        const float* x = start + from + (size_t)(4 * (lane >> 4)) * D + CT * (16 * w + (lane & 15));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const f32x2 x = *reinterpret_cast<const f32x2*>(start + from + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band);
-                H[rt][0][v] = x[0];
-                H[rt][1][v] = x[1];
+                const cols y = *reinterpret_cast<const cols*>(x + (size_t)(16 * rt + v) * D);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) H[rt][ct][v] = y[ct];
             }
     } else {
-        const int diag = map ? 2 * (16 * w + (lane & 15)) - 4 * (lane >> 4) : 1 << 20;
+        const int diag = map ? CT * (16 * w + (lane & 15)) - 4 * (lane >> 4) : 1 << 20;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) H[rt][ct][v] = 16 * rt + v == diag + ct ? 1.0f : 0.0f;
+    }
+    auto write_state = [&](float* to) {
+        const int lf = fresh(lane);
+        to += (size_t)(4 * (lf >> 4)) * D + CT * (16 * w + (lf & 15));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                H[rt][0][v] = 16 * rt + v == diag ? 1.0f : 0.0f;
-                H[rt][1][v] = 16 * rt + v == diag + 1 ? 1.0f : 0.0f;
+                cols y;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[ct] = H[rt][ct][v];
+                *reinterpret_cast<cols*>(to + (size_t)(16 * rt + v) * D) = y;
             }
-    }
+    };
+    if (!OUT && a.keep && !map && blockIdx.y == 0) write_state(a.keep + head * (size_t)(D * D));
     // columns of A's blocks (1, 0) and (3, 1) that belong to the diagonal blocks: zeros, never written again
     for (int e = t; e < 3 * 2 * 16 * 16; e += NT) sA[e >> 9][((e >> 8) & 1) * (a_blk(3, 1) - a_blk(1, 0)) * kBlk + blk((e >> 4) & 15, 16 + (e & 15))] = 0;
 
     // chunk loads in registers, one chunk ahead; tokens past `end` read as zeros: pieces of 16 bytes
-    constexpr int CPR = D / 8, RPP = NT / CPR;                     // pieces per row, rows per pass
-    static_assert(4 * RPP == GL, "four pieces of each kind per thread");
+    constexpr int CPR = D / 8, RPP = NT / CPR, PT = GL / RPP;      // pieces per row, rows per pass, pieces of each kind per thread
     const uint32_t rb = (uint32_t)heads * (2 * D);                 // bytes between tokens (heads <= chunk_heads(D))
-    u32x4 kd[4], vd[4], qd[4];
+    u32x4 kd[PT], vd[PT], qd[PT];
     auto rows = [&](const void* x, int c0, int end) {              // tokens c0 .. min(c0 + GL, end) - 1 of this head
         return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (2 * D),
                          end > c0 ? (uint32_t)(min(end - c0, GL) - 1) * rb + 2 * D : 0);
@@ -282,7 +300,7 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         const uint32_t tt = fresh(t), off = (tt / CPR) * rb + 16 * (tt % CPR);
         const rsrc_t rk = rows(a.k, c0, end), rv = rows(a.v, c0, end), rq = rows(OUT ? a.q : a.k, c0, end);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < PT; ++j) {
             kd[j] = row_ld4(rk, off + j * RPP * rb);
             if constexpr (OUT) qd[j] = row_ld4(rq, off + j * RPP * rb);
             vd[j] = map ? u32x4{0, 0, 0, 0} : row_ld4(rv, off + j * RPP * rb);
@@ -308,14 +326,14 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         const int at0 = pm<GL>(row, p0 + (u & 3)) + 4 * (u >> 2), at1 = pm<GL>(row, p0 + ((u + 1) & 3)) + 4 * (u >> 2);
         uint32_t odd = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < PT; ++j) {
             *reinterpret_cast<u32x2*>(&sK[at0 + pm<GL>(j * RPP, 0)]) = u32x2{kd[j][0], kd[j][1]};
             *reinterpret_cast<u32x2*>(&sK[at1 + pm<GL>(j * RPP, 0)]) = u32x2{kd[j][2], kd[j][3]};
             if constexpr (OUT) {
                 *reinterpret_cast<u32x2*>(&sQ[at0 + pm<GL>(j * RPP, 0)]) = u32x2{qd[j][0], qd[j][1]};
                 *reinterpret_cast<u32x2*>(&sQ[at1 + pm<GL>(j * RPP, 0)]) = u32x2{qd[j][2], qd[j][3]};
             }
-            *reinterpret_cast<u32x4*>(&sV[(row + j * RPP) * P::VS + c / 2]) = vd[j];
+            *reinterpret_cast<u32x4*>(&sV[(row + j * RPP) * P::VS + c]) = vd[j];
             if (j > 0 || row > 0)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) odd |= odd_bf16(kd[j][e]) | odd_bf16(vd[j][e]);
@@ -323,7 +341,7 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         if (odd) {
             int first = GL;
 #pragma unroll
-            for (int j = 3; j >= 0; --j) {
+            for (int j = PT - 1; j >= 0; --j) {
                 uint32_t x = 0;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x |= odd_bf16(kd[j][e]) | odd_bf16(vd[j][e]);
@@ -362,14 +380,14 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 
         // ---- scores: the 10 tiles on and below the diagonal of K K^T and of Q K^T, over the waves ----
         // (tile x = r (r + 1) / 2 + c; its indices are scalars of the wave, so that no code is repeated per tile)
-        constexpr int KD = 4 / NW, KT = KD + (6 + NW - 1) / NW, QT = 12 / NW;   // (tiles 10, 11 of Q K^T: zeros right of the diagonal)
+        constexpr int QT = 3;                                      // (tiles 10, 11 of Q K^T: zeros right of the diagonal)
         v4f pr[OUT ? QT : 1];
         const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
         const int at = pm<GL>(li, lg);                             // operand reads: row li, piece lg
 #pragma unroll
-        for (int y = 0; y < KT; ++y) {
-            const bool diag = y < KD;
-            const int x = diag ? w + NW * y : min(w + NW * (y - KD), 5);   // block, or tile x = r (r - 1) / 2 + c
+        for (int y = 0; y < 3; ++y) {
+            const bool diag = y == 0;
+            const int x = diag ? w : min(w + NW * (y - 1), 5);     // block, or tile x = r (r - 1) / 2 + c (the last one again where none is left)
             const int r = diag ? x : tile_row(x) + 1, c = diag ? x : x - r * (r - 1) / 2;
             const int ar = at + pm<GL>(16 * r, 0), ac = at + pm<GL>(16 * c, 0);
             const double gi = sG[16 * c + li];
@@ -430,15 +448,17 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
                 __builtin_amdgcn_sched_barrier(0);
             }
         // ---- K H and Q H ----
-        v4f R[4][2], O[OUT ? 4 : 1][2];
+        v4f R[4][CT], O[OUT ? 4 : 1][CT];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            R[r][0] = R[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
-            if constexpr (OUT) O[r][0] = O[r][1] = v4f{0.f, 0.f, 0.f, 0.f};
-        }
-        auto split_h = [&](int ks, u32x4 (&b)[2][3]) {
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
+            for (int ct = 0; ct < CT; ++ct) {
+                R[r][ct] = v4f{0.f, 0.f, 0.f, 0.f};
+                if constexpr (OUT) O[r][ct] = v4f{0.f, 0.f, 0.f, 0.f};
+            }
+        auto split_h = [&](int ks, u32x4 (&b)[CT][3]) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
                 float x[8];
                 uint32_t p[3][4];
 #pragma unroll
@@ -448,11 +468,11 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
                 for (int m = 0; m < 3; ++m) b[ct][m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
             }
         };
-        u32x4 hb[2][2][3];                                         // (the next step's parts are formed during a step)
+        u32x4 hb[2][CT][3];                                         // (the next step's parts are formed during a step)
         split_h(0, hb[0]);
 #pragma unroll
         for (int ks = 0; ks < D / 32; ++ks) {
-            const u32x4 (&b)[2][3] = hb[ks & 1];
+            const u32x4 (&b)[CT][3] = hb[ks & 1];
             if (ks + 1 < D / 32) split_h(ks + 1, hb[(ks + 1) & 1]);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -460,13 +480,13 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int m = 2; m >= 0; --m)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) R[r][ct] = mfma_bf16(ak, b[ct][m], R[r][ct]);
+                    for (int ct = 0; ct < CT; ++ct) R[r][ct] = mfma_bf16(ak, b[ct][m], R[r][ct]);
                 if constexpr (OUT) {
                     const u32x4 aq = *reinterpret_cast<const u32x4*>(&sQ[at + pm<GL>(16 * r, 4 * ks)]);
 #pragma unroll
                     for (int m = 2; m >= 0; --m)
 #pragma unroll
-                        for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_bf16(aq, b[ct][m], O[r][ct]);
+                        for (int ct = 0; ct < CT; ++ct) O[r][ct] = mfma_bf16(aq, b[ct][m], O[r][ct]);
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
@@ -478,19 +498,23 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
             const v4f bt = *reinterpret_cast<const v4f*>(&sB[16 * r + 4 * lg]);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                const uint32_t x = sV[(16 * r + 4 * lg + v) * P::VS + 16 * w + li];
-                R[r][0][v] = bt[v] * (lo_f32(x) - e[v] * R[r][0][v]);
-                R[r][1][v] = bt[v] * (hi_f32(x) - e[v] * R[r][1][v]);
+                const uint16_t* x = &sV[(16 * r + 4 * lg + v) * P::VS + CT * (16 * w + li)];
+                if constexpr (CT == 2) {
+                    const uint32_t y = *reinterpret_cast<const uint32_t*>(x);
+                    R[r][0][v] = bt[v] * (lo_f32(y) - e[v] * R[r][0][v]);
+                    R[r][CT - 1][v] = bt[v] * (hi_f32(y) - e[v] * R[r][CT - 1][v]);
+                } else {
+                    R[r][0][v] = bt[v] * (bf16_to_f32(*x) - e[v] * R[r][0][v]);
+                }
             }
-            if constexpr (OUT) {
-                O[r][0] *= e;
-                O[r][1] *= e;
-            }
+            if constexpr (OUT)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) O[r][ct] *= e;
         }
         if (w == NW - 1 && more) make_gates<GL>(al, be, te - ce, lane, s_gate[cur ^ 1], &s_cut[cur ^ 1]);
-        __syncthreads();                                           // A is written, Q is read
+        __syncthreads();                                           // A is written, Q and V are read
         if constexpr (OUT) {
-            // P in parts, in Q's place; right of the diagonal zeros
+            // P in parts, in the place of V and Q; right of the diagonal zeros
 #pragma unroll
             for (int y = 0; y < QT; ++y) {
                 const int x = w + NW * y;
@@ -499,14 +523,14 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     const float p = pr[y][v], p1 = p - top_f32(p);
-                    sQ[to + 8 * v] = (uint16_t)(__float_as_uint(p) >> 16);
-                    sQ[6 * kBlk + to + 8 * v] = (uint16_t)(__float_as_uint(p1) >> 16);
-                    sQ[12 * kBlk + to + 8 * v] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
+                    sQV[to + 8 * v] = (uint16_t)(__float_as_uint(p) >> 16);
+                    sQV[6 * kBlk + to + 8 * v] = (uint16_t)(__float_as_uint(p1) >> 16);
+                    sQV[12 * kBlk + to + 8 * v] = (uint16_t)(__float_as_uint(p1 - top_f32(p1)) >> 16);
                 }
             }
         }
         // ---- (I + A) M = R ----
-        u32x4 mp[2][2][3];                                         // M in parts: [32 tokens][ct][part]
+        u32x4 mp[2][CT][3];                                        // M in parts: [32 tokens][ct][part]
         const int ab = blk(li, 4 * lg);                            // operand reads: row li, piece lg
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -516,18 +540,20 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
 #pragma unroll
                 for (int m = 0; m < 3; ++m) x[m] = *reinterpret_cast<const u32x4*>(&sA[m][a_blk(r, j) * kBlk + ab]);
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) R[r][ct] = mfma_split(x, mp[j][ct], R[r][ct]);
+                for (int ct = 0; ct < CT; ++ct) R[r][ct] = mfma_split(x, mp[j][ct], R[r][ct]);
             }
             const v4f ti = *reinterpret_cast<const v4f*>(&sD[r][li * LA + 4 * lg]);
-            v4f m[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            v4f m[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) m[ct] = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int v = 0; v < 4; ++v)
 #pragma unroll
-                for (int ct = 0; ct < 2; ++ct) m[ct] = mfma4(ti[v], R[r][ct][v], m[ct]);
-            R[r][0] = m[0];
-            R[r][1] = m[1];
+                for (int ct = 0; ct < CT; ++ct) m[ct] = mfma4(ti[v], R[r][ct][v], m[ct]);
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
+            for (int ct = 0; ct < CT; ++ct) R[r][ct] = m[ct];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
                 const float y[4] = {R[r][ct][0], R[r][ct][1], R[r][ct][2], R[r][ct][3]};
                 uint32_t p[3][2];
                 split3<4>(y, p);
@@ -549,17 +575,30 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
                 for (int j = 0; j <= r / 2; ++j) {
                     u32x4 x[3];
 #pragma unroll
-                    for (int m = 0; m < 3; ++m) x[m] = *reinterpret_cast<const u32x4*>(&sQ[(6 * m + p_blk(r, j)) * kBlk + ab]);
+                    for (int m = 0; m < 3; ++m) x[m] = *reinterpret_cast<const u32x4*>(&sQV[(6 * m + p_blk(r, j)) * kBlk + ab]);
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) O[r][ct] = mfma_split(x, mp[j][ct], O[r][ct]);
+                    for (int ct = 0; ct < CT; ++ct) O[r][ct] = mfma_split(x, mp[j][ct], O[r][ct]);
                     __builtin_amdgcn_sched_barrier(0);
                 }
             const rsrc_t ro = rows(a.o, c0, ce);                   // rows past the end are left as they were
-            const uint32_t ooff = 4 * lg * rb + 4 * (16 * w + li);
+            if constexpr (CT == 2) {
+                const uint32_t ooff = 4 * lg * rb + 4 * (16 * w + li);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+                for (int r = 0; r < 4; ++r)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, pack_bf16(O[r][0][v], O[r][1][v]));
+                    for (int v = 0; v < 4; ++v) row_st(ro, ooff + (16 * r + v) * rb, pack_bf16(O[r][0][v], O[r][CT - 1][v]));
+            } else {
+                // lanes in pairs: the even one stores both columns of the rows v, the odd one those of v + 1
+                const bool up = li & 1;
+                const uint32_t ooff = (4 * lg + (li & 1)) * rb + 2 * (16 * w + (li & 14));
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int v = 0; v < 4; v += 2) {
+                        const float x = dpp<DPP_XOR1>(up ? O[r][0][v] : O[r][0][v + 1]);
+                        row_st(ro, ooff + (16 * r + v) * rb, up ? pack_bf16(x, O[r][0][v + 1]) : pack_bf16(O[r][0][v], x));
+                    }
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
         load(ce, te);                                              // (none left: zeros; a branch would keep the old rows alive)
@@ -570,9 +609,9 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
         for (int j = 0; j < 2; ++j) {
             const v4f w0 = *reinterpret_cast<const v4f*>(&sW[32 * j + 4 * lg]);
             const v4f w1 = *reinterpret_cast<const v4f*>(&sW[32 * j + 16 + 4 * lg]);
-            u32x4 b[2][3];
+            u32x4 b[CT][3];
 #pragma unroll
-            for (int ct = 0; ct < 2; ++ct) {
+            for (int ct = 0; ct < CT; ++ct) {
                 float x[8];
                 uint32_t p[3][4];
 #pragma unroll
@@ -586,14 +625,13 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
                 const uint16_t* from = &sK[kt + pm<GL>(32 * j, 4 * (rt >> 1)) + 4 * (rt & 1)];
                 const u32x2 k0 = lds_tr(from), k1 = lds_tr(from + pm<GL>(16, 0));
                 const u32x4 ak = {k0[0], k0[1], k1[0], k1[1]};
-                if (j == 0) {
-                    H[rt][0] *= egl;
-                    H[rt][1] *= egl;
-                }
+                if (j == 0)
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) H[rt][ct] *= egl;
 #pragma unroll
                 for (int m = 2; m >= 0; --m)
 #pragma unroll
-                    for (int ct = 0; ct < 2; ++ct) H[rt][ct] = mfma_bf16(ak, b[ct][m], H[rt][ct]);
+                    for (int ct = 0; ct < CT; ++ct) H[rt][ct] = mfma_bf16(ak, b[ct][m], H[rt][ct]);
                 if (rt % 4 == 3) __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -601,13 +639,7 @@ __global__ __launch_bounds__(GB<D>::NT, 2) void gdn_chunk_kernel(GdnSegArgs a) {
     }
     float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
     if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
-    if (!end) return;
-    const int lf = fresh(lane), lg = lf >> 4, band = 16 * w + (lf & 15);
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            *reinterpret_cast<f32x2*>(end + (size_t)(16 * rt + 4 * lg + v) * D + 2 * band) = f32x2{H[rt][0][v], H[rt][1][v]};
+    if (end) write_state(end);
 }
 
 // ---------------------------------------------------------------------------
@@ -690,6 +722,13 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int v = 0; v < 4; ++v) H[rt][v] = 16 * rt + v == diag ? 1.0f : 0.0f;
+    }
+    if (!OUT && a.keep && !map && blockIdx.y == 0) {
+        float* to = a.keep + head * (size_t)(D * D) + (size_t)(4 * (lane >> 4)) * D + 16 * w + (lane & 15);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) to[(size_t)(16 * rt + v) * D] = H[rt][v];
     }
     // columns of A's block that belong to the diagonal block: zeros, never written again
     for (int e = t; e < 3 * 16 * 16; e += NT) sA[e >> 8][blk((e >> 4) & 15, 16 + (e & 15))] = 0;
@@ -1087,27 +1126,412 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         for (int v = 0; v < 4; ++v) end[(size_t)(16 * rt + v) * D] = H[rt][v];
 }
 
-// Heads that the chunk kernels take: a chunk's rows lie within 32-bit byte offsets.
-constexpr size_t chunk_heads(int d) { return (size_t)(1 << 24) / d; }
+// ---------------------------------------------------------------------------
+// d = 16: chunks of 16 tokens, one wave a head and segment
+// ---------------------------------------------------------------------------
+// Every product is one 16 x 16 x 16 of the fp32 matrix instruction, each operand loaded in the
+// layout that the instruction takes (lane (lg, li), step v: row or column li, index 4 lg + v).  The
+// scores are formed transposed, so that their accumulators are the A operand of P M as they are;
+// only A goes through LDS, for block_solve.  Per key: the same factors as the larger kernel's.
+template <bool KDA, typename TI, bool OUT>
+__global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
+    constexpr int D = 16, CS = 16, LR = 20;
+    __shared__ __align__(16) float s_a[4][CS * LR];
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4, wv = threadIdx.x >> 6;
+    const size_t heads = (size_t)a.heads;
+    const size_t head = (size_t)blockIdx.x * 4 + wv;               // one head a wave (waves share nothing)
+    if (head >= heads) return;
+    const int len = a.lens ? min(max(a.lens[head / (unsigned)a.H], 0), a.T) : a.T;
+    const int t0 = (int)blockIdx.y * a.seg, te = min(len, t0 + a.seg);
+    const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
+    const bool map = !OUT && blockIdx.z;
+    if (map && blockIdx.y == 0) return;
+    const float* start = blockIdx.y == 0 ? a.first : a.start;
+    v4f H = {0.f, 0.f, 0.f, 0.f};                                  // H[4 lg + v][li]
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+        if (map) H[v] = 4 * lg + v == li ? 1.0f : 0.0f;
+        else if (start) H[v] = start[(blockIdx.y == 0 ? head * (size_t)(D * D) : soff) + (4 * lg + v) * D + li];
+    }
+    if (!OUT && a.keep && !map && blockIdx.y == 0)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.keep[head * (size_t)(D * D) + (4 * lg + v) * D + li] = H[v];
+    // token li: q, k channels 4 lg + v; tokens 4 lg + v: k, v channel li
+    struct Chunk {                                                 // (as loaded: widened on use)
+        Row4<TI> q, k;
+        Row4<float> ar;
+        TI kt[4], vt[4];
+        float at[4], al, be;
+    };
+    auto load = [&](int c0, Chunk& x) {                            // (past the end: the last token, zeroed on use)
+        const size_t th = (size_t)min(c0 + li, te - 1) * heads + head;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const size_t to = ((size_t)min(c0 + 4 * lg + v, te - 1) * heads + head) * D + li;
+            x.kt[v] = static_cast<const TI*>(a.k)[to];
+            x.vt[v] = static_cast<const TI*>(a.v)[to];
+            if constexpr (KDA) x.at[v] = a.alpha[to];
+        }
+        if (OUT) x.q.load(a.q, th * D + 4 * lg);
+        x.k.load(a.k, th * D + 4 * lg);
+        if constexpr (KDA) x.ar.load(a.alpha, th * D + 4 * lg);
+        else x.al = a.alpha[th];
+        x.be = a.beta[th];
+    };
+    auto fold = [](uint64_t m) { return (uint32_t)(m | m >> 16 | m >> 32 | m >> 48) & 0xffffu; };   // over the lane groups
+    Chunk cur, nxt;
+    if (t0 < te) load(t0, cur);
+    for (int c0 = t0; c0 < te;) {
+        int L = min(CS, te - c0);
+        float kr[4], qr[4] = {0.f, 0.f, 0.f, 0.f}, kt[4], vt[4];
+        cur.k.widen4(kr);
+        if (OUT) cur.q.widen4(qr);
+        // the chunk ends before a later token that is not finite
+        const bool oddk = !finite_f32(kr[0]) || !finite_f32(kr[1]) || !finite_f32(kr[2]) || !finite_f32(kr[3]) || !finite_f32(cur.be);
+        uint32_t cut = fold(__ballot(oddk));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            kt[v] = widen(cur.kt[v]);
+            vt[v] = map ? 0.0f : widen(cur.vt[v]);
+            uint64_t m = __ballot(!finite_f32(vt[v]));             // lane group lg: token 4 lg + v
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((m >> (16 * i)) & 0xffffu) cut |= 1u << (4 * i + v);
+        }
+        // decays: scalar g of token li, gi of tokens 4 lg + v; per key gr of token li, channels 4 lg + v, and gc
+        // of tokens 4 lg + v, channel li, after the first token
+        double g = 0.0, gl = 0.0, gi[4], gr[4], gc[4];
+        float e0[4], el[4];                                        // per key: e^{g_0}, e^{g_L} of channels 4 lg + v
+        if constexpr (!KDA) {
+            const float la = log_decay(cur.al);
+            cut |= fold(__ballot(!finite_f32(la)));
+            cut &= ~1u;
+            if (cut) L = min(L, __ffs(cut) - 1);
+            g = li < L ? (double)la : 0.0;
+            g = scan_step<0x111, 0xf>(g);
+            g = scan_step<0x112, 0xf>(g);
+            g = scan_step<0x114, 0xf>(g);
+            g = scan_step<0x118, 0xf>(g);
+            gl = __shfl(g, 15, 16);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) gi[v] = __shfl(g, 4 * lg + v, 16);
+        } else {
+            float ar[4], lr[4];
+            cur.ar.widen4(ar);
+            bool odd = false, far = false;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                lr[v] = log_decay(ar[v]);
+                odd |= !finite_f32(lr[v]);
+            }
+            cut |= fold(__ballot(odd));
+            cut &= ~1u;
+            if (cut) L = min(L, __ffs(cut) - 1);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                double x = li > 0 && li < L ? (double)lr[v] : 0.0;
+                x = scan_step<0x111, 0xf>(x);
+                x = scan_step<0x112, 0xf>(x);
+                x = scan_step<0x114, 0xf>(x);
+                gr[v] = scan_step<0x118, 0xf>(x);
+                far |= gr[v] < -kMaxDecay;
+            }
+            cut = fold(__ballot(far)) & ~1u;
+            if (cut) L = min(L, __ffs(cut) - 1);                   // (sums before it stand)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                e0[v] = __expf(__shfl(lr[v], 0, 16));
+                el[v] = __expf((float)__shfl(gr[v], L - 1, 16));
+            }
+            double sum = 0.0;                                      // this lane's four tokens, then those of the groups before
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int n = 4 * lg + v;
+                sum += n > 0 && n < L ? (double)log_decay(cur.at[v]) : 0.0;
+                gc[v] = sum;
+            }
+            const double s0 = __shfl(sum, li, 64), s1 = __shfl(sum, 16 + li, 64), s2 = __shfl(sum, 32 + li, 64);
+            const double before = lg == 0 ? 0.0 : lg == 1 ? s0 : lg == 2 ? s0 + s1 : s0 + s1 + s2;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) gc[v] += before;
+        }
+        const int next = c0 + L;
+        if (next < te) load(next, nxt);
+        const float beta = li < L ? cur.be : 0.0f;
+        // rows x (of K and Q) and y, token li; y of tokens 4 lg + v
+        float xk[4], xq[4], yr[4], yc[4];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const bool on = 4 * lg + v < L;
+            const float k0 = li < L ? kr[v] : 0.0f, q0 = li < L ? qr[v] : 0.0f;
+            vt[v] = on ? vt[v] : 0.0f;
+            kt[v] = on ? kt[v] : 0.0f;
+            if constexpr (KDA) {
+                float e, i;
+                exp_both(gr[v], e, i);
+                xk[v] = li < L ? e * k0 : 0.0f;
+                xq[v] = li < L ? e * q0 : 0.0f;
+                yr[v] = li < L ? i * k0 : 0.0f;
+                exp_both(gc[v], e, i);
+                yc[v] = on ? i * kt[v] : 0.0f;
+                H[v] *= e0[v];
+            } else {
+                xk[v] = k0, xq[v] = q0, yr[v] = k0;
+                yc[v] = on ? __expf((float)(gl - gi[v])) * kt[v] : 0.0f;
+            }
+        }
+        // transposed scores: [i = 4 lg + v][n = li]
+        v4f p = {0.f, 0.f, 0.f, 0.f}, s = p;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            s = mfma4(yr[v], xk[v], s);
+            if (OUT) p = mfma4(yr[v], xq[v], p);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int i = 4 * lg + v;
+            const float e = KDA ? 1.0f : __expf((float)(g - gi[v]));
+            s[v] = i < li ? -beta * (e * s[v]) : 0.0f;
+            p[v] = i <= li ? e * p[v] : 0.0f;
+        }
+        float* sa = s_a[wv];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        *reinterpret_cast<v4f*>(&sa[li * LR + 4 * lg]) = s;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        v4f own[3], R[1], O = {0.f, 0.f, 0.f, 0.f}, kh = O;
+        float below[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) own[i] = *reinterpret_cast<const v4f*>(&sa[(4 * lg + 1 + i) * LR + 4 * lg]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) below[i] = (li >> 2) > i ? sa[li * LR + 4 * i + lg] : 0.0f;
+        const float en = KDA ? 1.0f : __expf((float)g);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            kh = mfma4(en * xk[v], H[v], kh);
+            if (OUT) O = mfma4(en * xq[v], H[v], O);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) R[0][v] = __shfl(beta, 4 * lg + v, 16) * (vt[v] - kh[v]);
+        block_solve<1>(own, below, lg, R);
+        if constexpr (OUT) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) O = mfma4(p[v], R[0][v], O);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (4 * lg + v < L) tok_st<TI>(a.o, ((size_t)(c0 + 4 * lg + v) * heads + head) * D + li, O[v]);
+        }
+        if (!KDA) H *= __expf((float)gl);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) H = mfma4(yc[v], R[0][v], H);
+        if constexpr (KDA)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) H[v] *= el[v];
+        cur = nxt;
+        c0 = next;
+    }
+    float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
+    if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
+    if (end)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) end[(4 * lg + v) * D + li] = H[v];
+}
+
+// ---------------------------------------------------------------------------
+// few heads: segments of a prompt at once
+// ---------------------------------------------------------------------------
+// A segment is a linear map of the state before it: X' = G X + E, E the state that it leaves from
+// zeros, G the one that it leaves from the identity with every v = 0.  One launch computes E and
+// G of all segments, the scan joins them (X_{s+1} = G_s X_s + E_s, in E's place), and the last one
+// computes every segment's outputs from the state before it.  A workgroup of the scan owns 16
+// columns of a head's state, wave w its rows 16 w ..; both factors in three bf16 parts: G's rows are
+// split from registers, loaded four steps ahead, X's columns go through LDS.
+struct GdnScanArgs {
+    float* x;                 // [segments][heads][d*d]: E_s at s + 1, then the states before the segments
+    const float* map;         // G_s at s
+    float* fin;               // state after the last segment, or null: formed with the outputs
+    size_t stride;            // floats between segments
+    int n;                    // states to form: x[2] .. x[n]
+};
+constexpr int kScanAhead = 4;
+template <int D>
+__global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
+    constexpr int KS = D / 32;
+    __shared__ __align__(16) uint16_t s_x[2][3][pm_shorts<16>(D / 8)];   // [column][channel], in parts
+    const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const size_t at = blockIdx.x * (size_t)(D * D);
+    // G: row 16 w + li, channels 32 ks + 4 lg .. and 16 further (whole 64-byte runs of a row per load);
+    // X: rows 16 w + 4 lg + v of column li
+    const float* g0 = a.map + at + (size_t)(16 * w + li) * D + 4 * lg;
+    float* x0 = a.x + at + (size_t)(16 * w + 4 * lg) * D + 16 * blockIdx.y + li;
+    struct Step {
+        v4f g[KS][2], e;
+    };
+    auto load = [&](int s, Step& y) {                              // kScanAhead steps before their use
+        if (s > a.n) return;
+        const float* g = g0 + (s - 1) * a.stride;
+        const float* e = x0 + s * a.stride;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            y.g[ks][0] = *reinterpret_cast<const v4f*>(g + 32 * ks);
+            y.g[ks][1] = *reinterpret_cast<const v4f*>(g + 32 * ks + 16);
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v) y.e[v] = e[(size_t)v * D];
+    };
+    v4f x;
+    auto step = [&](int s, Step& y) {
+        const float z[4] = {x[0], x[1], x[2], x[3]};
+        uint32_t p[3][2];
+        split3<4>(z, p);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) *reinterpret_cast<u32x2*>(&s_x[s & 1][m][pm<16>(li, 4 * (w >> 1) + lg) + 4 * (w & 1)]) = u32x2{p[m][0], p[m][1]};
+        u32x4 g[KS][3];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const float f[8] = {y.g[ks][0][0], y.g[ks][0][1], y.g[ks][0][2], y.g[ks][0][3],
+                                y.g[ks][1][0], y.g[ks][1][1], y.g[ks][1][2], y.g[ks][1][3]};
+            uint32_t q[3][4];
+            split3<8>(f, q);
+#pragma unroll
+            for (int m = 0; m < 3; ++m) g[ks][m] = u32x4{q[m][0], q[m][1], q[m][2], q[m][3]};
+        }
+        lds_barrier();                                             // (loads stay in flight; the other half is written meanwhile)
+        v4f u[2] = {y.e, {0.f, 0.f, 0.f, 0.f}};                    // two chains
+        load(s + kScanAhead, y);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            u32x4 b[3];
+#pragma unroll
+            for (int m = 0; m < 3; ++m) b[m] = *reinterpret_cast<const u32x4*>(&s_x[s & 1][m][pm<16>(li, 4 * ks + lg)]);
+            u[ks & 1] = mfma_split(g[ks], b, u[ks & 1]);
+        }
+        x = u[0] + u[1];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x0[s * a.stride + (size_t)v * D] = x[v];
+    };
+    Step y[kScanAhead];
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = x0[a.stride + (size_t)v * D];
+#pragma unroll
+    for (int i = 0; i < kScanAhead; ++i) load(2 + i, y[i]);
+    for (int s = 2; s <= a.n; s += kScanAhead)
+#pragma unroll
+        for (int i = 0; i < kScanAhead; ++i)
+            if (s + i <= a.n) step(s + i, y[i]);
+    if (a.fin)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.fin[at + (size_t)(16 * w + 4 * lg + v) * D + 16 * blockIdx.y + li] = x[v];
+}
+
+// d = 16: one wave a head.
+__global__ __launch_bounds__(256) void gdn_scan16_kernel(GdnScanArgs a, int heads) {
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    const int head = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (head >= heads) return;
+    float* x0 = a.x + (size_t)head * 256 + 64 * lg + li;           // X: rows 4 lg + v of column li
+    const float* g0 = a.map + (size_t)head * 256 + 16 * li + 4 * lg;   // G: row li, channels 4 lg + v
+    v4f x;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] = x0[a.stride + 16 * v];
+    for (int s = 2; s <= a.n; ++s) {
+        const v4f g = *reinterpret_cast<const v4f*>(g0 + (s - 1) * a.stride);
+        v4f u;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) u[v] = x0[s * a.stride + 16 * v];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) u = mfma4(g[v], x[v], u);
+        x = u;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x0[s * a.stride + 16 * v] = x[v];
+    }
+    if (a.fin)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) a.fin[(size_t)head * 256 + (4 * lg + v) * 16 + li] = x[v];
+}
+
+// Heads that the chunk kernels take: at d >= 64 a chunk's rows lie within 32-bit byte offsets (d = 16:
+// 64-bit ones).  More heads take the recurrence itself.
+constexpr size_t chunk_heads(int d) { return d == 16 ? (size_t)INT32_MAX : (size_t)(1 << 24) / d; }
+// Tokens per segment, a multiple of 64.  Segments cost the prompt a second time (twice: states and
+// maps) and the scan, so they pay where the heads alone leave most CUs idle: up to `heads` heads,
+// enough segments for `want` workgroups (d = 16: waves).  Measured, bf16, replayed in a graph:
+//   d = 128: 16 heads, 16384 tokens 2435 us whole, 541, 359, 401 and 381 for 128, 256, 384 and 512
+//   workgroups (fp32: 3218; 752, 499, 581, 526; per key 4722; 1174, 688, 806, 732); 2048 tokens:
+//   32 heads 302 whole, 109 split; 64 heads 311, 179; 128 heads 313, 272; 64 heads, 512 tokens 79,
+//   65; 300 tokens 52, 50; 128 heads, 130 tokens 34, 41;
+//   d = 64: 16 heads, 16384 tokens 1524 whole, 337, 202, 170 and 184 for 128, 256, 512 and 768;
+//   64 heads, 2048 tokens 188, 82; 256 heads, 1024 tokens 109, 108;
+//   d = 16: 16 heads, 16384 tokens 2014 whole, 133, 99, 111 and 142 for 512, 1024, 2048 and 4096;
+//   64 heads, 4096 tokens 515, 125, 79, 71, 77; 512 heads, 2048 tokens (fp32, per key) 332, 332, 315,
+//   266, 264; 1024 heads, 1024 tokens 156, 156, 155, 164, 157.
+struct GdnSplit {
+    size_t heads, want;
+};
+constexpr GdnSplit kGdnSplit128{128, 256}, kGdnSplit64{256, 512}, kGdnSplit16{512, 2048};
+constexpr int kGdnWhole = 192;
+size_t segments_wanted(const lq_dims& d, int T) {
+    const size_t heads = (size_t)d.B * d.H;
+    const GdnSplit x = d.dk == 16 ? kGdnSplit16 : d.dk == 64 ? kGdnSplit64 : kGdnSplit128;
+    return T <= kGdnWhole || heads > x.heads ? 1 : x.want / heads;
+}
+int segment_tokens(const lq_dims& d, int T) {
+    const size_t chunks = ((size_t)T + 63) / 64, want = segments_wanted(d, T);
+    return (int)((chunks + want - 1) / want * 64);
+}
 
 template <int D, bool KDA, typename TI, bool OUT>
 hipError_t chunk_launch(dim3 grid, const GdnSegArgs& sa, hipStream_t s) {
-    if constexpr (!KDA && sizeof(TI) == 2)
+    if constexpr (D == 16)
+        return launch_kernel(LQ_KERNEL_PREFILL, gdn_small_kernel<KDA, TI, OUT>, dim3((grid.x + 3) / 4, grid.y, grid.z), dim3(256), s, sa);
+    else if constexpr (!KDA && sizeof(TI) == 2)
         return launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk_kernel<D, OUT>, grid, dim3(GB<D>::NT), s, sa);
     else
         return launch_kernel(LQ_KERNEL_PREFILL, gdn_chunk32_kernel<D, KDA, TI, OUT>, grid, dim3(GF32<D, KDA>::NT), s, sa);
 }
 
 template <int D, bool KDA, typename TI>
+hipError_t gdn_chunks(const lq_dims& d, const GdnPrefillArgs& args, void* workspace, hipStream_t s) {
+    const size_t heads = (size_t)args.heads;
+    const int seg = segment_tokens(d, args.T), segs = (int)(((size_t)args.T + seg - 1) / seg);
+    GdnSegArgs sa{args.h0, nullptr, nullptr, nullptr, args.h, nullptr, args.q, args.k, args.v, args.alpha, args.beta,
+                  args.lens, args.o, 0, args.T, args.H, args.heads, seg};
+    if (segs == 1) {
+        const dim3 grid((unsigned)heads);
+        return args.o ? chunk_launch<D, KDA, TI, true>(grid, sa, s) : chunk_launch<D, KDA, TI, false>(grid, sa, s);
+    }
+    // x[s]: the state before segment s (x[0]: of h0, where h is written over it), maps behind them
+    float* x = static_cast<float*>(workspace);
+    const size_t stride = heads * D * D;
+    const int n = args.o ? segs - 1 : segs;                        // states that the first pass and the scan form
+    float* map = x + (size_t)(segs + 1) * stride;
+    sa.seg_stride = stride;
+    sa.start = nullptr;
+    sa.end = x + stride;
+    sa.map = map;
+    sa.fin = nullptr;
+    if (args.o && args.h0 == args.h) sa.keep = x;
+    hipError_t e = chunk_launch<D, KDA, TI, false>(dim3((unsigned)heads, (unsigned)n, n > 1 ? 2 : 1), sa, s);
+    if (e != hipSuccess) return e;
+    if (n > 1 || !args.o) {
+        const GdnScanArgs sc{x, map, args.o ? nullptr : args.h, stride, n};
+        if constexpr (D == 16)
+            e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan16_kernel, dim3((unsigned)(heads + 3) / 4), dim3(256), s, sc, (int)heads);
+        else
+            e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan_kernel<D>, dim3((unsigned)heads, D / 16), dim3(4 * D), s, sc);
+        if (e != hipSuccess || !args.o) return e;
+    }
+    if (sa.keep) sa.first = x;
+    sa.start = x;
+    sa.end = sa.map = sa.keep = nullptr;
+    sa.fin = args.h;
+    return chunk_launch<D, KDA, TI, true>(dim3((unsigned)heads, (unsigned)segs), sa, s);
+}
+
+template <int D, bool KDA, typename TI>
 hipError_t gdn_prefill_t(const lq_dims& d, const GdnPrefillArgs& args, void* workspace, hipStream_t s) {
-    const dim3 grid((unsigned)args.heads);
-    if constexpr (D >= 64)
-        if (args.T > kGdnStepTokens && (size_t)args.heads <= chunk_heads(D)) {
-            GdnSegArgs sa{args.h0, nullptr, nullptr, nullptr, args.h, args.q, args.k, args.v, args.alpha, args.beta,
-                          args.lens, args.o, 0, args.T, args.H, args.heads, args.T};
-            return args.o ? chunk_launch<D, KDA, TI, true>(grid, sa, s) : chunk_launch<D, KDA, TI, false>(grid, sa, s);
-        }
-    return launch_kernel(LQ_KERNEL_PREFILL, gdn_step_kernel<D, KDA, TI>, grid, dim3(D >= 64 ? 256 : 64), s, args);
+    if (args.T > kGdnStepTokens && (size_t)args.heads <= chunk_heads(D)) return gdn_chunks<D, KDA, TI>(d, args, workspace, s);
+    return launch_kernel(LQ_KERNEL_PREFILL, gdn_step_kernel<D, KDA, TI>, dim3((unsigned)args.heads), dim3(D >= 64 ? 256 : 64), s, args);
 }
 
 template <int D>
@@ -1122,7 +1546,13 @@ hipError_t gdn_prefill_d(const lq_dims& d, const GdnPrefillArgs& args, void* wor
 
 }  // namespace
 
-size_t gdn_workspace_bytes(const lq_dims& d, int T) { return 0; }
+size_t gdn_workspace_bytes(const lq_dims& d, int T) {
+    const size_t heads = (size_t)d.B * d.H;
+    if (T <= kGdnStepTokens || heads > chunk_heads(d.dk)) return 0;
+    // segment_tokens gives at most min(want, chunks of 64) segments; that bound grows with T
+    const size_t segs = std::min(segments_wanted(d, T), ((size_t)T + 63) / 64);
+    return segs <= 1 ? 0 : (2 * segs + 1) * heads * d.dk * d.dv * sizeof(float);
+}
 
 hipError_t launch_gdn_prefill(const lq_dims& d, const float* h0, float* h, int T, const void* q, const void* k,
                               const void* v, const float* alpha, const float* beta, const int32_t* lens, void* o,
