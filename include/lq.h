@@ -537,7 +537,7 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  * reorders beams, closes gaps and clears rows.
  *   dst, src  host arrays of n_layers states (n_layers >= 1; d holds for all of them,
  *           except that src's have src_rows rows).  A layer's dst and src are the
- *           same arrays (in place: src_rows = d->B, at most 4096) or do not
+ *           same arrays (in place: src_rows = d->B, at most 2048) or do not
  *           overlap; different layers' arrays do not overlap;
  *   index   int32 [B] (device, 4-byte aligned): a row of src; LQ_ROW_CLEAR: an empty
  *           state (the codec of a zero state, no window); any other value, e.g.
@@ -550,7 +550,7 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  *           index: the positions of the rows that moved (0: cleared; pos NULL:
  *           0), the others are left as they were.
  * Errors: LQ_ERR_DIMS if n_layers or src_rows < 1; LQ_ERR_UNSUPPORTED in place with
- * B > 4096, or H > 2^17; LQ_ERR_OVERLAP; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ * B > 2048, or H > 2^17; LQ_ERR_OVERLAP; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
 enum { LQ_ROW_KEEP = -1, LQ_ROW_CLEAR = -2 };
 int lq_state_gather(const lq_dims *d, int32_t n_layers, const lq_state *dst, const lq_state *src,

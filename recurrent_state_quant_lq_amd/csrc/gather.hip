@@ -6,18 +6,20 @@
 // by many): the columns of a state's rows are independent of each other, so a workgroup takes a
 // slab of columns for every row, and per step loads the pieces of all the moved rows into
 // registers, passes a barrier, and only then stores.  The step's width follows from the number
-// of moved rows, which only the device knows: as many columns as the registers take.
+// of moved rows, which only the device knows: as many columns as the registers take.  Bound by memory:
+// 56 of 64 rows of two layers (32 heads, d = 128) 26 us (4.3 TB/s), a third of 256 rows 29 us (4.1).
 #include "gdn.h"
 
 namespace lq {
 namespace {
 
 constexpr int GT = 256;                  // threads
-constexpr int GP = 16;                   // pieces of 16 bytes per thread and step
+constexpr int GP = 8;                    // pieces of 16 bytes per thread and step: eight waves a SIMD
 constexpr int kCap = GT * GP;            // pieces per step
 static_assert(kGatherInPlace == kCap, "an in-place gather holds a piece of every row");
 constexpr int kLayers = 24;              // layers per launch (their pointers are kernel arguments: 3 KB)
 constexpr int kFields = 8;
+constexpr uint64_t kSlabs = 4096;
 
 struct GatherArgs {
     void* dst[kLayers][kFields];
@@ -26,10 +28,11 @@ struct GatherArgs {
     const int32_t* pos;       // or null: no window slots
     int32_t* pos_out;         // or null
     uint32_t units[kFields];  // per row: pieces of 16 bytes (numbers of 4: comp_idx, one log decay a slot)
-    uint32_t slab0[kFields + 1];         // first slab of each field
+    uint32_t slab0[kFields + 1];         // first slab of each field (a workgroup each)
     int B, src_rows, W, C;
     uint32_t slot[kFields];   // units per window slot, 0: codec
     bool small[kFields];      // units of 4 bytes
+    int shift;                // units per slab: 1 << shift
 };
 
 enum Field { F_SQ, F_ROW, F_COL, F_IDX, F_VAL, F_K, F_M, F_G };
@@ -39,26 +42,25 @@ __device__ __forceinline__ void move_rows(const GatherArgs& a, int layer, int f,
     const U* src = static_cast<const U*>(a.src[layer][f]);
     U* dst = static_cast<U*>(a.dst[layer][f]);
     const uint32_t units = a.units[f], slot = a.slot[f], W = a.W;
-    const uint32_t first = slab * GT, width = min((uint32_t)GT, units - first);
+    const uint32_t first = slab << a.shift, end = min(first + (1u << a.shift), units);
     // columns per step: a power of two, so that a step's pieces divide among the threads by shifts
-    int shift = 8;
+    int shift = a.shift;
     while (shift > 0 && (n << shift) > kCap) --shift;
-    for (uint32_t c0 = 0; c0 < width; c0 += 1u << shift) {
+    for (uint32_t c0 = first; c0 < end; c0 += 1u << shift) {
+        const uint32_t at = c0 + (threadIdx.x & ((1u << shift) - 1));   // (GT is a multiple of the columns: the same for all pieces)
+        const int row0 = threadIdx.x >> shift, rows = GT >> shift;
+        const int window = slot ? (int)(at / slot % W) : -1;
         U x[GP];
-        uint32_t to[GP];      // (row << 8 | column) + 1, 0: nothing to store
+        uint32_t on = 0;
 #pragma unroll
         for (int u = 0; u < GP; ++u) {
-            const int e = threadIdx.x + GT * u;
-            to[u] = 0;
-            if ((e >> shift) >= n) continue;
-            const int2 m = list[e >> shift];               // (dst row, src row; -2: cleared)
-            const uint32_t col = c0 + (e & ((1 << shift) - 1));
-            if (col >= width) continue;
-            const uint32_t at = first + col;
-            if (slot && (m.y < 0 || (int)(at / slot % W) >= a.pos[m.y])) continue;
-            to[u] = ((uint32_t)(e >> shift) << 8 | col) + 1;
-            if (m.y >= 0) {
-                x[u] = src[(size_t)m.y * units + at];
+            const int e = row0 + rows * u;
+            if (e >= n || at >= end) continue;
+            const int i = list[e].y;                       // (dst row, src row; -2: cleared)
+            if (window >= 0 && window >= a.pos[i]) continue;
+            on |= 1u << u;
+            if (i >= 0) {
+                x[u] = src[(size_t)i * units + at];
             } else {
                 // an empty state: zeros, column factors of 1, the first C rows as compensators
                 const uint32_t z = f == F_COL ? 0x3f800000u : f == F_IDX ? at % (uint32_t)a.C : 0u;
@@ -69,10 +71,7 @@ __device__ __forceinline__ void move_rows(const GatherArgs& a, int layer, int f,
         __syncthreads();                                   // every row's columns are read
 #pragma unroll
         for (int u = 0; u < GP; ++u)
-            if (to[u]) {
-                const uint32_t y = to[u] - 1;
-                dst[(size_t)list[y >> 8].x * units + first + (y & 255)] = x[u];
-            }
+            if ((on >> u) & 1u) dst[(size_t)list[row0 + rows * u].x * units + at] = x[u];
     }
 }
 
@@ -120,13 +119,21 @@ hipError_t launch_gather(const lq_dims& d, int n_layers, const lq_state* dst, co
     const bool per_key = d.decay_mode == LQ_DECAY_PER_KEY;
     const uint32_t units[kFields] = {H * dk * dk / 16, H * dk / 4, H * dk / 4, H * C, H * C * dk / 4,
                                      H * W * dk / 4, H * W * dk / 4, per_key ? H * W * dk / 4 : H * W};
+    // slabs: runs of 256 bytes to 4 KB of a row, as long as there are kSlabs of them.  Few rows that move cost a
+    // slab's latencies, many its steps.  Measured for 1024, 2048, 4096 and 8192 slabs: 24 layers, 64 rows of 16
+    // heads, 4 moved 19, 19, 22, 28 us; one layer, 256 rows of 32 heads, a third moved 34, 31, 29, 29; two
+    // layers, 64 rows, 56 moved 27, 28, 26, 31 (slabs of 4 KB: 63, 114, 91 us).
+    uint64_t all = 0;
+    for (int f = 0; f < kFields; ++f) all += f >= F_K && !pos ? 0 : units[f];
+    a.shift = 8;
+    while (a.shift > 4 && (all * n_layers >> a.shift) < kSlabs) --a.shift;
     a.slab0[0] = 0;
     for (int f = 0; f < kFields; ++f) {
         const bool window = f >= F_K;
         a.units[f] = window && !pos ? 0 : units[f];
         a.slot[f] = !window ? 0 : f == F_G && !per_key ? 1 : dk / 4;
         a.small[f] = f == F_IDX || (f == F_G && !per_key);
-        a.slab0[f + 1] = a.slab0[f] + (a.units[f] + GT - 1) / GT;
+        a.slab0[f + 1] = a.slab0[f] + (uint32_t)(((uint64_t)a.units[f] + (1u << a.shift) - 1) >> a.shift);
     }
     a.index = index;
     a.pos = pos;

@@ -28,7 +28,7 @@ struct VerifyArgs {
     int32_t* path;            // [B,P]
     int32_t* n_path;
     int32_t* next;
-    double* sums;             // workspace: [rounds][B][tiles]
+    double* sums;             // workspace: [B][tiles], then the rows' walks
     int B, W, N, V, P, replace;
 };
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
@@ -37,6 +37,6 @@ size_t verify_workspace_bytes(int B, int N, int V);
 // Rows of states.  Layer l of dst and src either the same arrays (in place) or disjoint ones.
 hipError_t launch_gather(const lq_dims& d, int n_layers, const lq_state* dst, const lq_state* src, int src_rows,
                          const int32_t* index, const int32_t* pos, int32_t* pos_out, hipStream_t s);
-constexpr int kGatherInPlace = 4096;    // rows of an in-place gather
+constexpr int kGatherInPlace = 2048;    // rows of an in-place gather
 
 }  // namespace lq

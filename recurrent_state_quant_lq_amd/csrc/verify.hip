@@ -17,10 +17,17 @@
 // and the nodes' numbers are compared as they are.
 //
 // A row of p (and q) is read where a sum is needed: after a rejection (S of the next test, or
-// the total of the draw) and for the draw.  Each launch of verify_sum_kernel covers the next
-// sum of every row, a tile of a row per workgroup, and walks on from the sums before it (the walk
-// is a few comparisons, so every wave repeats it); verify_pick_kernel, one workgroup a row, forms
-// what sums are left by itself, finds the tile and the token.
+// the total of the draw) and for the draw.  verify_sum_kernel walks every row to its first sum and
+// forms it, a tile of the row per wave (the walk is a few comparisons, so every wave repeats it).
+// verify_pick_kernel, one workgroup a row, forms what sums are left, finds the tile and the token.
+// Bound by the sum's reads and by the latencies before them (positions and nodes, the nodes'
+// values, the row): 64 rows of 131072 values with a draft 11 us and 7 for the pick (the rows partly in the
+// Infinity Cache), 256 rows of 50021 without 14 and 7, one row of 32000 5.4 and 6.6.  Nodes with several
+// children need a sum for each rejection, one after the other: trees of 32 nodes, 64 rows, 9 and 32 us (drafted
+// without replacement), 11 and 61 (with).  One and two further launches of the sum kernel before the pick took
+// 66 and 75 us, not 61, there (102 and 105, not 95), and the pick's sums with 256 threads 127, not 105.
+// A quad of a row is loaded without a bounds test where its whole tile is inside (24 us, not 9, with one per
+// quad).
 #include "gdn.h"
 
 #pragma clang fp contract(off)
@@ -28,30 +35,36 @@
 namespace lq {
 namespace {
 
-constexpr int VT = 256;                  // threads
-constexpr int VQ = 4;                    // quads of values per thread
-constexpr int TV = VT * VQ * 4;          // values per tile
+constexpr int VT = 256;                  // threads of a sum's workgroup
+constexpr int PT = 1024;                 // of a pick's: its own sums need as many loads in flight as a CU takes
+constexpr int VQ = 8;                    // quads of values per lane and tile
+constexpr int TV = 64 * VQ * 4;          // values per tile: one wave's
 
 int verify_tiles(int V) { return (V + TV - 1) / TV; }
-constexpr int kVerifyRounds = 1;
-
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 
 struct Walk {
     double c, S, Z;
     uint64_t rej;             // children of cur rejected so far
+    uint64_t line;            // accepted nodes
     int cur, len, last;
     bool summed;              // S is the sum over the current residual
+};
+// A row's walk between the launches.
+enum WalkState { W_TEST, W_DRAW, W_NONE, W_SKIP };   // waits for a sum for a test, for the draw; no draw; not a row
+struct Saved {
+    Walk x;
+    int state, pad;
 };
 
 // One row's nodes, lane n = node n, as every wave holds them.
 struct Nodes {
     int parent, token;        // parent -2: no such node
     double u, p, q;
-    uint64_t line;            // accepted nodes
     int limit;
     int lane;
     bool with_draft, with_root, replace;
+    bool live;                // the row's position is one of the window's
 };
 
 __device__ __forceinline__ int rl(int x, int n) { return __builtin_amdgcn_readlane(x, n); }
@@ -68,34 +81,33 @@ __device__ __forceinline__ const float* row_of(const float* x, const float* x0, 
 __device__ __forceinline__ Nodes load_nodes(const VerifyArgs& a, int b, int lane) {
     Nodes s;
     s.lane = lane;
-    s.line = 0;
     s.with_draft = a.draft != nullptr;
     s.with_root = a.target0 != nullptr;
     s.replace = a.replace != 0;
-    s.limit = min(a.P, a.W - a.pos[b]);
-    s.parent = -2;
-    s.token = 0;
-    s.u = s.p = s.q = 0.0;
-    if (lane < a.N) {
-        const int par = a.parent[(size_t)b * a.N + lane], t = a.token[(size_t)b * a.N + lane];
-        if (par >= -1 && par < lane && t >= 0 && t < a.V) {
-            s.parent = par;
-            s.token = t;
-            s.u = (double)a.u[(size_t)lane * a.B + b];
-            if (par >= 0 || s.with_root) {
-                s.p = (double)row_of(a.target, a.target0, par, b, a)[t];
-                if (s.with_draft) s.q = (double)row_of(a.draft, a.draft0, par, b, a)[t];
-            }
-        }
+    const int n = min(lane, a.N - 1);                      // (requested together)
+    const int pos = a.pos[b], par = a.parent[(size_t)b * a.N + n], t = a.token[(size_t)b * a.N + n];
+    const float u = a.u[(size_t)n * a.B + b];
+    s.limit = min(a.P, a.W - pos);
+    s.live = pos >= 0 && pos <= a.W;
+    const bool here = lane < a.N && par >= -1 && par < lane && t >= 0 && t < a.V && s.live;
+    s.parent = here ? par : -2;
+    s.token = here ? t : 0;
+    s.u = (double)u;
+    s.p = s.q = 0.0;
+    if (here && (par >= 0 || s.with_root)) {
+        const float p = row_of(a.target, a.target0, par, b, a)[t];
+        const float q = s.with_draft ? row_of(a.draft, a.draft0, par, b, a)[t] : 0.0f;
+        s.p = (double)p;
+        s.q = (double)q;
     }
     return s;
 }
 
-__device__ __forceinline__ Walk start_walk() { return Walk{0.0, 1.0, 1.0, 0, -1, 0, -1, false}; }
+__device__ __forceinline__ Walk start_walk() { return Walk{0.0, 1.0, 1.0, 0, 0, -1, 0, -1, false}; }
 
 // Walks on until a sum over the current residual is needed for the next test (true) or no
 // child is left to test (false).
-__device__ __forceinline__ bool walk_on(Nodes& s, Walk& x) {
+__device__ __forceinline__ bool walk_on(const Nodes& s, Walk& x) {
     for (;;) {
         const bool chosen = x.cur < 0 && !s.with_root;
         uint64_t kids = 0;
@@ -123,8 +135,7 @@ __device__ __forceinline__ bool walk_on(Nodes& s, Walk& x) {
             }
         }
         if (ok) {
-            s.line |= 1ull << n;
-            x = Walk{0.0, 1.0, 1.0, 0, n, x.len + 1, n, false};
+            x = Walk{0.0, 1.0, 1.0, 0, x.line | 1ull << n, n, x.len + 1, n, false};
             continue;
         }
         x.rej |= 1ull << n;
@@ -150,272 +161,230 @@ __device__ __forceinline__ Residual residual(const VerifyArgs& a, const Nodes& s
     const bool left = x.S > 0.0;                           // (nothing left: the target as it is)
     r.p = row_of(a.target, a.target0, x.cur, b, a);
     r.q = s.with_draft && left && x.rej ? row_of(a.draft, a.draft0, x.cur, b, a) : nullptr;
-    r.c = x.c;
+    r.c = r.q ? x.c : 0.0;
     r.out = !s.with_draft && left ? x.rej : 0;
     return r;
 }
 
-// The residual's values of this thread in a tile.
-__device__ __forceinline__ void tile_values(const Residual& r, const Nodes& s, int V, int tile, int t, double (&w)[VQ * 4]) {
-    const int base = tile * TV;
+// Value i of quad j of a lane in a tile: rounds of whole lines, or (RUN) a run of neighbours a lane.
+template <bool RUN>
+__device__ __forceinline__ int value_at(int tile, int j, int lane) { return tile * TV + (RUN ? lane * VQ + j : j * 64 + lane) * 4; }
+
+// p (0 where a token is left out) and q of this lane in a tile.
+template <bool RUN>
+__device__ __forceinline__ void load_tile(const Residual& r, const Nodes& s, int V, int tile, f4u (&p)[VQ], f4u (&q)[VQ]) {
 #pragma unroll
-    for (int j = 0; j < VQ; ++j) {
-        const int at = base + (j * VT + t) * 4;
-        float p[4] = {0.f, 0.f, 0.f, 0.f}, q[4] = {0.f, 0.f, 0.f, 0.f};
-        if (at + 4 <= V) {
-            const f4u x = *reinterpret_cast<const f4u*>(r.p + at);
+    for (int j = 0; j < VQ; ++j) p[j] = q[j] = f4u{0.f, 0.f, 0.f, 0.f};
+    if (tile * TV + TV <= V) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) p[e] = x[e];
-            if (r.q) {
-                const f4u y = *reinterpret_cast<const f4u*>(r.q + at);
+        for (int j = 0; j < VQ; ++j) p[j] = *reinterpret_cast<const f4u*>(r.p + value_at<RUN>(tile, j, s.lane));
+        if (r.q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) q[e] = y[e];
-            }
-        } else {
+            for (int j = 0; j < VQ; ++j) q[j] = *reinterpret_cast<const f4u*>(r.q + value_at<RUN>(tile, j, s.lane));
+    } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (at + e < V) {
-                    p[e] = r.p[at + e];
-                    if (r.q) q[e] = r.q[at + e];
-                }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const double y = r.q ? (double)p[e] - r.c * (double)q[e] : (double)p[e];
-            w[4 * j + e] = y > 0.0 ? y : 0.0;              // (NaN: nothing)
+        for (int i = 0; i < VQ * 4; ++i) {
+            const int at = value_at<RUN>(tile, i / 4, s.lane) + i % 4;
+            if (at < V) p[i / 4][i % 4] = r.p[at];
+            if (at < V && r.q) q[i / 4][i % 4] = r.q[at];
         }
     }
+    uint32_t out = 0;                                      // bit 4 j + e: left out
     for (uint64_t m = r.out; m; m &= m - 1) {
-        const int off = rl(s.token, __ffsll((unsigned long long)m) - 1) - base;
+        const int off = rl(s.token, __ffsll((unsigned long long)m) - 1) - tile * TV;
         if (off < 0 || off >= TV) continue;
-#pragma unroll
-        for (int j = 0; j < VQ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (off == (j * VT + t) * 4 + e) w[4 * j + e] = 0.0;
+        const int at = RUN ? off / (4 * VQ) : (off >> 2) & 63, bit = RUN ? off % (4 * VQ) : 4 * (off >> 8) + (off & 3);
+        if (s.lane == at) out |= 1u << bit;
     }
+    static_assert(VQ * 4 <= 32, "a bit for every value");
+    if (__any(out != 0))
+#pragma unroll
+        for (int i = 0; i < VQ * 4; ++i) p[i / 4][i % 4] = (out >> i) & 1u ? 0.0f : p[i / 4][i % 4];
+}
+// A value's share.
+__device__ __forceinline__ double share(const Residual& r, float p, float q) {
+    const double y = (double)p - r.c * (double)q;
+    return y > 0.0 ? y : 0.0;                              // (NaN: nothing)
 }
 
-// Sum over the workgroup, the same in every thread; s_x: one value a wave.
-__device__ __forceinline__ double block_sum(double x, double* s_x) {
+__device__ __forceinline__ double wave_sum(double x) {
     for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
-    if ((threadIdx.x & 63) == 0) s_x[threadIdx.x >> 6] = x;
-    __syncthreads();
-    double y = 0.0;
-#pragma unroll
-    for (int i = 0; i < VT / 64; ++i) y += s_x[i];
-    __syncthreads();
-    return y;
+    return x;
 }
 
-__device__ __forceinline__ double tile_sum(const Residual& r, const Nodes& s, int V, int tile, double* s_x) {
-    double w[VQ * 4], x = 0.0;
-    tile_values(r, s, V, tile, threadIdx.x, w);
+__device__ __forceinline__ double tile_sum(const Residual& r, const Nodes& s, int V, int tile) {
+    f4u p[VQ], q[VQ];
+    load_tile<false>(r, s, V, tile, p, q);
+    double x = 0.0;
 #pragma unroll
-    for (int e = 0; e < VQ * 4; ++e) x += w[e];
-    return block_sum(x, s_x);
+    for (int j = 0; j < VQ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x += share(r, p[j][e], q[j][e]);
+    return wave_sum(x);
 }
 
 // Sum of a row's tiles, the same in every wave.
 __device__ __forceinline__ double row_sum(const double* tiles, int n, int lane) {
     double x = 0.0;
     for (int i = lane; i < n; i += 64) x += tiles[i];
-    for (int m = 1; m < 64; m <<= 1) x += __shfl_xor(x, m, 64);
-    return x;
+    return wave_sum(x);
 }
 
-// Walks through the sums of the rounds before `rounds`.  Returns whether the walk needs another
-// sum: for a test, or (done) for the draw.
-__device__ __forceinline__ bool replay(const VerifyArgs& a, Nodes& s, Walk& x, int b, int rounds, int& used, bool& done) {
-    const int tiles = (a.V + TV - 1) / TV;
-    for (used = 0;;) {
-        done = !walk_on(s, x);
-        if (done && ((x.summed && x.S > 0.0) || (x.cur < 0 && !s.with_root))) return false;
-        if (used == rounds) return true;
-        const double S = row_sum(a.sums + ((size_t)used * a.B + b) * tiles, tiles, s.lane);
-        ++used;
-        if (done) {                                        // the draw's total
-            x.summed = true;
-            return false;
-        }
-        x.S = S;
-        x.summed = true;
-    }
+__device__ __forceinline__ WalkState state_of(bool test, const Nodes& s, const Walk& x) {
+    return test ? W_TEST : x.cur < 0 && !s.with_root ? W_NONE : W_DRAW;
 }
 
-__global__ __launch_bounds__(VT) void verify_sum_kernel(VerifyArgs a, int round) {
-    __shared__ double s_x[VT / 64];
-    const int tiles = (a.V + TV - 1) / TV;
-    const int b = blockIdx.x / (unsigned)tiles, tile = blockIdx.x % (unsigned)tiles, lane = threadIdx.x & 63;
-    const int pos = a.pos[b];
-    if (pos < 0 || pos > a.W) return;
-    Nodes s = load_nodes(a, b, lane);
-    Walk x = start_walk();
-    int used;
-    bool done;
-    if (!replay(a, s, x, b, round, used, done)) return;
-    const double y = tile_sum(residual(a, s, x, b), s, a.V, tile, s_x);
-    if (threadIdx.x == 0) a.sums[((size_t)round * a.B + b) * tiles + tile] = y;
-}
-
-__global__ __launch_bounds__(VT) void verify_pick_kernel(VerifyArgs a) {
-    __shared__ double s_x[VT / 64];
-    __shared__ int s_tile;
-    __shared__ double s_base;
-    __shared__ int s_pick[VT / 64], s_pos[VT / 64];
-    const int b = blockIdx.x, t = threadIdx.x, lane = t & 63, w = t >> 6;
-    const int pos = a.pos[b];
-    if (pos < 0 || pos > a.W) return;
-    const int tiles = (a.V + TV - 1) / TV;
-    Nodes s = load_nodes(a, b, lane);
-    Walk x = start_walk();
-    int used;
-    bool done;
-    const bool more = replay(a, s, x, b, kVerifyRounds, used, done);
-    double* sums = a.sums + ((size_t)(used > 0 ? used - 1 : 0) * a.B + b) * tiles;
-    if (more) {                                            // sums beyond the rounds: this workgroup alone
-        sums = a.sums + ((size_t)(kVerifyRounds - 1) * a.B + b) * tiles;
-        for (;;) {
-            const Residual r = residual(a, s, x, b);
-            for (int i = 0; i < tiles; ++i) {
-                const double y = tile_sum(r, s, a.V, i, s_x);
-                if (t == 0) sums[i] = y;
-            }
-            __threadfence_block();
-            __syncthreads();
-            if (done) break;
-            x.S = row_sum(sums, tiles, lane);
-            x.summed = true;
-            __syncthreads();
-            done = !walk_on(s, x);
-            if (done && x.summed && x.S > 0.0) break;
-        }
-    }
-    // the accepted nodes' indices grow along the path
+// The accepted nodes' indices grow along the path.
+__device__ __forceinline__ void write_path(const VerifyArgs& a, const Walk& x, int b, int t) {
     if (t < a.P) {
-        int n = -1;
-        uint64_t m = s.line;
-        for (int i = 0; m; ++i, m &= m - 1)
-            if (i == t) n = __ffsll((unsigned long long)m) - 1;
-        a.path[(size_t)b * a.P + t] = n;
+        uint64_t m = x.line;
+        for (int i = 0; i < t; ++i) m &= m - 1;
+        a.path[(size_t)b * a.P + t] = m ? __ffsll((unsigned long long)m) - 1 : -1;
     }
     if (t == 0) a.n_path[b] = x.len;
-    if (x.cur < 0 && !s.with_root) {
+}
+
+__device__ __forceinline__ Saved* saved(const VerifyArgs& a, int tiles, int b) {
+    return reinterpret_cast<Saved*>(a.sums + (size_t)a.B * tiles) + b;
+}
+
+__global__ __launch_bounds__(VT) void verify_sum_kernel(VerifyArgs a) {
+    const int tiles = (a.V + TV - 1) / TV, groups = (tiles + VT / 64 - 1) / (VT / 64);
+    const int b = blockIdx.x / (unsigned)groups, group = blockIdx.x % (unsigned)groups;
+    const int t = threadIdx.x, lane = t & 63;
+    Saved* to = saved(a, tiles, b);
+    const bool first = group == 0 && t == 0;
+    Walk x = start_walk();
+    const Nodes s = load_nodes(a, b, lane);
+    if (!s.live) {
+        if (first) to->state = W_SKIP;
+        return;
+    }
+    const WalkState state = state_of(walk_on(s, x), s, x);
+    if (first) {
+        to->x = x;
+        to->state = state;
+    }
+    if (group == 0 && state != W_TEST) write_path(a, x, b, t);
+    if (state == W_NONE) return;
+    const int tile = group * (VT / 64) + __builtin_amdgcn_readfirstlane(t >> 6);
+    if (tile >= tiles) return;
+    const double y = tile_sum(residual(a, s, x, b), s, a.V, tile);
+    if (lane == 0) a.sums[(size_t)b * tiles + tile] = y;
+}
+
+__global__ __launch_bounds__(PT) void verify_pick_kernel(VerifyArgs a) {
+    const int b = blockIdx.x, t = threadIdx.x, lane = t & 63;
+    const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int tiles = (a.V + TV - 1) / TV;
+    const Saved* from = saved(a, tiles, b);
+    int state = from->state;
+    if (state == W_SKIP) return;
+    if (state == W_NONE) {
         if (t == 0) a.next[b] = -1;
+        return;
+    }
+    Walk x = from->x;
+    double* sums = a.sums + (size_t)b * tiles;
+    Nodes s = load_nodes(a, b, lane);
+    double total = row_sum(sums, tiles, lane);
+    const bool later = state == W_TEST;
+    // further sums: this workgroup alone.  A draw from nothing is one from the target as it is.
+    while (state == W_TEST || (!(total > 0.0) && s.with_draft && x.rej && x.S > 0.0)) {
+        x.S = total;
+        x.summed = true;
+        if (state == W_TEST) state = walk_on(s, x) ? W_TEST : W_DRAW;
+        if (state == W_DRAW && x.summed && x.S > 0.0) break;       // (the draft ran out: that sum is the draw's)
+        __syncthreads();                                           // (the sums before are read)
+        const Residual r = residual(a, s, x, b);
+        for (int i = w; i < tiles; i += PT / 64) {
+            const double y = tile_sum(r, s, a.V, i);
+            if (lane == 0) sums[i] = y;
+        }
+        __syncthreads();
+        total = row_sum(sums, tiles, lane);
+    }
+    if (w != 0) return;
+    if (later) write_path(a, x, b, lane);
+    if (!(total > 0.0)) {
+        if (lane == 0) a.next[b] = -1;
         return;
     }
     // ---- the draw: the tile, then the token ----
-    if (w == 0) {
-        const double total = row_sum(sums, tiles, lane);
-        const double theta = (double)a.u[(size_t)a.N * a.B + b] * total;
-        double before = 0.0;
-        int tile = -1, last = -1;
-        double base = 0.0, lbase = 0.0;
-        for (int i0 = 0; i0 < tiles && tile < 0; i0 += 64) {
-            const int i = i0 + lane;
-            const double y = i < tiles ? sums[i] : 0.0;
-            double c = y;                                   // inclusive prefix sums
-            for (int m = 1; m < 64; m <<= 1) {
-                const double z = __shfl_up(c, m, 64);
-                if (lane >= m) c += z;
-            }
-            c += before;
-            const uint64_t over = __ballot(c > theta && y > 0.0), some = __ballot(y > 0.0);
-            if (some) {
-                const int n = 63 - __clzll((long long)some);
-                last = i0 + n;
-                lbase = rl(c, n) - rl(y, n);
-            }
-            if (over) {
-                const int n = __ffsll((unsigned long long)over) - 1;
-                tile = i0 + n;
-                base = rl(c, n) - rl(y, n);
-            }
-            before = rl(c, 63);
-        }
-        if (tile < 0) {                                     // (rounding, or a number of 1 and more)
-            tile = last;
-            base = lbase;
-        }
-        if (lane == 0) {
-            s_tile = total > 0.0 ? tile : -1;
-            s_base = theta - base;
-        }
-    }
-    __syncthreads();
-    if (s_tile < 0) {
-        if (t == 0) a.next[b] = -1;
-        return;
-    }
-    // values of the tile in index order: quad j of thread t holds 4 (256 j + t) ..
-    double v[VQ * 4];
-    tile_values(residual(a, s, x, b), s, a.V, s_tile, t, v);
-    double before = 0.0;
-    const double theta = s_base;
-    int pick = -1, last = -1;
-#pragma unroll
-    for (int j = 0; j < VQ; ++j) {
-        const double mine = ((v[4 * j] + v[4 * j + 1]) + v[4 * j + 2]) + v[4 * j + 3];
-        double c = mine;
+    const double theta = (double)a.u[(size_t)a.N * a.B + b] * total;
+    double before = 0.0, base = 0.0, lbase = 0.0;
+    int tile = -1, last = -1;
+    for (int i0 = 0; i0 < tiles && tile < 0; i0 += 64) {
+        const int i = i0 + lane;
+        const double y = i < tiles ? sums[i] : 0.0;
+        double c = y;                                      // inclusive prefix sums
         for (int m = 1; m < 64; m <<= 1) {
             const double z = __shfl_up(c, m, 64);
             if (lane >= m) c += z;
         }
-        if (lane == 63) s_x[w] = c;
-        __syncthreads();
-        double wave0 = before, all = before;
-#pragma unroll
-        for (int i = 0; i < VT / 64; ++i) {
-            if (i < w) wave0 += s_x[i];
-            all += s_x[i];
+        c += before;
+        const uint64_t over = __ballot(c > theta && y > 0.0), some = __ballot(y > 0.0);
+        if (some) {
+            const int n = 63 - __clzll((long long)some);
+            last = i0 + n;
+            lbase = rl(c, n) - rl(y, n);
         }
-        __syncthreads();
-        double y = wave0 + (c - mine);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            y += v[4 * j + e];
-            if (v[4 * j + e] > 0.0) {
-                const int at = s_tile * TV + (j * VT + t) * 4 + e;
-                if (pick < 0 && y > theta) pick = at;
-                last = at;
-            }
+        if (over) {
+            const int n = __ffsll((unsigned long long)over) - 1;
+            tile = i0 + n;
+            base = rl(c, n) - rl(y, n);
         }
-        before = all;
+        before = rl(c, 63);
     }
-    // the smallest index past theta, or the largest one that has a share
-    int lo = pick < 0 ? INT32_MAX : pick;
+    if (tile < 0) {                                        // (rounding, or a number of 1 and more)
+        tile = last;
+        base = lbase;
+    }
+    // a run of neighbours a lane: the lanes' prefix sums, then the values'
+    double v[VQ * 4], mine = 0.0;
+    {
+        const Residual r = residual(a, s, x, b);
+        f4u p[VQ], q[VQ];
+        load_tile<true>(r, s, a.V, tile, p, q);
+#pragma unroll
+        for (int e = 0; e < VQ * 4; ++e) {
+            v[e] = share(r, p[e / 4][e % 4], q[e / 4][e % 4]);
+            mine += v[e];
+        }
+    }
+    double c = mine;
     for (int m = 1; m < 64; m <<= 1) {
-        lo = min(lo, __shfl_xor(lo, m, 64));
-        last = max(last, __shfl_xor(last, m, 64));
+        const double z = __shfl_up(c, m, 64);
+        if (lane >= m) c += z;
     }
-    if (lane == 0) {
-        s_pick[w] = lo;
-        s_pos[w] = last;
-    }
-    __syncthreads();
-    if (t == 0) {
+    double y = base + (c - mine);
+    int pick = INT32_MAX, end = -1;
 #pragma unroll
-        for (int i = 1; i < VT / 64; ++i) {
-            lo = min(lo, s_pick[i]);
-            last = max(last, s_pos[i]);
+    for (int e = 0; e < VQ * 4; ++e) {
+        y += v[e];
+        if (v[e] > 0.0) {
+            end = value_at<true>(tile, 0, lane) + e;
+            if (pick == INT32_MAX && y > theta) pick = end;
         }
-        a.next[b] = lo == INT32_MAX ? last : lo;
     }
+    for (int m = 1; m < 64; m <<= 1) {                     // the smallest index past theta, or the largest that has a share
+        pick = min(pick, __shfl_xor(pick, m, 64));
+        end = max(end, __shfl_xor(end, m, 64));
+    }
+    if (lane == 0) a.next[b] = pick == INT32_MAX ? end : pick;
 }
 
 }  // namespace
 
 size_t verify_workspace_bytes(int B, int N, int V) {
-    return (size_t)kVerifyRounds * B * verify_tiles(V) * sizeof(double);
+    return (size_t)B * (verify_tiles(V) * sizeof(double) + sizeof(Saved));
 }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
-    for (int r = 0; r < kVerifyRounds; ++r) {
-        const hipError_t e = launch_kernel(LQ_KERNEL_VERIFY, verify_sum_kernel, dim3((unsigned)verify_tiles(a.V) * (unsigned)a.B),
-                                           dim3(VT), s, a, r);
-        if (e != hipSuccess) return e;
-    }
-    return launch_kernel(LQ_KERNEL_VERIFY, verify_pick_kernel, dim3(a.B), dim3(VT), s, a);
+    const int groups = (verify_tiles(a.V) + VT / 64 - 1) / (VT / 64);
+    const hipError_t e = launch_kernel(LQ_KERNEL_VERIFY, verify_sum_kernel, dim3((unsigned)groups * (unsigned)a.B), dim3(VT), s, a);
+    if (e != hipSuccess) return e;
+    return launch_kernel(LQ_KERNEL_VERIFY, verify_pick_kernel, dim3(a.B), dim3(PT), s, a);
 }
 
 }  // namespace lq

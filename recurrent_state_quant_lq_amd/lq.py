@@ -10,7 +10,9 @@ library is missing, loading fails loudly (there is no fallback).
 from __future__ import annotations
 
 import ctypes as ct
+import operator
 import os
+from array import array
 from dataclasses import dataclass
 
 import numpy as np
@@ -176,6 +178,7 @@ def _raise(fn, rc):
         raise LQError(fn, rc)
 
 
+_data_ptr = torch.Tensor.data_ptr
 _STATE_FIELDS = ("sq", "row_scale", "col_scale", "comp_idx", "comp_val", "buf_k", "buf_m", "buf_g")
 
 _SQ_ORDER: dict = {}
@@ -228,7 +231,7 @@ class LayerState:
     def __setattr__(self, name, value):
         """A field set anew drops what ready() keeps."""
         self.__dict__[name] = value
-        self.__dict__["_ready"] = None
+        self.__dict__["_ready"] = self.__dict__["_valid"] = None
 
     @staticmethod
     def allocate(d: lq_dims, device="cuda") -> "LayerState":
@@ -716,6 +719,31 @@ def lq_tree_verify(d: lq_dims, pos, parent, token, target, u, path, n_path, next
             path.data_ptr(), P, n_path.data_ptr(), next.data_ptr(), _ptr(workspace) if size else None, size)
 
 
+def _c_states(states, d, rows, dev, with_buffer):
+    """The C structs of several layers' states of d's dims but `rows` rows, each validated as
+    LayerState.ready does, in one pass over their addresses."""
+    addresses = array("Q")
+    want = lq_dims.from_buffer_copy(d)
+    want.B = rows
+    want = bytes(want)
+    for x in states:
+        v = x.__dict__["_valid"]
+        if v is None:
+            v = x.__dict__["_valid"] = [tuple(t for t in (getattr(x, f) for f in _STATE_FIELDS) if t is not None),
+                                        None, None]
+        now = (with_buffer, bytes(x.dims), *map(_data_ptr, v[0]))
+        if now != v[1]:
+            x.check(with_buffer)
+            v[1:] = now, x.sq.device
+        if v[2] != dev:
+            raise ValueError(f"states on {v[2]} and {dev}")
+        if now[1] != want and any(getattr(x.dims, f) != getattr(d, f) for f in ("H", "dk", "dv", "W", "C", "decay_mode")) \
+                or x.dims.B != rows:
+            raise ValueError("the states of a call differ in their dims")
+        addresses.extend(now[2:] if len(now) == 10 else [_ptr(getattr(x, f)) or 0 for f in _STATE_FIELDS])
+    return (lq_state * len(states)).from_buffer(addresses)
+
+
 def lq_state_gather(dst, src, index, pos=None, pos_out=None, stream=None):
     """Row b of every state in dst (a LayerState or a list, one a layer) becomes row index[b]
     (device int32 [B]; LQ_ROW_KEEP, LQ_ROW_CLEAR) of the state in src, which may be the same
@@ -726,16 +754,9 @@ def lq_state_gather(dst, src, index, pos=None, pos_out=None, stream=None):
         raise ValueError("dst and src: as many states each, one at least")
     d, rows = dst[0].dims, src[0].dims.B
     dev = dst[0].sq.device
-    same = ("H", "dk", "dv", "W", "C", "decay_mode")
-    for x in (*dst, *src):
-        if any(getattr(x.dims, n) != getattr(d, n) for n in same) or x.sq.device != dev:
-            raise ValueError("the states differ in their dims or devices")
-    if any(x.dims.B != d.B for x in dst) or any(x.dims.B != rows for x in src):
-        raise ValueError("the states of a side differ in their rows")
-    buf = pos is not None
-    n = len(dst)
-    cd = (lq_state * n)(*[x.ready(buf) for x in dst])
-    cs = (lq_state * n)(*[x.ready(buf) for x in src])
+    n, buf = len(dst), pos is not None
+    cd = _c_states(dst, d, d.B, dev, buf)
+    cs = cd if all(map(operator.is_, dst, src)) else _c_states(src, d, rows, dev, buf)
     items = [("index", index, (d.B,), torch.int32)]
     if pos is not None:
         items.append(("pos", pos, (rows,), torch.int32))

@@ -66,7 +66,8 @@ MAPS = {
 @pytest.mark.parametrize("kind", sorted(MAPS))
 @pytest.mark.parametrize("B,H,d,W,C,per_key,windows", [
     (1, 1, 16, 1, 0, False, True), (5, 3, 128, 16, 4, False, True), (9, 1, 64, 13, 1, True, True),
-    (33, 2, 16, 5, 8, False, True), (6, 2, 128, 32, 3, True, False), (300, 1, 16, 4, 2, False, True)])
+    (33, 2, 16, 5, 8, False, True), (6, 2, 128, 32, 3, True, False), (300, 1, 16, 4, 2, False, True),
+    (2048, 1, 16, 2, 1, False, True), (70, 9, 64, 16, 4, False, True)])
 def test_in_place(B, H, d, W, C, per_key, windows, kind):
     st = state(B + d, B, H, d, W, C, per_key)
     before = host(st)

@@ -133,7 +133,7 @@ def test_gather_argument_errors():
     assert call(pos_out=A) == lq.LQ_ERR_OVERLAP          # index itself
     assert call(pos=ct.c_void_p(0x7100000), pos_out=ct.c_void_p(0x7100004)) == lq.LQ_ERR_OVERLAP
     assert call(index=ct.c_void_p(0x10000010)) == lq.LQ_ERR_OVERLAP
-    assert call(_dims(B=4097), src=[_state(1)], rows=4097) == lq.LQ_ERR_UNSUPPORTED
+    assert call(_dims(B=2049), src=[_state(1)], rows=2049) == lq.LQ_ERR_UNSUPPORTED
     assert b"overlap" in L.lq_status_str(lq.LQ_ERR_OVERLAP)
 
 
