@@ -647,26 +647,21 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
 // ---------------------------------------------------------------------------
 // The same algebra with all operands in three bf16 parts (six products of nine: the others are at
 // most 2^-21 of a product, 2^-24.7 on average).  Wave w owns the 16 columns 16 w + li.
-// A decay per key channel: with g the prefix sums (64 bits, per channel) of the log decays after
-// the chunk's first token,
-//     H' = diag(e^{g_0}) H,  x_n = e^{g_n} o k_n (and q_n),  y_i = e^{-g_i} o k_i,
-//     A_{n,i} = beta_n <x_n, y_i>,  P_{n,i} = <e^{g_n} o q_n, y_i>,  R = beta (V - X H'),
-//     O = (e^g o Q) H' + P M,  H = diag(e^{g_L}) (H' + Y^T M),
-// so no exponential of a pair of tokens is formed.  e^{-g} grows: a chunk ends before a token
-// whose g passes kMaxDecay in a channel (e^{+-64} and its parts are in range), which is then the
-// first of the next chunk, and whose own decay goes to H as a factor of at most 1.
+// A decay per key channel: with f the prefix products (per channel) of the decays after the
+// chunk's first token,
+//     H' = diag(alpha_0) H,  x_n = f_n o k_n (and q_n),  y_i = k_i / f_i,
+//     A_{n,i} = beta_n <x_n, y_i>,  P_{n,i} = <f_n o q_n, y_i>,  R = beta (V - X H'),
+//     O = (f o Q) H' + P M,  H = diag(f_L) (H' + Y^T M),
+// so neither logarithms nor exponentials are formed.  f_n / f_i holds the roundings of the factors
+// between the two tokens, as the recurrence's own products do (one of 2^-24 a factor), and those of
+// at most one product and one reciprocal more.  1 / f grows: a chunk ends before a token whose f
+// leaves [kMinDecay, 1 / kMinDecay] in a channel (the parts are in range there), which is then the
+// first of the next chunk, and whose own decay goes to H as it is.
 constexpr int GF = 32;        // tokens per chunk
-constexpr double kMaxDecay = 64.0;
+constexpr float kMinDecay = 0x1p-92f;
 
-// e^x and e^{-x}, x in 64 bits: an exponent off by 2^-24 of itself would count at |x| up to kMaxDecay.
-__device__ __forceinline__ void exp_both(double x, float& e, float& inv) {
-    const double y = x * 1.4426950408889634;
-    const float hi = (float)y, lo = (float)(y - (double)hi) * 0.6931472f;
-    e = __builtin_amdgcn_exp2f(hi);
-    e += e * lo;
-    inv = __builtin_amdgcn_exp2f(-hi);
-    inv -= inv * lo;
-}
+// A prefix product leaves the range, or is no number.
+__device__ __forceinline__ bool decays_far(float f) { return !(f >= kMinDecay && f <= 1.0f / kMinDecay); }
 
 template <typename TI> struct Two;                                 // two neighbouring channels of a token
 template <> struct Two<float> { typedef u32x2 T; };
@@ -689,13 +684,13 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
     using P = GF32<D, KDA>;
     constexpr int NW = P::NW, NT = P::NT, RT = P::RT, QP = P::QP, ROWS = P::ROWS;
     constexpr int LA = 20, ES = sizeof(TI);
-    __shared__ __align__(16) uint16_t sK[3][ROWS];                 // K (per key: e^g o K) in parts
-    __shared__ __align__(16) uint16_t sY[3][KDA ? ROWS : 8];       // per key: e^{-g} o K in parts
-    __shared__ __align__(16) uint16_t sQ[3 * (OUT ? ROWS : 8)];    // Q (per key: e^g o Q), then P, in parts
+    __shared__ __align__(16) uint16_t sK[3][ROWS];                 // K (per key: f o K) in parts
+    __shared__ __align__(16) uint16_t sY[3][KDA ? ROWS : 8];       // per key: K / f in parts
+    __shared__ __align__(16) uint16_t sQ[3 * (OUT ? ROWS : 8)];    // Q (per key: f o Q), then P, in parts
     __shared__ __align__(16) uint16_t sA[3][kBlk];                 // -A left of the second diagonal block, in parts
     __shared__ __align__(16) float sD[2][16 * LA];                 // inverses of the diagonal blocks of I + A
     __shared__ std::conditional_t<KDA, GdnSteps<GF>, GdnGates<GF>> s_gate[KDA ? 1 : 2];   // of this chunk (and the next)
-    __shared__ __align__(16) float s_first[KDA ? D : 4], s_last[KDA ? D : 4];   // per key: e^{g_0}, e^{g_L}
+    __shared__ __align__(16) float s_first[KDA ? D : 4], s_last[KDA ? D : 4];   // per key: the first token's decay, f_L
     __shared__ int s_cut[2];
 
     const int t = threadIdx.x, lane = t & 63;
@@ -795,60 +790,38 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         const int c = 2 * pair, u = (c & 31) >> 2;                 // operand order of the channel's 32-block
         const int at = pm<GF>(n0, (c >> 5) * 4 + (u & 3)) + 4 * (u >> 2) + (c & 3);
         int first = GF;
-        [[maybe_unused]] double g[4][2];
+        [[maybe_unused]] f32x2 f[4];
         if constexpr (KDA) {
-            double s0 = 0.0, s1 = 0.0, mine0 = 0.0, mine1 = 0.0;
-            float l0 = 0.0f, l1 = 0.0f;
+            f32x2 run = {1.0f, 1.0f}, before = run, all = run;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool on = (int)n0 + e < L;
-                const float x0 = on ? log_decay(ad[e][0]) : 0.0f, x1 = on ? log_decay(ad[e][1]) : 0.0f;
-                if (n0 + e > 0) {                                  // (the first token's own decay is H's)
-                    s0 += (double)x0;
-                    s1 += (double)x1;
-                    if (!finite_f32(x0) || !finite_f32(x1)) first = min(first, (int)n0 + e);
-                } else {
-                    l0 = x0;
-                    l1 = x1;
-                }
-                g[e][0] = s0;
-                g[e][1] = s1;
+                const f32x2 x = {on ? ad[e][0] : 1.0f, on ? ad[e][1] : 1.0f};
+                if (n0 + e > 0) run *= x;                          // (the first token's own decay is H's)
+                else *reinterpret_cast<f32x2*>(&s_first[c]) = x;
+                f[e] = run;
             }
-            double* s_tot = reinterpret_cast<double*>(sY[0]);      // log decays of four tokens, in Y's place
-            static_assert(sizeof(sY) >= 8 * D * sizeof(double) || !KDA, "a total per channel and four tokens");
-            s_tot[quad * D + c] = s0;
-            s_tot[quad * D + c + 1] = s1;
-            if (quad == 0) {
-                s_first[c] = __expf(l0);
-                s_first[c + 1] = __expf(l1);
-            }
+            float* s_tot = reinterpret_cast<float*>(sY[0]);        // products of four tokens, in Y's place
+            static_assert(sizeof(sY) >= 8 * D * sizeof(float) || !KDA, "a total per channel and four tokens");
+            *reinterpret_cast<f32x2*>(&s_tot[quad * D + c]) = run;
             if (w == NW - 1 && lane < GF) {
                 const float b = lane < L ? be : 0.0f;
                 s_gate[0].b[lane] = b;
                 if (lane > 0 && !finite_f32(b)) atomicMin(&s_cut[cur], lane);
             }
             __syncthreads();
-            double gl0 = 0.0, gl1 = 0.0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (i == (int)quad) {
-                    mine0 = gl0;
-                    mine1 = gl1;
-                }
-                gl0 += s_tot[i * D + c];
-                gl1 += s_tot[i * D + c + 1];
+                if (i == (int)quad) before = all;
+                all *= *reinterpret_cast<const f32x2*>(&s_tot[i * D + c]);
             }
             __syncthreads();                                       // the totals are read
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                g[e][0] += mine0;
-                g[e][1] += mine1;
-                if (n0 + e > 0 && (g[e][0] < -kMaxDecay || g[e][1] < -kMaxDecay)) first = min(first, (int)n0 + e);
+                f[e] *= before;
+                if (n0 + e > 0 && (decays_far(f[e][0]) || decays_far(f[e][1]))) first = min(first, (int)n0 + e);
             }
-            if (quad == 0) {
-                s_last[c] = __expf((float)gl0);
-                s_last[c + 1] = __expf((float)gl1);
-            }
+            if (quad == 0) *reinterpret_cast<f32x2*>(&s_last[c]) = all;
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -856,11 +829,8 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
             if (n0 + e > 0 && (!finite_f32(k[0]) || !finite_f32(k[1]))) first = min(first, (int)n0 + e);
             float x[6] = {k[0], k[1], q[0], q[1], 0.f, 0.f};
             if constexpr (KDA) {
-                float e0, e1, i0, i1;
-                exp_both(g[e][0], e0, i0);
-                exp_both(g[e][1], e1, i1);
-                x[0] *= e0, x[1] *= e1, x[2] *= e0, x[3] *= e1;
-                x[4] = i0 * k[0], x[5] = i1 * k[1];
+                x[4] = __builtin_amdgcn_rcpf(f[e][0]) * k[0], x[5] = __builtin_amdgcn_rcpf(f[e][1]) * k[1];
+                x[0] *= f[e][0], x[1] *= f[e][1], x[2] *= f[e][0], x[3] *= f[e][1];
             }
             uint32_t p[3][3];
             split3<6>(x, p);
@@ -1085,7 +1055,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         __builtin_amdgcn_sched_barrier(0);
         load(ce, te);                                              // (none left: zeros)
         __builtin_amdgcn_sched_barrier(0);
-        // ---- H = e^{g_L} H + K^T (w o M); per key: e^{g_L} o (H + Y^T M) ----
+        // ---- H = e^{g_L} H + K^T (w o M); per key: f_L o (H + Y^T M) ----
         const int kt = pm<GF>(4 * lg + (li >> 2), li & 3);         // transposed reads: 4 tokens of 16 channels a lane group
         if constexpr (!KDA) {
             const v4f w0 = *reinterpret_cast<const v4f*>(&G.w[4 * lg]), w1 = *reinterpret_cast<const v4f*>(&G.w[16 + 4 * lg]);
@@ -1133,6 +1103,12 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
 // layout that the instruction takes (lane (lg, li), step v: row or column li, index 4 lg + v).  The
 // scores are formed transposed, so that their accumulators are the A operand of P M as they are;
 // only A goes through LDS, for block_solve.  Per key: the same factors as the larger kernel's.
+// The value of the lane that far before in the row of 16, 1 where there is none.
+template <int CTRL>
+__device__ __forceinline__ float dpp_one(float x) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(1.0f), __float_as_int(x), CTRL, 0xf, 0xf, false));
+}
+
 template <bool KDA, typename TI, bool OUT>
 __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
     constexpr int D = 16, CS = 16, LR = 20;
@@ -1198,10 +1174,10 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
             for (int i = 0; i < 4; ++i)
                 if ((m >> (16 * i)) & 0xffffu) cut |= 1u << (4 * i + v);
         }
-        // decays: scalar g of token li, gi of tokens 4 lg + v; per key gr of token li, channels 4 lg + v, and gc
-        // of tokens 4 lg + v, channel li, after the first token
-        double g = 0.0, gl = 0.0, gi[4], gr[4], gc[4];
-        float e0[4], el[4];                                        // per key: e^{g_0}, e^{g_L} of channels 4 lg + v
+        // decays: scalar g of token li, gi of tokens 4 lg + v; per key the products fr of token li, channels
+        // 4 lg + v, and fc of tokens 4 lg + v, channel li, after the first token
+        double g = 0.0, gl = 0.0, gi[4];
+        float fr[4], fc[4], e0[4], el[4];                          // per key: the first decay and f_L of channels 4 lg + v
         if constexpr (!KDA) {
             const float la = log_decay(cur.al);
             cut |= fold(__ballot(!finite_f32(la)));
@@ -1216,44 +1192,38 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) gi[v] = __shfl(g, 4 * lg + v, 16);
         } else {
-            float ar[4], lr[4];
+            float ar[4];
             cur.ar.widen4(ar);
-            bool odd = false, far = false;
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                lr[v] = log_decay(ar[v]);
-                odd |= !finite_f32(lr[v]);
-            }
-            cut |= fold(__ballot(odd));
             cut &= ~1u;
             if (cut) L = min(L, __ffs(cut) - 1);
+            bool far = false;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                double x = li > 0 && li < L ? (double)lr[v] : 0.0;
-                x = scan_step<0x111, 0xf>(x);
-                x = scan_step<0x112, 0xf>(x);
-                x = scan_step<0x114, 0xf>(x);
-                gr[v] = scan_step<0x118, 0xf>(x);
-                far |= gr[v] < -kMaxDecay;
+                float x = li > 0 && li < L ? ar[v] : 1.0f;
+                x *= dpp_one<0x111>(x);
+                x *= dpp_one<0x112>(x);
+                x *= dpp_one<0x114>(x);
+                fr[v] = x * dpp_one<0x118>(x);
+                far |= decays_far(fr[v]);
             }
             cut = fold(__ballot(far)) & ~1u;
-            if (cut) L = min(L, __ffs(cut) - 1);                   // (sums before it stand)
+            if (cut) L = min(L, __ffs(cut) - 1);                   // (products before it stand)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-                e0[v] = __expf(__shfl(lr[v], 0, 16));
-                el[v] = __expf((float)__shfl(gr[v], L - 1, 16));
+                e0[v] = __shfl(ar[v], 0, 16);
+                el[v] = __shfl(fr[v], L - 1, 16);
             }
-            double sum = 0.0;                                      // this lane's four tokens, then those of the groups before
+            float run = 1.0f;                                      // this lane's four tokens, then those of the groups before
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const int n = 4 * lg + v;
-                sum += n > 0 && n < L ? (double)log_decay(cur.at[v]) : 0.0;
-                gc[v] = sum;
+                run *= n > 0 && n < L ? cur.at[v] : 1.0f;
+                fc[v] = run;
             }
-            const double s0 = __shfl(sum, li, 64), s1 = __shfl(sum, 16 + li, 64), s2 = __shfl(sum, 32 + li, 64);
-            const double before = lg == 0 ? 0.0 : lg == 1 ? s0 : lg == 2 ? s0 + s1 : s0 + s1 + s2;
+            const float s0 = __shfl(run, li, 64), s1 = __shfl(run, 16 + li, 64), s2 = __shfl(run, 32 + li, 64);
+            const float before = lg == 0 ? 1.0f : lg == 1 ? s0 : lg == 2 ? s0 * s1 : s0 * s1 * s2;
 #pragma unroll
-            for (int v = 0; v < 4; ++v) gc[v] += before;
+            for (int v = 0; v < 4; ++v) fc[v] *= before;
         }
         const int next = c0 + L;
         if (next < te) load(next, nxt);
@@ -1267,13 +1237,10 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
             vt[v] = on ? vt[v] : 0.0f;
             kt[v] = on ? kt[v] : 0.0f;
             if constexpr (KDA) {
-                float e, i;
-                exp_both(gr[v], e, i);
-                xk[v] = li < L ? e * k0 : 0.0f;
-                xq[v] = li < L ? e * q0 : 0.0f;
-                yr[v] = li < L ? i * k0 : 0.0f;
-                exp_both(gc[v], e, i);
-                yc[v] = on ? i * kt[v] : 0.0f;
+                xk[v] = li < L ? fr[v] * k0 : 0.0f;
+                xq[v] = li < L ? fr[v] * q0 : 0.0f;
+                yr[v] = li < L ? __builtin_amdgcn_rcpf(fr[v]) * k0 : 0.0f;
+                yc[v] = on ? __builtin_amdgcn_rcpf(fc[v]) * kt[v] : 0.0f;
                 H[v] *= e0[v];
             } else {
                 xk[v] = k0, xq[v] = q0, yr[v] = k0;
