@@ -546,9 +546,9 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  *           rows; the window's slots before them move, later slots of dst stay.
  *           NULL: the windows are empty (after a prompt or a flush), and the
  *           states' buffers may be NULL;
- *   pos_out nullable int32 [B] (device, 4-byte aligned), not overlapping pos or
- *           index: the positions of the rows that moved (0: cleared; pos NULL:
- *           0), the others are left as they were.
+ *   pos_out nullable int32 [B] (device, 4-byte aligned), not overlapping pos,
+ *           index or a state: the positions of the rows that moved (0: cleared;
+ *           pos NULL: 0), the others are left as they were.
  * Errors: LQ_ERR_DIMS if n_layers or src_rows < 1; LQ_ERR_UNSUPPORTED in place with
  * B > 2048, or H > 2^17; LQ_ERR_OVERLAP; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */

@@ -139,6 +139,7 @@ int check_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const 
             if (row[f] == 0) continue;
             if (same ? x[f] != y[f] || S != B : overlap(x[f], B * row[f], y[f], S * row[f])) return LQ_ERR_OVERLAP;
             if (overlap(x[f], B * row[f], index, B * 4) || overlap(x[f], B * row[f], pos, S * 4)) return LQ_ERR_OVERLAP;
+            if (overlap(x[f], B * row[f], pos_out, B * 4) || overlap(y[f], S * row[f], pos_out, B * 4)) return LQ_ERR_OVERLAP;
         }
         for (int32_t m = 0; m < l; ++m)
             if (overlap(dst[l].sq, B * row[0], dst[m].sq, B * row[0]) ||

@@ -12,7 +12,6 @@ from __future__ import annotations
 import ctypes as ct
 import operator
 import os
-from array import array
 from dataclasses import dataclass
 
 import numpy as np
@@ -722,26 +721,26 @@ def lq_tree_verify(d: lq_dims, pos, parent, token, target, u, path, n_path, next
 def _c_states(states, d, rows, dev, with_buffer):
     """The C structs of several layers' states of d's dims but `rows` rows, each validated as
     LayerState.ready does, in one pass over their addresses."""
-    addresses = array("Q")
     want = lq_dims.from_buffer_copy(d)
     want.B = rows
     want = bytes(want)
+    structs = bytearray()
     for x in states:
         v = x.__dict__["_valid"]
         if v is None:
             v = x.__dict__["_valid"] = [tuple(t for t in (getattr(x, f) for f in _STATE_FIELDS) if t is not None),
-                                        None, None]
+                                        None, None, None]
         now = (with_buffer, bytes(x.dims), *map(_data_ptr, v[0]))
         if now != v[1]:
             x.check(with_buffer)
-            v[1:] = now, x.sq.device
+            v[1:] = now, x.sq.device, bytes(x.c_state())
         if v[2] != dev:
             raise ValueError(f"states on {v[2]} and {dev}")
-        if now[1] != want and any(getattr(x.dims, f) != getattr(d, f) for f in ("H", "dk", "dv", "W", "C", "decay_mode")) \
-                or x.dims.B != rows:
+        if now[1] != want and (x.dims.B != rows or any(
+                getattr(x.dims, f) != getattr(d, f) for f in ("H", "dk", "dv", "W", "C", "decay_mode"))):
             raise ValueError("the states of a call differ in their dims")
-        addresses.extend(now[2:] if len(now) == 10 else [_ptr(getattr(x, f)) or 0 for f in _STATE_FIELDS])
-    return (lq_state * len(states)).from_buffer(addresses)
+        structs += v[3]
+    return (lq_state * len(states)).from_buffer(structs)
 
 
 def lq_state_gather(dst, src, index, pos=None, pos_out=None, stream=None):

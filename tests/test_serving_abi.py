@@ -133,6 +133,8 @@ def test_gather_argument_errors():
     assert call(pos_out=A) == lq.LQ_ERR_OVERLAP          # index itself
     assert call(pos=ct.c_void_p(0x7100000), pos_out=ct.c_void_p(0x7100004)) == lq.LQ_ERR_OVERLAP
     assert call(index=ct.c_void_p(0x10000010)) == lq.LQ_ERR_OVERLAP
+    for at in (0x10000010, 0x20000010):                  # positions written into a state
+        assert call(pos_out=ct.c_void_p(at)) == lq.LQ_ERR_OVERLAP
     assert call(_dims(B=2049), src=[_state(1)], rows=2049) == lq.LQ_ERR_UNSUPPORTED
     assert b"overlap" in L.lq_status_str(lq.LQ_ERR_OVERLAP)
 
