@@ -205,6 +205,26 @@ __device__ __forceinline__ void make_gates(float alpha, float beta, int left, in
     }
 }
 
+// What the scan reads is kept (d >= 64) in the tiles of 16 x 16 that its lanes hold, each load a run of 1 KB: a
+// segment's states as the accumulators of this file's kernels hold them (whichever columns those are: the scan's
+// are independent), its map as the scan's operand, row li, columns 4 lg .. 4 lg + 3 of a tile.  (With both as
+// rows of the matrix, four runs of 64 bytes a load, a step of the scan took 2.4 us at d = 128, not 1.5.)
+__device__ __forceinline__ v4f* state_at(float* x, int tiles, int row_tile, int col_tile, int lane) {
+    return reinterpret_cast<v4f*>(x) + (size_t)(row_tile * tiles + col_tile) * 64 + lane;
+}
+template <int D>
+__device__ __forceinline__ v4f* map_at(float* map, int row, int col) {
+    return reinterpret_cast<v4f*>(map) + (size_t)((row >> 4) * (D / 16) + (col >> 4)) * 64 + ((col >> 2) & 3) * 16 + (row & 15);
+}
+// Accumulators (rows 4 lg + v, column li) as row 4 lg + li % 4, columns 4 (li / 4) + v.
+__device__ __forceinline__ v4f quad_rows(const v4f& x, int li) {
+    const bool odd = li & 1, up = li & 2;
+    const float a = dpp<DPP_XOR1>(odd ? x[0] : x[1]), b = dpp<DPP_XOR1>(odd ? x[2] : x[3]);
+    const float a0 = odd ? a : x[0], a1 = odd ? x[1] : a, b0 = odd ? b : x[2], b1 = odd ? x[3] : b;
+    const float c = dpp<DPP_XOR2>(up ? a0 : b0), e = dpp<DPP_XOR2>(up ? a1 : b1);
+    return up ? v4f{c, e, b0, b1} : v4f{a0, a1, c, e};
+}
+
 // (n, i) of a 16 x 32 operand block, and block (r, j) of a part of P (j <= r / 2) and of A (r >= 1).
 __device__ __forceinline__ constexpr int blk(int row, int i) { return pm<16>(row, (i & 15) >> 2) + 4 * ((i >> 4) & 1) + (i & 3); }
 constexpr int kBlk = pm_shorts<16>(4);
@@ -247,13 +267,17 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
     const bool map = !OUT && blockIdx.z;                           // the segment's map: from the identity, without values
     if (map && blockIdx.y == 0) return;
     const float* start = blockIdx.y == 0 ? a.first : a.start;
-    const size_t from = blockIdx.y == 0 ? head * (size_t)(D * D) : soff;
 
     // H[rt][ct][v] = H[16 rt + 4 lg + v][CT (16 w + li) + ct]
     typedef float cols __attribute__((ext_vector_type(CT)));
     v4f H[RT][CT];
-    if (!map && start) {
-        const float* x = start + from + (size_t)(4 * (lane >> 4)) * D + CT * (16 * w + (lane & 15));
+    if (!map && start && blockIdx.y > 0) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) H[rt][ct] = *state_at(const_cast<float*>(start) + soff, D / 16, rt, CT * w + ct, lane);
+    } else if (!map && start) {
+        const float* x = start + head * (size_t)(D * D) + (size_t)(4 * (lane >> 4)) * D + CT * (16 * w + (lane & 15));
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -637,9 +661,33 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk
     }
-    float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
-    if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
-    if (end) write_state(end);
+    if (map) {
+        const int lo = fresh(lane), li = lo & 15, lg = lo >> 4;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if constexpr (CT == 1) {
+                *map_at<D>(a.map + soff, 16 * rt + 4 * lg + (li & 3), 16 * w + (li & 12)) = quad_rows(H[rt][0], li);
+            } else {                                               // two columns a lane: the even lane the rows v = 0, 1
+                const bool odd = li & 1;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const float x0 = H[rt][0][v], x1 = H[rt][1][v], y0 = H[rt][0][2 + v], y1 = H[rt][1][2 + v];
+                    const float r0 = dpp<DPP_XOR1>(odd ? x0 : y0), r1 = dpp<DPP_XOR1>(odd ? x1 : y1);
+                    *map_at<D>(a.map + soff, 16 * rt + 4 * lg + 2 * (li & 1) + v, 32 * w + 2 * (li & 14)) =
+                        odd ? v4f{r0, r1, y0, y1} : v4f{x0, x1, r0, r1};
+                }
+            }
+        }
+        return;
+    }
+    if (a.end) {
+        const int lo = fresh(lane);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) *state_at(a.end + soff, D / 16, rt, CT * w + ct, lo) = H[rt][ct];
+    }
+    if (a.fin && blockIdx.y == gridDim.y - 1) write_state(a.fin + head * (size_t)(D * D));
 }
 
 // ---------------------------------------------------------------------------
@@ -705,8 +753,11 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
     const float* start = blockIdx.y == 0 ? a.first : a.start;
 
     v4f H[RT];                                                     // H[rt][v] = H[16 rt + 4 lg + v][16 w + li]
-    if (!map && start) {
-        const float* from = start + (blockIdx.y == 0 ? head * (size_t)(D * D) : soff) + (size_t)(4 * (lane >> 4)) * D + 16 * w + (lane & 15);
+    if (!map && start && blockIdx.y > 0) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) H[rt] = *state_at(const_cast<float*>(start) + soff, D / 16, rt, w, lane);
+    } else if (!map && start) {
+        const float* from = start + head * (size_t)(D * D) + (size_t)(4 * (lane >> 4)) * D + 16 * w + (lane & 15);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -1085,10 +1136,18 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         }
         __syncthreads();                                           // LDS is rewritten by the next chunk
     }
-    float* end = map ? a.map + soff : a.end ? a.end + soff : nullptr;
-    if (!map && a.fin && blockIdx.y == gridDim.y - 1) end = a.fin + head * (size_t)(D * D);
-    if (!end) return;
     const int lf = fresh(lane);
+    if (map) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            *map_at<D>(a.map + soff, 16 * rt + 4 * (lf >> 4) + (lf & 3), 16 * w + (lf & 12)) = quad_rows(H[rt], lf & 15);
+        return;
+    }
+    if (a.end)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) *state_at(a.end + soff, D / 16, rt, w, lf) = H[rt];
+    if (!a.fin || blockIdx.y < gridDim.y - 1) return;
+    float* end = a.fin + head * (size_t)(D * D);
     end += (size_t)(4 * (lf >> 4)) * D + 16 * w + (lf & 15);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
@@ -1320,31 +1379,28 @@ struct GdnScanArgs {
     int n;                    // states to form: x[2] .. x[n]
 };
 constexpr int kScanAhead = 4;
-template <int D>
+template <int D, int CT>                                           // CT: neighbouring columns in a lane's tiles
 __global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
     constexpr int KS = D / 32;
     __shared__ __align__(16) uint16_t s_x[2][3][pm_shorts<16>(D / 8)];   // [column][channel], in parts
     const int t = threadIdx.x, lane = t & 63, li = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
     const size_t at = blockIdx.x * (size_t)(D * D);
-    // G: row 16 w + li, channels 32 ks + 4 lg .. and 16 further (whole 64-byte runs of a row per load);
-    // X: rows 16 w + 4 lg + v of column li
-    const float* g0 = a.map + at + (size_t)(16 * w + li) * D + 4 * lg;
-    float* x0 = a.x + at + (size_t)(16 * w + 4 * lg) * D + 16 * blockIdx.y + li;
+    // G: row 16 w + li, channels 16 c + 4 lg + e; X: rows 16 w + 4 lg + v of the tile's column li
+    const float* g0 = a.map + at + (size_t)w * (16 * D) + 4 * lane;
+    float* x0 = reinterpret_cast<float*>(state_at(a.x + at, D / 16, w, blockIdx.y, lane));
     struct Step {
         v4f g[KS][2], e;
     };
     auto load = [&](int s, Step& y) {                              // kScanAhead steps before their use
         if (s > a.n) return;
         const float* g = g0 + (s - 1) * a.stride;
-        const float* e = x0 + s * a.stride;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-            y.g[ks][0] = *reinterpret_cast<const v4f*>(g + 32 * ks);
-            y.g[ks][1] = *reinterpret_cast<const v4f*>(g + 32 * ks + 16);
+            y.g[ks][0] = *reinterpret_cast<const v4f*>(g + 512 * ks);
+            y.g[ks][1] = *reinterpret_cast<const v4f*>(g + 512 * ks + 256);
         }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y.e[v] = e[(size_t)v * D];
+        y.e = *reinterpret_cast<const v4f*>(x0 + s * a.stride);
     };
     v4f x;
     auto step = [&](int s, Step& y) {
@@ -1374,12 +1430,10 @@ __global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
             u[ks & 1] = mfma_split(g[ks], b, u[ks & 1]);
         }
         x = u[0] + u[1];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) x0[s * a.stride + (size_t)v * D] = x[v];
+        *reinterpret_cast<v4f*>(x0 + s * a.stride) = x;
     };
     Step y[kScanAhead];
-#pragma unroll
-    for (int v = 0; v < 4; ++v) x[v] = x0[a.stride + (size_t)v * D];
+    x = *reinterpret_cast<const v4f*>(x0 + a.stride);
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i) load(2 + i, y[i]);
     for (int s = 2; s <= a.n; s += kScanAhead)
@@ -1388,7 +1442,7 @@ __global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
             if (s + i <= a.n) step(s + i, y[i]);
     if (a.fin)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) a.fin[at + (size_t)(16 * w + 4 * lg + v) * D + 16 * blockIdx.y + li] = x[v];
+        for (int v = 0; v < 4; ++v) a.fin[at + (size_t)(16 * w + 4 * lg + v) * D + CT * (16 * (blockIdx.y / CT) + li) + blockIdx.y % CT] = x[v];
 }
 
 // d = 16: one wave a head.
@@ -1423,12 +1477,13 @@ constexpr size_t chunk_heads(int d) { return d == 16 ? (size_t)INT32_MAX : (size
 // Tokens per segment, a multiple of 64.  Segments cost the prompt a second time (twice: states and
 // maps) and the scan, so they pay where the heads alone leave most CUs idle: up to `heads` heads,
 // enough segments for `want` workgroups (d = 16: waves).  Measured, bf16, replayed in a graph:
-//   d = 128: 16 heads, 16384 tokens 2435 us whole, 541, 359, 401 and 381 for 128, 256, 384 and 512
-//   workgroups (fp32: 3218; 752, 499, 581, 526; per key 4722; 1174, 688, 806, 732); 2048 tokens:
-//   32 heads 302 whole, 109 split; 64 heads 311, 179; 128 heads 313, 272; 64 heads, 512 tokens 79,
-//   65; 300 tokens 52, 50; 128 heads, 130 tokens 34, 41;
-//   d = 64: 16 heads, 16384 tokens 1524 whole, 337, 202, 170 and 184 for 128, 256, 512 and 768;
-//   64 heads, 2048 tokens 188, 82; 256 heads, 1024 tokens 109, 108;
+//   d = 128: 16 heads, 16384 tokens 2429 us whole, 534, 340, 378 and 328-337 for 128, 256, 384 and 512
+//   workgroups (fp32: 3235; 741, 486, 559, 501; per key 4232; 1052, 591, 703, 585); 2048 tokens: 32 heads
+//   302; 142, 103, 115, 110; 64 heads 310; 266, 175, 201, 183; 128 heads 312 whole, 272 for 256, 296
+//   for 512; 64 heads, 512 tokens 79; 72, 62, 61, 79; 300 tokens 51; 55, 49, 52, 52; 128 heads, 130
+//   tokens 34, 41 for 256;
+//   d = 64: 16 heads, 16384 tokens 1528 whole, 199, 170, 180 and 185 for 256, 512, 768 and 1024; 64 heads,
+//   2048 tokens 189; 101, 81, 84, 88; 256 heads, 1024 tokens 110; 108, 108, 115, 126;
 //   d = 16: 16 heads, 16384 tokens 2014 whole, 133, 99, 111 and 142 for 512, 1024, 2048 and 4096;
 //   64 heads, 4096 tokens 515, 125, 79, 71, 77; 512 heads, 2048 tokens (fp32, per key) 332, 332, 315,
 //   266, 264; 1024 heads, 1024 tokens 156, 156, 155, 164, 157.
@@ -1485,7 +1540,7 @@ hipError_t gdn_chunks(const lq_dims& d, const GdnPrefillArgs& args, void* worksp
         if constexpr (D == 16)
             e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan16_kernel, dim3((unsigned)(heads + 3) / 4), dim3(256), s, sc, (int)heads);
         else
-            e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan_kernel<D>, dim3((unsigned)heads, D / 16), dim3(4 * D), s, sc);
+            e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan_kernel<D, !KDA && sizeof(TI) == 2 ? D / 64 : 1>, dim3((unsigned)heads, D / 16), dim3(4 * D), s, sc);
         if (e != hipSuccess || !args.o) return e;
     }
     if (sa.keep) sa.first = x;
