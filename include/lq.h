@@ -538,7 +538,8 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  *   dst, src  host arrays of n_layers states (n_layers >= 1; d holds for all of them,
  *           except that src's have src_rows rows).  A layer's dst and src are the
  *           same arrays (in place: src_rows = d->B, at most 2048) or do not
- *           overlap; different layers' arrays do not overlap;
+ *           overlap; different layers' arrays do not overlap comp_idx and,
+ *           with a decay per head, buf_g need 4-byte alignment only;
  *   index   int32 [B] (device, 4-byte aligned): a row of src; LQ_ROW_CLEAR: an empty
  *           state (the codec of a zero state, no window); any other value, e.g.
  *           LQ_ROW_KEEP: the row is left as it was;

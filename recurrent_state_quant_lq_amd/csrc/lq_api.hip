@@ -40,8 +40,9 @@ int check_dims(const lq_dims* d) {
     return LQ_OK;
 }
 
-// Codec arrays (and, if with_buffer, the window buffer) present and aligned.
-int check_state(const lq_dims* d, const lq_state* st, bool with_buffer) {
+// Codec arrays (and, if with_buffer, the window buffer) present and aligned.  words: comp_idx and one log
+// decay a slot are read four bytes at a time.
+int check_state(const lq_dims* d, const lq_state* st, bool with_buffer, bool words = false) {
     if (!st) return LQ_ERR_NULL;
     const void* req[] = {st->sq, st->row_scale, st->col_scale};
     for (const void* p : req)
@@ -49,13 +50,14 @@ int check_state(const lq_dims* d, const lq_state* st, bool with_buffer) {
     if (d->C > 0 && (!st->comp_idx || !st->comp_val)) return LQ_ERR_NULL;
     for (const void* p : req)
         if (!aligned16(p)) return LQ_ERR_ALIGN;
-    if (d->C > 0 && (!aligned16(st->comp_idx) || !aligned16(st->comp_val))) return LQ_ERR_ALIGN;
+    if (d->C > 0 && (!(words ? aligned4(st->comp_idx) : aligned16(st->comp_idx)) || !aligned16(st->comp_val)))
+        return LQ_ERR_ALIGN;
     if (with_buffer) {
         const void* buf[] = {st->buf_k, st->buf_m, st->buf_g};
         for (const void* p : buf)
             if (!p) return LQ_ERR_NULL;
         for (const void* p : buf)
-            if (!aligned16(p)) return LQ_ERR_ALIGN;
+            if (p == st->buf_g && words && d->decay_mode == LQ_DECAY_SCALAR ? !aligned4(p) : !aligned16(p)) return LQ_ERR_ALIGN;
     }
     return LQ_OK;
 }
@@ -487,8 +489,8 @@ int lq_state_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, con
     if ((rc = check_indices({index}))) return rc;
     if (!aligned4(pos) || !aligned4(pos_out)) return LQ_ERR_ALIGN;
     for (int32_t l = 0; l < n_layers; ++l) {
-        if ((rc = check_state(d, dst + l, pos != nullptr))) return rc;
-        if ((rc = check_state(d, src + l, pos != nullptr))) return rc;
+        if ((rc = check_state(d, dst + l, pos != nullptr, true))) return rc;
+        if ((rc = check_state(d, src + l, pos != nullptr, true))) return rc;
     }
     if ((rc = check_gather(d, n_layers, dst, src, src_rows, index, pos, pos_out))) return rc;
     return finish(lq::launch_gather(*d, n_layers, dst, src, src_rows, index, pos, pos_out, (hipStream_t)stream));

@@ -110,6 +110,24 @@ def test_layers_at_once(layers):
     assert po.tolist() == [2, 0, 0, 0, 9, 4]
 
 
+@pytest.mark.parametrize("per_key", [False, True])
+def test_layers_of_one_allocation(per_key):
+    """Arrays of all layers in one tensor: a layer's compensator indices and log decays start at any word."""
+    layers, B, S, H, d, W, C = 3, 5, 3, 1, 16, 3, 1
+    parts = [[state(9 * i + l, n, H, d, W, C, per_key) for l in range(layers)] for i, n in ((0, B), (1, S))]
+    sts = []
+    for states in parts:
+        whole = {f: torch.stack([getattr(x, f) for x in states]) for f in FIELDS}
+        sts.append([lq.LayerState(x.dims, *[whole[f][l] for f in FIELDS]) for l, x in enumerate(states)])
+    assert any(x.comp_idx.data_ptr() % 16 for x in sts[0]) and (per_key or any(x.buf_g.data_ptr() % 16 for x in sts[0]))
+    index, pos = [2, lq.LQ_ROW_CLEAR, 0, lq.LQ_ROW_KEEP, 2], [3, 1, 2]
+    dev = lambda x: torch.tensor(x, dtype=torch.int32).cuda()
+    want = [expect(host(x), host(y), index, pos, C) for x, y in zip(*sts)]
+    lq.lq_state_gather(*sts, dev(index), dev(pos))
+    for x, w in zip(sts[0], want):
+        same(x, w)
+
+
 def test_rows_of_views():
     """Two halves of one batch as states of their own."""
     st = state(5, 8, 3, 64, 8, 4, False)

@@ -120,7 +120,9 @@ def test_gather_argument_errors():
     assert call(pos=B2) == lq.LQ_ERR_ALIGN and call(pos_out=B2) == lq.LQ_ERR_ALIGN
     for f in NAMES:
         assert call(dst=[_state(1, **{f: None})]) == lq.LQ_ERR_NULL, f
-        assert call(src=[_state(2, **{f: 0x20000004})]) == lq.LQ_ERR_ALIGN, f
+        at = 0x20000002 if f in ("comp_idx", "buf_g") else 0x20000004   # (those two are read in words of four bytes)
+        assert call(src=[_state(2, **{f: at})]) == lq.LQ_ERR_ALIGN, f
+    assert call(_dims(decay_mode=lq.LQ_DECAY_PER_KEY), src=[_state(2, buf_g=0x20000004)]) == lq.LQ_ERR_ALIGN
     # without positions only the codecs count
     assert call(dst=[_state(1, row_scale=None)], pos=None) == lq.LQ_ERR_NULL
     # overlaps: a shifted state, another number of rows in place, one array shared, two layers on one state
