@@ -45,9 +45,9 @@
  *   - Return value: LQ_OK or an LQ_ERR_* code.  Argument checks run first and
  *     make no HIP call; on any error nothing is enqueued.  LQ_ERR_HIP means a
  *     launch failed; lq_last_hip_error() gives the hipError_t.
- *   - Non-finite inputs are not checked; they propagate.  (lq_la_* and tree
- *     calls: an infinity may arrive as NaN, where its operand enters a product
- *     in parts.)
+ *   - Non-finite inputs are not checked; they propagate.  (lq_la_*, tree
+ *     calls and lq_gdn_prefill_ragged: an infinity may arrive as NaN, where its
+ *     operand enters a product in parts.)
  *   - Supported: dk = dv in {16, 64, 128}; 1 <= W <= 32; 0 <= C <= 8.  The
  *     plain calls take one window position for the whole batch (lockstep);
  *     the *_ragged calls take one per batch row from a device array.
@@ -59,7 +59,8 @@
  *     calls on disjoint row ranges may run at the same time on different
  *     streams.  Each (row, head) is computed the same way whatever the batch
  *     of its call, so the results do not depend on the split, except for the
- *     order of sums in lq_la_prefill's longer prompts of few heads (see there).
+ *     order of sums in lq_la_prefill's and lq_gdn_prefill_ragged's longer prompts
+ *     of few heads (see there).
  */
 #ifndef LQ_H
 #define LQ_H
@@ -302,7 +303,9 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
 /*
  * The gated delta rule over a padded batch of prompts: outputs of up to T tokens
  * a row and the states after them, from any starting states.  The recurrence of
- * lq_gdn_decode_step, in chunks (T <= 4: token after token), accumulated in fp32.
+ * lq_gdn_decode_step, in chunks (T <= 4: token after token), accumulated in fp32
+ * from operands that keep fp32's 24 bits (with fp32 tokens or a decay per key
+ * channel, d >= 64, a product of two of them is off by at most 2^-21 of itself).
  *   h0     nullable fp32 [B,H,dk,dv]: the state before the prompt (NULL: zeros);
  *   h      fp32 [B,H,dk,dv], out: the state after it; h == h0 is allowed,
  *          any other overlap is not;
@@ -319,7 +322,13 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  * T = 0 (or a row with no tokens) copies h0 to h.  A token that is not finite
  * reaches its own and later tokens only (a v its own column only).  The result of
  * a row does not depend on earlier calls, on the workspace's content or on what
- * other rows hold.
+ * other rows hold.  The order of its sums depends on B*H and T: where the heads of
+ * a batch leave most of the GPU idle, a prompt is cut into segments whose number
+ * follows from both, and such a prompt in a batch of another size, or padded to
+ * another T, agrees to rounding, not bit for bit.  Every call with T > 4 (and at
+ * most 2^17 heads at d = 128, 2^18 at d = 64) that needs no workspace
+ * (lq_gdn_workspace_bytes = 0) computes a row in the same order, so that there its
+ * bits are the same whatever B and T.
  * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30;
  * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
