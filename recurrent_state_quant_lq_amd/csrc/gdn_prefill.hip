@@ -839,7 +839,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
     auto store = [&](int cur, int L) {
         const uint32_t tt = fresh(t), pair = tt % PR, quad = tt / PR, n0 = 4 * quad;
         const int c = 2 * pair, u = (c & 31) >> 2;                 // operand order of the channel's 32-block
-        const int at = pm<GF>(n0, (c >> 5) * 4 + (u & 3)) + 4 * (u >> 2) + (c & 3);
+        const int at = pm<GF>(n0, (c >> 5) * 4 + (u & 3)) + 4 * ((u >> 2) ^ (u & 1)) + (c & 3);   // (odd pieces: halves swapped)
         int first = GF;
         [[maybe_unused]] f32x2 f[4];
         if constexpr (KDA) {
@@ -1008,7 +1008,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
             uint32_t p[3][4];
             u32x4 b[3];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = H[2 * ks + e / 4][e % 4];
+            for (int e = 0; e < 8; ++e) x[e] = lg & 1 ? H[2 * ks + (e < 4)][e % 4] : H[2 * ks + e / 4][e % 4];
             split3<8>(x, p);
 #pragma unroll
             for (int m = 0; m < 3; ++m) b[m] = u32x4{p[m][0], p[m][1], p[m][2], p[m][3]};
@@ -1107,7 +1107,8 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
         load(ce, te);                                              // (none left: zeros)
         __builtin_amdgcn_sched_barrier(0);
         // ---- H = e^{g_L} H + K^T (w o M); per key: f_L o (H + Y^T M) ----
-        const int kt = pm<GF>(4 * lg + (li >> 2), li & 3);         // transposed reads: 4 tokens of 16 channels a lane group
+        // transposed reads: 4 tokens of 16 channels a lane group, one half of each piece
+        const int kt = pm<GF>(4 * lg + (li >> 2), li & 3), kh[2] = {kt + 4 * (li & 1), kt + 4 * (~li & 1)};
         if constexpr (!KDA) {
             const v4f w0 = *reinterpret_cast<const v4f*>(&G.w[4 * lg]), w1 = *reinterpret_cast<const v4f*>(&G.w[16 + 4 * lg]);
             float x[8];
@@ -1125,7 +1126,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
             u32x4 y[3];
 #pragma unroll
             for (int m = 0; m < 3; ++m) {
-                const uint16_t* from = &sC[m][kt + pm<GF>(0, 4 * (rt >> 1)) + 4 * (rt & 1)];
+                const uint16_t* from = &sC[m][kh[rt & 1] + pm<GF>(0, 4 * (rt >> 1))];
                 const u32x2 k0 = lds_tr(from), k1 = lds_tr(from + pm<GF>(16, 0));
                 y[m] = u32x4{k0[0], k0[1], k1[0], k1[1]};
             }
