@@ -33,7 +33,9 @@ struct GdnPrefillArgs {
 // Per token p = (D H)^T k, z = (D H)^T q, u = beta (v - p), H <- D H + k u^T,
 // o = z + (k . q) u: one pass over the state for both sums and one for the update.  Lane t
 // holds the columns 4 (t % (D/4)) .. +3 of the rows t / (D/4) + RPP p; tokens come through
-// LDS, kGdnStepTokens at a time, requested with the state.
+// LDS, kGdnStepTokens at a time, requested with the state.  Bound by memory: one token of 2048 heads
+// (d = 128, bf16) 50 us, 5.4 TB/s of the states read and written.  Up to four tokens take it: its token costs
+// one pass over registers, a chunk's products the same whatever it holds.
 template <int D, bool KDA, typename TI>
 __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
     constexpr int CP = D / 4, NT = D >= 64 ? 256 : 64, RPP = NT / CP, NP = D / RPP, NW = NT / 64, ST = kGdnStepTokens;
@@ -154,6 +156,13 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
 // forms for all columns (block_solve against the identity), on the fp32 instruction.
 // A product of a masked zero with a value that is not finite would spread it to earlier tokens: a
 // chunk ends before such a token, which is then the first of its chunk.
+// Bound by the two issue ports of a SIMD in turn: 2048 heads of 512 tokens (d = 128) 515 us, vector 0.56 and
+// matrix 0.53 of the waves' time (two waves a SIMD; 0.96 PFLOP/s of matrix work, a large product of the library
+// 1.22, both with the clock that the power leaves); LDS 0.42.  Four waves of 32 columns, since each wave reads
+// all of K and Q: eight of 16 took 588 us.  Not kept: the parts of H formed in between the products by
+// the scheduler's groups (577), the inverses' steps in between K H (544 to 615), the halves of every second
+// piece swapped as in the kernel of 32 tokens (the same at d = 128; 164, not 141, for 512 heads of 1024 tokens
+// at d = 64).
 constexpr int GL = 64;        // tokens per chunk
 
 struct GdnSegArgs {
@@ -705,6 +714,14 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
 // at most one product and one reciprocal more.  1 / f grows: a chunk ends before a token whose f
 // leaves [kMinDecay, 1 / kMinDecay] in a channel (the parts are in range there), which is then the
 // first of the next chunk, and whose own decay goes to H as it is.
+// Every second piece of an operand row has its halves swapped, in LDS and in H's order on its way to the
+// products: the transposed reads, half a piece each, then use all banks (1024 heads of 512 tokens, per key,
+// 458, not 474 us).
+// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 458 us (bf16): two workgroups
+// a CU, vector 0.58, matrix 0.43 of the waves' time; of a chunk's time a quarter is the forming of the rows'
+// parts.  fp32, 192 heads of up to 1021 tokens 213 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
+// (vector 0.42, matrix 0.38); 512 heads of 512 tokens 220 us (0.62, 0.57).  Six bf16 products
+// take 96 cycles where the fp32 instruction takes 256.
 constexpr int GF = 32;        // tokens per chunk
 constexpr float kMinDecay = 0x1p-92f;
 
@@ -1163,6 +1180,8 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
 // layout that the instruction takes (lane (lg, li), step v: row or column li, index 4 lg + v).  The
 // scores are formed transposed, so that their accumulators are the A operand of P M as they are;
 // only A goes through LDS, for block_solve.  Per key: the same factors as the larger kernel's.
+// Bound by a wave's chain of dependent products, two waves a SIMD (vector 0.53, matrix 0.25): 2048 heads of
+// 512 tokens 107 us, per key 106.
 // The value of the lane that far before in the row of 16, 1 where there is none.
 template <int CTRL>
 __device__ __forceinline__ float dpp_one(float x) {
@@ -1371,7 +1390,8 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
 // G of all segments, the scan joins them (X_{s+1} = G_s X_s + E_s, in E's place), and the last one
 // computes every segment's outputs from the state before it.  A workgroup of the scan owns 16
 // columns of a head's state, wave w its rows 16 w ..; both factors in three bf16 parts: G's rows are
-// split from registers, loaded four steps ahead, X's columns go through LDS.
+// split from registers, loaded four steps ahead, X's columns go through LDS.  A step is a chain (barrier, LDS,
+// twelve products) of 1.5 us whatever the heads: 16 heads at d = 128, 8 segments 12 us, 16 segments 24.
 struct GdnScanArgs {
     float* x;                 // [segments][heads][d*d]: E_s at s + 1, then the states before the segments
     const float* map;         // G_s at s
