@@ -329,7 +329,7 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  * most 2^17 heads at d = 128, 2^18 at d = 64) that needs no workspace
  * (lq_gdn_workspace_bytes = 0) computes a row in the same order, so that there its
  * bits are the same whatever B and T.
- * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30;
+ * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30 or B*H > 2^23;
  * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
 int lq_gdn_prefill_ragged(const lq_dims *d, const lq_state *st, const float *h0, float *h, int32_t T,
@@ -527,7 +527,7 @@ int lq_tree_commit(const lq_dims *d, const lq_state *st, const int32_t *pos, int
  * 16); outputs may not overlap inputs.  workspace: at least
  * lq_verify_workspace_bytes(d, N, V) bytes, as lq_gdn_prefill_ragged's.
  * Errors: LQ_ERR_DIMS if N, P or V < 1, P > N or replace is not 0 or 1;
- * LQ_ERR_UNSUPPORTED if N > 64, V > 2^30 or B V > 2^40; LQ_ERR_NULL, LQ_ERR_ALIGN,
+ * LQ_ERR_UNSUPPORTED if N > 64, V > 2^30, B > 2^21 or B V > 2^36; LQ_ERR_NULL, LQ_ERR_ALIGN,
  * LQ_ERR_WORKSPACE.
  */
 int lq_tree_verify(const lq_dims *d, const int32_t *pos, int32_t N, const int32_t *parent,

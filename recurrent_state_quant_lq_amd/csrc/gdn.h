@@ -13,9 +13,12 @@ hipError_t launch_gdn_prefill(const lq_dims& d, const float* h0, float* h, int T
                               void* workspace, hipStream_t s);
 size_t gdn_workspace_bytes(const lq_dims& d, int T);
 constexpr int kGdnMaxTokens = 1 << 30;  // token counts and their rounding up to chunks stay in 32 bits
+constexpr int kGdnMaxHeads = 1 << 23;   // a launch counts its threads in 32 bits
 constexpr int kGdnStepTokens = 4;       // prompts of up to this many tokens run as the recurrence
 
 // Drafted trees against the target's probabilities.
+constexpr int kVerifyRows = 1 << 21;    // a launch counts its threads in 32 bits
+constexpr int64_t kVerifyValues = (int64_t)1 << 36;
 struct VerifyArgs {
     const int32_t* pos;
     const int32_t* parent;    // [B,N]

@@ -111,7 +111,7 @@ int check_verify(const lq_dims* d, int32_t N, int32_t V) {
     int rc = check_dims(d);
     if (rc) return rc;
     if (N < 1 || V < 1) return LQ_ERR_DIMS;
-    if (N > lq::kTreeMax || V > (1 << 30) || (int64_t)d->B * V > (int64_t)1 << 40) return LQ_ERR_UNSUPPORTED;
+    if (N > lq::kTreeMax || V > (1 << 30) || d->B > lq::kVerifyRows || (int64_t)d->B * V > lq::kVerifyValues) return LQ_ERR_UNSUPPORTED;
     return LQ_OK;
 }
 
@@ -447,7 +447,7 @@ int lq_gdn_prefill_ragged(const lq_dims* d, const lq_state* st, const float* h0,
     if (h0 && !aligned16(h0)) return LQ_ERR_ALIGN;
     if (lens && !aligned4(lens)) return LQ_ERR_ALIGN;
     if (T < 0) return LQ_ERR_POS;
-    if (T > lq::kGdnMaxTokens) return LQ_ERR_UNSUPPORTED;
+    if (T > lq::kGdnMaxTokens || (int64_t)d->B * d->H > lq::kGdnMaxHeads) return LQ_ERR_UNSUPPORTED;
     if (T > 0 && (rc = check_tokens(d, q, k, v, alpha, beta, o, false))) return rc;
     if ((rc = check_workspace(lq_gdn_workspace_bytes(d, T), workspace, workspace_bytes))) return rc;
     const hipStream_t s = (hipStream_t)stream;

@@ -43,6 +43,7 @@ def test_prompt_argument_errors():
     assert call(_dims(dk=96, dv=96)) == lq.LQ_ERR_UNSUPPORTED
     assert call(T=-1) == lq.LQ_ERR_POS
     assert call(T=(1 << 30) + 1) == lq.LQ_ERR_UNSUPPORTED
+    assert call(_dims(B=1 << 12, H=(1 << 11) + 1, dk=16, dv=16)) == lq.LQ_ERR_UNSUPPORTED
     assert call(h=None) == lq.LQ_ERR_NULL and call(h=B4) == lq.LQ_ERR_ALIGN
     assert call(h0=B4) == lq.LQ_ERR_ALIGN and call(lens=B2) == lq.LQ_ERR_ALIGN
     for name in ("q", "k", "v", "al", "be"):
@@ -89,7 +90,8 @@ def test_verify_argument_errors():
     assert call(_dims(B=0)) == lq.LQ_ERR_DIMS
     for kw in (dict(N=0), dict(N=-1), dict(P=0), dict(P=9), dict(V=0), dict(V=-5), dict(rep=2), dict(rep=-1)):
         assert call(**kw) == lq.LQ_ERR_DIMS, kw
-    for kw in (dict(N=65), dict(V=(1 << 30) + 1), dict(d=_dims(B=1 << 20), V=(1 << 20) + 1)):
+    for kw in (dict(N=65), dict(V=(1 << 30) + 1), dict(d=_dims(B=1 << 20), V=(1 << 16) + 1),
+               dict(d=_dims(B=(1 << 21) + 1))):
         assert call(**kw) == lq.LQ_ERR_UNSUPPORTED, kw
     for name in ("pos", "parent", "token", "t", "u", "path", "n_path", "nxt"):
         assert call(**{name: None}) == lq.LQ_ERR_NULL, name
