@@ -717,10 +717,10 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
 // Every second piece of an operand row has its halves swapped, in LDS and in H's order on its way to the
 // products: the transposed reads, half a piece each, then use all banks (1024 heads of 512 tokens, per key,
 // 458, not 474 us).
-// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 458 us (bf16): two workgroups
-// a CU, vector 0.58, matrix 0.43 of the waves' time; of a chunk's time a quarter is the forming of the rows'
-// parts.  fp32, 192 heads of up to 1021 tokens 213 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
-// (vector 0.42, matrix 0.38); 512 heads of 512 tokens 220 us (0.62, 0.57).  Six bf16 products
+// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 455 us (bf16): two workgroups
+// a CU, vector 0.66, matrix 0.47, LDS 0.55 of the time; a quarter of a chunk's is the forming of the rows'
+// parts.  fp32, 192 heads of up to 1021 tokens 211 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
+// (0.45, 0.39, 0.39); 512 heads of 512 tokens 216 us (0.67, 0.59, 0.58).  Six bf16 products
 // take 96 cycles where the fp32 instruction takes 256.
 constexpr int GF = 32;        // tokens per chunk
 constexpr float kMinDecay = 0x1p-92f;
