@@ -7,7 +7,9 @@
 // slab of columns for every row, and per step loads the pieces of all the moved rows into
 // registers, passes a barrier, and only then stores.  The step's width follows from the number
 // of moved rows, which only the device knows: as many columns as the registers take.  Bound by memory:
-// 56 of 64 rows of two layers (32 heads, d = 128) 26 us (4.3 TB/s), a third of 256 rows 29 us (4.1).
+// 56 of 64 rows of two layers (32 heads, d = 128) 26 us (4.4 TB/s), a third of 256 rows 26 us (4.5), from and to
+// states that no cache holds.  Stores pass by the caches (kept there they push out what other workgroups are about to
+// read: 39 and 34 us); loads do not (many rows may read one: 38 and 30 us).
 #include "gdn.h"
 
 namespace lq {
@@ -71,7 +73,7 @@ __device__ __forceinline__ void move_rows(const GatherArgs& a, int layer, int f,
         __syncthreads();                                   // every row's columns are read
 #pragma unroll
         for (int u = 0; u < GP; ++u)
-            if ((on >> u) & 1u) dst[(size_t)list[row0 + rows * u].x * units + at] = x[u];
+            if ((on >> u) & 1u) __builtin_nontemporal_store(x[u], &dst[(size_t)list[row0 + rows * u].x * units + at]);
     }
 }
 
@@ -121,8 +123,8 @@ hipError_t launch_gather(const lq_dims& d, int n_layers, const lq_state* dst, co
                                      H * W * dk / 4, H * W * dk / 4, per_key ? H * W * dk / 4 : H * W};
     // slabs: runs of 256 bytes to 4 KB of a row, as long as there are kSlabs of them.  Few rows that move cost a
     // slab's latencies, many its steps.  Measured for 1024, 2048, 4096 and 8192 slabs: 24 layers, 64 rows of 16
-    // heads, 4 moved 19, 19, 22, 28 us; one layer, 256 rows of 32 heads, a third moved 34, 31, 29, 29; two
-    // layers, 64 rows, 56 moved 27, 28, 26, 31 (slabs of 4 KB: 63, 114, 91 us).
+    // heads, 4 moved 20, 16, 17, 23 us; one layer, 256 rows of 32 heads, a third moved 29, 26, 26, 26; two
+    // layers, 64 rows, 56 moved 29, 28, 26, 28.
     uint64_t all = 0;
     for (int f = 0; f < kFields; ++f) all += f >= F_K && !pos ? 0 : units[f];
     a.shift = 8;
