@@ -19,15 +19,16 @@
 // A row of p (and q) is read where a sum is needed: after a rejection (S of the next test, or
 // the total of the draw) and for the draw.  verify_sum_kernel walks every row to its first sum and
 // forms it, a tile of the row per wave (the walk is a few comparisons, so every wave repeats it).
-// verify_pick_kernel, one workgroup a row, forms what sums are left, finds the tile and the token.
+// verify_pick_kernel, one workgroup a row, forms what sums are left, finds the tile and the token; with many
+// or small rows it does all of it (kAloneRows).
 // Bound by the sum's reads and by the latencies before them (positions and nodes, the nodes'
 // values, the row): 64 rows of 131072 values with a draft 11 us and 7 for the pick (the rows partly in the
-// Infinity Cache), 256 rows of 50021 without 14 and 7, one row of 32000 5.4 and 6.6.  Nodes with several
-// children need a sum for each rejection, one after the other: trees of 32 nodes, 64 rows, 9 and 32 us (drafted
-// without replacement), 11 and 61 (with).  One and two further launches of the sum kernel before the pick took
-// 66 and 75 us, not 61, there (102 and 105, not 95), and the pick's sums with 256 threads 127, not 105.
-// A quad of a row is loaded without a bounds test where its whole tile is inside (24 us, not 9, with one per
-// quad).
+// Infinity Cache), one row of 32000 5.4 and 6.6; alone, 256 rows of 50021 without a draft 18 (two
+// launches: 14 and 7).  Nodes with several children need a sum for each rejection, one after the other, each at
+// the 64 bytes a cycle that a CU takes: trees of 32 nodes, 64 rows, 9 and 32 us (drafted without replacement),
+// 11 and 60 (with).  One and two further launches of the sum kernel before the pick took 66 and 75 us, not 61,
+// there (102 and 105, not 95), and the pick's sums with 256 threads 127, not 105.  A quad of a row is loaded
+// without a bounds test where its whole tile is inside (24 us, not 9, with one per quad).
 #include "gdn.h"
 
 #pragma clang fp contract(off)
@@ -40,6 +41,14 @@ constexpr int PT = 1024;                 // of a pick's: its own sums need as ma
 constexpr int VQ = 8;                    // quads of values per lane and tile
 constexpr int TV = 64 * VQ * 4;          // values per tile: one wave's
 
+// verify_pick_kernel alone: one launch less, a row's first sum by one workgroup.  It pays with a workgroup for every
+// CU, and with rows so small that a workgroup's reads take no longer than a launch.  Calls with two launches and
+// with one, us, 8 nodes with a draft / 5 without: 1 row of 4000 values 13.2, 11.6 / 13.1, 11.4; of 16000 13.5,
+// 12.2 / 12.8, 11.1; of 32000 13.1, 13.4 / 13.7, 11.8; of 65536 14.4, 14.5 / 14.1, 12.4; of 131072 14.5, 20.0 /
+// 14.2, 16.6; 64 rows of 32000 16.5, 16.7 / 15.6, 14.6; of 65536 16.9, 18.8 / 15.8, 14.5; of 131072 21.3, 23.3 /
+// 17.7, 19.1; 256 rows of 32000 23.0, 19.9 / 19.9, 18.3; of 65536 31.1, 26.3 / 25.2, 20.1; of 131072 51.8,
+// 49.2 / 34.4, 29.1.
+constexpr int kAloneRows = 256, kAloneValues = 1 << 16;     // values of a row; with a draft a quarter
 int verify_tiles(int V) { return (V + TV - 1) / TV; }
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -273,20 +282,39 @@ __global__ __launch_bounds__(VT) void verify_sum_kernel(VerifyArgs a) {
     if (lane == 0) a.sums[(size_t)b * tiles + tile] = y;
 }
 
+// ALONE: without verify_sum_kernel before it.
+template <bool ALONE>
 __global__ __launch_bounds__(PT) void verify_pick_kernel(VerifyArgs a) {
     const int b = blockIdx.x, t = threadIdx.x, lane = t & 63;
     const int w = __builtin_amdgcn_readfirstlane(t >> 6);
     const int tiles = (a.V + TV - 1) / TV;
     const Saved* from = saved(a, tiles, b);
-    int state = from->state;
-    if (state == W_SKIP) return;
+    int state = ALONE ? W_SKIP : from->state;
+    if (!ALONE && state == W_SKIP) return;
+    Walk x = start_walk();
+    Nodes s;
+    if (ALONE) {
+        s = load_nodes(a, b, lane);
+        if (!s.live) return;
+        state = state_of(walk_on(s, x), s, x);
+        if (w == 0 && state != W_TEST) write_path(a, x, b, lane);
+    }
     if (state == W_NONE) {
         if (t == 0) a.next[b] = -1;
         return;
     }
-    Walk x = from->x;
     double* sums = a.sums + (size_t)b * tiles;
-    Nodes s = load_nodes(a, b, lane);
+    if (ALONE) {
+        const Residual r = residual(a, s, x, b);
+        for (int i = w; i < tiles; i += PT / 64) {
+            const double y = tile_sum(r, s, a.V, i);
+            if (lane == 0) sums[i] = y;
+        }
+        __syncthreads();
+    } else {
+        x = from->x;
+        s = load_nodes(a, b, lane);
+    }
     double total = row_sum(sums, tiles, lane);
     const bool later = state == W_TEST;
     // further sums: this workgroup alone.  A draw from nothing is one from the target as it is.
@@ -381,10 +409,12 @@ size_t verify_workspace_bytes(int B, int N, int V) {
 }
 
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s) {
+    if (a.B >= kAloneRows || (int64_t)a.V * (a.draft ? 4 : 1) <= kAloneValues)
+        return launch_kernel(LQ_KERNEL_VERIFY, verify_pick_kernel<true>, dim3(a.B), dim3(PT), s, a);
     const int groups = (verify_tiles(a.V) + VT / 64 - 1) / (VT / 64);
     const hipError_t e = launch_kernel(LQ_KERNEL_VERIFY, verify_sum_kernel, dim3((unsigned)groups * (unsigned)a.B), dim3(VT), s, a);
     if (e != hipSuccess) return e;
-    return launch_kernel(LQ_KERNEL_VERIFY, verify_pick_kernel, dim3(a.B), dim3(PT), s, a);
+    return launch_kernel(LQ_KERNEL_VERIFY, verify_pick_kernel<false>, dim3(a.B), dim3(PT), s, a);
 }
 
 }  // namespace lq

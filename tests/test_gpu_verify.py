@@ -107,12 +107,15 @@ def test_many_siblings_that_are_rejected(mode, cut):
     """A draft far from the target: most children are rejected, several sums a row."""
     check(case(3, 24, 40, 5003, W=32, mode=mode, bushy=3.0, noise=4.0, cut=cut))
     check(case(4, 24, 16, 60, W=32, mode=mode, bushy=9.0, noise=4.0, cut=cut))
+    check(case(5, 9, 16, 70001, W=32, mode=mode, bushy=4.0, noise=4.0, cut=cut))     # (first sums by a launch of their own)
 
 
 @pytest.mark.parametrize("mode", ["with", "none"])
 def test_a_large_vocabulary_and_many_rows(mode):
     check(case(6, 2, 4, 300007, mode=mode))
     check(case(7, 400, 3, 50, mode=mode, W=4))
+    check(case(8, 256, 2, 70001, mode=mode, W=4))
+    check(case(8, 5, 12, 70001, mode=mode, root=False))
 
 
 def test_the_path_is_cut_at_P_and_at_the_window():
@@ -130,7 +133,7 @@ def test_positions_outside_the_window_leave_a_row():
     check(c)
 
 
-@pytest.mark.parametrize("V", [5, 5000])
+@pytest.mark.parametrize("V", [5, 5000, 70001])
 def test_rows_with_nothing_left(V):
     """A target whose mask leaves nothing, one of a single token, NaN, a draft equal to the target,
     a draft that covers the target, numbers at the ends of [0, 1)."""
@@ -171,9 +174,10 @@ def test_without_replacement_the_draft_runs_out():
     check(c)
 
 
+@pytest.mark.parametrize("V", [9001, 70001])
 @pytest.mark.parametrize("mode", ["without", "none"])
-def test_streams_graphs_and_workspaces(mode):
-    c = case(13, 9, 20, 9001, mode=mode, noise=2.0, bushy=2.0)
+def test_streams_graphs_and_workspaces(mode, V):
+    c = case(13, 9, 20, V, mode=mode, noise=2.0, bushy=2.0)
     N, B, V = c["target"].shape
     d = lq.make_dims(B, 1, 16, 16, 16, 0)
     want = run(c)
@@ -194,7 +198,7 @@ def test_streams_graphs_and_workspaces(mode):
     with torch.cuda.graph(graph):
         lq.lq_tree_verify(d, *args, *outs[0], workspace=ws[0], **kw)
     for r in range(3):                                     # other numbers every replay
-        other = case(20 + r, 9, 20, 9001, mode=mode, noise=2.0, bushy=2.0)
+        other = case(20 + r, 9, 20, V, mode=mode, noise=2.0, bushy=2.0)
         for x, y in zip(args, ("pos", "parent", "token", "target", "u")):
             x.copy_(other[y] if torch.is_tensor(other[y]) else torch.tensor(other[y], dtype=torch.int32))
         kw["target0"].copy_(other["target0"])
