@@ -717,7 +717,9 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
 // Every second piece of an operand row has its halves swapped, in LDS and in H's order on its way to the
 // products: the transposed reads, half a piece each, then use all banks (1024 heads of 512 tokens, per key,
 // 458, not 474 us).
-// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 455 us (bf16): two workgroups
+// bf16 values are loaded by lanes in pairs, two columns of every second row each (512 heads of 1024 tokens at
+// d = 64, per key, 206, not 214 us, with a load a value).
+// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 445 us (bf16): two workgroups
 // a CU, vector 0.66, matrix 0.47, LDS 0.55 of the time; a quarter of a chunk's is the forming of the rows'
 // parts.  fp32, 192 heads of up to 1021 tokens 211 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
 // (0.45, 0.39, 0.39); 512 heads of 512 tokens 216 us (0.67, 0.59, 0.58).  Six bf16 products
@@ -803,7 +805,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
     const uint32_t rb = (uint32_t)heads * (ES * D);                // bytes between tokens (heads <= chunk_heads(D))
     typename Two<TI>::T kd[4], qd[4];
     f32x2 ad[KDA ? 4 : 1];
-    float vd[8];
+    uint32_t vd[ES == 4 ? 8 : 4];                                  // bf16: lanes in pairs, two columns of every second row
     auto rows = [&](const void* x, int c0, int end, uint32_t es) { // tokens c0 .. min(c0 + GF, end) - 1 of this head
         return make_rows(static_cast<const char*>(x) + ((size_t)c0 * heads + head) * (es * D),
                          end > c0 ? (uint32_t)(min(end - c0, GF) - 1) * (uint32_t)heads * (es * D) + es * D : 0);
@@ -827,15 +829,29 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
 #pragma unroll
             for (int e = 0; e < 4; ++e) ad[e] = __builtin_bit_cast(f32x2, row_ld2(ra, (n0 + e) * rba + 8 * pair));
         }
-        const uint32_t ln = tt & 63, voff = 4 * (ln >> 4) * rb + ES * (16 * w + (ln & 15));
+        const uint32_t ln = tt & 63;
+        const uint32_t voff = ES == 4 ? 4 * (ln >> 4) * rb + 4 * (16 * w + (ln & 15))
+                                      : (4 * (ln >> 4) + (ln & 1)) * rb + 2 * (16 * w + (ln & 14));
+        constexpr int VR = ES == 4 ? 4 : 2;                        // loads per block of 16 tokens
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                if (map) vd[4 * r + v] = 0.0f;
-                else if constexpr (ES == 4) vd[4 * r + v] = __uint_as_float(row_ld(rv, voff + (16 * r + v) * rb));
-                else vd[4 * r + v] = bf16_to_f32(__builtin_bit_cast(uint16_t, __builtin_amdgcn_raw_buffer_load_b16(rv, voff + (16 * r + v) * rb, 0, 0)));
+            for (int v = 0; v < VR; ++v) vd[VR * r + v] = map ? 0u : row_ld(rv, voff + (16 * r + 4 / VR * v) * rb);
+    };
+    auto values = [&](int r, float (&x)[4]) {                      // as accumulators hold them: tokens 16 r + 4 lg + v
+        if constexpr (ES == 4) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[v] = __uint_as_float(vd[4 * r + v]);
+        } else {
+            const bool up = lane & 1;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float l = lo_f32(vd[2 * r + j]), h = hi_f32(vd[2 * r + j]);
+                const float other = dpp<DPP_XOR1>(up ? l : h);
+                x[2 * j] = up ? other : l;
+                x[2 * j + 1] = up ? h : other;
             }
+        }
     };
     float al = 1.0f, be = 0.0f;                                    // gates of the next chunk: the last wave's
     auto load_gates = [&](int c0) {
@@ -909,13 +925,23 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
                 if constexpr (KDA) *reinterpret_cast<uint32_t*>(&sY[m][at + 8 * e]) = p[m][2];
             }
         }
+        if constexpr (ES == 4) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-                const int n = 16 * r + 4 * ((int)(tt & 63) >> 4) + v;
-                if (n > 0 && !finite_f32(vd[4 * r + v])) first = min(first, n);
-            }
+                for (int v = 0; v < 4; ++v) {
+                    const int n = 16 * r + 4 * ((int)(tt & 63) >> 4) + v;
+                    if (n > 0 && !finite_f32(__uint_as_float(vd[4 * r + v]))) first = min(first, n);
+                }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int n = 16 * r + 4 * ((int)(tt & 63) >> 4) + 2 * j + (int)(tt & 1);
+                    if (n > 0 && odd_bf16(vd[2 * r + j])) first = min(first, n);
+                }
+        }
         if (first < GF) atomicMin(&s_cut[cur], first);
     };
     __syncthreads();                                               // the first gates (and s_cut) are written
@@ -1051,8 +1077,10 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
                 R[r] *= e;
                 O[r] *= e;
             }
+            float x[4];
+            values(r, x);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) R[r][v] = bt[v] * (vd[4 * r + v] - R[r][v]);
+            for (int v = 0; v < 4; ++v) R[r][v] = bt[v] * (x[v] - R[r][v]);
         }
         if (w == NW - 1) {
             if constexpr (KDA) load_gates(ce);
@@ -1499,7 +1527,7 @@ constexpr size_t chunk_heads(int d) { return d == 16 ? (size_t)INT32_MAX : (size
 // maps) and the scan, so they pay where the heads alone leave most CUs idle: up to `heads` heads,
 // enough segments for `want` workgroups (d = 16: waves).  Measured, bf16, replayed in a graph:
 //   d = 128: 16 heads, 16384 tokens 2429 us whole, 534, 340, 378 and 328-337 for 128, 256, 384 and 512
-//   workgroups (fp32: 3235; 741, 486, 559, 501; per key 4232; 1052, 591, 703, 585); 2048 tokens: 32 heads
+//   workgroups (fp32: 3235; 741, 486, 559, 501; per key 4232; 1052, 544, 703, 585); 2048 tokens: 32 heads
 //   302; 142, 103, 115, 110; 64 heads 310; 266, 175, 201, 183; 128 heads 312 whole, 272 for 256, 296
 //   for 512; 64 heads, 512 tokens 79; 72, 62, 61, 79; 300 tokens 51; 55, 49, 52, 52; 128 heads, 130
 //   tokens 34, 41 for 256;

@@ -100,7 +100,8 @@ def load() -> ct.CDLL:
         L.lq_verify_workspace_bytes.argtypes = [D, I, I]
         L.lq_verify_workspace_bytes.restype = ct.c_size_t
         L.lq_state_gather.argtypes = [D, I, S, S, I, P, P, P, P]
-        for f in ("lq_gdn_prefill_ragged", "lq_tree_verify", "lq_state_gather", "lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
+        for f in ("lq_gdn_prefill_ragged", "lq_tree_verify", "lq_state_gather",
+                  "lq_gdn_decode_step", "lq_gdn_window_flush", "lq_gdn_decode_step_flush", "lq_gdn_prefill",
                   "lq_la_prefill", "lq_la_decode_step", "lq_la_decode_step_ragged", "lq_gdn_tree_step",
                   "lq_la_tree_step", "lq_tree_commit",
                   "lq_gdn_decode_step_flush_ragged", "lq_gdn_decode_step_ragged",
