@@ -498,8 +498,9 @@ int lq_tree_commit(const lq_dims *d, const lq_state *st, const int32_t *pos, int
  * w = max(p - c q, 0).  Without a draft (draft NULL: its tokens were certain, e.g.
  * looked up) a child is accepted if u_n S < p(t), and a rejection takes p(t) out of
  * p and of S.  Where nothing is left (S <= 0) the node's other children are not
- * tested and the next token is drawn from p itself; where Z <= 0 it is drawn
- * from what is left.  All of it is computed in 64 bits.
+ * tested and the next token is drawn from p itself, as it is where S stays above
+ * 0 by rounding but no w is positive; where Z <= 0 it is drawn from what is left.
+ * All of it is computed in 64 bits.
  *   d       B (rows) and W (window) only;
  *   pos     int32 [B], buffered tokens of row b, 0..W; a row outside is left
  *           untouched.  At most min(P, W - pos[b]) nodes are accepted, as many as

@@ -10,8 +10,9 @@
 // is the recursion p_{r+1} = max(p_r - q_r, 0) / its sum, since max(max(a, 0) - b, 0) =
 // max(a - b, 0) for b >= 0; a rejected token has p_r(t) < q_r(t), so it drops out of every later
 // p by itself.  Without draft probabilities q is 1 at the child's token: u S < p(t), and a
-// rejection takes t out of p.  Where the walk ends, the next token is drawn from p_r by its
-// distribution function.
+// rejection takes t out of p and of S.  Where the walk ends, the next token is drawn from p_r by its
+// distribution function; if no value of p_r is positive, from p (without draft probabilities S is 1 less
+// the rejected values, so that where a row sums to less than 1 it stays above 0 when all of them are).
 //
 // Everything after the loads is in 64 bits: the sums' order then moves a border by 2^-50 of it,
 // and the nodes' numbers are compared as they are.
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(PT) void verify_pick_kernel(VerifyArgs a) {
     double total = row_sum(sums, tiles, lane);
     const bool later = state == W_TEST;
     // further sums: this workgroup alone.  A draw from nothing is one from the target as it is.
-    while (state == W_TEST || (!(total > 0.0) && s.with_draft && x.rej && x.S > 0.0)) {
+    while (state == W_TEST || (!(total > 0.0) && x.rej && x.S > 0.0)) {
         x.S = total;
         x.summed = true;
         if (state == W_TEST) state = walk_on(s, x) ? W_TEST : W_DRAW;
