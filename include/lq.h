@@ -524,7 +524,7 @@ int lq_tree_commit(const lq_dims *d, const lq_state *st, const int32_t *pos, int
  *   n_path  int32 [B], out;   next  int32 [B], out: the token after them (-1 if no
  *           value after the path is positive, or if target0 is NULL and nothing was
  *           accepted).
- * Probabilities that are NaN count as 0.  All arrays 4-byte aligned (the workspace
+ * Probabilities that are NaN or below 0 count as 0.  All arrays 4-byte aligned (the workspace
  * 16); outputs may not overlap inputs.  workspace: at least
  * lq_verify_workspace_bytes(d, N, V) bytes, as lq_gdn_prefill_ragged's.
  * Errors: LQ_ERR_DIMS if N, P or V < 1, P > N or replace is not 0 or 1;

@@ -113,3 +113,43 @@ def test_a_whole_support_that_is_rejected_without_a_draft(values, V, at_end):
     path, nxt = check(V, [-1] + [0] * N, [1] + tokens, [0.5] + u + [at_end],
                       torch.stack([p] + [none] * N), sure)
     assert path == [0] and nxt in tokens
+
+
+NAN = float("nan")
+
+
+@pytest.mark.parametrize("V", [4, 5003, 70001])
+def test_nan_at_a_child_counts_as_zero(V):
+    """The child with NaN is rejected and changes nothing for the ones after it, nor for the draw."""
+    p, q = torch.zeros(V), torch.full((V,), 0.25 / V)
+    p[:4] = torch.tensor([0.1, NAN, 0.6, 0.3])
+    none = torch.zeros(2, V)
+    assert check(V, [-1, -1], [1, 2], [0.2, 0.2, 0.5], none, p)[0] == [1]
+    path, nxt = check(V, [-1, -1], [1, 2], [0.2, 0.9, 0.3], none, p)      # both rejected: 2 is not drawn
+    assert (path, nxt) == ([], 3)
+    q[1], q[2] = NAN, 0.5
+    for replace in (True, False):
+        p[1] = 0.0
+        assert check(V, [-1, -1], [1, 2], [0.2, 0.2, 0.5], none, p, none, q, replace)[0] == [1]
+        p[1] = 0.01                                        # more than none: accepted
+        assert check(V, [-1, -1], [1, 2], [0.99, 0.2, 0.5], none, p, none, q, replace)[0] == [0]
+    q[2], q[3] = 0.9, NAN                                  # its whole share stays after a rejection
+    assert check(V, [-1], [2], [0.99, 0.4], none[:1], p, none[:1], q) == ([], 3)
+
+
+@pytest.mark.parametrize("mode", ["with", "without", "none"])
+@pytest.mark.parametrize("V", [7, 5003, 70001])
+@pytest.mark.parametrize("seed", range(6))
+def test_nan_anywhere_counts_as_zero(seed, V, mode):
+    """A third of both distributions NaN, drafted tokens among them; siblings and a chain."""
+    g = torch.Generator().manual_seed(100 * seed + V)
+    N = 8
+    logits = 2.0 * torch.randn(N + 1, V, generator=g)
+    spoil = lambda x: torch.where(torch.rand(x.shape, generator=g) < 0.33, NAN, x)
+    t, q = spoil(torch.softmax(logits, -1)), spoil(torch.softmax(logits + 2.0 * torch.randn(N + 1, V, generator=g), -1))
+    parent = [-1, -1, -1, 0, 0, 1, 2, 2] if seed % 2 else [-1] * N
+    token = [int(torch.topk(torch.nan_to_num(t[N] if n < 3 else q[N]), 4).indices[n % 4]) if n % 3 else
+             int(torch.randint(V, (1,), generator=g)) for n in range(N)]
+    u = (torch.rand(N + 1, generator=g) * (1.0 if seed < 3 else 0.1)).tolist()
+    d = dict(draft=q[:N], draft0=q[N], replace=mode == "with") if mode != "none" else {}
+    check(V, parent, token, u, t[:N], t[N], **d)
