@@ -330,7 +330,6 @@ __global__ __launch_bounds__(PT) void verify_pick_kernel(VerifyArgs a) {
         x.S = total;
         x.summed = true;
         if (state == W_TEST) state = walk_on(s, x) ? W_TEST : W_DRAW;
-        if (state == W_DRAW && x.summed && x.S > 0.0) break;       // (the draft ran out: that sum is the draw's)
         __syncthreads();                                           // (the sums before are read)
         const Residual r = residual(a, s, x, b);
         for (int i = w; i < tiles; i += PT / 64) {
