@@ -184,6 +184,10 @@ struct GdnSegArgs {
     int seg;                  // tokens per segment
 };
 
+// A segment after the first without tokens: what the row holds stays, and only the last one has to write it.
+template <bool OUT>
+__device__ __forceinline__ bool past_end(int t0, int len) { return t0 >= len && !(OUT && blockIdx.y == gridDim.y - 1); }
+
 template <int L>
 struct GdnGates {
     double g[L];
@@ -274,7 +278,7 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
     const int te = min(len, t0 + a.seg);
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
     const bool map = !OUT && blockIdx.z;                           // the segment's map: from the identity, without values
-    if (map && blockIdx.y == 0) return;
+    if (blockIdx.y ? past_end<OUT>(t0, len) : map) return;
     const float* start = blockIdx.y == 0 ? a.first : a.start;
 
     // H[rt][ct][v] = H[16 rt + 4 lg + v][CT (16 w + li) + ct]
@@ -768,7 +772,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
     const int te = min(len, t0 + a.seg);
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
     const bool map = !OUT && blockIdx.z;
-    if (map && blockIdx.y == 0) return;
+    if (blockIdx.y ? past_end<OUT>(t0, len) : map) return;
     const float* start = blockIdx.y == 0 ? a.first : a.start;
 
     v4f H[RT];                                                     // H[rt][v] = H[16 rt + 4 lg + v][16 w + li]
@@ -1228,7 +1232,7 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
     const int t0 = (int)blockIdx.y * a.seg, te = min(len, t0 + a.seg);
     const size_t soff = blockIdx.y * a.seg_stride + head * (size_t)(D * D);
     const bool map = !OUT && blockIdx.z;
-    if (map && blockIdx.y == 0) return;
+    if (blockIdx.y ? past_end<OUT>(t0, len) : map) return;
     const float* start = blockIdx.y == 0 ? a.first : a.start;
     v4f H = {0.f, 0.f, 0.f, 0.f};                                  // H[4 lg + v][li]
 #pragma unroll
@@ -1424,8 +1428,17 @@ struct GdnScanArgs {
     float* x;                 // [segments][heads][d*d]: E_s at s + 1, then the states before the segments
     const float* map;         // G_s at s
     float* fin;               // state after the last segment, or null: formed with the outputs
+    const int32_t* lens;      // per batch row, or null: T
     size_t stride;            // floats between segments
+    int T, H, seg;
     int n;                    // states to form: x[2] .. x[n]
+
+    // The last state that tokens change: it stays for the segments after it (a product with the identity would
+    // lose infinities, NaN and the sign of zeros).
+    __device__ __forceinline__ int last(size_t head) const {
+        const int len = lens ? min(max(lens[head / (unsigned)H], 0), T) : T;
+        return min(n, max(1, (len + seg - 1) / seg));
+    }
 };
 constexpr int kScanAhead = 4;
 template <int D, int CT>                                           // CT: neighbouring columns in a lane's tiles
@@ -1438,11 +1451,12 @@ __global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
     // G: row 16 w + li, channels 16 c + 4 lg + e; X: rows 16 w + 4 lg + v of the tile's column li
     const float* g0 = a.map + at + (size_t)w * (16 * D) + 4 * lane;
     float* x0 = reinterpret_cast<float*>(state_at(a.x + at, D / 16, w, blockIdx.y, lane));
+    const int last = a.last(blockIdx.x);
     struct Step {
         v4f g[KS][2], e;
     };
     auto load = [&](int s, Step& y) {                              // kScanAhead steps before their use
-        if (s > a.n) return;
+        if (s > last) return;
         const float* g = g0 + (s - 1) * a.stride;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
@@ -1485,10 +1499,11 @@ __global__ __launch_bounds__(4 * D) void gdn_scan_kernel(GdnScanArgs a) {
     x = *reinterpret_cast<const v4f*>(x0 + a.stride);
 #pragma unroll
     for (int i = 0; i < kScanAhead; ++i) load(2 + i, y[i]);
-    for (int s = 2; s <= a.n; s += kScanAhead)
+    for (int s = 2; s <= last; s += kScanAhead)
 #pragma unroll
         for (int i = 0; i < kScanAhead; ++i)
-            if (s + i <= a.n) step(s + i, y[i]);
+            if (s + i <= last) step(s + i, y[i]);
+    if (last < a.n) *reinterpret_cast<v4f*>(x0 + a.n * a.stride) = x;
     if (a.fin)
 #pragma unroll
         for (int v = 0; v < 4; ++v) a.fin[at + (size_t)(16 * w + 4 * lg + v) * D + CT * (16 * (blockIdx.y / CT) + li) + blockIdx.y % CT] = x[v];
@@ -1504,7 +1519,8 @@ __global__ __launch_bounds__(256) void gdn_scan16_kernel(GdnScanArgs a, int head
     v4f x;
 #pragma unroll
     for (int v = 0; v < 4; ++v) x[v] = x0[a.stride + 16 * v];
-    for (int s = 2; s <= a.n; ++s) {
+    const int last = a.last(head);
+    for (int s = 2; s <= last; ++s) {
         const v4f g = *reinterpret_cast<const v4f*>(g0 + (s - 1) * a.stride);
         v4f u;
 #pragma unroll
@@ -1515,6 +1531,9 @@ __global__ __launch_bounds__(256) void gdn_scan16_kernel(GdnScanArgs a, int head
 #pragma unroll
         for (int v = 0; v < 4; ++v) x0[s * a.stride + 16 * v] = x[v];
     }
+    if (last < a.n)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) x0[a.n * a.stride + 16 * v] = x[v];
     if (a.fin)
 #pragma unroll
         for (int v = 0; v < 4; ++v) a.fin[(size_t)head * 256 + (4 * lg + v) * 16 + li] = x[v];
@@ -1585,7 +1604,7 @@ hipError_t gdn_chunks(const lq_dims& d, const GdnPrefillArgs& args, void* worksp
     hipError_t e = chunk_launch<D, KDA, TI, false>(dim3((unsigned)heads, (unsigned)n, n > 1 ? 2 : 1), sa, s);
     if (e != hipSuccess) return e;
     if (n > 1 || !args.o) {
-        const GdnScanArgs sc{x, map, args.o ? nullptr : args.h, stride, n};
+        const GdnScanArgs sc{x, map, args.o ? nullptr : args.h, args.lens, stride, args.T, args.H, seg, n};
         if constexpr (D == 16)
             e = launch_kernel(LQ_KERNEL_PREFILL, gdn_scan16_kernel, dim3((unsigned)(heads + 3) / 4), dim3(256), s, sc, (int)heads);
         else
