@@ -319,6 +319,10 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  *   workspace  device memory of at least lq_gdn_workspace_bytes(d, T) bytes,
  *          16-byte aligned (NULL if that is 0), used until the call's work on
  *          `stream` is done: calls that may run at the same time need their own.
+ * With a decay per key channel and T > 4 the operands also hold up to 32 tokens' decays and
+ * their inverses, of up to 2^92: results are finite where products of a key's value
+ * and beta (v - k^T D H) stay below 2^64, and the strongest decays leave 24 bits to states
+ * from 2^-68 and to keys and queries from 2^-45 on.
  * T = 0 (or a row with no tokens) copies h0 to h.  A token that is not finite
  * reaches its own and later tokens only (a v its own column only).  The result of
  * a row does not depend on earlier calls, on the workspace's content or on what
