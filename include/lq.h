@@ -552,8 +552,10 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  *   dst, src  host arrays of n_layers states (n_layers >= 1; d holds for all of them,
  *           except that src's have src_rows rows).  A layer's dst and src are the
  *           same arrays (in place: src_rows = d->B, at most 2048) or do not
- *           overlap; different layers' arrays do not overlap comp_idx and,
- *           with a decay per head, buf_g need 4-byte alignment only;
+ *           overlap.  No array that is written (dst's, pos_out) overlaps another
+ *           one of the call, of whichever layer or field; what is only read may be
+ *           shared.  comp_idx and, with a decay per head, buf_g need 4-byte
+ *           alignment only;
  *   index   int32 [B] (device, 4-byte aligned): a row of src; LQ_ROW_CLEAR: an empty
  *           state (the codec of a zero state, no window); any other value, e.g.
  *           LQ_ROW_KEEP: the row is left as it was;
@@ -561,11 +563,11 @@ size_t lq_verify_workspace_bytes(const lq_dims *d, int32_t N, int32_t V);
  *           rows; the window's slots before them move, later slots of dst stay.
  *           NULL: the windows are empty (after a prompt or a flush), and the
  *           states' buffers may be NULL;
- *   pos_out nullable int32 [B] (device, 4-byte aligned), not overlapping pos,
- *           index or a state: the positions of the rows that moved (0: cleared;
+ *   pos_out nullable int32 [B] (device, 4-byte aligned): the positions of the rows that moved (0: cleared;
  *           pos NULL: 0), the others are left as they were.
  * Errors: LQ_ERR_DIMS if n_layers or src_rows < 1; LQ_ERR_UNSUPPORTED in place with
- * B > 2048, or H > 2^17; LQ_ERR_OVERLAP; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ * B > 2048, or H > 2^17, or more layers than the host has memory to compare; LQ_ERR_OVERLAP;
+ * LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
 enum { LQ_ROW_KEEP = -1, LQ_ROW_CLEAR = -2 };
 int lq_state_gather(const lq_dims *d, int32_t n_layers, const lq_state *dst, const lq_state *src,

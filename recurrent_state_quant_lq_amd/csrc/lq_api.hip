@@ -4,8 +4,11 @@
 #include "la.h"
 #include "lq_internal.h"
 
+#include <algorithm>
 #include <atomic>
+#include <memory>
 #include <mutex>
+#include <new>
 #include <vector>
 
 namespace {
@@ -115,14 +118,25 @@ int check_verify(const lq_dims* d, int32_t N, int32_t V) {
     return LQ_OK;
 }
 
-// Whether [a, a + n) and [b, b + m) share a byte.
-bool overlap(const void* a, size_t n, const void* b, size_t m) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return a && b && x < y + m && y < x + n;
+// Bytes [at, end) that a call reads or writes; written in the lowest bit of end (the arrays consist of words).
+struct Range {
+    uintptr_t at, end;
+};
+// Whether a written range shares a byte with another one (sorts them).
+bool any_overlap(Range* r, size_t n) {
+    std::sort(r, r + n, [](const Range& a, const Range& b) { return a.at < b.at; });
+    uintptr_t all = 0, written = 0;      // ends of the ranges, and of the written ones, before r[i]
+    for (size_t i = 0; i < n; ++i) {
+        const bool out = r[i].end & 1;
+        if (r[i].at < (out ? all : written)) return true;
+        const uintptr_t end = r[i].end & ~(uintptr_t)1;
+        all = std::max(all, end);
+        written = std::max(written, out ? end : 0);
+    }
+    return false;
 }
 
-// A gather's layers: the same arrays in place, or apart; and apart from one another (the int8
-// states stand for their layers there).
+// A gather's layers: the same arrays in place, or apart; whatever is written apart from all else.
 int check_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const lq_state* src, int32_t src_rows,
                  const int32_t* index, const int32_t* pos, int32_t* pos_out) {
     const size_t H = d->H, dk = d->dk, C = d->C, W = d->W, gd = d->decay_mode == LQ_DECAY_PER_KEY ? dk : 1;
@@ -130,6 +144,17 @@ int check_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const 
                            H * W * dk * 4, H * W * dk * 4, H * W * gd * 4};
     const size_t B = d->B, S = src_rows;
     const int fields = pos ? 8 : 5;
+    constexpr size_t kHere = 512;        // 31 layers with their windows, out of place
+    const size_t most = (size_t)n_layers * 16 + 3;
+    Range here[kHere];
+    const std::unique_ptr<Range[]> more(most > kHere ? new (std::nothrow) Range[most] : nullptr);
+    if (most > kHere && !more) return LQ_ERR_UNSUPPORTED;
+    Range* const r = most > kHere ? more.get() : here;
+    size_t n = 0;
+    auto add = [&](const void* x, size_t bytes, bool written) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(x);
+        if (x) r[n++] = Range{at, at + bytes + written};
+    };
     for (int32_t l = 0; l < n_layers; ++l) {
         const void* x[8] = {dst[l].sq, dst[l].row_scale, dst[l].col_scale, dst[l].comp_idx, dst[l].comp_val,
                             dst[l].buf_k, dst[l].buf_m, dst[l].buf_g};
@@ -139,18 +164,15 @@ int check_gather(const lq_dims* d, int32_t n_layers, const lq_state* dst, const 
         if (same && B > lq::kGatherInPlace) return LQ_ERR_UNSUPPORTED;
         for (int f = 0; f < fields; ++f) {
             if (row[f] == 0) continue;
-            if (same ? x[f] != y[f] || S != B : overlap(x[f], B * row[f], y[f], S * row[f])) return LQ_ERR_OVERLAP;
-            if (overlap(x[f], B * row[f], index, B * 4) || overlap(x[f], B * row[f], pos, S * 4)) return LQ_ERR_OVERLAP;
-            if (overlap(x[f], B * row[f], pos_out, B * 4) || overlap(y[f], S * row[f], pos_out, B * 4)) return LQ_ERR_OVERLAP;
+            if (same && (x[f] != y[f] || S != B)) return LQ_ERR_OVERLAP;
+            add(x[f], B * row[f], true);
+            if (!same) add(y[f], S * row[f], false);
         }
-        for (int32_t m = 0; m < l; ++m)
-            if (overlap(dst[l].sq, B * row[0], dst[m].sq, B * row[0]) ||
-                overlap(dst[l].sq, B * row[0], src[m].sq, S * row[0]) ||
-                overlap(src[l].sq, S * row[0], dst[m].sq, B * row[0]))
-                return LQ_ERR_OVERLAP;
     }
-    if (overlap(pos_out, B * 4, index, B * 4) || overlap(pos_out, B * 4, pos, S * 4)) return LQ_ERR_OVERLAP;
-    return LQ_OK;
+    add(index, B * 4, false);
+    add(pos, S * 4, false);
+    add(pos_out, B * 4, true);
+    return any_overlap(r, n) ? LQ_ERR_OVERLAP : LQ_OK;
 }
 
 int finish(hipError_t e) {
