@@ -82,7 +82,7 @@ enum lq_status {
     LQ_ERR_ALIGN = 6,         /* a pointer is misaligned (see conventions) */
     LQ_ERR_HIP = 7,           /* kernel launch failed, see lq_last_hip_error() */
     LQ_ERR_WORKSPACE = 8,     /* workspace smaller than the call's lq_*_workspace_bytes() */
-    LQ_ERR_OVERLAP = 9        /* lq_state_gather: arrays overlap other than as the same state */
+    LQ_ERR_OVERLAP = 9        /* arrays overlap where they may not (lq_state_gather, lq_gdn_prefill_ragged) */
 };
 
 enum lq_decay_mode { LQ_DECAY_SCALAR = 0, LQ_DECAY_PER_KEY = 1 };
@@ -334,7 +334,7 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  * (lq_gdn_workspace_bytes = 0) computes a row in the same order, so that there its
  * bits are the same whatever B and T.
  * Errors: LQ_ERR_POS if T < 0, LQ_ERR_UNSUPPORTED if T > 2^30 or B*H > 2^23;
- * LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
+ * LQ_ERR_OVERLAP (h and h0); LQ_ERR_WORKSPACE; LQ_ERR_NULL, LQ_ERR_ALIGN.
  */
 int lq_gdn_prefill_ragged(const lq_dims *d, const lq_state *st, const float *h0, float *h, int32_t T,
                           const void *q, const void *k, const void *v, const float *alpha,

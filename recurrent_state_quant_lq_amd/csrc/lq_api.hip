@@ -118,6 +118,12 @@ int check_verify(const lq_dims* d, int32_t N, int32_t V) {
     return LQ_OK;
 }
 
+// Whether [a, a + n) and [b, b + n) share a byte without being the same.
+bool shifted(const void* a, const void* b, size_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && x < y + n && y < x + n;
+}
+
 // Bytes [at, end) that a call reads or writes; written in the lowest bit of end (the arrays consist of words).
 struct Range {
     uintptr_t at, end;
@@ -470,6 +476,7 @@ int lq_gdn_prefill_ragged(const lq_dims* d, const lq_state* st, const float* h0,
     if (lens && !aligned4(lens)) return LQ_ERR_ALIGN;
     if (T < 0) return LQ_ERR_POS;
     if (T > lq::kGdnMaxTokens || (int64_t)d->B * d->H > lq::kGdnMaxHeads) return LQ_ERR_UNSUPPORTED;
+    if (h0 && shifted(h0, h, (size_t)d->B * d->H * d->dk * d->dv * sizeof(float))) return LQ_ERR_OVERLAP;
     if (T > 0 && (rc = check_tokens(d, q, k, v, alpha, beta, o, false))) return rc;
     if ((rc = check_workspace(lq_gdn_workspace_bytes(d, T), workspace, workspace_bytes))) return rc;
     const hipStream_t s = (hipStream_t)stream;

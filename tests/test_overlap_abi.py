@@ -83,3 +83,17 @@ def test_fields_that_are_not_the_same():
     x = [list(s) for s in dst]
     x[0][5] = x[1][5] = x[0][0]
     assert _gather(d, x, src, 2, pos=None, pos_out=A) == lq.LQ_ERR_OVERLAP      # (the index)
+
+
+@pytest.mark.parametrize("T", [0, 4, 300])
+def test_prompt_states_that_are_shifted(T):
+    """h is h0 or apart from it; what is accepted is shown by the check after it (the workspace's, or the queries')."""
+    d = _dims()
+    size, h = d.B * d.H * d.dk * d.dv * 4, 0x10000000
+    call = lambda h0, q: lq.load().lq_gdn_prefill_ragged(ct.byref(d), None, ct.c_void_p(h0), ct.c_void_p(h), T, q, A, A, A,
+                                                         A, None, A, None, 0, None)
+    for off in (16, size - 16, 16 - size, -16):
+        assert call(h + off, A) == lq.LQ_ERR_OVERLAP
+    if T:
+        for off in (0, size, -size):
+            assert call(h + off, None) == lq.LQ_ERR_NULL
