@@ -7,9 +7,9 @@
 // slab of columns for every row, and per step loads the pieces of all the moved rows into
 // registers, passes a barrier, and only then stores.  The step's width follows from the number
 // of moved rows, which only the device knows: as many columns as the registers take.  Bound by memory:
-// 56 of 64 rows of two layers (32 heads, d = 128) 26 us (4.4 TB/s), a third of 256 rows 26 us (4.5), from and to
-// states that no cache holds.  Stores pass by the caches (kept there they push out what other workgroups are about to
-// read: 39 and 34 us); loads do not (many rows may read one: 38 and 30 us).
+// 56 of 64 rows of two layers (32 heads, d = 128) 25 us (4.5 TB/s), a third of 256 rows 23 us one call at a time and 31
+// through six states in turn, which no cache holds.  Stores pass by the caches (kept there they push out what
+// other workgroups are about to read: 38 and 35 us); loads do not (many rows may read one).
 #include "gdn.h"
 
 namespace lq {
@@ -122,7 +122,7 @@ hipError_t launch_gather(const lq_dims& d, int n_layers, const lq_state* dst, co
     const uint32_t units[kFields] = {H * dk * dk / 16, H * dk / 4, H * dk / 4, H * C, H * C * dk / 4,
                                      H * W * dk / 4, H * W * dk / 4, per_key ? H * W * dk / 4 : H * W};
     // slabs: runs of 256 bytes to 4 KB of a row, as long as there are kSlabs of them.  Few rows that move cost a
-    // slab's latencies, many its steps.  Measured for 1024, 2048, 4096 and 8192 slabs: 24 layers, 64 rows of 16
+    // slab's latencies, many its steps.  Measured (stores through the caches) for 1024, 2048, 4096 and 8192 slabs: 24 layers, 64 rows of 16
     // heads, 4 moved 20, 16, 17, 23 us; one layer, 256 rows of 32 heads, a third moved 29, 26, 26, 26; two
     // layers, 64 rows, 56 moved 29, 28, 26, 28.
     uint64_t all = 0;

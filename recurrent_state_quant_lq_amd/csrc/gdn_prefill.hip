@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void gdn_step_kernel(GdnPrefillArgs a) {
 // forms for all columns (block_solve against the identity), on the fp32 instruction.
 // A product of a masked zero with a value that is not finite would spread it to earlier tokens: a
 // chunk ends before such a token, which is then the first of its chunk.
-// Bound by the two issue ports of a SIMD in turn: 2048 heads of 512 tokens (d = 128) 515 us, vector 0.56 and
+// Bound by the two issue ports of a SIMD in turn: 2048 heads of 512 tokens (d = 128) 512 to 565 us, vector 0.56 and
 // matrix 0.53 of the waves' time (two waves a SIMD; 0.96 PFLOP/s of matrix work, a large product of the library
 // 1.22, both with the clock that the power leaves); LDS 0.42.  Four waves of 32 columns, since each wave reads
 // all of K and Q: eight of 16 took 588 us.  Not kept: the parts of H formed in between the products by
@@ -725,10 +725,13 @@ __global__ __launch_bounds__(GB<D>::NT, GB<D>::WPE) void gdn_chunk_kernel(GdnSeg
 // 458, not 474 us).
 // bf16 values are loaded by lanes in pairs, two columns of every second row each (512 heads of 1024 tokens at
 // d = 64, per key, 206, not 214 us, with a load a value).
-// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 445 us (bf16): two workgroups
-// a CU, vector 0.66, matrix 0.47, LDS 0.55 of the time; a quarter of a chunk's is the forming of the rows'
-// parts.  fp32, 192 heads of up to 1021 tokens 211 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
-// (0.45, 0.39, 0.39); 512 heads of 512 tokens 216 us (0.67, 0.59, 0.58).  Six bf16 products
+// Bound by vector, matrix and LDS time in turn.  Per key, 1024 heads of 512 tokens 465 to 485 us (bf16): two workgroups
+// a CU, vector 0.70, matrix 0.48, LDS 0.56 of the time; a quarter of a chunk's is the forming of the rows'
+// parts.  That is with decays of down to 2^-2.9 a token, whole chunks; if one channel of a head decays faster, a chunk
+// holds the 92 / -log2(alpha) tokens after its first one, each cut one is loaded and split twice, and the time grows: 730 us at
+// 2^-4, 1220 at 2^-8, 2370 at 2^-16, 14000 where a channel forgets every token (chunks of one).  fp32, 192 heads of
+// up to 1021 tokens 209 us: one workgroup a CU, the longest row's 32 chunks, 6.6 us each
+// (0.45, 0.39, 0.39); 512 heads of 512 tokens 216 to 226 us (0.67, 0.59, 0.58).  Six bf16 products
 // take 96 cycles where the fp32 instruction takes 256.
 constexpr int GF = 32;        // tokens per chunk
 constexpr float kMinDecay = 0x1p-92f;
@@ -1226,7 +1229,7 @@ __global__ __launch_bounds__((GF32<D, KDA>::NT), 4) void gdn_chunk32_kernel(GdnS
 // scores are formed transposed, so that their accumulators are the A operand of P M as they are;
 // only A goes through LDS, for block_solve.  Per key: the same factors as the larger kernel's.
 // Bound by a wave's chain of dependent products, two waves a SIMD (vector 0.53, matrix 0.25): 2048 heads of
-// 512 tokens 107 us, per key 106.
+// 512 tokens 106 us, per key 107 (142 if a channel takes 2^-8 a token, 273 at 2^-16, 1400 where one forgets every token).
 // The value of the lane that far before in the row of 16, 1 where there is none.
 template <int CTRL>
 __device__ __forceinline__ float dpp_one(float x) {
@@ -1448,8 +1451,9 @@ __global__ __launch_bounds__(256) void gdn_small_kernel(GdnSegArgs a) {
 // G of all segments, the scan joins them (X_{s+1} = G_s X_s + E_s, in E's place), and the last one
 // computes every segment's outputs from the state before it.  A workgroup of the scan owns 16
 // columns of a head's state, wave w its rows 16 w ..; both factors in three bf16 parts: G's rows are
-// split from registers, loaded four steps ahead, X's columns go through LDS.  A step is a chain (barrier, LDS,
-// twelve products) of 1.5 us whatever the heads: 16 heads at d = 128, 8 segments 12 us, 16 segments 24.
+// split from registers, loaded four steps ahead, X's columns go through LDS.  A step takes 1.5 us whatever the heads:
+// every workgroup of a head splits the same G, so that the two waves a SIMD fill 0.59 of the vector port, and the chain of
+// barrier, LDS and twelve products waits for 0.28 of it.  16 heads at d = 128: 8 segments 12 us, 16 segments 24.
 struct GdnScanArgs {
     float* x;                 // [segments][heads][d*d]: E_s at s + 1, then the states before the segments
     const float* map;         // G_s at s

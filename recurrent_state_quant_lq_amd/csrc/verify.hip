@@ -24,10 +24,11 @@
 // or small rows it does all of it (kAloneRows).
 // Bound by the sum's reads and by the latencies before them (positions and nodes, the nodes'
 // values, the row): 64 rows of 131072 values with a draft 11 us and 7 for the pick (the rows partly in the
-// Infinity Cache), one row of 32000 5.4 and 6.6; alone, 256 rows of 50021 without a draft 18 (two
-// launches: 14 and 7).  Nodes with several children need a sum for each rejection, one after the other, each at
-// the 64 bytes a cycle that a CU takes: trees of 32 nodes, 64 rows, 9 and 32 us (drafted without replacement),
-// 11 and 60 (with).  One and two further launches of the sum kernel before the pick took 66 and 75 us, not 61,
+// Infinity Cache), one row of 32000 5.5 and 6.3; alone, 256 rows of 50021 without a draft 18 (two
+// launches: 14 and 7), 51 MB in all, waits 0.6 of the waves' time.  Nodes with several children need a sum for each
+// rejection, one after the other, on one CU: both rows at its 64 bytes a cycle, and as long again eight vector
+// operations a value beside that.  Trees of 32 nodes, 64 rows, 28 to 55 us by what is rejected (drafted without
+// replacement; the first sum 11 of them), 57 to 91 (with).  One and two further launches of the sum kernel before the pick took 66 and 75 us, not 61,
 // there (102 and 105, not 95), and the pick's sums with 256 threads 127, not 105.  A quad of a row is loaded
 // without a bounds test where its whole tile is inside (24 us, not 9, with one per quad).
 #include "gdn.h"
