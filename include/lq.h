@@ -326,11 +326,11 @@ int lq_gdn_prefill(const lq_dims *d, const lq_state *st, float *h, int32_t T,
  * With a decay per key channel and T > 4 the operands also hold up to 32 tokens' decays and
  * their inverses, of up to 2^92: results are finite where products of a key's value
  * and beta (v - k^T D H) stay below 2^64, and the strongest decays leave 24 bits to states
- * from 2^-68 and to keys and queries from 2^-45 on.  Its time then depends on the decays: a
- * chunk ends where a channel has lost 2^-92 since the chunk's first token (1024 heads of 512
- * tokens, d = 128, bf16: 465 us with any decays down to 2^-2.9 a token, 730 if one channel of
- * each head takes 2^-4, 1220 at 2^-8, 2370 at 2^-16, 14000 if it forgets every token;
- * lq_gdn_prefill 993 us always).
+ * from 2^-68 and to keys and queries from 2^-45 on (a decay below 2^-92 may count as 0).
+ * Its time then depends on the decays: a chunk ends where a channel has lost 2^-92 since
+ * the chunk's first token.  1024 heads of 512 tokens, d = 128, bf16: 465 us with any decays
+ * down to 2^-2.9 a token, 730 if one channel of each head takes 2^-4, 1220 at 2^-8, 2370
+ * at 2^-16, 14000 if it forgets every token; lq_gdn_prefill 993 us always.
  * T = 0 (or a row with no tokens) copies h0 to h.  A token that is not finite
  * reaches its own and later tokens only (a v its own column only).  The result of
  * a row does not depend on earlier calls, on the workspace's content or on what
